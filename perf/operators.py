@@ -205,17 +205,19 @@ def prepare(case, seed):
         dtype = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[case["dtype"]]
         shapes, groups = _clip_shapes(case)
         total = sum(a * b for a, b in shapes)
-        pad = len(shapes) if case["odd"] else 0
-        flat = torch.randn(total + pad, generator=gen, device="cuda").mul_(1e-2).to(dtype)
+        gap = 1 if case["odd"] else 0      # an element between tensors: addresses aligned to the element alone
+        flat = torch.zeros(total + gap * len(shapes), dtype=dtype, device="cuda")
         out_flat = torch.zeros_like(flat)
-        grads, out, pos = [], [], 0
+        values = torch.randn(total, generator=gen, device="cuda").mul_(1e-2).to(dtype)
+        grads, out, pos, taken = [], [], 0, 0
         for a, b in shapes:
-            pos += 1 if case["odd"] else 0      # an address that is aligned to the element alone
+            pos += gap
             grads.append(flat[pos:pos + a * b].view(a, b))
             out.append(out_flat[pos:pos + a * b].view(a, b))
-            pos += a * b
+            grads[-1].copy_(values[taken:taken + a * b].view(a, b))
+            pos, taken = pos + a * b, taken + a * b
         norm = 1e-2 * math.sqrt(total / case["groups"])
-        state = dict(op="clip", grads=grads, out=out, out_flat=out_flat, groups=groups, n_groups=case["groups"],
+        state = dict(op="clip", grads=grads, out=out, flat=flat, out_flat=out_flat, groups=groups, n_groups=case["groups"],
                      max_norm=norm * (0.3 if case["clipped"] else 3.0))
         if own:
             import quantized_lora_fine_lq_amd as lq
@@ -271,70 +273,63 @@ def _constants(w):
 def _weight(w):
     """W' [N, K] as float32 (exactly bfloat16 values)."""
     N, K = w["N"], w["K"]
-    nb = K // BLOCK
-    c = _constants(w)
+    codes = w["codes"]
     if w["kind"] == "codebook":
-        out = torch.empty(N, K, device=c.device)
-        shifts = torch.arange(8, device=c.device, dtype=torch.int32)
-        for b in (1, 2, 3, 4):
-            rows = (w["row_bits"] == b).nonzero()[:, 0]
-            if rows.numel() == 0:
-                continue
-            at = w["row_offset"][rows][:, None] + torch.arange(nb * b * 8, device=c.device)
-            body = w["codes"][at].reshape(-1, nb, b, 8).int()
-            code = torch.zeros(rows.numel(), nb, BLOCK, device=c.device, dtype=torch.int32)
-            for p in range(b):
-                code += ((body[:, :, p, :, None] >> shifts) & 1).reshape(-1, nb, BLOCK) << p
-            out[rows] = torch.gather(w["levels"][rows], 1, code.reshape(rows.numel(), K).long())
+        k, p = torch.arange(K, device=codes.device), torch.arange(4, device=codes.device)
+        b = w["row_bits"].int()[:, None, None]
+        at = (k // BLOCK * 8)[None, :, None] * b + (k % BLOCK // 8)[:, None] + 8 * torch.minimum(p, b - 1)
+        bit = (codes[at + w["row_offset"][:-1, None, None]] >> (k % 8).to(torch.uint8)[:, None]) & 1
+        code = ((bit * (p < b)) << p).sum(2)
+        out = torch.gather(w["levels"], 1, code)
     else:
-        codes = w["codes"]
         both = torch.stack([codes >> 4, codes & 15], 1).reshape(-1)
-        out = w["levels"][both.int()].reshape(N, K)
-    out = (out.reshape(-1, BLOCK) * c[:, None]).to(torch.bfloat16).float()
+        out = w["levels"][both.int()]
+    out = (out.reshape(-1, BLOCK) * _constants(w)[:, None]).to(torch.bfloat16).float()
     return out.reshape(N, K)
 
 
+def _owners(st):
+    """The adapters side by side: for column j of all R = sum of r_a columns, its adapter, its place
+    in it and its scale; and on [M, R], where the column belongs to the token's adapter."""
+    dev = st["ids"].device
+    r = torch.tensor([A.shape[0] for A, _, _ in st["adapters"]])
+    owner = torch.repeat_interleave(torch.arange(len(r)), r)
+    place = torch.arange(owner.numel()) - (r.cumsum(0) - r)[owner]
+    scale = torch.tensor([alpha / A.shape[0] for A, _, alpha in st["adapters"]])[owner]
+    owner, place, scale = owner.to(dev), place.to(dev), scale.to(dev)
+    return owner, place, scale, (st["ids"][:, None] == owner).float()
+
+
 def _plain_forward(st):
-    W, X = _weight(st["w"]), st["X"].float()
-    H = X @ W.T
+    X = st["X"].float()
+    A = torch.cat([A for A, _, _ in st["adapters"]]).float()
+    B = torch.cat([B for _, B, _ in st["adapters"]], 1).float()
+    owner, place, scale, on = _owners(st)
+    T = (X @ A.T) * on
+    H = X @ _weight(st["w"]).T + (T * scale) @ B.T
     t = torch.zeros(X.shape[0], max(A.shape[0] for A, _, _ in st["adapters"]), device=X.device)
-    for a, (A, B, alpha) in enumerate(st["adapters"]):
-        rows = (st["ids"] == a).nonzero()[:, 0]
-        if rows.numel() == 0:
-            continue
-        r = A.shape[0]
-        ta = X[rows] @ A.float().T
-        t[rows, :r] = ta
-        H[rows] += (alpha / r) * (ta @ B.float().T)
+    t.index_add_(1, place, T)      # a token's columns but its own adapter's are zero
     return {"H": H.to(st["out"]), "t": t}
 
 
 def _plain_backward(st):
-    W, X, G = _weight(st["w"]), st["X"].float(), st["G"].float()
-    gx = G @ W
-    dA, dB = [], []
-    for a, (A, B, alpha) in enumerate(st["adapters"]):
-        rows = (st["ids"] == a).nonzero()[:, 0]
-        r = A.shape[0]
-        s = alpha / r
-        Xa, Ga = X[rows], G[rows]
-        t = Xa @ A.float().T if st["t"] is None else st["t"][rows, :r]
-        u = Ga @ B.float()
-        gx[rows] += s * (u @ A.float())
-        dA.append(s * (u.T @ Xa))
-        dB.append(s * (Ga.T @ t))
-    return {"grad_X": gx.to(torch.bfloat16), "dA": torch.cat(dA), "dB": torch.cat([d.reshape(-1) for d in dB])}
+    X, G = st["X"].float(), st["G"].float()
+    A = torch.cat([A for A, _, _ in st["adapters"]]).float()
+    B = torch.cat([B for _, B, _ in st["adapters"]], 1).float()
+    owner, place, scale, on = _owners(st)
+    T = (X @ A.T if st["t"] is None else st["t"][:, place]) * on * scale
+    U = (G @ B) * on * scale
+    gx = G @ _weight(st["w"]) + U @ A
+    dB = torch.split(G.T @ T, [B.shape[1] for _, B, _ in st["adapters"]], 1)
+    return {"grad_X": gx.to(torch.bfloat16), "dA": U.T @ X, "dB": torch.cat([d.reshape(-1) for d in dB])}
 
 
 def _plain_clip(st):
-    sq = torch.zeros(st["n_groups"], device=st["grads"][0].device)
-    for g, x in zip(st["groups"], st["grads"]):
-        xf = x.float()
-        sq[g] += (xf * xf).sum()
-    norms = sq.sqrt()
+    # the jobs' gradients are equal shares of one buffer (zeros between the tensors)
+    x = st["flat"].float().view(st["n_groups"], -1)
+    norms = (x * x).sum(1).sqrt()
     coef = (st["max_norm"] / (norms + EPS)).clamp(max=1.0)
-    for g, x, o in zip(st["groups"], st["grads"], st["out"]):
-        o.copy_((x.float() * coef[g]).to(x.dtype))
+    st["out_flat"].copy_((x * coef[:, None]).view(-1))
     return {"norms": norms, "grads": st["out_flat"]}
 
 
