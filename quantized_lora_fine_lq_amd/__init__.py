@@ -528,3 +528,8 @@ def quantize_codebook(W, row_bits, thresholds, blocksize: int = 64):
                                     _ptr(thresholds), _ptr(codes), _ptr(absmax), _stream(W.device)),
            "lq_quantize_codebook")
     return codes, absmax, row_offset
+
+
+# many adapters over one projection, gradient norms and clipping
+from .adapters import (AdapterSet, GradList, adapter_route, adapters_backward, adapters_forward,  # noqa: E402
+                       clip_grad_norm, grad_norm)

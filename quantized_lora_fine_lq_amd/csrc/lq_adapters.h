@@ -1,0 +1,103 @@
+// Internal declarations of the many-adapter path (include/lq_adapters.h).
+#pragma once
+
+#include "../../include/lq_adapters.h"
+#include "lq_internal.h"
+
+namespace lq {
+
+// A route's arrays (lq_adapter_route): sorted positions by adapter.
+struct Route {
+  const int32_t* off;    // [n + 2]
+  const int32_t* perm;   // [M] token of a sorted position
+  const int32_t* sid;    // [M] adapter of a sorted position (n: none)
+};
+inline int64_t route_words(int64_t M, int32_t n) { return ((int64_t)n + 2 + 3) / 4 * 4 + 2 * ((M + 3) / 4 * 4); }
+inline Route route_view(const int32_t* p, int64_t M, int32_t n) {
+  const int64_t a = ((int64_t)n + 2 + 3) / 4 * 4, b = (M + 3) / 4 * 4;
+  return Route{p, p + a, p + a + b};
+}
+hipError_t launch_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_t* route, hipStream_t s);
+
+// The set as the kernels see it. rs: row stride (floats) of the t and u
+// workspaces, r_max rounded up to a multiple of 8.
+struct AdapterView {
+  const lq_adapter* tab;   // device
+  int32_t n;
+  int32_t r_max;
+  int32_t rs;
+};
+
+// Row form over routed tokens: out[m][j] = sum_c Q[m][c] R_a[j][c], j < r_a.
+struct DownJob {
+  const uint16_t* Q;       // [M, C] bf16
+  int64_t C;               // C % 8 == 0
+  const uint16_t* rbase;   // R_a at rbase + C * row8_a, or null: A_a of the table
+  float* out;              // [M, rs] (zero from r_a to rs)
+  float* save;             // [M, r_max] or null (zero past r_a and for tokens without an adapter)
+};
+hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
+                               hipStream_t s);
+
+// The adapters transposed for the backward: at [K, r8] at K * row8_a
+// (zero columns past r_a) and bt [r, N] at N * row8_a; either may be null.
+hipError_t launch_adapter_transpose(const AdapterView& v, int64_t N, int64_t K, uint16_t* at, uint16_t* bt,
+                                    hipStream_t s);
+
+// Column form over routed tokens: out_a[j][c] = scale_a sum over a's tokens
+// of P[m][j] Q[m][c], written [r, C] at C * row_a, or transposed [C, r].
+struct ColReq {
+  const float* P;      // [M, pstride]
+  int32_t pstride;
+  const uint16_t* Q;   // [M, C] bf16, C % 8 == 0
+  int64_t C;
+  float* out;
+  int transposed;
+  float* part;         // adapter_col_ws_floats
+};
+size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs);
+hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const AdapterView& v, const Route& rt,
+                              hipStream_t s);
+
+// out[token][c] = sum_k A[token][k] Bt[c][k] + s_a sum_j L[token][j] Lb_a(c, j)
+// over the sorted positions; Lb_a = B_a (lt null) or A_a^T from lt (+ Ncols *
+// row8_a, [Ncols, r8]).
+struct AdapterGemm {
+  const uint16_t* A;     // [M, Kc]
+  int64_t M, Ncols, Kc;
+  const uint16_t* Bt;    // [Ncols, ldb], ldb % 64 == 0, zero from Kc to ldb
+  int64_t ldb;
+  const float* L;        // [M, rs]
+  AdapterView v;
+  const uint16_t* lt;
+  Route rt;
+  void* out;             // [M, Ncols] bf16 or float32
+  int out_f32;
+  const uint16_t* zeros; // 16 zero bytes, read past Kc
+};
+hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s);
+// [N, K] -> [K, ldb] bf16 (zero columns from N to ldb), and 16 zero bytes at zeros.
+hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out, hipStream_t s);
+hipError_t launch_zero16(uint16_t* p, hipStream_t s);
+
+// ---- gradient lists ----------------------------------------------------------
+struct GradPiece {
+  void* data;
+  int32_t count;
+  int32_t dtype;
+};
+struct GradSlot {
+  int32_t first, count;        // pieces
+  int32_t group;
+  int32_t group_first;         // first slot of the group
+  int32_t group_count;         // slots of the group
+  int32_t pad[3];
+};
+constexpr int kGradThreads = 256;
+hipError_t launch_grad_squares(const GradSlot* slots, const GradPiece* pieces, int32_t n_slots, double* part,
+                               hipStream_t s);
+hipError_t launch_grad_norms(const GradSlot* slots, int32_t n_slots, const double* part, float* norms, hipStream_t s);
+hipError_t launch_grad_clip(const GradSlot* slots, const GradPiece* in, const GradPiece* out, int32_t n_slots,
+                            const double* part, float max_norm, float eps, float* norms, hipStream_t s);
+
+}  // namespace lq

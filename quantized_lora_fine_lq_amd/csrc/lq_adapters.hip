@@ -1,0 +1,423 @@
+// Many adapters over one projection: the route (tokens sorted by adapter) and
+// the skinny products t = A_a x, u = B_a^T g, dA_a = s u^T X, dB_a = s G^T t.
+//
+// QLoRA (Heng's Blog), introduction: h = dequant(W0_NF4) x + (alpha/r) B A x,
+// here with an adapter (A, B, alpha, r) per token.
+#include <algorithm>
+
+#include "lq_adapters.h"
+#include "lq_device.h"
+
+namespace lq {
+namespace {
+
+__device__ __forceinline__ u32x4_t ld16(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// ===========================================================================
+// Route: a stable counting sort of the tokens by adapter, by one workgroup.
+// Wave w owns a contiguous run of tokens; pass 1 counts its tokens per adapter
+// in LDS (integer additions: their order does not matter), the counts are
+// scanned over adapters and waves, and pass 2 gives each token of a 64-token
+// group its place among the group's equal ids from ten ballots (one per bit of
+// the id). Bound by the latency of its few dependent passes.
+// ===========================================================================
+constexpr int RT_WAVES = 16;
+
+__global__ __launch_bounds__(64 * RT_WAVES) void k_adapter_route(const int32_t* __restrict__ ids, int64_t M, int n,
+                                                                 int32_t* __restrict__ off,
+                                                                 int32_t* __restrict__ perm,
+                                                                 int32_t* __restrict__ sid) {
+  extern __shared__ int32_t cnt[];   // [RT_WAVES][keys], then the wave sums of the scan
+  const int keys = n + 1;
+  int32_t* wsum = cnt + RT_WAVES * keys;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t per = ((M + RT_WAVES - 1) / RT_WAVES + 63) / 64 * 64;
+  const int64_t m0 = min(M, wave * per), m1 = min(M, m0 + per);
+  for (int i = threadIdx.x; i < RT_WAVES * keys; i += 64 * RT_WAVES) cnt[i] = 0;
+  __syncthreads();
+  for (int64_t m = m0 + lane; m < m1; m += 64) {
+    const int id = ids[m];
+    atomicAdd(&cnt[wave * keys + ((uint32_t)id < (uint32_t)n ? id : n)], 1);
+  }
+  __syncthreads();
+  // totals per key (thread k; keys <= 1024), waves' counts to exclusive sums
+  const int k = threadIdx.x;
+  int total = 0;
+  if (k < keys)
+    for (int w = 0; w < RT_WAVES; ++w) {
+      const int c = cnt[w * keys + k];
+      cnt[w * keys + k] = total;
+      total += c;
+    }
+  int inc = total;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 63) wsum[wave] = inc;
+  __syncthreads();
+  int base = inc - total;
+  for (int w = 0; w < wave; ++w) base += wsum[w];
+  if (k < keys) {
+    off[k] = base;
+    if (k == n) off[n + 1] = (int32_t)M;
+    for (int w = 0; w < RT_WAVES; ++w) cnt[w * keys + k] += base;
+  }
+  __syncthreads();
+  for (int64_t g = m0; g < m1; g += 64) {
+    const int64_t m = g + lane;
+    const bool live = m < m1;
+    const int id = live ? ids[m] : 0;
+    const int key = (uint32_t)id < (uint32_t)n ? id : n;
+    uint64_t peers = __ballot(live);
+#pragma unroll
+    for (int b = 0; b < 10; ++b) {
+      const uint64_t one = __ballot((key >> b) & 1);
+      peers &= ((key >> b) & 1) ? one : ~one;
+    }
+    const int rank = __popcll(peers & ((uint64_t(1) << lane) - 1));
+    volatile int32_t* c = &cnt[wave * keys + key];
+    const int start = *c;                      // the wave's LDS operations run in order:
+    __builtin_amdgcn_wave_barrier();           // every lane reads before the group's first lane of a key adds
+    if (live && rank == 0) *c = start + __popcll(peers);
+    __builtin_amdgcn_wave_barrier();
+    if (live) {
+      perm[start + rank] = (int32_t)m;
+      sid[start + rank] = key;
+    }
+  }
+}
+
+// Item b of the segments [off[a], off[a + 1]), a < nseg, cut into pieces of
+// `rows` sorted positions: its segment, first position and row count. With
+// slot: the index of the piece among those of segments with more than one, or
+// -1. Every wave finds the item for itself (uniform results); false past the
+// last item.
+struct Item {
+  int seg, start, count, slot;
+};
+__device__ __forceinline__ bool find_item(const int32_t* __restrict__ off, int nseg, int rows, int b, Item& it) {
+  const int lane = threadIdx.x & 63;
+  int base = 0, sbase = 0;
+  for (int a0 = 0; a0 < nseg; a0 += 64) {
+    const int a = a0 + lane;
+    int lo = 0, len = 0;
+    if (a < nseg) {
+      lo = off[a];
+      len = off[a + 1] - lo;
+    }
+    const int c = (len + rows - 1) / rows, cs = c > 1 ? c : 0;
+    int inc = c, incs = cs;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(inc, d), os = __shfl_up(incs, d);
+      if (lane >= d) {
+        inc += o;
+        incs += os;
+      }
+    }
+    const int first = base + inc - c;
+    const uint64_t hit = __ballot(b >= first && b < first + c);
+    if (hit) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      const int k = b - __shfl(first, l);
+      const int s = __shfl(lo, l) + k * rows;
+      const int e = __shfl(lo + len, l);
+      const int sl = __shfl(cs > 0 ? sbase + incs - cs : -1, l);
+      it.seg = uniform(a0 + l);
+      it.start = uniform(s);
+      it.count = uniform(min(rows, e - s));
+      it.slot = uniform(sl < 0 ? -1 : sl + k);
+      return true;
+    }
+    base += uniform(__shfl(inc, 63));
+    sbase += uniform(__shfl(incs, 63));
+  }
+  return false;
+}
+
+// ===========================================================================
+// Row form: 16 routed tokens of one adapter per workgroup; its W waves take
+// contiguous runs of 64-column blocks, MFMA 16x16x32 with tokens as rows and
+// the adapter's rows as columns, both straight from memory into registers.
+// The waves' partial sums meet in LDS and are added in wave order.
+// ===========================================================================
+template <int JT, int W>
+__global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt) {
+  __shared__ f32x4_t part[W][JT][64];
+  const DownJob jb = blockIdx.y ? j1 : j0;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  Item it;
+  if (!find_item(rt.off, v.n + 1, 16, (int)blockIdx.x, it)) return;
+  if (it.seg == v.n) {   // tokens without an adapter
+    if (jb.save)
+      for (int i = threadIdx.x; i < it.count * v.r_max; i += 64 * W)
+        jb.save[(int64_t)rt.perm[it.start + i / v.r_max] * v.r_max + i % v.r_max] = 0.0f;
+    return;
+  }
+  const lq_adapter ad = v.tab[it.seg];
+  const int r = min(ad.r, 16 * JT);
+  const int64_t C = jb.C;
+  const uint16_t* R = jb.rbase ? jb.rbase + C * ad.row8 : ad.A;
+  const uint16_t* q = jb.Q + (int64_t)rt.perm[it.start + min(li, it.count - 1)] * C;
+  const uint16_t* rr[JT];
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt) rr[jt] = R + (int64_t)min(16 * jt + li, r - 1) * C;
+  f32x4_t acc[JT];
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt) acc[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int64_t blocks = (C + 63) / 64, per = (blocks + W - 1) / W;
+  const int64_t b0 = min(blocks, wave * per), b1 = min(blocks, b0 + per);
+  for (int64_t b = b0; b < b1; ++b) {
+    u32x4_t a[2], w[2][JT];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t c = 64 * b + 16 * lg + 8 * h;
+      const bool ok = c + 8 <= C;
+      const int64_t o = ok ? c : 0;
+      a[h] = ld16(q + o);
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt) w[h][jt] = ld16(rr[jt] + o);
+      if (!ok) {
+        a[h] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int jt = 0; jt < JT; ++jt) w[h][jt] = a[h];
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt)
+        acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[h]), as_bf16x8(w[h][jt]), acc[jt], 0, 0, 0);
+  }
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt) part[wave][jt][lane] = acc[jt];
+  __syncthreads();
+  for (int i = threadIdx.x; i < JT * 64; i += 64 * W) {
+    const int jt = i >> 6, ln = i & 63, j = 16 * jt + (ln & 15);
+    f32x4_t sum = part[0][jt][ln];
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum += part[w][jt][ln];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = 4 * (ln >> 4) + e;
+      if (row >= it.count) continue;
+      const int64_t token = rt.perm[it.start + row];
+      const float x = j < r ? sum[e] : 0.0f;
+      if (j < v.rs) jb.out[token * v.rs + j] = x;
+      if (jb.save && j < v.r_max) jb.save[token * v.r_max + j] = x;
+    }
+  }
+}
+
+// at[k][j] = A[j][k] (j < r8, zero past r), bt[j][n] = B[n][j]
+__global__ __launch_bounds__(256) void k_adapter_transpose(AdapterView v, int64_t N, int64_t K,
+                                                           uint16_t* __restrict__ at, uint16_t* __restrict__ bt) {
+  const lq_adapter ad = v.tab[blockIdx.y];
+  const int r = ad.r, r8 = (r + 7) & ~7;
+  const int64_t na = at ? K * r8 : 0, nb = bt ? N * r : 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < na + nb; i += (int64_t)gridDim.x * 256) {
+    if (i < na) {
+      const int64_t j = i / K, k = i % K;
+      at[K * ad.row8 + k * r8 + j] = j < r ? ad.A[j * K + k] : (uint16_t)0;
+    } else {
+      const int64_t n = (i - na) / r, j = (i - na) % r;
+      bt[N * ad.row8 + j * N + n] = ad.B[n * r + j];
+    }
+  }
+}
+
+// ===========================================================================
+// Column form: out_a[j][c] = s_a sum_m P[m][j] Q[m][c] over a's tokens. One
+// workgroup per 128 columns and run of at most `rows` sorted positions; 32
+// tokens per step. P (float32) is split into three bfloat16 terms, hi + mid +
+// lo = P exactly (3 x 8 significand bits), so the products carry float32 P on
+// the bf16 matrix cores; all three go into the same accumulators. P and Q
+// tiles lie in LDS with tokens as rows and are read transposed
+// (ds_read_b64_tr_b16: the 16 lanes of a group point at 4 rows of 16 elements,
+// lane l gets column l of the 4 rows). Tokens past the segment are zero in
+// both, so no neighbour's infinity or NaN enters.
+// ===========================================================================
+constexpr int CQ_PITCH = 128 + 8;
+
+__device__ __forceinline__ uint32_t bf16_bits(float v) { return pack_bf16x2(v, 0.0f) & 0xFFFFu; }
+
+// lane's 8 values k = 8 lg + [0, 8) of column li, from rows of `pitch` elements
+__device__ __forceinline__ u32x4_t tr_frag(const uint16_t* base, int pitch, int li, int lg) {
+  typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) v4b* lds_p;
+  const uint16_t* p = base + (8 * lg + (li >> 2)) * pitch + 4 * (li & 3);
+  const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)p));
+  const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)(p + 4 * pitch)));
+  return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+}
+
+template <int JT>
+__global__ __launch_bounds__(256) void k_adapter_col(ColReq q0, ColReq q1, unsigned tiles0, int rows, AdapterView v,
+                                                     Route rt) {
+  constexpr int PP = 16 * JT + 8;
+  __shared__ __attribute__((aligned(16))) uint16_t sQ[32 * CQ_PITCH];
+  __shared__ __attribute__((aligned(16))) uint16_t sP[3 * 32 * PP];
+  const bool second = blockIdx.x >= tiles0;
+  const ColReq rq = second ? q1 : q0;
+  Item it;
+  if (!find_item(rt.off, v.n, rows, (int)blockIdx.y, it)) return;
+  const lq_adapter ad = v.tab[it.seg];
+  const int r = min(ad.r, 16 * JT);
+  const int64_t C = rq.C, c0 = (int64_t)(second ? blockIdx.x - tiles0 : blockIdx.x) * 128;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  f32x4_t acc[JT][2];
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) acc[jt][ct] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int mb = 0; mb < it.count; mb += 32) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = threadIdx.x + 256 * u, row = i >> 4, cc = 8 * (i & 15);
+      u32x4_t x = {0u, 0u, 0u, 0u};
+      if (mb + row < it.count && c0 + cc + 8 <= C) x = ld16(rq.Q + (int64_t)rt.perm[it.start + mb + row] * C + c0 + cc);
+      *reinterpret_cast<u32x4_t*>(sQ + row * CQ_PITCH + cc) = x;
+    }
+    for (int i = threadIdx.x; i < 32 * 16 * JT; i += 256) {
+      const int row = i / (16 * JT), j = i % (16 * JT);
+      float x = 0.0f;
+      if (mb + row < it.count && j < r) x = rq.P[(int64_t)rt.perm[it.start + mb + row] * rq.pstride + j];
+      const float hi = bf16lo_to_f32(bf16_bits(x)), y = x - hi;
+      const float mid = bf16lo_to_f32(bf16_bits(y));
+      sP[row * PP + j] = (uint16_t)bf16_bits(hi);
+      sP[(32 + row) * PP + j] = (uint16_t)bf16_bits(mid);
+      sP[(64 + row) * PP + j] = (uint16_t)bf16_bits(y - mid);
+    }
+    __syncthreads();
+    u32x4_t b[2];
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) b[ct] = tr_frag(sQ + 32 * wave + 16 * ct, CQ_PITCH, li, lg);
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt) {
+        const u32x4_t a = tr_frag(sP + 32 * t * PP + 16 * jt, PP, li, lg);
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+          acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b[ct]), acc[jt][ct], 0, 0, 0);
+      }
+    __syncthreads();
+  }
+  // lane: column li of each tile, rows j = 4 lg + e
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+      const int64_t c = c0 + 32 * wave + 16 * ct + li;
+      if (c >= C) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = 16 * jt + 4 * lg + e;
+        if (j >= r) continue;
+        if (it.slot >= 0) rq.part[((int64_t)it.slot * v.rs + j) * C + c] = acc[jt][ct][e];
+        else if (rq.transposed) rq.out[C * ad.row + c * r + j] = ad.scale * acc[jt][ct][e];
+        else rq.out[(ad.row + (int64_t)j) * C + c] = ad.scale * acc[jt][ct][e];
+      }
+    }
+}
+
+// Joins the runs of adapters with more than one, in order, and writes the zero
+// gradients of adapters without tokens.
+__global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1, int nreq, int rows, AdapterView v,
+                                                            Route rt) {
+  const int a = blockIdx.y, lane = threadIdx.x & 63;
+  int before = 0;   // slots of the adapters before a
+  for (int b = lane; b < a; b += 64) {
+    const int c = (rt.off[b + 1] - rt.off[b] + rows - 1) / rows;
+    before += c > 1 ? c : 0;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
+  const int runs = (rt.off[a + 1] - rt.off[a] + rows - 1) / rows;
+  if (runs == 1) return;
+  const lq_adapter ad = v.tab[a];
+  const int64_t n0 = ad.r * q0.C, n1 = nreq > 1 ? ad.r * q1.C : 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n0 + n1; i += (int64_t)gridDim.x * 256) {
+    const ColReq& q = i < n0 ? q0 : q1;
+    const int64_t e = i < n0 ? i : i - n0, j = e / q.C, c = e % q.C;
+    float sum = 0.0f;
+    for (int k = 0; k < runs; ++k) sum += q.part[((int64_t)(before + k) * v.rs + j) * q.C + c];
+    sum *= ad.scale;
+    q.out[q.C * ad.row + (q.transposed ? c * ad.r + j : e)] = sum;
+  }
+}
+
+// Sorted positions per workgroup of the column form: enough workgroups for
+// the chip, but runs of at least 256 tokens so that the partial sums stay few.
+int col_rows(int64_t M, int64_t cols) {
+  const int64_t tiles = (cols + 127) / 128;
+  int64_t rows = M * tiles / 512 / 32 * 32;
+  return (int)std::max<int64_t>(256, std::min<int64_t>(rows, 4096));
+}
+
+}  // namespace
+
+hipError_t launch_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_t* route, hipStream_t s) {
+  LQ_DASSERT(M >= 1 && M < (int64_t(1) << 31) && n >= 1 && n <= LQ_ADAPTERS_MAX);
+  const Route r = route_view(route, M, n);
+  const size_t lds = (size_t)(RT_WAVES * (n + 1) + RT_WAVES) * sizeof(int32_t);
+  hipLaunchKernelGGL(k_adapter_route, dim3(1), dim3(64 * RT_WAVES), lds, s, ids, M, n, const_cast<int32_t*>(r.off),
+                     const_cast<int32_t*>(r.perm), const_cast<int32_t*>(r.sid));
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
+                               hipStream_t s) {
+  if (njobs < 1 || njobs > 2) return hipErrorInvalidValue;
+  const DownJob j0 = jobs[0], j1 = jobs[njobs - 1];
+  // one item per 16 tokens, and one more per adapter (or none) for its remainder
+  const dim3 grid((unsigned)((M + 15) / 16 + std::min<int64_t>(v.n + 1, M)), (unsigned)njobs);
+  if (v.r_max <= 16) hipLaunchKernelGGL((k_adapter_down<1, 8>), grid, dim3(512), 0, s, j0, j1, M, v, rt);
+  else if (v.r_max <= 32) hipLaunchKernelGGL((k_adapter_down<2, 8>), grid, dim3(512), 0, s, j0, j1, M, v, rt);
+  else if (v.r_max <= 64) hipLaunchKernelGGL((k_adapter_down<4, 8>), grid, dim3(512), 0, s, j0, j1, M, v, rt);
+  else hipLaunchKernelGGL((k_adapter_down<8, 4>), grid, dim3(256), 0, s, j0, j1, M, v, rt);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_transpose(const AdapterView& v, int64_t N, int64_t K, uint16_t* at, uint16_t* bt,
+                                    hipStream_t s) {
+  const int64_t most = (N + K) * v.rs;
+  const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 255) / 256, std::max(16, 4096 / v.n)));
+  hipLaunchKernelGGL(k_adapter_transpose, dim3(gx, (unsigned)v.n), dim3(256), 0, s, v, N, K, at, bt);
+  return hipGetLastError();
+}
+
+// A segment of more than one run of `rows` has at most 2 len / rows of them.
+size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs) {
+  const int64_t rows = 256;
+  return (size_t)(2 * ((M + rows - 1) / rows)) * rs * C;
+}
+
+hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const AdapterView& v, const Route& rt,
+                              hipStream_t s) {
+  if (nreq < 1 || nreq > 2) return hipErrorInvalidValue;
+  const ColReq q0 = reqs[0], q1 = reqs[nreq - 1];
+  const int rows = col_rows(M, q0.C + (nreq > 1 ? q1.C : 0));
+  const unsigned t0 = (unsigned)((q0.C + 127) / 128), t1 = nreq > 1 ? (unsigned)((q1.C + 127) / 128) : 0u;
+  const dim3 grid(t0 + t1, (unsigned)((M + rows - 1) / rows + std::min<int64_t>(v.n, M)));
+  switch ((v.r_max + 15) / 16) {
+#define LQ_AC(JT) case JT: hipLaunchKernelGGL(k_adapter_col<JT>, grid, dim3(256), 0, s, q0, q1, t0, rows, v, rt); break;
+    LQ_AC(1) LQ_AC(2) LQ_AC(3) LQ_AC(4) LQ_AC(5) LQ_AC(6) LQ_AC(7) LQ_AC(8)
+#undef LQ_AC
+    default: return hipErrorInvalidValue;
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t most = (int64_t)v.r_max * (q0.C + (nreq > 1 ? q1.C : 0));
+  const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 255) / 256, std::max(32, 4096 / v.n)));
+  hipLaunchKernelGGL(k_adapter_col_reduce, dim3(gx, (unsigned)v.n), dim3(256), 0, s, q0, q1, nreq, rows, v, rt);
+  return hipGetLastError();
+}
+
+}  // namespace lq

@@ -7,28 +7,10 @@
 #include <cstring>
 #include <vector>
 
-#include "lq_internal.h"
+#include "lq_host.h"
 
-namespace {
+namespace lq {
 
-using namespace lq;
-
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool valid_dtype(int32_t d) { return d == LQ_F32 || d == LQ_BF16 || d == LQ_F16; }
-
-int launch_status(hipError_t e) { return e == hipSuccess ? LQ_OK : LQ_ERR_LAUNCH; }
-
-// Alignment of a device pointer (a null pointer passes; nullness is checked
-// separately). Bulk tensors are read and written with 16-byte vector
-// accesses; per-element arrays need their natural alignment.
-constexpr uintptr_t kVec = 16;
-bool al(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-// W of the NF4 quantizer and the profiling pass: four elements per access
-uintptr_t w_align(int32_t dtype) { return dtype == LQ_F32 ? 16 : 8; }
-
-// Validate a weight descriptor and turn it into the kernels' view.
 int check_qweight(const lq_qweight* w, QWeight* out) {
   if (!w) return LQ_ERR_ARG;
   if (w->format != LQ_FMT_NF4 && w->format != LQ_FMT_CODEBOOK) return LQ_ERR_ARG;
@@ -57,6 +39,17 @@ int check_qweight(const lq_qweight* w, QWeight* out) {
   return LQ_OK;
 }
 
+}  // namespace lq
+
+namespace {
+
+using namespace lq;
+
+bool valid_dtype(int32_t d) { return d == LQ_F32 || d == LQ_BF16 || d == LQ_F16; }
+
+// W of the NF4 quantizer and the profiling pass: four elements per access
+uintptr_t w_align(int32_t dtype) { return dtype == LQ_F32 ? 16 : 8; }
+
 // Forward path choice: the GEMV kernel for decode-sized M, else the MFMA
 // GEMM. LQ_FORCE_PATH=gemm forces the GEMM at any M (for tests).
 bool use_gemv(const QWeight& w, int64_t M) {
@@ -65,22 +58,6 @@ bool use_gemv(const QWeight& w, int64_t M) {
   if (f && std::strcmp(f, "gemm") == 0) return false;
   return true;
 }
-
-// Carves a caller workspace into aligned pieces; ok() is false if the pieces
-// ran past its size (the entry points size the workspace first, so this is a
-// bounds assert on that arithmetic).
-struct Carver {
-  char* base;
-  size_t cap;
-  size_t used = 0;
-  Carver(void* p, size_t bytes) : base((char*)p), cap(bytes) {}
-  template <class T> T* take(size_t count) {
-    T* p = reinterpret_cast<T*>(base + used);
-    used += align_up(count * sizeof(T));
-    return p;
-  }
-  bool ok() const { return used <= cap; }
-};
 
 // Row layout of a codebook weight (host arrays): widths in 1..4, offsets the
 // prefix sums of K*b/8; thresholds (optional) finite and strictly increasing.
@@ -117,9 +94,14 @@ int debug_check_rows(int64_t N, int64_t K, const uint8_t* bits_d, const int64_t*
   return LQ_OK;
 #endif
 }
-int debug_check_weight(const QWeight& q, hipStream_t s) {
+
+}  // namespace
+
+int lq::debug_check_weight(const QWeight& q, hipStream_t s) {
   return q.format == LQ_FMT_CODEBOOK ? debug_check_rows(q.N, q.K, q.row_bits, q.row_offset, s) : LQ_OK;
 }
+
+namespace {
 
 // Column parts of t = X A^T in the forward: only for the NF4 GEMV, which adds
 // them while staging t (the GEMM takes t whole: summing parts in its LoRA
