@@ -1,0 +1,680 @@
+// Many adapters at decode sizes (up to 64 tokens), NF4 weight:
+//   t[m] = A_a x[m],  h[m] = W' x[m] + s_a B_a t[m],  a = ids[m],
+// without sorting the tokens: a wave holds one id per lane, so the tokens of
+// an adapter are one ballot. Bound by reading the packed weight once and, per
+// code, by the lookup, product and rounding that make its bfloat16 weight.
+//
+// QLoRA (Heng's Blog), introduction: h = dequant(W0_NF4) x + (alpha/r) B A x.
+#include <algorithm>
+
+#include "lq_adapters.h"
+#include "lq_device.h"
+
+namespace lq {
+namespace {
+
+__device__ __forceinline__ u32x4_t ld16(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int read_lane(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ uint64_t read_lane(uint64_t v, int l) {
+  return (uint64_t)(uint32_t)read_lane((int)(uint32_t)v, l) | ((uint64_t)(uint32_t)read_lane((int)(uint32_t)(v >> 32), l) << 32);
+}
+__device__ __forceinline__ int first_bit(uint64_t m) { return uniform(__ffsll((unsigned long long)m) - 1); }
+// set bits of m below the lane
+__device__ __forceinline__ int bits_below(uint64_t m) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+__device__ __forceinline__ f32x4_t zero4() { return f32x4_t{0.f, 0.f, 0.f, 0.f}; }
+
+// The lane's token's adapter, or -1.
+__device__ __forceinline__ int lane_key(const int32_t* ids, int M, int n) {
+  const int lane = threadIdx.x & 63;
+  const int id = lane < M ? ids[lane] : -1;
+  return (uint32_t)id < (uint32_t)n ? id : -1;
+}
+
+// ===========================================================================
+// t = A_a x: one workgroup per adapter in use (workgroup b takes the b-th in
+// token order) and column part, 16 of its tokens at a time; the waves split
+// the part's columns. The parts' sums go to t [parts][M][rs]; the projection
+// adds them. The workgroups past the adapters' lay X out for the projection's
+// fragments (xp, see XPack): a load of 16 rows is then 1 KB in one piece, where
+// the rows themselves are 64 pieces of 16 bytes in 32 cache lines.
+// ===========================================================================
+// XPack: 16 bytes for (stage s, token tile tt, sub-step u, lane) at
+// ((s TT + tt) 4 + u) 64 + lane: token 16 tt + lane % 16, columns 128 s + 32 (lane / 16) + 8 u
+// of X, zero past K.
+__device__ __forceinline__ int xp_units(int64_t K, int TT) { return (int)((K + 127) / 128) * TT * 256; }
+
+template <int JT, int W>
+__global__ __launch_bounds__(64 * W) void k_decode_down(const uint16_t* __restrict__ X, int M, int64_t K,
+                                                        AdapterView v, const int32_t* __restrict__ ids,
+                                                        float* __restrict__ t, u32x4_t* __restrict__ xp, int TT,
+                                                        int wgs) {
+  __shared__ f32x4_t part[W][JT][64];
+  if ((int)blockIdx.x >= wgs) {
+    const int workers = ((int)gridDim.x - wgs) * (int)gridDim.y * 64 * W;
+    int i = (((int)blockIdx.x - wgs) * (int)gridDim.y + (int)blockIdx.y) * 64 * W + (int)threadIdx.x;
+    for (; i < xp_units(K, TT); i += workers) {
+      const int ln = i & 63, u = (i >> 6) & 3, tt = (i >> 8) % TT, s = (i >> 8) / TT;
+      const int64_t k = 128 * (int64_t)s + 32 * (ln >> 4) + 8 * u;
+      u32x4_t x = {0u, 0u, 0u, 0u};
+      if (k < K) x = ld16(X + (int64_t)min(16 * tt + (ln & 15), M - 1) * K + k);
+      xp[i] = x;
+    }
+    return;
+  }
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  const int key = lane_key(ids, M, v.n);
+  uint64_t left = __ballot(key >= 0), mine = 0;
+  int a = -1;
+  for (int b = 0; left; ++b) {
+    const int k = __shfl(key, __ffsll((unsigned long long)left) - 1);
+    const uint64_t same = __ballot(key == k);
+    if (b == (int)blockIdx.x) {
+      a = uniform(k);
+      mine = same;
+      break;
+    }
+    left &= ~same;
+  }
+  if (a < 0) return;
+  const lq_adapter ad = v.tab[a];
+  const int r = min(ad.r, 16 * JT), count = __popcll(mine);
+  const uint16_t* rr[JT];
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt) rr[jt] = ad.A + (int64_t)min(16 * jt + li, r - 1) * K;
+  const int all = (int)(K / 64), per = (all + gridDim.y - 1) / gridDim.y;
+  const int first = min(all, (int)blockIdx.y * per), blocks = min(all, first + per);   // this part's 64-column blocks
+  t += (int64_t)blockIdx.y * M * v.rs;
+  for (int t0 = 0; t0 < count; t0 += 16) {
+    // token of row i of this 16: the (t0 + i)-th set bit of `mine`
+    int tok = 0;
+    {
+      uint64_t m = mine;
+      const int want = min(t0 + li, count - 1);
+      for (int i = 0; i < want; ++i) m &= m - 1;
+      tok = __ffsll((unsigned long long)m) - 1;
+    }
+    const uint16_t* q = X + (int64_t)tok * K;
+    f32x4_t acc[JT];
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) acc[jt] = zero4();
+    constexpr int UB = JT <= 2 ? 4 : 1;   // blocks of 64 columns in flight
+    for (int b = first + wave; b < blocks; b += W * UB) {
+      u32x4_t x[UB][2], w[UB][2][JT];
+#pragma unroll
+      for (int u = 0; u < UB; ++u) {
+        const int64_t c = 64 * (int64_t)min(b + W * u, blocks - 1) + 16 * lg;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[u][h] = ld16(q + c + 8 * h);
+#pragma unroll
+          for (int jt = 0; jt < JT; ++jt) w[u][h][jt] = ld16(rr[jt] + c + 8 * h);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UB; ++u)
+        if (b + W * u < blocks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int jt = 0; jt < JT; ++jt)
+              acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[u][h]), as_bf16x8(w[u][h][jt]), acc[jt], 0, 0, 0);
+    }
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) part[wave][jt][lane] = acc[jt];
+    __syncthreads();
+    for (int i = threadIdx.x; i < JT * 64 * 4; i += 64 * W) {
+      const int e = i & 3, ln = (i >> 2) & 63, jt = i >> 8, j = 16 * jt + (ln & 15);
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) sum += part[w][jt][ln][e];
+      const int row = 4 * (ln >> 4) + e;
+      if (t0 + row >= count) continue;
+      uint64_t m = mine;
+      for (int k = 0; k < t0 + row; ++k) m &= m - 1;
+      const int token = __ffsll((unsigned long long)m) - 1;
+      if (j < v.rs) t[token * v.rs + j] = j < r ? sum : 0.0f;
+    }
+    __syncthreads();
+  }
+}
+
+// ===========================================================================
+// The projection. A workgroup owns RG groups of 16 weight rows; its W waves
+// take the 128-wide stages of the contraction in turn (the two stages of a
+// 128-byte line of codes in the same iteration) and their partial sums meet in
+// LDS at the end. Per stage and row group, lane (li, lg) loads 32 codes of row
+// li, decodes them into the A operand of four MFMA 16x16x32, and multiplies TT
+// tiles of 16 tokens; X comes from the L2.
+//
+// A code byte becomes two levels through an LDS table of level pairs, held
+// once per bank pair: entry e of slot s at 8 (32 e + s), and lane l reads slot
+// l % 32, so no two lanes of a half wave ever meet in a bank. With one copy
+// (2 KB) two thirds of the lookups' cycles were bank conflicts.
+// ===========================================================================
+struct DecodeParams {
+  const uint16_t* X;
+  const u32x4_t* xp;   // X in fragment order (more than one token tile)
+  int M;
+  const int32_t* ids;
+  AdapterView v;
+  const float* t;      // [parts][M, rs], or null: formed here (few ranks in use)
+  int parts;
+  float* t_out;        // [M, r_max], or null
+  void* out;
+  QWeight w;
+  Nf4Levels lv;
+};
+
+constexpr int DC_PAIRS = 256 * 32;   // f32x2_t, 64 KB
+constexpr int DC_TR = 32;            // largest sum of ranks, each rounded up to 16, whose t the kernel forms itself
+
+template <int RG, int XT, int AT>
+struct DcStage {
+  u32x4_t code[RG];
+  u32x4_t x[XT][4];   // one token tile: its X ahead with the codes
+  u32x4_t a[AT][4];   // and, where the kernel forms t, 16 rows of A each
+  int bl;             // the lane's 64-block (the last one where that lies past the row)
+};
+
+__device__ __forceinline__ float term_of(float v, int t) {
+  const float hi = bf16lo_to_f32(pack_bf16x2(v, 0.0f));
+  if (t == 0) return hi;
+  const float mid = bf16lo_to_f32(pack_bf16x2(v - hi, 0.0f));
+  return t == 1 ? mid : v - hi - mid;
+}
+
+// floats of LDS after the pair table: constants, then the partial sums of t or
+// of one token tile
+template <int RG, int W>
+__host__ __device__ constexpr int dc_floats(int nb) {
+  const int c = (16 * RG * (nb + 1) + 3) / 4 * 4, red = W * RG * 272;
+  return c > red ? c : red;
+}
+size_t dc_lds_bytes(int rg, int tt, int w, int nb, int rs, bool tk) {
+  const int c = (16 * rg * (nb + 1) + 3) / 4 * 4, red = w * rg * 272;
+  return DC_PAIRS * sizeof(f32x2_t) +
+         4 * (size_t)((c > red ? c : red) + (tk ? 16 * DC_TR + DC_TR / 16 * w * 256 : 16 * tt * rs));
+}
+
+// The adapters' part as steps of 32 contraction columns (4 runs of 8; TERMS
+// copies of an adapter's runs), dealt to the waves in turn. Lane l holds the
+// adapter of token l; the first token of each adapter in use leads it, and the
+// leaders' step counts, summed over the lanes, number the steps.
+struct DcSteps {
+  lq_adapter ad;     // the lane's token's adapter (leaders' entries are used)
+  uint64_t same;     // its tokens
+  int first, count;  // its steps (0 unless the lane leads)
+  int total;
+};
+template <int TERMS>
+__device__ __forceinline__ DcSteps dc_steps(const lq_adapter& ad, int key) {
+  DcSteps st;
+  st.ad = ad;
+  // the tokens of the lane's adapter, from one ballot per bit of the key
+  uint64_t peers = __ballot(key >= 0);
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {
+    const uint64_t one = __ballot((key >> b) & 1);
+    peers &= ((key >> b) & 1) ? one : ~one;
+  }
+  st.same = peers;
+  const bool leads = key >= 0 && bits_below(peers) == 0;
+  st.count = leads ? (TERMS * ((st.ad.r + 7) >> 3) + 3) >> 2 : 0;   // at most 12
+  st.first = 0;
+  st.total = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {   // the sum over the lanes below, bit by bit
+    const uint64_t one = __ballot((st.count >> b) & 1);
+    st.first += bits_below(one) << b;
+    st.total += __popcll(one) << b;
+  }
+  return st;
+}
+
+// Step k as every lane needs it, with the weight-side operand loaded.
+template <int RG>
+struct DcStep {
+  u32x4_t w[RG];
+  uint64_t same;
+  float scale;
+  int term, j0;
+  bool live;
+};
+template <int RG, int TERMS>
+__device__ __forceinline__ void dc_step(const DcSteps& st, int k, int64_t n0, int64_t N, DcStep<RG>& o) {
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int l = first_bit(__ballot(k >= st.first && k < st.first + st.count));
+  const uint16_t* B = reinterpret_cast<const uint16_t*>(read_lane((uint64_t)reinterpret_cast<uintptr_t>(st.ad.B), l));
+  const int r = read_lane(st.ad.r, l), runs = (r + 7) >> 3;
+  const int run = 4 * (k - read_lane(st.first, l)) + lg;
+  o.scale = __int_as_float(read_lane(__float_as_int(st.ad.scale), l));
+  o.same = read_lane(st.same, l);
+  o.live = run < TERMS * runs;
+  o.term = o.live ? run / runs : 0;
+  o.j0 = o.live ? 8 * (run - o.term * runs) : 0;
+#pragma unroll
+  for (int g = 0; g < RG; ++g) {
+    const uint16_t* b = B + min(n0 + 16 * g + li, N - 1) * r;
+    if (r % 8 == 0) {
+      o.w[g] = ld16(b + o.j0);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = o.j0 + 2 * e;
+        const uint32_t x = b[min(j, r - 1)], y = b[min(j + 1, r - 1)];
+        o.w[g][e] = (j < r ? x : 0u) | ((j + 1 < r ? y : 0u) << 16);
+      }
+    }
+  }
+}
+// Adds step o: each product goes to its own tokens' columns alone.
+template <int RG, int TT>
+__device__ __forceinline__ void dc_apply(const DcStep<RG>& o, const float* sT, int tstride, int M, f32x4_t (&acc)[RG][TT]) {
+  const int lane = threadIdx.x & 63, li = lane & 15;
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt) {
+    if (!((o.same >> (16 * tt)) & 0xFFFF)) continue;
+    const int m = 16 * tt + li;
+    const bool mine = (o.same >> m) & 1;
+    const float* tr = sT + min(m, M - 1) * tstride + o.j0;
+    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(tr), y = *reinterpret_cast<const f32x4_t*>(tr + 4);
+    u32x4_t tv;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      tv[e] = pack_bf16x2(term_of(o.scale * x[2 * e], o.term), term_of(o.scale * x[2 * e + 1], o.term));
+      tv[2 + e] = pack_bf16x2(term_of(o.scale * y[2 * e], o.term), term_of(o.scale * y[2 * e + 1], o.term));
+    }
+    const u32x4_t none = {0u, 0u, 0u, 0u};
+    if (!o.live) tv = none;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      const f32x4_t d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(o.live ? o.w[g] : none), as_bf16x8(tv), zero4(), 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[g][tt][e] += mine ? d[e] : 0.0f;
+    }
+  }
+}
+
+template <int RG, int TT, int W, bool DQ, bool OUT_F32, int TA>
+__global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char dc_lds[];
+  constexpr int TERMS = OUT_F32 ? 3 : 2;
+  constexpr bool XA = TT == 1;   // X is loaded a stage ahead, with the codes
+  constexpr bool TK = TA > 0;    // t formed here, TA groups of 16 rows of A
+  constexpr int XT = 1, AT = TK ? TA : 1;
+  f32x2_t* sPair = reinterpret_cast<f32x2_t*>(dc_lds);
+  float* sC = reinterpret_cast<float*>(dc_lds + DC_PAIRS * sizeof(f32x2_t));
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  const int64_t N = p.w.N, K = p.w.K;
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * RG;
+  const int nb = (int)(K / 64), pitch = nb + 1, ns = (nb + 1) / 2;
+  const int tstride = TK ? DC_TR : p.v.rs;
+  float* sT = sC + dc_floats<RG, W>(nb);                          // t [16 TT][tstride]
+  f32x4_t* sP = reinterpret_cast<f32x4_t*>(sT + 16 * DC_TR);      // TK: the waves' sums of t [TA][W][64]
+
+  const int key = lane_key(p.ids, p.M, p.v.n);   // the first load of a chain: id, table entry, A and B
+  const uint8_t* crow[RG];
+#pragma unroll
+  for (int g = 0; g < RG; ++g) crow[g] = p.w.codes + min(n0 + 16 * g + li, N - 1) * (K / 2) + 16 * (lg & 1);
+  const uint16_t* xrow = p.X + (int64_t)min(li, p.M - 1) * K + 32 * (lg & 1);   // TT == 1
+  const uint16_t* arow[AT];
+  auto load = [&](int s, DcStage<RG, XT, AT>& st) {
+    const int bl = 2 * min(s, ns - 1) + (lg >> 1);
+    st.bl = min(bl, nb - 1);
+#pragma unroll
+    for (int g = 0; g < RG; ++g) st.code[g] = ld16(crow[g] + (int64_t)st.bl * 32);
+    if constexpr (XA)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) st.x[0][u] = ld16(xrow + (int64_t)st.bl * 64 + 8 * u);
+  };
+  auto load_a = [&](DcStage<RG, XT, AT>& st) {
+#pragma unroll
+    for (int j = 0; j < AT; ++j)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) st.a[j][u] = ld16(arow[j] + (int64_t)st.bl * 64 + 8 * u);
+  };
+
+  // Loads return in order, so a chain (id, table entry, then A and B) that
+  // started behind the codes would wait for them at every link: the pair table
+  // covers the ids' latency, and the codes follow the entries' load.
+  // The pair table: lane l of a wave writes slot l % 32 of entries e + l / 32
+#pragma unroll
+  for (int k = 0; k < 128 / W; ++k) {
+    const int e = 2 * (wave + W * k);   // even: e and e + 1 share their first level
+    const float first = p.lv.q[e >> 4], lo = p.lv.q[e & 15], hi = p.lv.q[(e & 15) + 1];
+    sPair[32 * e + lane] = f32x2_t{first, lane < 32 ? lo : hi};
+  }
+  const lq_adapter mine = p.v.tab[max(key, 0)];
+  DcStage<RG, XT, AT> s0, s1;
+  load(wave, s0);
+  load(wave + W, s1);
+  const DcSteps steps = dc_steps<TERMS>(mine, key);
+  if constexpr (TK) {
+    // row li of the j-th 16 rows in use, adapter after adapter (any valid row past the last)
+    uint64_t left = __ballot(steps.count > 0);
+#pragma unroll
+    for (int j = 0; j < AT; ++j) arow[j] = p.X + 32 * (lg & 1);
+    for (int jt = 0; left; left &= left - 1) {
+      const int l = first_bit(left);
+      const uint16_t* A = reinterpret_cast<const uint16_t*>(read_lane((uint64_t)reinterpret_cast<uintptr_t>(steps.ad.A), l));
+      const int r = read_lane(steps.ad.r, l);
+      for (int j0 = 0; j0 < r; j0 += 16, ++jt) {
+#pragma unroll
+        for (int j = 0; j < AT; ++j)
+          if (j == jt) arow[j] = A + (int64_t)min(j0 + li, r - 1) * K + 32 * (lg & 1);
+      }
+    }
+    load_a(s0);
+    load_a(s1);
+  }
+  DcStep<RG> step;
+  const float mean = DQ ? *p.w.qc.dq_mean : 0.0f;
+  if (DQ && nb % 16 == 0) {
+    const int cpr = nb / 16;
+    for (int i = threadIdx.x; i < 16 * RG * cpr; i += 64 * W) {
+      const int rr = i / cpr, cb = i - rr * cpr;
+      const int64_t blk = min(n0 + rr, N - 1) * nb + 16 * cb;
+      const u32x4_t q8 = ld16(p.w.qc.absmax_q + blk);
+      const float s2 = p.w.qc.dq_scale[blk >> 8];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        sC[rr * pitch + 16 * cb + e] = __builtin_fmaf(e4m3_decode((q8[e >> 2] >> (8 * (e & 3))) & 0xFFu), s2, mean);
+    }
+  } else {
+    for (int i = threadIdx.x; i < 16 * RG * nb; i += 64 * W) {
+      const int rr = i / nb, bl = i - rr * nb;
+      const int64_t blk = min(n0 + rr, N - 1) * nb + bl;
+      sC[rr * pitch + bl] = DQ ? __builtin_fmaf(e4m3_decode(p.w.qc.absmax_q[blk]), p.w.qc.dq_scale[blk >> 8], mean)
+                               : p.w.qc.absmax[blk];
+    }
+  }
+  if (wave < steps.total) dc_step<RG, TERMS>(steps, wave, n0, N, step);
+  if constexpr (!TK) {
+    // t: its parts added (in order), tokens without an adapter and the columns past a rank 0
+    const int nt = p.M * p.v.rs;
+    for (int i0 = 0; i0 < nt; i0 += 64 * W) {
+      const int i = min(i0 + (int)threadIdx.x, nt - 1), m = i / p.v.rs;
+      float part[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) part[k] = p.t[(int64_t)min(k, p.parts - 1) * nt + i];
+      float sum = part[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) sum += k < p.parts ? part[k] : 0.0f;
+      if (__shfl(key, m) < 0) sum = 0.0f;
+      if (i0 + (int)threadIdx.x < nt) {
+        sT[i] = sum;
+        const int j = i - m * p.v.rs;
+        if (blockIdx.x == 0 && p.t_out && j < p.v.r_max) p.t_out[m * p.v.r_max + j] = sum;
+      }
+    }
+  }
+  __syncthreads();
+
+  f32x4_t acc[RG][TT];
+#pragma unroll
+  for (int g = 0; g < RG; ++g)
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) acc[g][tt] = zero4();
+  f32x4_t tacc[AT];
+#pragma unroll
+  for (int j = 0; j < AT; ++j) tacc[j] = zero4();
+  auto lora = [&]() {
+    for (int k = wave; k < steps.total; k += W) {
+      const DcStep<RG> cur = step;
+      if (k + W < steps.total) dc_step<RG, TERMS>(steps, k + W, n0, N, step);   // the next one's loads
+      dc_apply<RG, TT>(cur, sT, tstride, p.M, acc);
+    }
+  };
+  if constexpr (!TK) lora();
+
+  const uint32_t slot = 8 * (lane & 31);
+  constexpr int GB = RG < 2 ? RG : 2;   // row groups per batch of lookups
+  for (int s = wave; s < ns; s += 2 * W) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (s + half * W >= ns) break;
+      DcStage<RG, XT, AT>& st = half ? s1 : s0;
+      u32x4_t x[TT][4];
+      if constexpr (XA) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[0][u] = st.x[0][u];
+      } else {
+        const u32x4_t* xs = p.xp + (int64_t)(s + half * W) * (TT * 256) + lane;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int tt = 0; tt < TT; ++tt) x[tt][u] = xs[(tt * 4 + u) * 64];
+      }
+      // K / 64 odd: the last stage's second block lies past the row and adds
+      // zeros (its X too: 0 times an infinity is not 0; XPack holds zeros there)
+      if ((nb & 1) && s + half * W == ns - 1) {
+        if constexpr (XA)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (lg >= 2) x[0][u] = u32x4_t{0u, 0u, 0u, 0u};
+            if constexpr (TK)
+#pragma unroll
+              for (int j = 0; j < AT; ++j)
+                if (lg >= 2) st.a[j][u] = u32x4_t{0u, 0u, 0u, 0u};
+          }
+      }
+      float cp[RG];
+#pragma unroll
+      for (int g = 0; g < RG; ++g) cp[g] = sC[(16 * g + li) * pitch + st.bl];
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if constexpr (TK)
+#pragma unroll
+          for (int j = 0; j < AT; ++j)   // tokens as rows, rows of A as columns
+            tacc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[0][u]), as_bf16x8(st.a[j][u]), tacc[j], 0, 0, 0);
+#pragma unroll
+        for (int g0 = 0; g0 < RG; g0 += GB) {
+          f32x2_t q[GB][4];
+#pragma unroll
+          for (int g = 0; g < GB; ++g)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              // address: byte 0 the slot, byte 1 the code byte
+              const uint32_t at = __builtin_amdgcn_perm(st.code[g0 + g][u], slot, 0x0C0C0400u + (b << 8));
+              q[g][b] = *reinterpret_cast<const f32x2_t*>(dc_lds + at);
+            }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int g = 0; g < GB; ++g) {
+            u32x4_t wv;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) wv[b] = pack_bf16x2(q[g][b].x * cp[g0 + g], q[g][b].y * cp[g0 + g]);
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt)
+              acc[g0 + g][tt] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wv), as_bf16x8(x[tt][u]), acc[g0 + g][tt], 0, 0, 0);
+          }
+        }
+      }
+      load(s + (2 + half) * W, st);
+      if constexpr (TK) load_a(st);
+    }
+  }
+  if constexpr (TK) {
+    // t: the waves' sums in order, an adapter's columns at its tokens' rows, from column 0
+#pragma unroll
+    for (int j = 0; j < AT; ++j) sP[(j * W + wave) * 64 + lane] = tacc[j];
+    __syncthreads();
+    for (int i0 = 0; i0 < p.M * DC_TR; i0 += 64 * W) {
+      const int i = min(i0 + (int)threadIdx.x, p.M * DC_TR - 1), m = i / DC_TR, j = i % DC_TR;
+      const int mk = __shfl(key, m);
+      float sum = 0.0f;
+      uint64_t left = __ballot(steps.count > 0);
+      for (int jt = 0; left; left &= left - 1) {
+        const int l = first_bit(left);
+        const int r = read_lane(steps.ad.r, l);
+        if (mk == read_lane(key, l) && j < r) {
+#pragma unroll
+          for (int w = 0; w < W; ++w) sum += sP[((jt + (j >> 4)) * W + w) * 64 + 16 * (m >> 2) + (j & 15)][m & 3];
+        }
+        jt += (r + 15) >> 4;
+      }
+      if (i0 + (int)threadIdx.x < p.M * DC_TR) {
+        sT[i] = sum;
+        if (blockIdx.x == 0 && p.t_out && j < p.v.r_max) p.t_out[m * p.v.r_max + j] = sum;
+      }
+    }
+    __syncthreads();
+    lora();
+  }
+
+  // the waves' sums, one token tile at a time, over the constants' space. A lane
+  // holds token li, rows 4 lg + [0, 4) of each row group; lane l of a group lies
+  // at 16-byte slot l + l / 16 of 68, so that the readers (consecutive threads:
+  // consecutive rows of one token) hit distinct banks.
+  f32x4_t* sR = reinterpret_cast<f32x4_t*>(sC);   // [W][RG][68]
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt) {
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < RG; ++g) sR[(wave * RG + g) * 68 + lane + lg] = acc[g][tt];
+    __syncthreads();
+    for (int i = threadIdx.x; i < RG * 64; i += 64 * W) {
+      const int quad = i & 3, g = (i >> 2) % RG, m = i / (4 * RG);
+      f32x4_t h = sR[g * 68 + m + 17 * quad];
+#pragma unroll
+      for (int w = 1; w < W; ++w) h += sR[(w * RG + g) * 68 + m + 17 * quad];
+      const int64_t n = n0 + 16 * g + 4 * quad;
+      if (16 * tt + m >= p.M || n >= N) continue;
+      const int64_t o = (int64_t)(16 * tt + m) * N + n;
+      if (N % 4 == 0) {
+        if (OUT_F32) {
+          float* f = reinterpret_cast<float*>(p.out) + o;   // 4-byte aligned
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = h[e];
+        } else {
+          uint2 v;
+          v.x = pack_bf16x2(h[0], h[1]);
+          v.y = pack_bf16x2(h[2], h[3]);
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + o) = v;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (n + e >= N) break;
+          if (OUT_F32) reinterpret_cast<float*>(p.out)[o + e] = h[e];
+          else reinterpret_cast<uint16_t*>(p.out)[o + e] = (uint16_t)(pack_bf16x2(h[e], 0.f) & 0xFFFFu);
+        }
+      }
+    }
+  }
+}
+
+template <int RG, int TT, int W, int TK>
+hipError_t launch_rg(const DecodeParams& p, bool f32, hipStream_t s) {
+  const dim3 grid((unsigned)((p.w.N + 16 * RG - 1) / (16 * RG))), block(64 * W);
+  const size_t lds = dc_lds_bytes(RG, TT, W, (int)(p.w.K / 64), p.v.rs, TK > 0);
+  const bool dq = p.w.qc.absmax == nullptr;
+  if (dq && f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, true, TK>), grid, block, lds, s, p);
+  else if (dq) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, false, TK>), grid, block, lds, s, p);
+  else if (f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, true, TK>), grid, block, lds, s, p);
+  else hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, false, TK>), grid, block, lds, s, p);
+  return hipGetLastError();
+}
+
+constexpr int kCus = 256;
+constexpr size_t kLdsBytes = 160 * 1024;
+
+// Row groups per workgroup, one workgroup per CU (the pair table takes 64 KB
+// of LDS): the shortest queue of the longest CU, a workgroup costing its row
+// groups and about two more for its start and its X.
+int decode_rg(int64_t N, int64_t K, int tt, int rs, bool tk) {
+  const int64_t groups = (N + 15) / 16;
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int rg = 1; rg <= 4; rg *= 2) {
+    if (dc_lds_bytes(rg, tt, rg == 1 && tt == 1 && !tk ? 16 : 8, (int)(K / 64), rs, tk) > kLdsBytes) break;
+    const int64_t sets = (groups + rg - 1) / rg, c = (sets + kCus - 1) / kCus * (rg + 2);
+    if (c <= cost) {
+      cost = c;
+      best = rg;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+// NF4, at most 64 tokens, and one row group's constants within the LDS that the
+// tables (64 KB) and t (at most 32 KB) leave.
+bool adapter_decode_supported(const QWeight& w, int64_t M) {
+  return w.format == LQ_FMT_NF4 && M <= 64 && w.K <= 49152;
+}
+static bool adapter_decode_forms_t(int64_t M, const AdapterView& v) {
+  return M <= 16 && std::min<int64_t>(M, v.n) * ((v.r_max + 15) / 16 * 16) <= DC_TR;
+}
+
+// Token tiles of the projection, and the workspace: t's parts, and X in
+// fragment order for more than one tile.
+static int token_tiles(int64_t M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
+static int adapter_decode_parts(const QWeight& w, int64_t M, const AdapterView& v);
+static size_t t_bytes(const QWeight& w, int64_t M, const AdapterView& v) {
+  return ((size_t)adapter_decode_parts(w, M, v) * M * v.rs * sizeof(float) + 255) / 256 * 256;
+}
+size_t adapter_decode_ws_bytes(const QWeight& w, int64_t M, const AdapterView& v) {
+  const int tt = token_tiles(M);
+  return t_bytes(w, M, v) + (tt > 1 ? (size_t)((w.K + 127) / 128) * tt * 256 * 16 : 0);
+}
+
+// Column parts of t: with few adapters the columns are shared by several
+// workgroups, at least eight 64-column blocks each.
+static int adapter_decode_parts(const QWeight& w, int64_t M, const AdapterView& v) {
+  if (adapter_decode_forms_t(M, v)) return 1;
+  const int64_t wgs = std::min<int64_t>(M, v.n);
+  int parts = 1;
+  while (parts < 8 && wgs * parts * 2 <= kCus && w.K / 64 / (parts * 2) >= 8) parts *= 2;
+  return parts;
+}
+
+hipError_t launch_adapter_decode(const QWeight& w, const uint16_t* X, int64_t M, const int32_t* ids,
+                                 const AdapterView& v, void* ws, float* t_save, void* H, bool f32, hipStream_t s) {
+  if (!adapter_decode_supported(w, M)) return hipErrorInvalidValue;
+  const bool tk = adapter_decode_forms_t(M, v);
+  const int parts = adapter_decode_parts(w, M, v), tt = token_tiles(M);
+  float* t_ws = reinterpret_cast<float*>(ws);
+  u32x4_t* xp = reinterpret_cast<u32x4_t*>(reinterpret_cast<char*>(ws) + t_bytes(w, M, v));
+  DecodeParams p{X, xp, (int)M, ids, v, tk ? nullptr : t_ws, parts, t_save, H, w, tables().lv};
+  if (!tk) {
+    const int wgs = (int)std::min<int64_t>(M, v.n);
+    const dim3 grid((unsigned)(wgs + (tt > 1 ? std::max(1, 64 / parts) : 0)), (unsigned)parts);
+    const int jt = (v.r_max + 15) / 16;
+#define LQ_DD(JT, W) hipLaunchKernelGGL((k_decode_down<JT, W>), grid, dim3(64 * W), 0, s, X, (int)M, w.K, v, ids, t_ws, xp, tt, wgs)
+    if (jt <= 1) LQ_DD(1, 16);
+    else if (jt <= 2) LQ_DD(2, 16);
+    else if (jt <= 4) LQ_DD(4, 8);
+    else LQ_DD(8, 8);
+#undef LQ_DD
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int rg = decode_rg(w.N, w.K, tt, v.rs, tk);
+  if (tk) {
+    const bool one = std::min<int64_t>(M, v.n) * ((v.r_max + 15) / 16) == 1;
+    if (rg == 4) return one ? launch_rg<4, 1, 8, 1>(p, f32, s) : launch_rg<4, 1, 8, 2>(p, f32, s);
+    if (rg == 2) return one ? launch_rg<2, 1, 8, 1>(p, f32, s) : launch_rg<2, 1, 8, 2>(p, f32, s);
+    return one ? launch_rg<1, 1, 8, 1>(p, f32, s) : launch_rg<1, 1, 8, 2>(p, f32, s);
+  }
+#define LQ_RG(TT)                                              \
+  do {                                                         \
+    if (rg == 4) return launch_rg<4, TT, 8, 0>(p, f32, s); \
+    if (rg == 2) return launch_rg<2, TT, 8, 0>(p, f32, s); \
+    return launch_rg<1, TT, TT == 1 ? 16 : 8, 0>(p, f32, s); \
+  } while (0)
+  if (M <= 16) LQ_RG(1);
+  if (M <= 32) LQ_RG(2);
+  LQ_RG(4);
+#undef LQ_RG
+}
+
+}  // namespace lq

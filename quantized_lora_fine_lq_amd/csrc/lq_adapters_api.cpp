@@ -41,8 +41,10 @@ size_t route_bytes(int64_t M, int32_t n) { return (size_t)route_words(M, n) * si
 
 int64_t ldb_of(int64_t n) { return (n + 63) / 64 * 64; }
 
-// route, t, W'
+// route, t, W'; at decode sizes what that path keeps
 size_t forward_ws(const QWeight& q, int64_t M, const AdapterView& v) {
+  if (adapter_decode_supported(q, M))
+    return align_up(adapter_decode_ws_bytes(q, M, v));
   return align_up(route_bytes(M, v.n)) + align_up((size_t)M * v.rs * sizeof(float)) +
          align_up((size_t)q.N * q.K * sizeof(uint16_t));
 }
@@ -103,8 +105,10 @@ int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const
   hipStream_t s = (hipStream_t)stream;
   if ((st = debug_check_weight(q, s)) != LQ_OK) return st;
   Carver cv(workspace, ws_bytes);
-  int32_t* rws = cv.take<int32_t>(route_words(M, v.n));
+  if (adapter_decode_supported(q, M))
+    return launch_status(launch_adapter_decode(q, X, M, ids, v, workspace, t_save, H, h_dtype == LQ_F32, s));
   float* t = cv.take<float>((size_t)M * v.rs);
+  int32_t* rws = cv.take<int32_t>(route_words(M, v.n));
   uint16_t* wd = cv.take<uint16_t>((size_t)q.N * q.K);
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
 
