@@ -4,6 +4,7 @@
 //
 // QLoRA (Heng's Blog), introduction: h = dequant(W0_NF4) x + (alpha/r) B A x.
 #include <algorithm>
+#include <type_traits>
 
 #include "lq_adapters.h"
 #include "lq_device.h"
@@ -23,145 +24,144 @@ __device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
 }
 
 
-// Term `t` of v = hi + mid (+ lo): bfloat16 values, each the rounding of what
-// the ones before leave.
-__device__ __forceinline__ float term_of(float v, int t) {
-  const float hi = bf16lo_to_f32(pack_bf16x2(v, 0.0f));
-  if (t == 0) return hi;
-  const float mid = bf16lo_to_f32(pack_bf16x2(v - hi, 0.0f));
-  return t == 1 ? mid : v - hi - mid;
+// Wait until at most `n` of the wave's memory operations are outstanding.
+template <int n>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
 }
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-// Lane (li, lg)'s operands of one step of 32 contraction columns of adapter
-// ad's term: runs of 8 columns, TERMS copies of the r columns rounded up to
-// whole runs. Weight side: row c of Lb (8 values of a run); token side: term of
-// s * L[token] at the same run.
-template <bool BWD>
-__device__ __forceinline__ u32x4_t lora_weight(const AdapterGemm& p, const lq_adapter& ad, int64_t c, int j0,
-                                               bool live) {
-  const int64_t cc = min(c, p.Ncols - 1);
-  u32x4_t o;
-  if (BWD) {
-    const int r8 = (ad.r + 7) & ~7;
-    o = ld16(p.lt + p.Ncols * ad.row8 + cc * r8 + j0);
-  } else if (ad.r % 8 == 0) {
-    o = ld16(ad.B + cc * ad.r + j0);
-  } else {
-    const uint16_t* b = ad.B + cc * ad.r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = j0 + 2 * e;
-      const uint32_t x = b[min(j, ad.r - 1)], y = b[min(j + 1, ad.r - 1)];
-      o[e] = (j < ad.r ? x : 0u) | ((j + 1 < ad.r ? y : 0u) << 16);
-    }
-  }
-  if (!live) o = u32x4_t{0u, 0u, 0u, 0u};
-  return o;
-}
-__device__ __forceinline__ u32x4_t lora_token(const AdapterGemm& p, float s, int64_t token, int j0, int term,
-                                              bool live) {
-  const float* l = p.L + token * p.v.rs + j0;
-  const f32x4_t x = *reinterpret_cast<const f32x4_t*>(l), y = *reinterpret_cast<const f32x4_t*>(l + 4);
-  u32x4_t o;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    o[e] = pack_bf16x2(term_of(s * x[2 * e], term), term_of(s * x[2 * e + 1], term));
-    o[2 + e] = pack_bf16x2(term_of(s * y[2 * e], term), term_of(s * y[2 * e + 1], term));
-  }
-  if (!live) o = u32x4_t{0u, 0u, 0u, 0u};
-  return o;
-}
-
-// The adapters' part of a wave's CT x RT tiles of 16 x 16 (weight rows c0 ..,
-// sorted positions p0 ..), before the main loop. A tile whose 16 tokens share
-// an adapter accumulates into acc; in a tile with several, each adapter's
-// product is formed apart and added to its own tokens' columns alone, so that
-// one adapter's infinities and NaN cannot reach another's tokens.
-template <int CT, int RT, int TERMS, bool BWD>
-__device__ __forceinline__ void lora_init(const AdapterGemm& p, int64_t p0, int64_t c0, f32x4_t (&acc)[CT][RT]) {
-  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int64_t pend = min(p0 + 16 * RT, p.M);
-  int64_t pos = p0;
-  while (pos < pend) {
-    const int a = uniform(p.rt.sid[pos]);
-    if (a >= p.v.n) break;   // sorted: the rest has none
-    const int64_t send = min((int64_t)uniform(p.rt.off[a + 1]), pend);
-    const lq_adapter ad = p.v.tab[a];
-    const int runs = (ad.r + 7) >> 3, total = TERMS * runs;
-    for (int q0 = 0; q0 < total; q0 += 4) {
-      const int run = q0 + lg;
-      const bool live = run < total;
-      const int term = live ? run / runs : 0, j0 = live ? 8 * (run - term * runs) : 0;
-      u32x4_t w[CT];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) w[ct] = lora_weight<BWD>(p, ad, c0 + 16 * ct + li, j0, live);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int64_t t0 = p0 + 16 * rt, t1 = min(t0 + 16, pend);
-        if (t0 < send && t1 > pos) {
-          const u32x4_t x = lora_token(p, ad.scale, p.rt.perm[min(t0 + li, p.M - 1)], j0, term, live);
-          const bool whole = pos <= t0 && send >= t1;
-          const bool mine = t0 + li >= pos && t0 + li < send;
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            if (whole) {
-              acc[ct][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w[ct]), as_bf16x8(x), acc[ct][rt], 0, 0, 0);
-            } else {
-              const f32x4_t d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w[ct]), as_bf16x8(x),
-                                                                        f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[ct][rt][e] += mine ? d[e] : 0.0f;
-            }
-          }
-        }
-      }
-    }
-    pos = send;
-  }
-}
-
-// Tile 256 positions x BN weight rows, 8 waves; 64-wide steps, two LDS buffers
-// filled by memory-to-LDS loads one step ahead. Row r of a tile keeps its
-// 16-byte chunk c at slot c ^ (r % 8), so fragment reads of 8 rows hit distinct
+// Tile 256 positions x BN weight rows, 64-wide steps, 8 waves in two groups of
+// four (one wave of each group per SIMD). The groups work one slot apart:
+// while one group's waves multiply (16 MFMA each), the other's read their next
+// fragments from LDS and issue memory-to-LDS loads, so matrix unit and LDS are
+// busy at once; a barrier ends every slot. Row r of an LDS tile keeps its
+// 16-byte chunk c at slot c ^ (r % 8): fragment reads of 8 rows hit distinct
 // banks. The matrix product is taken with weights as rows and tokens as
 // columns: a lane then holds 4 consecutive outputs of one token.
+//
+// BN = 256: waves 2 (tokens) x 4 (weight rows) of 128 x 64. A step is four
+// quadrants, X0 Y0, X0 Y1, X1 Y1, X1 Y0, of 64 tokens x 32 weight rows; two
+// buffers (128 KB), each refilled part by part as soon as both groups have
+// read the part, which puts five to seven quadrants between a load and its
+// use. BN = 128: waves 4 x 2 of 64 x 64, two halves a step, three buffers.
 template <int BN, bool OUT_F32, bool BWD>
 __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
-  constexpr int WN = BN == 256 ? 4 : 2, WM = 8 / WN;       // waves over weight rows, tokens
-  constexpr int CT = BN / WN / 16, RT = GM / WM / 16;      // 16 x 16 tiles per wave
-  constexpr int QA = GM / 64, QB = BN / 64;                // 16-byte loads per thread and tile
+  constexpr bool BIG = BN == 256;
+  constexpr int WN = BIG ? 4 : 2, WM = 8 / WN;         // waves over weight rows, tokens
+  constexpr int CT = BN / WN / 16, RT = GM / WM / 16;  // 16 x 16 tiles per wave
+  constexpr int RING = BIG ? 2 : 3;
+  constexpr int XP = BIG ? 2 : 1;                      // parts of the token tile (each 64 rows of a wave's)
+  constexpr int QX = GM / 64 / XP, QY = BN / 64 / 2;   // 16-byte loads per thread and part
   struct __attribute__((aligned(16))) Lds {
-    uint16_t a[2][GM * GK];
-    uint16_t b[2][BN * GK];
+    uint16_t x[RING][GM * GK];
+    uint16_t y[RING][BN * GK];
   };
   __shared__ Lds lds;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
   const int wn = wave % WN, wm = wave / WN;
   const int64_t tiles_m = (p.M + GM - 1) / GM, tiles_n = (p.Ncols + BN - 1) / BN;
   const int64_t total = tiles_m * tiles_n;
   // XCD x (workgroups x, x + 8, ...) takes a contiguous range of tiles, the
   // token tiles inner
-  const int64_t x = blockIdx.x % 8, per = total / 8, rem = total % 8;
-  const int64_t t = x * per + min(x, rem) + blockIdx.x / 8;
+  const int64_t xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
+  const int64_t t = xcd * per + min(xcd, rem) + blockIdx.x / 8;
   const int64_t m0 = t % tiles_m * GM, n0 = t / tiles_m * BN;
 
-  const uint16_t *pa[QA], *pb[QB];
-  const int sub = lane >> 3, ch = (lane & 7) ^ sub;        // row in the instruction's 8, chunk read
+  // A load instruction of a wave fills 8 LDS rows (lane l: row l / 8, slot
+  // l % 8). Part i of the token tile: rows 64 i .. of every wave's 128 (all
+  // rows for BN = 128); part i of the weight tile: rows 16 CT / 2 i .. of every
+  // wave's 16 CT.
+  const int sub = lane >> 3, ch = (lane & 7) ^ sub;
+  auto xrow = [&](int part, int q) {   // first tile row of the wave's q-th load
+    const int k = wave * QX + q;       // 8-row groups 0 .. 8 QX - 1 of the part
+    return BIG ? (k >> 3) * 128 + part * 64 + (k & 7) * 8 : k * 8;
+  };
+  auto yrow = [&](int part, int q) {
+    const int k = wave * QY + q, per_wave = 16 * CT / 2 / 8;
+    return (k / per_wave) * 16 * CT + part * 8 * CT + (k % per_wave) * 8;
+  };
+  const uint16_t *px[XP][QX], *py[2][QY];
 #pragma unroll
-  for (int q = 0; q < QA; ++q) {
-    const int64_t pos = min(m0 + (wave * QA + q) * 8 + sub, p.M - 1);
-    pa[q] = p.A + (int64_t)p.rt.perm[pos] * p.Kc;
-  }
+  for (int i = 0; i < XP; ++i)
 #pragma unroll
-  for (int q = 0; q < QB; ++q) pb[q] = p.Bt + min(n0 + (wave * QB + q) * 8 + sub, p.Ncols - 1) * p.ldb + 8 * ch;
-  auto stage = [&](int buf, int64_t k0) {
-    const bool ok = k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (Bt is zero there, but 0 * NaN is not)
+    for (int q = 0; q < QX; ++q) px[i][q] = p.A + (int64_t)p.rt.perm[min(m0 + xrow(i, q) + sub, p.M - 1)] * p.Kc + 8 * ch;
 #pragma unroll
-    for (int q = 0; q < QA; ++q)
-      load_lds16(ok ? pa[q] + k0 + 8 * ch : p.zeros, lds.a[buf] + (wave * QA + q) * 8 * GK);
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int q = 0; q < QB; ++q) load_lds16(pb[q] + k0, lds.b[buf] + (wave * QB + q) * 8 * GK);
+    for (int q = 0; q < QY; ++q) py[i][q] = p.Bt + min(n0 + yrow(i, q) + sub, p.Ncols - 1) * p.ldb + 8 * ch;
+  const int nk = (int)((p.Kc + GK - 1) / GK);
+
+  // The adapters' part: an adapter's [hi | mid (| lo)] columns of the terms
+  // against as many copies of Lb, in steps of 64 (columns past the last are
+  // zero on both sides). Of a tile whose tokens share one adapter it is simply
+  // the end of the contraction, steps nk .. nk + nl - 1 of the main loop.
+  constexpr int TERMS = OUT_F32 ? 3 : 2;
+  struct Adapter {
+    int64_t lo, hi;          // its sorted positions inside the tile
+    const uint16_t* base;    // Lb
+    int stride, runs;        // of Lb: elements a row, runs of 8 columns
+    int live, steps;         // runs of all terms, steps of 8 of them
+  };
+  const int64_t mend = min(m0 + GM, p.M);
+  auto adapter_at = [&](int64_t pos) {   // the adapter at a position of the tile; steps 0: none
+    Adapter s{pos, mend, nullptr, 8, 1, 0, 0};
+    if (pos >= mend) return s;
+    const int a = uniform(p.rt.sid[pos]);
+    if (a >= p.v.n) return s;
+    s.hi = min((int64_t)uniform(p.rt.off[a + 1]), mend);
+    const lq_adapter ad = p.v.tab[a];
+    const int r8 = (ad.r + 7) & ~7;
+    s.base = !p.lt_all && ad.r % 8 == 0 ? ad.B : p.lt + p.Ncols * ad.row8;
+    s.stride = r8;
+    s.runs = r8 >> 3;
+    s.live = TERMS * s.runs;
+    s.steps = (s.live + 7) >> 3;
+    return s;
+  };
+  auto lora_x = [&](const Adapter& s, int kt, int i, int buf) {
+    const int c = 8 * kt + ch;   // this lane's run of 8 columns
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int64_t pos = min(m0 + xrow(i, q) + sub, p.M - 1);
+      load_lds16(c < s.live ? p.terms + pos * 3 * p.v.rs + 8 * c : p.zeros, lds.x[buf] + xrow(i, q) * GK);
+    }
+  };
+  auto lora_y = [&](const Adapter& s, int kt, int i, int buf) {
+    const int c = 8 * kt + ch;
+#pragma unroll
+    for (int q = 0; q < QY; ++q) {
+      const int64_t n = min(n0 + yrow(i, q) + sub, p.Ncols - 1);
+      load_lds16(c < s.live ? s.base + n * s.stride + 8 * (c % s.runs) : p.zeros, lds.y[buf] + yrow(i, q) * GK);
+    }
+  };
+
+  // Part i of step it into its buffer; Plain: a whole step of the base
+  // contraction. Past the last step zeros, into a buffer that nobody reads any
+  // more: the count of outstanding loads, on which the waits rely, stays the
+  // same.
+  Adapter whole{0, 0, nullptr, 8, 1, 0, 0};   // the tile's one adapter, if it has one
+  typedef std::integral_constant<bool, true> Plain;
+  typedef std::integral_constant<bool, false> Any;
+  auto load_x = [&](auto plain, int it, int i, int buf) {
+    if (plain.value || it < nk) {
+      const int64_t k0 = (int64_t)it * GK;
+      const bool ok = plain.value || !BWD || k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (0 * NaN is not 0)
+#pragma unroll
+      for (int q = 0; q < QX; ++q) load_lds16(ok ? px[i][q] + k0 : p.zeros, lds.x[buf] + xrow(i, q) * GK);
+    } else {
+      lora_x(whole, it - nk, i, buf);
+    }
+  };
+  auto load_y = [&](auto plain, int it, int i, int buf) {
+    if (plain.value || it < nk) {
+      const int64_t k0 = (int64_t)it * GK;
+#pragma unroll
+      for (int q = 0; q < QY; ++q) load_lds16(py[i][q] + k0, lds.y[buf] + yrow(i, q) * GK);
+    } else {
+      lora_y(whole, it - nk, i, buf);
+    }
   };
 
   f32x4_t acc[CT][RT];
@@ -169,32 +169,166 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  stage(0, 0);
-  const int64_t pw = m0 + wm * 16 * RT, cw = n0 + wn * 16 * CT;
-  lora_init<CT, RT, OUT_F32 ? 3 : 2, BWD>(p, pw, cw, acc);
-  __syncthreads();
-  const int nk = (int)((p.Kc + GK - 1) / GK);
-  for (int it = 0; it < nk; ++it) {
-    const int buf = it & 1;
-    if (it + 1 < nk) stage(buf ^ 1, (int64_t)(it + 1) * GK);
-    const uint16_t* sa = lds.a[buf] + (wm * 16 * RT + li) * GK;
-    const uint16_t* sb = lds.b[buf] + (wn * 16 * CT + li) * GK;
+  u32x4_t fx[2][4], fy[2][2][CT / 2];   // [k half][tile], weight side [part][k half][tile]
+  const int slot0 = 8 * (lg ^ (li & 7)), slot1 = 8 * ((4 + lg) ^ (li & 7));
+  const int ox = (wm * 16 * RT + li) * GK, oy = (wn * 16 * CT + li) * GK;
+  auto read_x = [&](int i, int buf) {
+    const uint16_t* b = lds.x[buf] + ox + i * 64 * GK;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int slot = 8 * ((4 * u + lg) ^ (li & 7));
-      u32x4_t fa[RT], fb[CT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) fa[rt] = ld16(sa + 16 * rt * GK + slot);
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) fb[ct] = ld16(sb + 16 * ct * GK + slot);
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          acc[ct][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fb[ct]), as_bf16x8(fa[rt]), acc[ct][rt], 0, 0, 0);
+    for (int r = 0; r < 4; ++r) {
+      fx[0][r] = ld16(b + 16 * r * GK + slot0);
+      fx[1][r] = ld16(b + 16 * r * GK + slot1);
     }
-    __syncthreads();
+  };
+  auto read_y = [&](int i, int buf) {
+    const uint16_t* b = lds.y[buf] + oy + i * 8 * CT * GK;
+#pragma unroll
+    for (int c = 0; c < CT / 2; ++c) {
+      fy[i][0][c] = ld16(b + 16 * c * GK + slot0);
+      fy[i][1][c] = ld16(b + 16 * c * GK + slot1);
+    }
+  };
+  auto end_memory = [&]() {   // the fragments have arrived: a part may be refilled after the barrier
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto multiply = [&](int xi, int yi) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < CT / 2; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[yi * (CT / 2) + c][xi * 4 + r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              as_bf16x8(fy[yi][u][c]), as_bf16x8(fx[u][r]), acc[yi * (CT / 2) + c][xi * 4 + r], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  const bool late = wave >= 4;   // the group that works one slot behind
+  Adapter next = adapter_at(m0);
+  if (next.steps && next.hi == mend) whole = next;
+  const int nsteps = nk + whole.steps;
+  int it = 0, buf = 0;
+  auto step = [&](auto plain) {
+    if constexpr (BIG) {
+      read_x(0, buf);
+      read_y(0, buf);
+      load_x(plain, it + 1, 1, buf ^ 1);
+      wait_vm<10>();          // Y1 of this step
+      end_memory();
+      multiply(0, 0);
+      read_y(1, buf);
+      load_x(plain, it + 2, 0, buf);
+      wait_vm<10>();          // X1 of this step
+      end_memory();
+      multiply(0, 1);
+      read_x(1, buf);
+      load_y(plain, it + 2, 0, buf);
+      end_memory();
+      multiply(1, 1);
+      load_y(plain, it + 2, 1, buf);
+      wait_vm<10>();          // X0 and Y0 of the next step
+      end_memory();
+      multiply(1, 0);
+      buf ^= 1;
+    } else {
+      const int b2 = buf == 0 ? 2 : buf - 1;   // buffer of step it + 2
+      read_x(0, buf);
+      read_y(0, buf);
+      load_x(plain, it + 2, 0, b2);
+      end_memory();
+      multiply(0, 0);
+      read_y(1, buf);
+      load_y(plain, it + 2, 0, b2);
+      load_y(plain, it + 2, 1, b2);
+      wait_vm<QX + 2 * QY>();   // the next step
+      end_memory();
+      multiply(0, 1);
+      buf = buf == 2 ? 0 : buf + 1;
+    }
+    ++it;
+  };
+  if constexpr (BIG) {
+    load_x(Any(), 0, 0, 0);
+    load_y(Any(), 0, 0, 0);
+    load_y(Any(), 0, 1, 0);
+    load_x(Any(), 0, 1, 0);
+    load_x(Any(), 1, 0, 1);
+    load_y(Any(), 1, 0, 1);
+    load_y(Any(), 1, 1, 1);
+    wait_vm<10>();
+  } else {
+    load_x(Any(), 0, 0, 0);
+    load_y(Any(), 0, 0, 0);
+    load_y(Any(), 0, 1, 0);
+    load_x(Any(), 1, 0, 1);
+    load_y(Any(), 1, 0, 1);
+    load_y(Any(), 1, 1, 1);
+    wait_vm<QX + 2 * QY>();
+  }
+  barrier();
+  if (late) barrier();
+  const int nplain = nk - 3;   // steps that load whole steps of the contraction: without a branch
+  while (it < nplain) step(Plain());
+  while (it < nsteps) step(Any());
+  if (!late) barrier();   // as many barriers as the other group
+  wait_vm<0>();           // the loads past the last step, before the workgroup's LDS is given up
+
+  const int64_t pw = m0 + wm * 16 * RT, cw = n0 + wn * 16 * CT;
+
+  // A tile of several adapters: one after the other, each one's products formed
+  // apart and added to its own tokens' columns alone, so that an adapter's
+  // infinities and NaN stay with its tokens.
+  if (!whole.steps && next.steps) {
+    Adapter cur = next;
+    int kt = 0;
+    barrier();   // everyone has read the last step
+    lora_x(cur, 0, 0, 0);
+    if constexpr (XP == 2) lora_x(cur, 0, 1, 0);
+    lora_y(cur, 0, 0, 0);
+    lora_y(cur, 0, 1, 0);
+    for (int b = 0; cur.steps; b ^= 1) {
+      const int64_t lo = cur.lo, hi = cur.hi;
+      if (++kt >= cur.steps) {
+        cur = adapter_at(cur.hi);
+        kt = 0;
+      }
+      wait_vm<0>();
+      barrier();   // this step has landed, and the other buffer is read
+      if (cur.steps) {
+        lora_x(cur, kt, 0, b ^ 1);
+        if constexpr (XP == 2) lora_x(cur, kt, 1, b ^ 1);
+        lora_y(cur, kt, 0, b ^ 1);
+        lora_y(cur, kt, 1, b ^ 1);
+      }
+      read_y(0, b);
+      read_y(1, b);
+#pragma unroll
+      for (int xi = 0; xi < XP; ++xi) {
+        read_x(xi, b);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int64_t pos = pw + 16 * (xi * 4 + r) + li;
+          const bool mine = pos >= lo && pos < hi;
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            f32x4_t d = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fy[c / (CT / 2)][u][c % (CT / 2)]), as_bf16x8(fx[u][r]),
+                                                          d, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[c][xi * 4 + r][e] += mine ? d[e] : 0.0f;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
   }
 
   // lane: token position pw + 16 rt + li, outputs cw + 16 ct + 4 lg + [0, 4)
@@ -253,16 +387,12 @@ __global__ __launch_bounds__(256) void k_transpose_weight(const uint16_t* __rest
   }
 }
 
-__global__ void k_zero16(uint32_t* p) {
-  if (threadIdx.x < 4) p[threadIdx.x] = 0u;
-}
-
 template <int BN>
 hipError_t launch_tile(const AdapterGemm& g, hipStream_t s) {
   const int64_t tiles = ((g.M + GM - 1) / GM) * ((g.Ncols + BN - 1) / BN);
   LQ_DASSERT(tiles > 0 && tiles < (int64_t(1) << 31));
   const dim3 grid((unsigned)tiles), block(G_THREADS);
-  if (g.lt) hipLaunchKernelGGL((k_adapter_gemm<BN, false, true>), grid, block, 0, s, g);
+  if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm<BN, false, true>), grid, block, 0, s, g);
   else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm<BN, true, false>), grid, block, 0, s, g);
   else hipLaunchKernelGGL((k_adapter_gemm<BN, false, false>), grid, block, 0, s, g);
   return hipGetLastError();
@@ -281,11 +411,6 @@ hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int6
   LQ_DASSERT(K % 64 == 0 && ldb % 64 == 0 && ldb >= N && ldb < N + 64);
   hipLaunchKernelGGL(k_transpose_weight, dim3((unsigned)(ldb / 64), (unsigned)(K / 64)), dim3(256), 0, s, w, N, K, ldb,
                      out);
-  return hipGetLastError();
-}
-
-hipError_t launch_zero16(uint16_t* p, hipStream_t s) {
-  hipLaunchKernelGGL(k_zero16, dim3(1), dim3(64), 0, s, reinterpret_cast<uint32_t*>(p));
   return hipGetLastError();
 }
 

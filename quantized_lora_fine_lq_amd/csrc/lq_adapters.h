@@ -19,8 +19,7 @@ inline Route route_view(const int32_t* p, int64_t M, int32_t n) {
 }
 hipError_t launch_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_t* route, hipStream_t s);
 
-// The set as the kernels see it. rs: row stride (floats) of the t and u
-// workspaces, r_max rounded up to a multiple of 8.
+// The set as the kernels see it. rs: r_max rounded up to a multiple of 8.
 struct AdapterView {
   const lq_adapter* tab;   // device
   int32_t n;
@@ -28,57 +27,69 @@ struct AdapterView {
   int32_t rs;
 };
 
-// Row form over routed tokens: out[m][j] = sum_c Q[m][c] R_a[j][c], j < r_a.
+// s_a t and s_a u travel between the kernels as three bfloat16 terms, hi + mid
+// + lo = the float32 value exactly (3 x 8 significand bits), in sorted order:
+// row p holds the token of sorted position p, its hi terms in columns [0, r8),
+// mid in [r8, 2 r8), lo in [2 r8, 3 r8) with r8 = r_a rounded up to a multiple
+// of 8 (zero columns past r_a); row stride 3 rs. Rows of tokens without an
+// adapter are not written. The matrix kernels take two terms for a bfloat16
+// result and three for a float32 one.
+inline size_t terms_elems(int64_t M, const AdapterView& v) { return (size_t)M * 3 * v.rs; }
+
+// Row form over routed tokens: t[m][j] = sum_c Q[m][c] R_a[j][c], j < r_a, as
+// terms of s_a t; or, with Q null, the terms of a given t.
 struct DownJob {
-  const uint16_t* Q;       // [M, C] bf16
+  const uint16_t* Q;       // [M, C] bf16, or null
   int64_t C;               // C % 8 == 0
   const uint16_t* rbase;   // R_a at rbase + C * row8_a, or null: A_a of the table
-  float* out;              // [M, rs] (zero from r_a to rs)
-  float* save;             // [M, r_max] or null (zero past r_a and for tokens without an adapter)
+  const float* given;      // Q null: t [M, r_max]
+  uint16_t* terms;
+  float* save;             // t [M, r_max] or null (zero past r_a and for tokens without an adapter)
 };
+// zeros: 16 bytes, written with zeros (for the matrix kernels)
 hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
-                               hipStream_t s);
+                               uint16_t* zeros, hipStream_t s);
 
-// The adapters transposed for the backward: at [K, r8] at K * row8_a
-// (zero columns past r_a) and bt [r, N] at N * row8_a; either may be null.
-hipError_t launch_adapter_transpose(const AdapterView& v, int64_t N, int64_t K, uint16_t* at, uint16_t* bt,
-                                    hipStream_t s);
+// The adapters re-laid for the matrix kernels: at = A^T [K, r8] at K * row8_a,
+// bt = B^T [r, N] at N * row8_a, bp = B [N, r8] at N * row8_a of the adapters
+// whose rank is not a multiple of 8 (zero columns past r_a). Each may be null.
+hipError_t launch_adapter_relayout(const AdapterView& v, int64_t N, int64_t K, uint16_t* at, uint16_t* bt, uint16_t* bp,
+                                   hipStream_t s);
 
-// Column form over routed tokens: out_a[j][c] = scale_a sum over a's tokens
-// of P[m][j] Q[m][c], written [r, C] at C * row_a, or transposed [C, r].
+// Column form over routed tokens: out_a[j][c] = sum over a's tokens of
+// (s_a P)[m][j] Q[m][c], written [r, C] at C * row_a, or transposed [C, r].
 struct ColReq {
-  const float* P;      // [M, pstride]
-  int32_t pstride;
-  const uint16_t* Q;   // [M, C] bf16, C % 8 == 0
+  const uint16_t* terms;   // of s_a P
+  const uint16_t* Q;       // [M, C] bf16, C % 8 == 0
   int64_t C;
   float* out;
   int transposed;
-  float* part;         // adapter_col_ws_floats
+  float* part;             // adapter_col_ws_floats
 };
 size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs);
 hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const AdapterView& v, const Route& rt,
-                              hipStream_t s);
+                              const uint16_t* zeros, hipStream_t s);
 
-// out[token][c] = sum_k A[token][k] Bt[c][k] + s_a sum_j L[token][j] Lb_a(c, j)
-// over the sorted positions; Lb_a = B_a (lt null) or A_a^T from lt (+ Ncols *
-// row8_a, [Ncols, r8]).
+// out[token][c] = sum_k A[token][k] Bt[c][k] + sum_j (s_a L)[token][j] Lb_a(c, j)
+// over the sorted positions; Lb_a(c, j): row c of lt + Ncols * row8_a
+// [Ncols, r8]; of B_a itself where lt_all is 0 and r_a % 8 == 0.
 struct AdapterGemm {
-  const uint16_t* A;     // [M, Kc]
+  const uint16_t* A;       // [M, Kc]
   int64_t M, Ncols, Kc;
-  const uint16_t* Bt;    // [Ncols, ldb], ldb % 64 == 0, zero from Kc to ldb
+  const uint16_t* Bt;      // [Ncols, ldb], ldb % 64 == 0, zero from Kc to ldb
   int64_t ldb;
-  const float* L;        // [M, rs]
+  const uint16_t* terms;   // of s_a L
   AdapterView v;
   const uint16_t* lt;
+  int lt_all;
   Route rt;
-  void* out;             // [M, Ncols] bf16 or float32
+  void* out;               // [M, Ncols] bf16 or float32
   int out_f32;
-  const uint16_t* zeros; // 16 zero bytes, read past Kc
+  const uint16_t* zeros;   // 16 zero bytes
 };
 hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s);
-// [N, K] -> [K, ldb] bf16 (zero columns from N to ldb), and 16 zero bytes at zeros.
+// [N, K] -> [K, ldb] bf16 (zero columns from N to ldb)
 hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out, hipStream_t s);
-hipError_t launch_zero16(uint16_t* p, hipStream_t s);
 
 // Decode sizes (NF4, M <= 64): the whole forward without a route, in one or
 // two launches.

@@ -138,18 +138,31 @@ __device__ __forceinline__ bool find_item(const int32_t* __restrict__ off, int n
   return false;
 }
 
+// The three bfloat16 terms of v.
+__device__ __forceinline__ void split3(float v, uint16_t (&o)[3]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const uint32_t b = pack_bf16x2(v, 0.0f) & 0xFFFFu;
+    o[k] = (uint16_t)b;
+    v -= bf16lo_to_f32(b);
+  }
+}
+
 // ===========================================================================
 // Row form: 16 routed tokens of one adapter per workgroup; its W waves take
 // contiguous runs of 64-column blocks, MFMA 16x16x32 with tokens as rows and
-// the adapter's rows as columns, both straight from memory into registers.
-// The waves' partial sums meet in LDS and are added in wave order.
+// the adapter's rows as columns, both straight from memory into registers, a
+// wave's next U blocks loading while the current ones are multiplied. The
+// waves' partial sums meet in LDS and are added in wave order.
 // ===========================================================================
-template <int JT, int W>
-__global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt) {
+template <int JT, int W, int U>
+__global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt,
+                                                         uint16_t* zeros) {
   __shared__ f32x4_t part[W][JT][64];
   const DownJob jb = blockIdx.y ? j1 : j0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 8) zeros[threadIdx.x] = 0;
   Item it;
   if (!find_item(rt.off, v.n + 1, 16, (int)blockIdx.x, it)) return;
   if (it.seg == v.n) {   // tokens without an adapter
@@ -159,7 +172,25 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
     return;
   }
   const lq_adapter ad = v.tab[it.seg];
-  const int r = min(ad.r, 16 * JT);
+  const int r = min(ad.r, 16 * JT), r8 = (r + 7) & ~7;
+  auto put = [&](int row, int j, float x) {   // x = t[row][j]
+    const int64_t pos = it.start + row;
+    if (jb.save && j < v.r_max) jb.save[(int64_t)rt.perm[pos] * v.r_max + j] = x;
+    if (j < r8) {
+      uint16_t o[3];
+      split3(ad.scale * x, o);
+      uint16_t* d = jb.terms + pos * 3 * v.rs + j;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) d[k * r8] = o[k];
+    }
+  };
+  if (!jb.Q) {
+    for (int i = threadIdx.x; i < it.count * r8; i += 64 * W) {
+      const int row = i / r8, j = i - row * r8;
+      put(row, j, j < r ? jb.given[(int64_t)rt.perm[it.start + row] * v.r_max + j] : 0.0f);
+    }
+    return;
+  }
   const int64_t C = jb.C;
   const uint16_t* R = jb.rbase ? jb.rbase + C * ad.row8 : ad.A;
   const uint16_t* q = jb.Q + (int64_t)rt.perm[it.start + min(li, it.count - 1)] * C;
@@ -169,81 +200,94 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
   f32x4_t acc[JT];
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt) acc[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int64_t blocks = (C + 63) / 64, per = (blocks + W - 1) / W;
-  const int64_t b0 = min(blocks, wave * per), b1 = min(blocks, b0 + per);
-  for (int64_t b = b0; b < b1; ++b) {
-    u32x4_t a[2], w[2][JT];
+  const int blocks = (int)((C + 63) / 64), per = (blocks + W - 1) / W;
+  const int b0 = min(blocks, wave * per), b1 = min(blocks, b0 + per);
+  struct Set {
+    u32x4_t a[U][2], w[U][2][JT];
+  };
+  auto load = [&](int b, Set& s) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t c = 64 * b + 16 * lg + 8 * h;
-      const bool ok = c + 8 <= C;
-      const int64_t o = ok ? c : 0;
-      a[h] = ld16(q + o);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int jt = 0; jt < JT; ++jt) w[h][jt] = ld16(rr[jt] + o);
-      if (!ok) {
-        a[h] = u32x4_t{0u, 0u, 0u, 0u};
+      for (int h = 0; h < 2; ++h) {
+        const int64_t c = 64 * (int64_t)(b + u) + 16 * lg + 8 * h;
+        const bool ok = b + u < b1 && c + 8 <= C;   // past the end: zeros in place of columns 0 .. 7
+        const int64_t o = ok ? c : 0;
+        s.a[u][h] = ld16(q + o);
 #pragma unroll
-        for (int jt = 0; jt < JT; ++jt) w[h][jt] = a[h];
+        for (int jt = 0; jt < JT; ++jt) s.w[u][h][jt] = ld16(rr[jt] + o);
+        if (!ok) {
+          s.a[u][h] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int jt = 0; jt < JT; ++jt) s.w[u][h][jt] = u32x4_t{0u, 0u, 0u, 0u};
+        }
       }
-    }
+  };
+  auto mul = [&](const Set& s) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int jt = 0; jt < JT; ++jt)
-        acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[h]), as_bf16x8(w[h][jt]), acc[jt], 0, 0, 0);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int jt = 0; jt < JT; ++jt)
+          acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(s.a[u][h]), as_bf16x8(s.w[u][h][jt]), acc[jt], 0, 0, 0);
+  };
+  Set s0, s1;
+  if (b0 < b1) load(b0, s0);
+  for (int b = b0; b < b1; b += 2 * U) {
+    if (b + U < b1) load(b + U, s1);
+    mul(s0);
+    if (b + U >= b1) break;
+    if (b + 2 * U < b1) load(b + 2 * U, s0);
+    mul(s1);
   }
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt) part[wave][jt][lane] = acc[jt];
   __syncthreads();
-  for (int i = threadIdx.x; i < JT * 64; i += 64 * W) {
-    const int jt = i >> 6, ln = i & 63, j = 16 * jt + (ln & 15);
-    f32x4_t sum = part[0][jt][ln];
+  for (int i = threadIdx.x; i < JT * 256; i += 64 * W) {
+    // consecutive threads: consecutive columns of one token
+    const int row = i / (16 * JT), j = i % (16 * JT), jt = j >> 4;
+    if (row >= it.count) continue;
+    const int ln = 16 * (row >> 2) + (j & 15);
+    float sum = part[0][jt][ln][row & 3];
 #pragma unroll
-    for (int w = 1; w < W; ++w) sum += part[w][jt][ln];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = 4 * (ln >> 4) + e;
-      if (row >= it.count) continue;
-      const int64_t token = rt.perm[it.start + row];
-      const float x = j < r ? sum[e] : 0.0f;
-      if (j < v.rs) jb.out[token * v.rs + j] = x;
-      if (jb.save && j < v.r_max) jb.save[token * v.r_max + j] = x;
-    }
+    for (int w = 1; w < W; ++w) sum += part[w][jt][ln][row & 3];
+    put(row, j, j < r ? sum : 0.0f);
   }
 }
 
-// at[k][j] = A[j][k] (j < r8, zero past r), bt[j][n] = B[n][j]
-__global__ __launch_bounds__(256) void k_adapter_transpose(AdapterView v, int64_t N, int64_t K,
-                                                           uint16_t* __restrict__ at, uint16_t* __restrict__ bt) {
+// at[k][j] = A[j][k], bp[n][j] = B[n][j] (j < r8, zero past r), bt[j][n] = B[n][j]
+__global__ __launch_bounds__(256) void k_adapter_relayout(AdapterView v, int64_t N, int64_t K,
+                                                          uint16_t* __restrict__ at, uint16_t* __restrict__ bt,
+                                                          uint16_t* __restrict__ bp) {
   const lq_adapter ad = v.tab[blockIdx.y];
   const int r = ad.r, r8 = (r + 7) & ~7;
-  const int64_t na = at ? K * r8 : 0, nb = bt ? N * r : 0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < na + nb; i += (int64_t)gridDim.x * 256) {
+  const int64_t na = at ? K * r8 : 0, nb = bt ? N * r : 0, np = bp && r % 8 ? N * r8 : 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < na + nb + np; i += (int64_t)gridDim.x * 256) {
     if (i < na) {
       const int64_t j = i / K, k = i % K;
       at[K * ad.row8 + k * r8 + j] = j < r ? ad.A[j * K + k] : (uint16_t)0;
-    } else {
+    } else if (i < na + nb) {
       const int64_t n = (i - na) / r, j = (i - na) % r;
       bt[N * ad.row8 + j * N + n] = ad.B[n * r + j];
+    } else {
+      const int64_t n = (i - na - nb) / r8, j = (i - na - nb) % r8;
+      bp[N * ad.row8 + n * r8 + j] = j < r ? ad.B[n * r + j] : (uint16_t)0;
     }
   }
 }
 
 // ===========================================================================
-// Column form: out_a[j][c] = s_a sum_m P[m][j] Q[m][c] over a's tokens. One
+// Column form: out_a[j][c] = sum_m (s_a P)[m][j] Q[m][c] over a's tokens. One
 // workgroup per 128 columns and run of at most `rows` sorted positions; 32
-// tokens per step. P (float32) is split into three bfloat16 terms, hi + mid +
-// lo = P exactly (3 x 8 significand bits), so the products carry float32 P on
-// the bf16 matrix cores; all three go into the same accumulators. P and Q
-// tiles lie in LDS with tokens as rows and are read transposed
+// tokens per step. P comes as three bfloat16 terms, so the products carry
+// float32 P on the bf16 matrix cores; all three go into the same accumulators.
+// P and Q tiles lie in LDS with tokens as rows and are read transposed
 // (ds_read_b64_tr_b16: the 16 lanes of a group point at 4 rows of 16 elements,
 // lane l gets column l of the 4 rows). Tokens past the segment are zero in
 // both, so no neighbour's infinity or NaN enters.
 // ===========================================================================
 constexpr int CQ_PITCH = 128 + 8;
-
-__device__ __forceinline__ uint32_t bf16_bits(float v) { return pack_bf16x2(v, 0.0f) & 0xFFFFu; }
 
 // lane's 8 values k = 8 lg + [0, 8) of column li, from rows of `pitch` elements
 __device__ __forceinline__ u32x4_t tr_frag(const uint16_t* base, int pitch, int li, int lg) {
@@ -267,7 +311,7 @@ __global__ __launch_bounds__(256) void k_adapter_col(ColReq q0, ColReq q1, unsig
   Item it;
   if (!find_item(rt.off, v.n, rows, (int)blockIdx.y, it)) return;
   const lq_adapter ad = v.tab[it.seg];
-  const int r = min(ad.r, 16 * JT);
+  const int r = min(ad.r, 16 * JT), r8 = (r + 7) & ~7;
   const int64_t C = rq.C, c0 = (int64_t)(second ? blockIdx.x - tiles0 : blockIdx.x) * 128;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
@@ -284,15 +328,12 @@ __global__ __launch_bounds__(256) void k_adapter_col(ColReq q0, ColReq q1, unsig
       if (mb + row < it.count && c0 + cc + 8 <= C) x = ld16(rq.Q + (int64_t)rt.perm[it.start + mb + row] * C + c0 + cc);
       *reinterpret_cast<u32x4_t*>(sQ + row * CQ_PITCH + cc) = x;
     }
-    for (int i = threadIdx.x; i < 32 * 16 * JT; i += 256) {
-      const int row = i / (16 * JT), j = i % (16 * JT);
-      float x = 0.0f;
-      if (mb + row < it.count && j < r) x = rq.P[(int64_t)rt.perm[it.start + mb + row] * rq.pstride + j];
-      const float hi = bf16lo_to_f32(bf16_bits(x)), y = x - hi;
-      const float mid = bf16lo_to_f32(bf16_bits(y));
-      sP[row * PP + j] = (uint16_t)bf16_bits(hi);
-      sP[(32 + row) * PP + j] = (uint16_t)bf16_bits(mid);
-      sP[(64 + row) * PP + j] = (uint16_t)bf16_bits(y - mid);
+    for (int i = threadIdx.x; i < 3 * 32 * 2 * JT; i += 256) {   // 8 columns of one term and token each
+      const int c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, k = i / (64 * JT);
+      u32x4_t x = {0u, 0u, 0u, 0u};
+      if (mb + row < it.count && 8 * c8 < r8)
+        x = ld16(rq.terms + (int64_t)(it.start + mb + row) * 3 * v.rs + k * r8 + 8 * c8);
+      *reinterpret_cast<u32x4_t*>(sP + (32 * k + row) * PP + 8 * c8) = x;
     }
     __syncthreads();
     u32x4_t b[2];
@@ -321,8 +362,8 @@ __global__ __launch_bounds__(256) void k_adapter_col(ColReq q0, ColReq q1, unsig
         const int j = 16 * jt + 4 * lg + e;
         if (j >= r) continue;
         if (it.slot >= 0) rq.part[((int64_t)it.slot * v.rs + j) * C + c] = acc[jt][ct][e];
-        else if (rq.transposed) rq.out[C * ad.row + c * r + j] = ad.scale * acc[jt][ct][e];
-        else rq.out[(ad.row + (int64_t)j) * C + c] = ad.scale * acc[jt][ct][e];
+        else if (rq.transposed) rq.out[C * ad.row + c * r + j] = acc[jt][ct][e];
+        else rq.out[(ad.row + (int64_t)j) * C + c] = acc[jt][ct][e];
       }
     }
 }
@@ -348,7 +389,6 @@ __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1
     const int64_t e = i < n0 ? i : i - n0, j = e / q.C, c = e % q.C;
     float sum = 0.0f;
     for (int k = 0; k < runs; ++k) sum += q.part[((int64_t)(before + k) * v.rs + j) * q.C + c];
-    sum *= ad.scale;
     q.out[q.C * ad.row + (q.transposed ? c * ad.r + j : e)] = sum;
   }
 }
@@ -373,23 +413,25 @@ hipError_t launch_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_
 }
 
 hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
-                               hipStream_t s) {
+                               uint16_t* zeros, hipStream_t s) {
   if (njobs < 1 || njobs > 2) return hipErrorInvalidValue;
   const DownJob j0 = jobs[0], j1 = jobs[njobs - 1];
   // one item per 16 tokens, and one more per adapter (or none) for its remainder
   const dim3 grid((unsigned)((M + 15) / 16 + std::min<int64_t>(v.n + 1, M)), (unsigned)njobs);
-  if (v.r_max <= 16) hipLaunchKernelGGL((k_adapter_down<1, 8>), grid, dim3(512), 0, s, j0, j1, M, v, rt);
-  else if (v.r_max <= 32) hipLaunchKernelGGL((k_adapter_down<2, 8>), grid, dim3(512), 0, s, j0, j1, M, v, rt);
-  else if (v.r_max <= 64) hipLaunchKernelGGL((k_adapter_down<4, 8>), grid, dim3(512), 0, s, j0, j1, M, v, rt);
-  else hipLaunchKernelGGL((k_adapter_down<8, 4>), grid, dim3(256), 0, s, j0, j1, M, v, rt);
+#define LQ_AD(JT, W, U) hipLaunchKernelGGL((k_adapter_down<JT, W, U>), grid, dim3(64 * W), 0, s, j0, j1, M, v, rt, zeros)
+  if (v.r_max <= 16) LQ_AD(1, 16, 2);
+  else if (v.r_max <= 32) LQ_AD(2, 16, 2);
+  else if (v.r_max <= 64) LQ_AD(4, 16, 1);
+  else LQ_AD(8, 8, 1);
+#undef LQ_AD
   return hipGetLastError();
 }
 
-hipError_t launch_adapter_transpose(const AdapterView& v, int64_t N, int64_t K, uint16_t* at, uint16_t* bt,
-                                    hipStream_t s) {
-  const int64_t most = (N + K) * v.rs;
+hipError_t launch_adapter_relayout(const AdapterView& v, int64_t N, int64_t K, uint16_t* at, uint16_t* bt, uint16_t* bp,
+                                   hipStream_t s) {
+  const int64_t most = (at ? K * v.rs : 0) + (bt ? N * v.rs : 0) + (bp ? N * v.rs : 0);
   const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 255) / 256, std::max(16, 4096 / v.n)));
-  hipLaunchKernelGGL(k_adapter_transpose, dim3(gx, (unsigned)v.n), dim3(256), 0, s, v, N, K, at, bt);
+  hipLaunchKernelGGL(k_adapter_relayout, dim3(gx, (unsigned)v.n), dim3(256), 0, s, v, N, K, at, bt, bp);
   return hipGetLastError();
 }
 
@@ -400,7 +442,8 @@ size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs) {
 }
 
 hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const AdapterView& v, const Route& rt,
-                              hipStream_t s) {
+                              const uint16_t* zeros, hipStream_t s) {
+  (void)zeros;
   if (nreq < 1 || nreq > 2) return hipErrorInvalidValue;
   const ColReq q0 = reqs[0], q1 = reqs[nreq - 1];
   const int rows = col_rows(M, q0.C + (nreq > 1 ? q1.C : 0));

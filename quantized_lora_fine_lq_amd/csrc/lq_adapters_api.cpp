@@ -41,22 +41,29 @@ size_t route_bytes(int64_t M, int32_t n) { return (size_t)route_words(M, n) * si
 
 int64_t ldb_of(int64_t n) { return (n + 63) / 64 * 64; }
 
-// route, t, W'; at decode sizes what that path keeps
-size_t forward_ws(const QWeight& q, int64_t M, const AdapterView& v) {
-  if (adapter_decode_supported(q, M))
-    return align_up(adapter_decode_ws_bytes(q, M, v));
-  return align_up(route_bytes(M, v.n)) + align_up((size_t)M * v.rs * sizeof(float)) +
-         align_up((size_t)q.N * q.K * sizeof(uint16_t));
+bool any_odd_rank(const lq_adapter_set* set) {
+  for (int32_t a = 0; a < set->n; ++a)
+    if (set->host[a].r % 8) return true;
+  return false;
 }
 
-// route, u, t, A^T and B^T of the adapters, W' and its transpose, partial
-// sums of dA and dB, 16 zero bytes
+size_t bytes16(size_t elems) { return align_up(elems * sizeof(uint16_t)); }
+
+// route, terms of t, W', zeros, B of ranks that are no multiple of 8; at
+// decode sizes what that path keeps
+size_t forward_ws(const QWeight& q, int64_t M, const AdapterView& v, const lq_adapter_set* set) {
+  if (adapter_decode_supported(q, M)) return align_up(adapter_decode_ws_bytes(q, M, v));
+  return align_up(route_bytes(M, v.n)) + bytes16(terms_elems(M, v)) + bytes16((size_t)q.N * q.K) + bytes16(8) +
+         (any_odd_rank(set) ? bytes16((size_t)sum_r8(set) * q.N) : 0);
+}
+
+// route, terms of u and t, A^T and B^T of the adapters, W' and its transpose,
+// partial sums of dA and dB, zeros
 size_t backward_ws(const QWeight& q, int64_t M, const AdapterView& v, int64_t r8) {
-  return align_up(route_bytes(M, v.n)) + 2 * align_up((size_t)M * v.rs * sizeof(float)) +
-         align_up((size_t)r8 * q.K * sizeof(uint16_t)) + align_up((size_t)r8 * q.N * sizeof(uint16_t)) +
-         align_up((size_t)q.N * q.K * sizeof(uint16_t)) + align_up((size_t)q.K * ldb_of(q.N) * sizeof(uint16_t)) +
+  return align_up(route_bytes(M, v.n)) + 2 * bytes16(terms_elems(M, v)) + bytes16((size_t)r8 * q.K) +
+         bytes16((size_t)r8 * q.N) + bytes16((size_t)q.N * q.K) + bytes16((size_t)q.K * ldb_of(q.N)) +
          align_up(adapter_col_ws_floats(M, q.K, v.rs) * sizeof(float)) +
-         align_up(adapter_col_ws_floats(M, q.N, v.rs) * sizeof(float)) + align_up(16);
+         align_up(adapter_col_ws_floats(M, q.N, v.rs) * sizeof(float)) + bytes16(8);
 }
 
 }  // namespace
@@ -84,7 +91,7 @@ size_t lq_adapters_forward_workspace(const lq_qweight* w, int64_t M, const lq_ad
   QWeight q;
   AdapterView v;
   if (check_qweight(w, &q) != LQ_OK || !valid_M(M) || check_set(set, q.N, q.K, &v) != LQ_OK) return 0;
-  return forward_ws(q, M, v);
+  return forward_ws(q, M, v, set);
 }
 
 int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const lq_adapter_set* set,
@@ -101,15 +108,17 @@ int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const
     return LQ_ERR_ARG;
   if (!valid_M(M)) return LQ_ERR_SHAPE;
   if (h_dtype != LQ_BF16 && h_dtype != LQ_F32) return LQ_ERR_UNSUPPORTED;
-  if (!workspace || ws_bytes < forward_ws(q, M, v)) return LQ_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < forward_ws(q, M, v, set)) return LQ_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   if ((st = debug_check_weight(q, s)) != LQ_OK) return st;
   Carver cv(workspace, ws_bytes);
   if (adapter_decode_supported(q, M))
     return launch_status(launch_adapter_decode(q, X, M, ids, v, workspace, t_save, H, h_dtype == LQ_F32, s));
-  float* t = cv.take<float>((size_t)M * v.rs);
   int32_t* rws = cv.take<int32_t>(route_words(M, v.n));
+  uint16_t* terms = cv.take<uint16_t>(terms_elems(M, v));
   uint16_t* wd = cv.take<uint16_t>((size_t)q.N * q.K);
+  uint16_t* zeros = cv.take<uint16_t>(8);
+  uint16_t* bp = any_odd_rank(set) ? cv.take<uint16_t>((size_t)sum_r8(set) * q.N) : nullptr;
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
 
   hipError_t e = hipSuccess;
@@ -118,10 +127,11 @@ int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const
     route = rws;
   }
   const Route rt = route_view(route, M, v.n);
-  const DownJob job{X, q.K, nullptr, t, t_save};
-  if ((e = launch_adapter_down(&job, 1, M, v, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  if (bp && (e = launch_adapter_relayout(v, q.N, q.K, nullptr, nullptr, bp, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  const DownJob job{X, q.K, nullptr, nullptr, terms, t_save};
+  if ((e = launch_adapter_down(&job, 1, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   if ((e = launch_dequant(q, wd, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  const AdapterGemm g{X, M, q.N, q.K, wd, q.K, t, v, nullptr, rt, H, h_dtype == LQ_F32 ? 1 : 0, nullptr};
+  const AdapterGemm g{X, M, q.N, q.K, wd, q.K, terms, v, bp, 0, rt, H, h_dtype == LQ_F32 ? 1 : 0, zeros};
   return launch_status(launch_adapter_gemm(g, s));
 }
 
@@ -152,8 +162,8 @@ int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t*
   if ((st = debug_check_weight(q, s)) != LQ_OK) return st;
   Carver cv(workspace, ws_bytes);
   int32_t* rws = cv.take<int32_t>(route_words(M, v.n));
-  float* u = cv.take<float>((size_t)M * v.rs);
-  float* t = cv.take<float>((size_t)M * v.rs);
+  uint16_t* u = cv.take<uint16_t>(terms_elems(M, v));
+  uint16_t* t = cv.take<uint16_t>(terms_elems(M, v));
   uint16_t* at = cv.take<uint16_t>((size_t)r8 * q.K);
   uint16_t* bt = cv.take<uint16_t>((size_t)r8 * q.N);
   uint16_t* wd = cv.take<uint16_t>((size_t)q.N * q.K);
@@ -173,24 +183,23 @@ int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t*
   const Route rt = route_view(route, M, v.n);
   const bool need_u = grad_X || dA;
   if (need_u) {
-    e = launch_adapter_transpose(v, q.N, q.K, grad_X ? at : nullptr, bt, s);
+    e = launch_adapter_relayout(v, q.N, q.K, grad_X ? at : nullptr, bt, nullptr, s);
     if (e != hipSuccess) return LQ_ERR_LAUNCH;
   }
   DownJob jobs[2];
   int nj = 0;
-  if (need_u) jobs[nj++] = DownJob{G, q.N, bt, u, nullptr};
-  if (need_t) jobs[nj++] = DownJob{X, q.K, nullptr, t, nullptr};
-  if (nj && (e = launch_adapter_down(jobs, nj, M, v, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  if (need_u) jobs[nj++] = DownJob{G, q.N, bt, nullptr, u, nullptr};
+  if (dB) jobs[nj++] = DownJob{t_saved ? nullptr : X, q.K, nullptr, t_saved, t, nullptr};
+  if (nj && (e = launch_adapter_down(jobs, nj, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   ColReq cols[2];
   int nc = 0;
-  if (dB) cols[nc++] = ColReq{t_saved ? t_saved : t, t_saved ? v.r_max : v.rs, G, q.N, dB, 1, part_b};
-  if (dA) cols[nc++] = ColReq{u, v.rs, X, q.K, dA, 0, part_a};
-  if (nc && (e = launch_adapter_col(cols, nc, M, v, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  if (dB) cols[nc++] = ColReq{t, G, q.N, dB, 1, part_b};
+  if (dA) cols[nc++] = ColReq{u, X, q.K, dA, 0, part_a};
+  if (nc && (e = launch_adapter_col(cols, nc, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   if (!grad_X) return LQ_OK;
   if ((e = launch_dequant(q, wd, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   if ((e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  if ((e = launch_zero16(zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  const AdapterGemm g{G, M, q.K, q.N, wt, ldb, u, v, at, rt, grad_X, 0, zeros};
+  const AdapterGemm g{G, M, q.K, q.N, wt, ldb, u, v, at, 1, rt, grad_X, 0, zeros};
   return launch_status(launch_adapter_gemm(g, s));
 }
 
