@@ -17,7 +17,6 @@ inline Route route_view(const int32_t* p, int64_t M, int32_t n) {
   const int64_t a = ((int64_t)n + 2 + 3) / 4 * 4, b = (M + 3) / 4 * 4;
   return Route{p, p + a, p + a + b};
 }
-hipError_t launch_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_t* route, hipStream_t s);
 
 // The set as the kernels see it. rs: r_max rounded up to a multiple of 8.
 struct AdapterView {
@@ -50,11 +49,15 @@ struct DownJob {
 hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
                                uint16_t* zeros, hipStream_t s);
 
-// The adapters re-laid for the matrix kernels: at = A^T [K, r8] at K * row8_a,
-// bt = B^T [r, N] at N * row8_a, bp = B [N, r8] at N * row8_a of the adapters
-// whose rank is not a multiple of 8 (zero columns past r_a). Each may be null.
-hipError_t launch_adapter_relayout(const AdapterView& v, int64_t N, int64_t K, uint16_t* at, uint16_t* bt, uint16_t* bp,
-                                   hipStream_t s);
+// Preparation, one launch of independent parts, each left out where its
+// pointer is null: the route of ids; an NF4 weight decoded to wd (W' [N, K], or
+// with ldb W'^T [K, ldb], zero columns from N on); the adapters re-laid for the
+// matrix kernels: at = A^T [K, r8] at K * row8_a, bt = B^T [r, N] at N *
+// row8_a, bp = B [N, r8] at N * row8_a of the adapters whose rank is not a
+// multiple of 8 (zero columns past r_a).
+hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, const QWeight& w, uint16_t* wd,
+                               int64_t ldb, const AdapterView& v, uint16_t* at, uint16_t* bt, uint16_t* bp,
+                               hipStream_t s);
 
 // Column form over routed tokens: out_a[j][c] = sum over a's tokens of
 // (s_a P)[m][j] Q[m][c], written [r, C] at C * row_a, or transposed [C, r].
@@ -68,7 +71,7 @@ struct ColReq {
 };
 size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs);
 hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const AdapterView& v, const Route& rt,
-                              const uint16_t* zeros, hipStream_t s);
+                              hipStream_t s);
 
 // out[token][c] = sum_k A[token][k] Bt[c][k] + sum_j (s_a L)[token][j] Lb_a(c, j)
 // over the sorted positions; Lb_a(c, j): row c of lt + Ncols * row8_a

@@ -19,37 +19,54 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // Wave w owns a contiguous run of tokens; pass 1 counts its tokens per adapter
 // in LDS (integer additions: their order does not matter), the counts are
 // scanned over adapters and waves, and pass 2 gives each token of a 64-token
-// group its place among the group's equal ids from ten ballots (one per bit of
-// the id). Bound by the latency of its few dependent passes.
+// group its place among the group's equal ids from ballots (one per bit of
+// the id). Bound by the latency of its few dependent passes; the first
+// RT_KEEP groups of a wave keep their ids in registers between the passes.
 // ===========================================================================
-constexpr int RT_WAVES = 16;
+constexpr int RT_WAVES = 16, RT_KEEP = 4;
 
-__global__ __launch_bounds__(64 * RT_WAVES) void k_adapter_route(const int32_t* __restrict__ ids, int64_t M, int n,
-                                                                 int32_t* __restrict__ off,
-                                                                 int32_t* __restrict__ perm,
-                                                                 int32_t* __restrict__ sid) {
-  extern __shared__ int32_t cnt[];   // [RT_WAVES][keys], then the wave sums of the scan
-  const int keys = n + 1;
+struct RouteJob {
+  const int32_t* ids;   // null: no route wanted
+  int64_t M;
+  int32_t n;
+  int32_t *off, *perm, *sid;
+};
+constexpr size_t route_lds_bytes(int n) { return (size_t)(RT_WAVES * (n + 1) + RT_WAVES) * sizeof(int32_t); }
+
+__device__ __forceinline__ void route_tokens(const RouteJob& jb, int32_t* cnt) {
+  const int n = jb.n, keys = n + 1;
+  const int64_t M = jb.M;
   int32_t* wsum = cnt + RT_WAVES * keys;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t per = ((M + RT_WAVES - 1) / RT_WAVES + 63) / 64 * 64;
   const int64_t m0 = min(M, wave * per), m1 = min(M, m0 + per);
+  int keep[RT_KEEP];
+#pragma unroll
+  for (int g = 0; g < RT_KEEP; ++g) keep[g] = jb.ids[min(m0 + 64 * g + lane, M - 1)];
   for (int i = threadIdx.x; i < RT_WAVES * keys; i += 64 * RT_WAVES) cnt[i] = 0;
   __syncthreads();
-  for (int64_t m = m0 + lane; m < m1; m += 64) {
-    const int id = ids[m];
-    atomicAdd(&cnt[wave * keys + ((uint32_t)id < (uint32_t)n ? id : n)], 1);
-  }
+  auto key_of = [&](int id) { return (uint32_t)id < (uint32_t)n ? id : n; };
+#pragma unroll
+  for (int g = 0; g < RT_KEEP; ++g)
+    if (m0 + 64 * g + lane < m1) atomicAdd(&cnt[wave * keys + key_of(keep[g])], 1);
+  for (int64_t m = m0 + 64 * RT_KEEP + lane; m < m1; m += 64) atomicAdd(&cnt[wave * keys + key_of(jb.ids[m])], 1);
   __syncthreads();
   // totals per key (thread k; keys <= 1024), waves' counts to exclusive sums
   const int k = threadIdx.x;
   int total = 0;
-  if (k < keys)
+  if (k < keys) {
+    int c[RT_WAVES];
+#pragma unroll
+    for (int w = 0; w < RT_WAVES; ++w) c[w] = cnt[w * keys + k];
+#pragma unroll
     for (int w = 0; w < RT_WAVES; ++w) {
-      const int c = cnt[w * keys + k];
-      cnt[w * keys + k] = total;
-      total += c;
+      const int x = c[w];
+      c[w] = total;
+      total += x;
     }
+#pragma unroll
+    for (int w = 0; w < RT_WAVES; ++w) cnt[w * keys + k] = c[w];
+  }
   int inc = total;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
@@ -59,21 +76,23 @@ __global__ __launch_bounds__(64 * RT_WAVES) void k_adapter_route(const int32_t* 
   if (lane == 63) wsum[wave] = inc;
   __syncthreads();
   int base = inc - total;
-  for (int w = 0; w < wave; ++w) base += wsum[w];
+#pragma unroll
+  for (int w = 0; w < RT_WAVES; ++w) base += w < wave ? wsum[w] : 0;
   if (k < keys) {
-    off[k] = base;
-    if (k == n) off[n + 1] = (int32_t)M;
+    jb.off[k] = base;
+    if (k == n) jb.off[n + 1] = (int32_t)M;
+#pragma unroll
     for (int w = 0; w < RT_WAVES; ++w) cnt[w * keys + k] += base;
   }
   __syncthreads();
-  for (int64_t g = m0; g < m1; g += 64) {
+  int bits = 0;
+  while ((n >> bits) != 0) ++bits;
+  auto place = [&](int64_t g, int id) {
     const int64_t m = g + lane;
     const bool live = m < m1;
-    const int id = live ? ids[m] : 0;
-    const int key = (uint32_t)id < (uint32_t)n ? id : n;
+    const int key = key_of(id);
     uint64_t peers = __ballot(live);
-#pragma unroll
-    for (int b = 0; b < 10; ++b) {
+    for (int b = 0; b < bits; ++b) {
       const uint64_t one = __ballot((key >> b) & 1);
       peers &= ((key >> b) & 1) ? one : ~one;
     }
@@ -84,10 +103,149 @@ __global__ __launch_bounds__(64 * RT_WAVES) void k_adapter_route(const int32_t* 
     if (live && rank == 0) *c = start + __popcll(peers);
     __builtin_amdgcn_wave_barrier();
     if (live) {
-      perm[start + rank] = (int32_t)m;
-      sid[start + rank] = key;
+      jb.perm[start + rank] = (int32_t)m;
+      jb.sid[start + rank] = key;
     }
+  };
+#pragma unroll
+  for (int g = 0; g < RT_KEEP; ++g)
+    if (m0 + 64 * g < m1) place(m0 + 64 * g, keep[g]);
+  for (int64_t g = m0 + 64 * RT_KEEP; g < m1; g += 64) place(g, g + lane < m1 ? jb.ids[g + lane] : 0);
+}
+
+// ===========================================================================
+// Preparation, one launch: workgroup 0 builds the route, the others decode the
+// NF4 weight (as it lies, or transposed for the backward) and re-lay the
+// adapters; none of it depends on the rest. Bound by writing the bfloat16
+// weight.
+// ===========================================================================
+constexpr int PW_K = 256;                 // decoded per workgroup: 64 weight rows x PW_K columns
+constexpr int PW_PITCH = PW_K + 16;       // bf16 per LDS row: the transposing reads of 4 rows hit distinct banks
+constexpr int RL_C = 128;                 // re-laid per workgroup: RL_C rows of A^T or B
+
+struct PrepJob {
+  RouteJob route;
+  QWeight w;
+  Nf4Levels lv;
+  uint16_t* wd;          // W' [N, K], or transposed [K, ldb] (zero columns past N); null: not wanted
+  int64_t ldb;           // 0: not transposed
+  AdapterView v;
+  uint16_t *at, *bt, *bp;
+  unsigned route_wgs, weight_wgs, per_adapter, at_wgs, b_wgs;
+};
+
+template <bool DQ>
+__device__ __forceinline__ void prep_weight(const PrepJob& p, unsigned wg, unsigned char* lds) {
+  f32x2_t* sPair = reinterpret_cast<f32x2_t*>(lds);
+  uint16_t* sW = reinterpret_cast<uint16_t*>(lds + 256 * sizeof(f32x2_t));
+  const int64_t N = p.w.N, K = p.w.K;
+  const unsigned kt = (unsigned)((K + PW_K - 1) / PW_K);
+  // transposed: row tiles inner, so that neighbours write the same lines of W'^T
+  const unsigned nt = (unsigned)((N + 63) / 64);
+  const int64_t n0 = 64 * (int64_t)(p.ldb ? wg % nt : wg / kt), k0 = PW_K * (int64_t)(p.ldb ? wg / nt : wg % kt);
+  const int row = threadIdx.x >> 4, piece = threadIdx.x & 15;
+  const int64_t n = n0 + row, k = k0 + 16 * piece;
+  const bool live = n < N && k < K;
+  uint32_t code[2] = {0u, 0u};
+  float c = 0.0f;
+  if (live) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.w.codes + (n * K + k) / 2);
+    code[0] = src[0];
+    code[1] = src[1];
+    const int64_t blk = (n * K + k) >> 6;
+    c = DQ ? __builtin_fmaf(e4m3_decode(p.w.qc.absmax_q[blk]), p.w.qc.dq_scale[blk >> 8], *p.w.qc.dq_mean)
+           : p.w.qc.absmax[blk];
   }
+  if (threadIdx.x < 256) sPair[threadIdx.x] = f32x2_t{p.lv.q[threadIdx.x >> 4], p.lv.q[threadIdx.x & 15]};
+  __syncthreads();
+  u32x4_t o[2];
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const f32x2_t q = sPair[(code[b >> 2] >> (8 * (b & 3))) & 0xFFu];
+    o[b >> 2][b & 3] = pack_bf16x2(q.x * c, q.y * c);
+  }
+  if (!p.ldb) {
+    if (live) {
+      u32x4_t* dst = reinterpret_cast<u32x4_t*>(p.wd + n * K + k);
+      dst[0] = o[0];
+      dst[1] = o[1];
+    }
+    return;
+  }
+  if (!live) o[0] = o[1] = u32x4_t{0u, 0u, 0u, 0u};
+  u32x4_t* st = reinterpret_cast<u32x4_t*>(sW + row * PW_PITCH + 16 * piece);
+  st[0] = o[0];
+  st[1] = o[1];
+  __syncthreads();
+  // wave w: columns 16 w of the tile; lane (li, lg): column li, rows 32 h + 8 lg + [0, 8)
+  typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) v4b* lds_p;
+  const int wave = threadIdx.x >> 6, li = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
+  const int64_t kk = k0 + 16 * wave + li;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint16_t* src = sW + (32 * h + 8 * lg + (li >> 2)) * PW_PITCH + 16 * wave + 4 * (li & 3);
+    const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)src));
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)(src + 4 * PW_PITCH)));
+    if (kk < K) *reinterpret_cast<u32x4_t*>(p.wd + kk * p.ldb + n0 + 32 * h + 8 * lg) = u32x4_t{a[0], a[1], b[0], b[1]};
+  }
+}
+
+// at[k][j] = A[j][k], bp[n][j] = B[n][j] (j < r8, zero past r), bt[j][n] = B[n][j],
+// through an LDS tile of RL_C rows (k or n) x r8.
+__device__ __forceinline__ void prep_adapter(const PrepJob& p, unsigned a, unsigned wg, unsigned char* lds) {
+  uint16_t* s = reinterpret_cast<uint16_t*>(lds);
+  const lq_adapter ad = p.v.tab[a];
+  const int r = min(ad.r, 128), r8 = (r + 7) & ~7, pitch = r8 + 2;   // an odd count of 4-byte words
+  const int64_t N = p.w.N, K = p.w.K;
+  const bool of_a = wg < p.at_wgs;
+  const int64_t x0 = RL_C * (int64_t)(of_a ? wg : wg - p.at_wgs), X = of_a ? K : N;
+  if (x0 >= X) return;
+  const int rows = (int)min((int64_t)RL_C, X - x0);
+  if (of_a) {
+    for (int i = threadIdx.x; i < r8 * RL_C; i += 1024) {
+      const int j = i / RL_C, x = i % RL_C;
+      s[x * pitch + j] = j < r && x < rows ? ad.A[j * K + x0 + x] : (uint16_t)0;
+    }
+    __syncthreads();
+    uint16_t* out = p.at + K * ad.row8 + x0 * r8;
+    for (int i = threadIdx.x; i < rows * r8 / 2; i += 1024) {
+      const int x = i / (r8 / 2), j = 2 * (i % (r8 / 2));
+      reinterpret_cast<uint32_t*>(out)[i] = *reinterpret_cast<const uint32_t*>(s + x * pitch + j);
+    }
+    return;
+  }
+  const uint16_t* B = ad.B + x0 * r;
+  for (int i = threadIdx.x; i < rows * r; i += 1024) s[i / r * pitch + i % r] = B[i];
+  __syncthreads();
+  if (p.bt)
+    for (int i = threadIdx.x; i < r * RL_C; i += 1024) {
+      const int j = i / RL_C, x = i % RL_C;
+      if (x < rows) p.bt[N * ad.row8 + j * N + x0 + x] = s[x * pitch + j];
+    }
+  if (p.bp && r % 8)
+    for (int i = threadIdx.x; i < rows * r8; i += 1024) {
+      const int x = i / r8, j = i % r8;
+      p.bp[N * ad.row8 + (x0 + x) * r8 + j] = j < r ? s[x * pitch + j] : (uint16_t)0;
+    }
+}
+
+__global__ __launch_bounds__(1024) void k_adapter_prep(PrepJob p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char prep_lds[];
+  unsigned wg = blockIdx.x;
+  if (wg < p.route_wgs) {
+    route_tokens(p.route, reinterpret_cast<int32_t*>(prep_lds));
+    return;
+  }
+  wg -= p.route_wgs;
+  if (wg < p.weight_wgs) {
+    if (p.w.qc.absmax) prep_weight<false>(p, wg, prep_lds);
+    else prep_weight<true>(p, wg, prep_lds);
+    return;
+  }
+  wg -= p.weight_wgs;
+  prep_adapter(p, wg / p.per_adapter, wg % p.per_adapter, prep_lds);
 }
 
 // Item b of the segments [off[a], off[a + 1]), a < nseg, cut into pieces of
@@ -210,7 +368,7 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t c = 64 * (int64_t)(b + u) + 16 * lg + 8 * h;
+        const int64_t c = 64 * (int64_t)(b + u) + 32 * h + 8 * lg;   // 64 bytes of each row a load
         const bool ok = b + u < b1 && c + 8 <= C;   // past the end: zeros in place of columns 0 .. 7
         const int64_t o = ok ? c : 0;
         s.a[u][h] = ld16(q + o);
@@ -256,38 +414,18 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
   }
 }
 
-// at[k][j] = A[j][k], bp[n][j] = B[n][j] (j < r8, zero past r), bt[j][n] = B[n][j]
-__global__ __launch_bounds__(256) void k_adapter_relayout(AdapterView v, int64_t N, int64_t K,
-                                                          uint16_t* __restrict__ at, uint16_t* __restrict__ bt,
-                                                          uint16_t* __restrict__ bp) {
-  const lq_adapter ad = v.tab[blockIdx.y];
-  const int r = ad.r, r8 = (r + 7) & ~7;
-  const int64_t na = at ? K * r8 : 0, nb = bt ? N * r : 0, np = bp && r % 8 ? N * r8 : 0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < na + nb + np; i += (int64_t)gridDim.x * 256) {
-    if (i < na) {
-      const int64_t j = i / K, k = i % K;
-      at[K * ad.row8 + k * r8 + j] = j < r ? ad.A[j * K + k] : (uint16_t)0;
-    } else if (i < na + nb) {
-      const int64_t n = (i - na) / r, j = (i - na) % r;
-      bt[N * ad.row8 + j * N + n] = ad.B[n * r + j];
-    } else {
-      const int64_t n = (i - na - nb) / r8, j = (i - na - nb) % r8;
-      bp[N * ad.row8 + n * r8 + j] = j < r ? ad.B[n * r + j] : (uint16_t)0;
-    }
-  }
-}
-
 // ===========================================================================
 // Column form: out_a[j][c] = sum_m (s_a P)[m][j] Q[m][c] over a's tokens. One
-// workgroup per 128 columns and run of at most `rows` sorted positions; 32
-// tokens per step. P comes as three bfloat16 terms, so the products carry
-// float32 P on the bf16 matrix cores; all three go into the same accumulators.
-// P and Q tiles lie in LDS with tokens as rows and are read transposed
-// (ds_read_b64_tr_b16: the 16 lanes of a group point at 4 rows of 16 elements,
-// lane l gets column l of the 4 rows). Tokens past the segment are zero in
-// both, so no neighbour's infinity or NaN enters.
+// workgroup per 256 columns (64 a wave) and run of at most `rows` sorted
+// positions; 32 tokens per step. P comes as three bfloat16 terms, so the
+// products carry float32 P on the bf16 matrix cores; all three go into the same
+// accumulators. P and Q tiles lie in LDS with tokens as rows, double buffered
+// (the next step's loads are in flight while one is multiplied), and are read
+// transposed (ds_read_b64_tr_b16: the 16 lanes of a group point at 4 rows of 16
+// elements, lane l gets column l of the 4 rows). Tokens past the segment are
+// zero in both, so no neighbour's infinity or NaN enters.
 // ===========================================================================
-constexpr int CQ_PITCH = 128 + 8;
+constexpr int CQ_COLS = 256, CQ_PITCH = CQ_COLS + 16;
 
 // lane's 8 values k = 8 lg + [0, 8) of column li, from rows of `pitch` elements
 __device__ __forceinline__ u32x4_t tr_frag(const uint16_t* base, int pitch, int li, int lg) {
@@ -303,59 +441,87 @@ __device__ __forceinline__ u32x4_t tr_frag(const uint16_t* base, int pitch, int 
 template <int JT>
 __global__ __launch_bounds__(256) void k_adapter_col(ColReq q0, ColReq q1, unsigned tiles0, int rows, AdapterView v,
                                                      Route rt) {
-  constexpr int PP = 16 * JT + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t sQ[32 * CQ_PITCH];
-  __shared__ __attribute__((aligned(16))) uint16_t sP[3 * 32 * PP];
+  constexpr int PP = 16 * JT + 16;
+  constexpr int PQ = (3 * 32 * 2 * JT + 255) / 256;   // 16-byte pieces of P per thread
+  __shared__ __attribute__((aligned(16))) uint16_t sQ[2][32 * CQ_PITCH];
+  __shared__ __attribute__((aligned(16))) uint16_t sP[2][3 * 32 * PP];
   const bool second = blockIdx.x >= tiles0;
   const ColReq rq = second ? q1 : q0;
   Item it;
   if (!find_item(rt.off, v.n, rows, (int)blockIdx.y, it)) return;
   const lq_adapter ad = v.tab[it.seg];
   const int r = min(ad.r, 16 * JT), r8 = (r + 7) & ~7;
-  const int64_t C = rq.C, c0 = (int64_t)(second ? blockIdx.x - tiles0 : blockIdx.x) * 128;
+  const int64_t C = rq.C, c0 = (int64_t)(second ? blockIdx.x - tiles0 : blockIdx.x) * CQ_COLS;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
-  f32x4_t acc[JT][2];
+  // thread: columns 8 (t % 32) of tokens t / 32 + 8 u of Q; pieces of 8 columns
+  // of (term, token) of P
+  const int qc = 8 * (threadIdx.x & 31), qr = threadIdx.x >> 5;
+  const bool qin = c0 + qc + 8 <= C;
+  u32x4_t xq[4], xp[PQ];
+  int tok[4];
+  auto tokens = [&](int mb) {   // of the step's rows (a valid one past the end)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) tok[u] = rt.perm[it.start + min(mb + qr + 8 * u, it.count - 1)];
+  };
+  auto load = [&](int mb) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      xq[u] = ld16(rq.Q + (int64_t)tok[u] * C + (qin ? c0 + qc : 0));
+      if (!qin || mb + qr + 8 * u >= it.count) xq[u] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int k = 0; k < PQ; ++k) {
+      const int i = threadIdx.x + 256 * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, term = min(i / (64 * JT), 2);
+      const bool ok = mb + row < it.count && 8 * c8 < r8;
+      xp[k] = ld16(rq.terms + (int64_t)(it.start + min(mb + row, it.count - 1)) * 3 * v.rs + (ok ? term * r8 + 8 * c8 : 0));
+      if (!ok) xp[k] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+  };
+  auto store = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) *reinterpret_cast<u32x4_t*>(sQ[b] + (qr + 8 * u) * CQ_PITCH + qc) = xq[u];
+#pragma unroll
+    for (int k = 0; k < PQ; ++k) {
+      const int i = threadIdx.x + 256 * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, term = i / (64 * JT);
+      if (term < 3) *reinterpret_cast<u32x4_t*>(sP[b] + (32 * term + row) * PP + 8 * c8) = xp[k];
+    }
+  };
+  f32x4_t acc[JT][4];
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
-    for (int ct = 0; ct < 2; ++ct) acc[jt][ct] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int mb = 0; mb < it.count; mb += 32) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int i = threadIdx.x + 256 * u, row = i >> 4, cc = 8 * (i & 15);
-      u32x4_t x = {0u, 0u, 0u, 0u};
-      if (mb + row < it.count && c0 + cc + 8 <= C) x = ld16(rq.Q + (int64_t)rt.perm[it.start + mb + row] * C + c0 + cc);
-      *reinterpret_cast<u32x4_t*>(sQ + row * CQ_PITCH + cc) = x;
-    }
-    for (int i = threadIdx.x; i < 3 * 32 * 2 * JT; i += 256) {   // 8 columns of one term and token each
-      const int c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, k = i / (64 * JT);
-      u32x4_t x = {0u, 0u, 0u, 0u};
-      if (mb + row < it.count && 8 * c8 < r8)
-        x = ld16(rq.terms + (int64_t)(it.start + mb + row) * 3 * v.rs + k * r8 + 8 * c8);
-      *reinterpret_cast<u32x4_t*>(sP + (32 * k + row) * PP + 8 * c8) = x;
-    }
+    for (int ct = 0; ct < 4; ++ct) acc[jt][ct] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  tokens(0);
+  load(0);
+  tokens(32);
+  int b = 0;
+  for (int mb = 0; mb < it.count; mb += 32, b ^= 1) {
+    store(b);
     __syncthreads();
-    u32x4_t b[2];
+    if (mb + 32 < it.count) {
+      load(mb + 32);
+      tokens(mb + 64);
+    }
+    u32x4_t fq[4];
 #pragma unroll
-    for (int ct = 0; ct < 2; ++ct) b[ct] = tr_frag(sQ + 32 * wave + 16 * ct, CQ_PITCH, li, lg);
+    for (int ct = 0; ct < 4; ++ct) fq[ct] = tr_frag(sQ[b] + 64 * wave + 16 * ct, CQ_PITCH, li, lg);
 #pragma unroll
     for (int t = 0; t < 3; ++t)
 #pragma unroll
       for (int jt = 0; jt < JT; ++jt) {
-        const u32x4_t a = tr_frag(sP + 32 * t * PP + 16 * jt, PP, li, lg);
+        const u32x4_t a = tr_frag(sP[b] + 32 * t * PP + 16 * jt, PP, li, lg);
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct)
-          acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b[ct]), acc[jt][ct], 0, 0, 0);
+        for (int ct = 0; ct < 4; ++ct)
+          acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(fq[ct]), acc[jt][ct], 0, 0, 0);
       }
-    __syncthreads();
   }
   // lane: column li of each tile, rows j = 4 lg + e
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
-    for (int ct = 0; ct < 2; ++ct) {
-      const int64_t c = c0 + 32 * wave + 16 * ct + li;
+    for (int ct = 0; ct < 4; ++ct) {
+      const int64_t c = c0 + 64 * wave + 16 * ct + li;
       if (c >= C) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -396,19 +562,45 @@ __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1
 // Sorted positions per workgroup of the column form: enough workgroups for
 // the chip, but runs of at least 256 tokens so that the partial sums stay few.
 int col_rows(int64_t M, int64_t cols) {
-  const int64_t tiles = (cols + 127) / 128;
-  int64_t rows = M * tiles / 512 / 32 * 32;
+  const int64_t tiles = (cols + CQ_COLS - 1) / CQ_COLS;
+  int64_t rows = M * tiles / 384 / 32 * 32;
   return (int)std::max<int64_t>(256, std::min<int64_t>(rows, 4096));
 }
 
 }  // namespace
 
-hipError_t launch_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_t* route, hipStream_t s) {
-  LQ_DASSERT(M >= 1 && M < (int64_t(1) << 31) && n >= 1 && n <= LQ_ADAPTERS_MAX);
-  const Route r = route_view(route, M, n);
-  const size_t lds = (size_t)(RT_WAVES * (n + 1) + RT_WAVES) * sizeof(int32_t);
-  hipLaunchKernelGGL(k_adapter_route, dim3(1), dim3(64 * RT_WAVES), lds, s, ids, M, n, const_cast<int32_t*>(r.off),
-                     const_cast<int32_t*>(r.perm), const_cast<int32_t*>(r.sid));
+hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, const QWeight& w, uint16_t* wd,
+                               int64_t ldb, const AdapterView& v, uint16_t* at, uint16_t* bt, uint16_t* bp,
+                               hipStream_t s) {
+  LQ_DASSERT(!wd || w.format == LQ_FMT_NF4);
+  PrepJob p{};
+  size_t lds = 0;
+  if (route) {
+    const Route r = route_view(route, M, v.n);
+    p.route = RouteJob{ids, M, v.n, const_cast<int32_t*>(r.off), const_cast<int32_t*>(r.perm), const_cast<int32_t*>(r.sid)};
+    p.route_wgs = 1;
+    lds = route_lds_bytes(v.n);
+  }
+  p.w = w;
+  p.lv = tables().lv;
+  p.wd = wd;
+  p.ldb = ldb;
+  if (wd) {
+    p.weight_wgs = (unsigned)(((w.N + 63) / 64) * ((w.K + PW_K - 1) / PW_K));
+    lds = std::max(lds, 256 * sizeof(f32x2_t) + (ldb ? (size_t)64 * PW_PITCH * 2 : 0));
+  }
+  p.v = v;
+  p.at = at;
+  p.bt = bt;
+  p.bp = bp;
+  p.at_wgs = at ? (unsigned)((w.K + RL_C - 1) / RL_C) : 0;
+  p.b_wgs = bt || bp ? (unsigned)((w.N + RL_C - 1) / RL_C) : 0;
+  p.per_adapter = p.at_wgs + p.b_wgs;
+  if (p.per_adapter) lds = std::max(lds, (size_t)RL_C * (v.rs + 2) * 2);
+  const int64_t grid = (int64_t)p.route_wgs + p.weight_wgs + (int64_t)v.n * p.per_adapter;
+  LQ_DASSERT(grid < (int64_t(1) << 31) && lds <= 65536);
+  if (grid == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_adapter_prep, dim3((unsigned)grid), dim3(1024), lds, s, p);
   return hipGetLastError();
 }
 
@@ -420,18 +612,10 @@ hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const 
   const dim3 grid((unsigned)((M + 15) / 16 + std::min<int64_t>(v.n + 1, M)), (unsigned)njobs);
 #define LQ_AD(JT, W, U) hipLaunchKernelGGL((k_adapter_down<JT, W, U>), grid, dim3(64 * W), 0, s, j0, j1, M, v, rt, zeros)
   if (v.r_max <= 16) LQ_AD(1, 16, 2);
-  else if (v.r_max <= 32) LQ_AD(2, 16, 2);
-  else if (v.r_max <= 64) LQ_AD(4, 16, 1);
+  else if (v.r_max <= 32) LQ_AD(2, 8, 2);
+  else if (v.r_max <= 64) LQ_AD(4, 8, 1);
   else LQ_AD(8, 8, 1);
 #undef LQ_AD
-  return hipGetLastError();
-}
-
-hipError_t launch_adapter_relayout(const AdapterView& v, int64_t N, int64_t K, uint16_t* at, uint16_t* bt, uint16_t* bp,
-                                   hipStream_t s) {
-  const int64_t most = (at ? K * v.rs : 0) + (bt ? N * v.rs : 0) + (bp ? N * v.rs : 0);
-  const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 255) / 256, std::max(16, 4096 / v.n)));
-  hipLaunchKernelGGL(k_adapter_relayout, dim3(gx, (unsigned)v.n), dim3(256), 0, s, v, N, K, at, bt, bp);
   return hipGetLastError();
 }
 
@@ -442,12 +626,12 @@ size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs) {
 }
 
 hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const AdapterView& v, const Route& rt,
-                              const uint16_t* zeros, hipStream_t s) {
-  (void)zeros;
+                              hipStream_t s) {
   if (nreq < 1 || nreq > 2) return hipErrorInvalidValue;
   const ColReq q0 = reqs[0], q1 = reqs[nreq - 1];
   const int rows = col_rows(M, q0.C + (nreq > 1 ? q1.C : 0));
-  const unsigned t0 = (unsigned)((q0.C + 127) / 128), t1 = nreq > 1 ? (unsigned)((q1.C + 127) / 128) : 0u;
+  const unsigned t0 = (unsigned)((q0.C + CQ_COLS - 1) / CQ_COLS);
+  const unsigned t1 = nreq > 1 ? (unsigned)((q1.C + CQ_COLS - 1) / CQ_COLS) : 0u;
   const dim3 grid(t0 + t1, (unsigned)((M + rows - 1) / rows + std::min<int64_t>(v.n, M)));
   switch ((v.r_max + 15) / 16) {
 #define LQ_AC(JT) case JT: hipLaunchKernelGGL(k_adapter_col<JT>, grid, dim3(256), 0, s, q0, q1, t0, rows, v, rt); break;

@@ -57,11 +57,12 @@ size_t forward_ws(const QWeight& q, int64_t M, const AdapterView& v, const lq_ad
          (any_odd_rank(set) ? bytes16((size_t)sum_r8(set) * q.N) : 0);
 }
 
-// route, terms of u and t, A^T and B^T of the adapters, W' and its transpose,
-// partial sums of dA and dB, zeros
+// route, terms of u and t, A^T and B^T of the adapters, W'^T (and W' of a
+// codebook weight, which is transposed from it), partial sums of dA and dB, zeros
 size_t backward_ws(const QWeight& q, int64_t M, const AdapterView& v, int64_t r8) {
   return align_up(route_bytes(M, v.n)) + 2 * bytes16(terms_elems(M, v)) + bytes16((size_t)r8 * q.K) +
-         bytes16((size_t)r8 * q.N) + bytes16((size_t)q.N * q.K) + bytes16((size_t)q.K * ldb_of(q.N)) +
+         bytes16((size_t)r8 * q.N) + (q.format == LQ_FMT_NF4 ? 0 : bytes16((size_t)q.N * q.K)) +
+         bytes16((size_t)q.K * ldb_of(q.N)) +
          align_up(adapter_col_ws_floats(M, q.K, v.rs) * sizeof(float)) +
          align_up(adapter_col_ws_floats(M, q.N, v.rs) * sizeof(float)) + bytes16(8);
 }
@@ -84,7 +85,10 @@ int lq_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_t* route, s
   if (!ids || !route || !al(ids, 4) || !al(route, kVec)) return LQ_ERR_ARG;
   if (!valid_M(M) || n < 1 || n > LQ_ADAPTERS_MAX) return LQ_ERR_SHAPE;
   if (bytes < route_bytes(M, n)) return LQ_ERR_WORKSPACE;
-  return launch_status(launch_adapter_route(ids, M, n, route, (hipStream_t)stream));
+  QWeight none{};
+  const AdapterView v{nullptr, n, 0, 0};
+  return launch_status(launch_adapter_prep(ids, M, route, none, nullptr, 0, v, nullptr, nullptr, nullptr,
+                                           (hipStream_t)stream));
 }
 
 size_t lq_adapters_forward_workspace(const lq_qweight* w, int64_t M, const lq_adapter_set* set) {
@@ -121,16 +125,13 @@ int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const
   uint16_t* bp = any_odd_rank(set) ? cv.take<uint16_t>((size_t)sum_r8(set) * q.N) : nullptr;
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
 
-  hipError_t e = hipSuccess;
-  if (!route) {
-    if ((e = launch_adapter_route(ids, M, v.n, rws, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-    route = rws;
-  }
-  const Route rt = route_view(route, M, v.n);
-  if (bp && (e = launch_adapter_relayout(v, q.N, q.K, nullptr, nullptr, bp, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  const bool nf4 = q.format == LQ_FMT_NF4;
+  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, nf4 ? wd : nullptr, 0, v, nullptr, nullptr, bp, s);
+  if (e == hipSuccess && !nf4) e = launch_dequant(q, wd, s);
+  if (e != hipSuccess) return LQ_ERR_LAUNCH;
+  const Route rt = route_view(route ? route : rws, M, v.n);
   const DownJob job{X, q.K, nullptr, nullptr, terms, t_save};
   if ((e = launch_adapter_down(&job, 1, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  if ((e = launch_dequant(q, wd, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   const AdapterGemm g{X, M, q.N, q.K, wd, q.K, terms, v, bp, 0, rt, H, h_dtype == LQ_F32 ? 1 : 0, zeros};
   return launch_status(launch_adapter_gemm(g, s));
 }
@@ -166,7 +167,7 @@ int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t*
   uint16_t* t = cv.take<uint16_t>(terms_elems(M, v));
   uint16_t* at = cv.take<uint16_t>((size_t)r8 * q.K);
   uint16_t* bt = cv.take<uint16_t>((size_t)r8 * q.N);
-  uint16_t* wd = cv.take<uint16_t>((size_t)q.N * q.K);
+  uint16_t* wd = q.format == LQ_FMT_NF4 ? nullptr : cv.take<uint16_t>((size_t)q.N * q.K);
   const int64_t ldb = ldb_of(q.N);
   uint16_t* wt = cv.take<uint16_t>((size_t)q.K * ldb);
   float* part_a = cv.take<float>(adapter_col_ws_floats(M, q.K, v.rs));
@@ -175,17 +176,11 @@ int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t*
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
   if (!grad_X && !dA && !dB) return LQ_OK;
 
-  hipError_t e = hipSuccess;
-  if (!route) {
-    if ((e = launch_adapter_route(ids, M, v.n, rws, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-    route = rws;
-  }
-  const Route rt = route_view(route, M, v.n);
-  const bool need_u = grad_X || dA;
-  if (need_u) {
-    e = launch_adapter_relayout(v, q.N, q.K, grad_X ? at : nullptr, bt, nullptr, s);
-    if (e != hipSuccess) return LQ_ERR_LAUNCH;
-  }
+  const bool need_u = grad_X || dA, nf4 = q.format == LQ_FMT_NF4;
+  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, grad_X && nf4 ? wt : nullptr, ldb, v,
+                                     grad_X ? at : nullptr, need_u ? bt : nullptr, nullptr, s);
+  if (e != hipSuccess) return LQ_ERR_LAUNCH;
+  const Route rt = route_view(route ? route : rws, M, v.n);
   DownJob jobs[2];
   int nj = 0;
   if (need_u) jobs[nj++] = DownJob{G, q.N, bt, nullptr, u, nullptr};
@@ -195,10 +190,12 @@ int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t*
   int nc = 0;
   if (dB) cols[nc++] = ColReq{t, G, q.N, dB, 1, part_b};
   if (dA) cols[nc++] = ColReq{u, X, q.K, dA, 0, part_a};
-  if (nc && (e = launch_adapter_col(cols, nc, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  if (nc && (e = launch_adapter_col(cols, nc, M, v, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   if (!grad_X) return LQ_OK;
-  if ((e = launch_dequant(q, wd, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  if ((e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  if (!nf4) {
+    if ((e = launch_dequant(q, wd, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+    if ((e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  }
   const AdapterGemm g{G, M, q.K, q.N, wt, ldb, u, v, at, 1, rt, grad_X, 0, zeros};
   return launch_status(launch_adapter_gemm(g, s));
 }
