@@ -31,6 +31,55 @@ __device__ __forceinline__ void wait_vm() {
 }
 __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
 
+// The adapter of the sorted positions from pos on, inside a tile that ends at
+// mend: its columns are steps of 64 (8 runs of 8) of TERMS copies of Lb.
+struct Adapter {
+  int64_t lo, hi;          // its positions inside the tile
+  const uint16_t* base;    // Lb
+  int stride, runs;        // of Lb: elements a row, runs of 8 columns
+  int live, steps;         // runs of all terms, steps of 8 of them (0: no adapter)
+};
+template <int TERMS>
+__device__ __forceinline__ Adapter adapter_at(const AdapterGemm& p, int64_t pos, int64_t mend) {
+  Adapter s{pos, mend, nullptr, 8, 1, 0, 0};
+  if (pos >= mend) return s;
+  const int a = uniform(p.rt.sid[pos]);
+  if (a >= p.v.n) return s;
+  s.hi = min((int64_t)uniform(p.rt.off[a + 1]), mend);
+  const lq_adapter ad = p.v.tab[a];
+  const int r8 = (ad.r + 7) & ~7;
+  s.base = !p.lt_all && ad.r % 8 == 0 ? ad.B : p.lt + p.Ncols * ad.row8;
+  s.stride = r8;
+  s.runs = r8 >> 3;
+  s.live = TERMS * s.runs;
+  s.steps = (s.live + 7) >> 3;
+  return s;
+}
+
+// A lane's 4 consecutive outputs c .. c + 3 of one token.
+template <bool OUT_F32>
+__device__ __forceinline__ void store4(const AdapterGemm& p, int64_t row, int64_t c, const f32x4_t& v) {
+  if (p.Ncols % 4 == 0) {
+    if (c >= p.Ncols) return;
+    if (OUT_F32) {
+      float* o = reinterpret_cast<float*>(p.out) + row + c;   // 4-byte aligned
+      o[0] = v[0]; o[1] = v[1]; o[2] = v[2]; o[3] = v[3];
+    } else {
+      uint2 o;
+      o.x = pack_bf16x2(v[0], v[1]);
+      o.y = pack_bf16x2(v[2], v[3]);
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + row + c) = o;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c + e >= p.Ncols) break;
+      if (OUT_F32) reinterpret_cast<float*>(p.out)[row + c + e] = v[e];
+      else reinterpret_cast<uint16_t*>(p.out)[row + c + e] = (uint16_t)(pack_bf16x2(v[e], 0.f) & 0xFFFFu);
+    }
+  }
+}
+
 // Tile 256 positions x BN weight rows, 64-wide steps, 8 waves in two groups of
 // four (one wave of each group per SIMD). The groups work one slot apart:
 // while one group's waves multiply (16 MFMA each), the other's read their next
@@ -98,28 +147,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   // zero on both sides). Of a tile whose tokens share one adapter it is simply
   // the end of the contraction, steps nk .. nk + nl - 1 of the main loop.
   constexpr int TERMS = OUT_F32 ? 3 : 2;
-  struct Adapter {
-    int64_t lo, hi;          // its sorted positions inside the tile
-    const uint16_t* base;    // Lb
-    int stride, runs;        // of Lb: elements a row, runs of 8 columns
-    int live, steps;         // runs of all terms, steps of 8 of them
-  };
   const int64_t mend = min(m0 + GM, p.M);
-  auto adapter_at = [&](int64_t pos) {   // the adapter at a position of the tile; steps 0: none
-    Adapter s{pos, mend, nullptr, 8, 1, 0, 0};
-    if (pos >= mend) return s;
-    const int a = uniform(p.rt.sid[pos]);
-    if (a >= p.v.n) return s;
-    s.hi = min((int64_t)uniform(p.rt.off[a + 1]), mend);
-    const lq_adapter ad = p.v.tab[a];
-    const int r8 = (ad.r + 7) & ~7;
-    s.base = !p.lt_all && ad.r % 8 == 0 ? ad.B : p.lt + p.Ncols * ad.row8;
-    s.stride = r8;
-    s.runs = r8 >> 3;
-    s.live = TERMS * s.runs;
-    s.steps = (s.live + 7) >> 3;
-    return s;
-  };
   auto lora_x = [&](const Adapter& s, int kt, int i, int buf) {
     const int c = 8 * kt + ch;   // this lane's run of 8 columns
 #pragma unroll
@@ -210,7 +238,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   };
 
   const bool late = wave >= 4;   // the group that works one slot behind
-  Adapter next = adapter_at(m0);
+  Adapter next = adapter_at<TERMS>(p, m0, mend);
   if (next.steps && next.hi == mend) whole = next;
   const int nsteps = nk + whole.steps;
   int it = 0, buf = 0;
@@ -295,7 +323,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
     for (int b = 0; cur.steps; b ^= 1) {
       const int64_t lo = cur.lo, hi = cur.hi;
       if (++kt >= cur.steps) {
-        cur = adapter_at(cur.hi);
+        cur = adapter_at<TERMS>(p, cur.hi, mend);
         kt = 0;
       }
       wait_vm<0>();
@@ -339,28 +367,150 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
     const int64_t row = (int64_t)p.rt.perm[pos] * p.Ncols;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      const int64_t c = cw + 16 * ct + 4 * lg;
-      const f32x4_t v = acc[ct][rt];
-      if (p.Ncols % 4 == 0) {
-        if (c >= p.Ncols) continue;
-        if (OUT_F32) {
-          float* o = reinterpret_cast<float*>(p.out) + row + c;
-          o[0] = v[0]; o[1] = v[1]; o[2] = v[2]; o[3] = v[3];
-        } else {
-          uint2 o;
-          o.x = pack_bf16x2(v[0], v[1]);
-          o.y = pack_bf16x2(v[2], v[3]);
-          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + row + c) = o;
-        }
-      } else {
+      store4<OUT_F32>(p, row, cw + 16 * ct + 4 * lg, acc[ct][rt]);
+    }
+  }
+}
+
+// Few tokens or a small weight: tiles of 64 positions x 64 weight rows, 4 waves
+// of 32 x 32, so that the tiles cover the chip; a ring of four LDS buffers (64
+// KB: two workgroups per CU), loads three steps ahead, one barrier a step. The
+// adapters' steps follow the base contraction's in the same ring: of a tile of
+// one adapter they accumulate, of one with several each goes to its own
+// tokens' columns alone.
+constexpr int SM = 64, SN = 64, S_THREADS = 256, S_RING = 4;
+
+template <bool OUT_F32, bool BWD>
+__global__ __launch_bounds__(S_THREADS, 2) void k_adapter_gemm_small(AdapterGemm p) {
+  constexpr int TERMS = OUT_F32 ? 3 : 2;
+  struct __attribute__((aligned(16))) Lds {
+    uint16_t x[S_RING][SM * GK];
+    uint16_t y[S_RING][SN * GK];
+  };
+  __shared__ Lds lds;
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  const int wn = wave & 1, wm = wave >> 1;
+  const int64_t tiles_m = (p.M + SM - 1) / SM, tiles_n = (p.Ncols + SN - 1) / SN;
+  const int64_t total = tiles_m * tiles_n;
+  const int64_t xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
+  const int64_t t = xcd * per + min(xcd, rem) + blockIdx.x / 8;
+  const int64_t m0 = t % tiles_m * SM, n0 = t / tiles_m * SN, mend = min(m0 + SM, p.M);
+
+  const int sub = lane >> 3, ch = (lane & 7) ^ sub;
+  const uint16_t *px[2], *py[2], *pt[2];
+  int64_t ny[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (c + e >= p.Ncols) break;
-          if (OUT_F32) reinterpret_cast<float*>(p.out)[row + c + e] = v[e];
-          else reinterpret_cast<uint16_t*>(p.out)[row + c + e] = (uint16_t)(pack_bf16x2(v[e], 0.f) & 0xFFFFu);
+  for (int q = 0; q < 2; ++q) {
+    const int row = (wave * 2 + q) * 8 + sub;
+    const int64_t pos = min(m0 + row, p.M - 1);
+    px[q] = p.A + (int64_t)p.rt.perm[pos] * p.Kc + 8 * ch;
+    pt[q] = p.terms + pos * 3 * p.v.rs;
+    ny[q] = min(n0 + row, p.Ncols - 1);
+    py[q] = p.Bt + ny[q] * p.ldb + 8 * ch;
+  }
+  const int nk = (int)((p.Kc + GK - 1) / GK);
+  Adapter src = adapter_at<TERMS>(p, m0, mend);   // the adapter whose steps are loaded next
+  int kt = 0;
+  // the next step of the sequence (base contraction, then adapter after
+  // adapter) into buffer buf; past the end zeros
+  auto load = [&](int it, int buf) {
+    if (it < nk) {
+      const int64_t k0 = (int64_t)it * GK;
+      const bool ok = !BWD || k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (0 * NaN is not 0)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        load_lds16(ok ? px[q] + k0 : p.zeros, lds.x[buf] + (wave * 2 + q) * 8 * GK);
+        load_lds16(py[q] + k0, lds.y[buf] + (wave * 2 + q) * 8 * GK);
+      }
+      return;
+    }
+    const int c = 8 * kt + ch;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      load_lds16(c < src.live ? pt[q] + 8 * c : p.zeros, lds.x[buf] + (wave * 2 + q) * 8 * GK);
+      load_lds16(c < src.live ? src.base + ny[q] * src.stride + 8 * (c % src.runs) : p.zeros,
+                 lds.y[buf] + (wave * 2 + q) * 8 * GK);
+    }
+    if (src.steps && ++kt >= src.steps) {
+      src = adapter_at<TERMS>(p, src.hi, mend);
+      kt = 0;
+    }
+  };
+  f32x4_t acc[2][2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) acc[c][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
+  const int ox = (wm * 32 + li) * GK, oy = (wn * 32 + li) * GK;
+  u32x4_t fx[2][2], fy[2][2];
+  auto read = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        fx[u][i] = ld16(lds.x[buf] + ox + 16 * i * GK + slot[u]);
+        fy[u][i] = ld16(lds.y[buf] + oy + 16 * i * GK + slot[u]);
+      }
+  };
+  Adapter cur = src;   // the adapter whose steps are multiplied next
+#pragma unroll
+  for (int it = 0; it < S_RING - 1; ++it) load(it, it);
+  int it = 0;
+  auto turn = [&]() {   // step it is in LDS, and step it - 1 read by everyone
+    wait_vm<(S_RING - 2) * 4>();
+    barrier();
+    load(it + S_RING - 1, (it + S_RING - 1) % S_RING);
+    read(it % S_RING);
+  };
+  auto multiply = [&]() {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fy[u][c]), as_bf16x8(fx[u][r]), acc[c][r], 0, 0, 0);
+  };
+  const bool whole = cur.steps && cur.hi == mend;
+  const int last = nk + (whole ? cur.steps : 0);
+  for (; it < last; ++it) {
+    turn();
+    multiply();
+  }
+  if (!whole) {
+    int k = 0;
+    for (; cur.steps; ++it) {
+      turn();
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int64_t pos = m0 + wm * 32 + 16 * r + li;
+        const bool mine = pos >= cur.lo && pos < cur.hi;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          f32x4_t d = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fy[u][c]), as_bf16x8(fx[u][r]), d, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[c][r][e] += mine ? d[e] : 0.0f;
         }
       }
+      if (++k >= cur.steps) {
+        cur = adapter_at<TERMS>(p, cur.hi, mend);
+        k = 0;
+      }
     }
+  }
+  wait_vm<0>();   // the loads past the last step, before the workgroup's LDS is given up
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int64_t pos = m0 + wm * 32 + 16 * r + li;
+    if (pos >= p.M) continue;
+    const int64_t row = (int64_t)p.rt.perm[pos] * p.Ncols;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) store4<OUT_F32>(p, row, n0 + wn * 32 + 16 * c + 4 * lg, acc[c][r]);
   }
 }
 
@@ -398,12 +548,30 @@ hipError_t launch_tile(const AdapterGemm& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+hipError_t launch_small(const AdapterGemm& g, hipStream_t s) {
+  const int64_t tiles = ((g.M + SM - 1) / SM) * ((g.Ncols + SN - 1) / SN);
+  LQ_DASSERT(tiles > 0 && tiles < (int64_t(1) << 31));
+  const dim3 grid((unsigned)tiles), block(S_THREADS);
+  if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm_small<false, true>), grid, block, 0, s, g);
+  else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm_small<true, false>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((k_adapter_gemm_small<false, false>), grid, block, 0, s, g);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s) {
   LQ_DASSERT(g.M > 0 && g.Ncols > 0 && g.Kc > 0 && g.Kc % 8 == 0 && g.ldb % 64 == 0 && g.ldb >= g.Kc);
-  const int64_t big = ((g.M + GM - 1) / GM) * ((g.Ncols + 255) / 256);
-  return big >= 256 ? launch_tile<256>(g, s) : launch_tile<128>(g, s);
+  // Rounds of a chip full of tiles times a tile's time per step: 1.7 us
+  // (256 x 256), 1.05 (256 x 128) and, with two workgroups per CU, 0.3 (64 x 64)
+  // as measured over K = 4096.
+  auto cost = [&](int64_t m, int64_t n, int64_t slots, double us) {
+    const int64_t tiles = ((g.M + m - 1) / m) * ((g.Ncols + n - 1) / n);
+    return (double)((tiles + slots - 1) / slots) * us;
+  };
+  const double c256 = cost(256, 256, 256, 1.7), c128 = cost(256, 128, 256, 1.05), c64 = cost(64, 64, 512, 0.3);
+  if (c64 < c128 && c64 < c256) return launch_small(g, s);
+  return c256 <= c128 ? launch_tile<256>(g, s) : launch_tile<128>(g, s);
 }
 
 hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out,

@@ -154,6 +154,68 @@ def test_backward(lq, torch, case):
     check_backward(lq, torch, Layer(lq, torch, N, K, M, ranks, ids, weight), saved)
 
 
+def reference64(torch, L, t=None):
+    """The oracle's formulas in float64 torch on the device, for the large shapes: outputs and absolute sums."""
+    W, X, G = torch.from_numpy(L.Wd).cuda(), L.X.double(), L.G.double()
+    H, mH, gx, mX = X @ W.T, X.abs() @ W.abs().T, G @ W, G.abs() @ W.abs()
+    lH, lX = torch.zeros_like(H), torch.zeros_like(gx)
+    dA, dB = [], []
+    for a, (A, B, alpha) in enumerate(L.adapters):
+        m = (L.ids_dev == a).nonzero()[:, 0]
+        A, B, s = A.double(), B.double(), L.host[a][2]
+        tm = X[m] @ A.T if t is None else t[m, :A.shape[0]].double()
+        u = G[m] @ B
+        ta, ua = X[m].abs() @ A.abs().T, G[m].abs() @ B.abs()
+        H[m] += s * (X[m] @ A.T) @ B.T
+        lH[m] = s * ta @ B.abs().T
+        gx[m] += s * u @ A
+        lX[m] = s * ua @ A.abs()
+        dA.append((s * u.T @ X[m], s * ua.T @ X[m].abs()))
+        dB.append((s * G[m].T @ tm, s * G[m].abs().T @ (ta if t is None else tm.abs())))
+    return (H, mH, lH), (gx, mX, lX), dA, dB
+
+
+LARGE = [
+    # N, K, M, ranks, ids, weight: tiles of 256 x 128 (first three) and 256 x 256, uneven edges
+    (4104, 192, 2047, [16, 8, 64, 24], "runs", "nf4_dq"),
+    (4099, 64, 1800, [16] * 9, "mixed", "nf4_f32"),
+    (4096, 320, 2048, [40], "runs", "codebook"),
+    (8184, 128, 4001, [64, 16, 128], "runs", "nf4_dq"),
+    (8192, 64, 4096, [32, 7, 16, 8], "mixed", "nf4_f32"),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=str)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_large_forward(lq, torch, case, out):
+    N, K, M, ranks, ids, weight = case
+    L = Layer(lq, torch, N, K, M, ranks, ids, weight)
+    H, _ = lq.adapters_forward(L.qw, L.X, L.set, L.ids_dev, out_dtype=torch.float32 if out == "f32" else torch.bfloat16)
+    (ref, mag, lora), _, _, _ = reference64(torch, L)
+    bound = (K + 3 * max(ranks) + 8) * U * (mag + lora) + K * U * lora
+    if out == "bf16":
+        bound += 2.0 ** -16 * lora + 2.0 ** -8 * ref.abs() + 2.0 ** -130
+    assert ((H.double() - ref).abs() <= bound).all()
+
+
+# the backward's result is [M, K], its contraction N: the same tiles with N and K exchanged
+@pytest.mark.parametrize("case", [(200, 4096, 2047, [16, 8, 64, 24], "runs", "nf4_dq"),
+                                  (64, 4096, 1800, [16] * 9, "mixed", "codebook"),
+                                  (136, 8192, 4001, [64, 16, 128], "runs", "nf4_dq"),
+                                  (328, 8192, 4096, [32, 7, 16, 8], "mixed", "nf4_f32")], ids=str)
+def test_large_backward(lq, torch, case):
+    N, K, M, ranks, ids, weight = case
+    L = Layer(lq, torch, N, K, M, ranks, ids, weight)
+    gx, dA, dB = lq.adapters_backward(L.qw, L.X, L.G, L.set, L.ids_dev)
+    _, (ref, mag, lora), rA, rB = reference64(torch, L)
+    bound = (N + 3 * max(ranks) + 8) * U * (mag + lora) + N * U * lora + 2.0 ** -16 * lora + 2.0 ** -8 * ref.abs()
+    assert ((gx.double() - ref).abs() <= bound + 2.0 ** -130).all()
+    for a, (da, db) in enumerate(L.set.split(dA, dB)):
+        tokens = int((L.ids == a).sum())
+        assert ((da.double() - rA[a][0]).abs() <= (3 * tokens + N + 16) * U * rA[a][1]).all()
+        assert ((db.double() - rB[a][0]).abs() <= (3 * tokens + K + 16) * U * rB[a][1]).all()
+
+
 @pytest.mark.parametrize("M,n", [(1, 1), (2, 3), (63, 5), (64, 64), (65, 1), (1000, 40), (5000, 1000), (4096, 7)])
 def test_route(lq, torch, M, n):
     rng = np.random.default_rng(M * 1001 + n)
