@@ -44,20 +44,22 @@ struct DownJob {
   const float* given;      // Q null: t [M, r_max]
   uint16_t* terms;
   float* save;             // t [M, r_max] or null (zero past r_a and for tokens without an adapter)
+  float* part;             // adapter_down_ws_floats(M, C, rs)
 };
-// zeros: 16 bytes, written with zeros (for the matrix kernels)
+size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs);
 hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
-                               uint16_t* zeros, hipStream_t s);
+                               const uint16_t* zeros, hipStream_t s);
 
 // Preparation, one launch of independent parts, each left out where its
-// pointer is null: the route of ids; an NF4 weight decoded to wd (W' [N, K], or
+// pointer is null: 16 zero bytes (read by the other kernels in place of what
+// lies past an end); the route of ids; an NF4 weight decoded to wd (W' [N, K], or
 // with ldb W'^T [K, ldb], zero columns from N on); the adapters re-laid for the
 // matrix kernels: at = A^T [K, r8] at K * row8_a, bt = B^T [r, N] at N *
 // row8_a, bp = B [N, r8] at N * row8_a of the adapters whose rank is not a
 // multiple of 8 (zero columns past r_a).
 hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, const QWeight& w, uint16_t* wd,
                                int64_t ldb, const AdapterView& v, uint16_t* at, uint16_t* bt, uint16_t* bp,
-                               hipStream_t s);
+                               uint16_t* zeros, hipStream_t s);
 
 // Column form over routed tokens: out_a[j][c] = sum over a's tokens of
 // (s_a P)[m][j] Q[m][c], written [r, C] at C * row_a, or transposed [C, r].

@@ -119,8 +119,9 @@ __device__ __forceinline__ void route_tokens(const RouteJob& jb, int32_t* cnt) {
 // adapters; none of it depends on the rest. Bound by writing the bfloat16
 // weight.
 // ===========================================================================
-constexpr int PW_K = 256;                 // decoded per workgroup: 64 weight rows x PW_K columns
-constexpr int PW_PITCH = PW_K + 16;       // bf16 per LDS row: the transposing reads of 4 rows hit distinct banks
+constexpr int PW_T = 128;                 // transposed: tiles of PW_T weight rows x PW_T columns
+constexpr int PW_PITCH = PW_T + 16;       // bf16 per LDS row: the transposing reads of 4 rows hit distinct banks
+constexpr int PW_FLAT = 4;                // as it lies: pieces of 16 codes per thread, all in flight together
 constexpr int RL_C = 128;                 // re-laid per workgroup: RL_C rows of A^T or B
 
 struct PrepJob {
@@ -131,64 +132,97 @@ struct PrepJob {
   int64_t ldb;           // 0: not transposed
   AdapterView v;
   uint16_t *at, *bt, *bp;
+  uint16_t* zeros;       // 16 bytes, cleared
   unsigned route_wgs, weight_wgs, per_adapter, at_wgs, b_wgs;
 };
+
+// 16 codes (one 64-block's) and what makes their constant.
+struct RawCodes {
+  uint32_t code[2], q8;
+  float c, s2;
+};
+template <bool DQ>
+__device__ __forceinline__ RawCodes load_codes(const QWeight& w, int64_t e) {
+  RawCodes r{};
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(w.codes + e / 2);
+  r.code[0] = src[0];
+  r.code[1] = src[1];
+  const int64_t blk = e >> 6;
+  if (DQ) {
+    r.q8 = w.qc.absmax_q[blk];
+    r.s2 = w.qc.dq_scale[blk >> 8];
+  } else {
+    r.c = w.qc.absmax[blk];
+  }
+  return r;
+}
+template <bool DQ>
+__device__ __forceinline__ void decode16(const RawCodes& r, float mean, const f32x2_t* sPair, u32x4_t (&o)[2]) {
+  const float c = DQ ? __builtin_fmaf(e4m3_decode(r.q8), r.s2, mean) : r.c;
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const f32x2_t q = sPair[(r.code[b >> 2] >> (8 * (b & 3))) & 0xFFu];
+    o[b >> 2][b & 3] = pack_bf16x2(q.x * c, q.y * c);
+  }
+}
 
 template <bool DQ>
 __device__ __forceinline__ void prep_weight(const PrepJob& p, unsigned wg, unsigned char* lds) {
   f32x2_t* sPair = reinterpret_cast<f32x2_t*>(lds);
   uint16_t* sW = reinterpret_cast<uint16_t*>(lds + 256 * sizeof(f32x2_t));
   const int64_t N = p.w.N, K = p.w.K;
-  const unsigned kt = (unsigned)((K + PW_K - 1) / PW_K);
-  // transposed: row tiles inner, so that neighbours write the same lines of W'^T
-  const unsigned nt = (unsigned)((N + 63) / 64);
-  const int64_t n0 = 64 * (int64_t)(p.ldb ? wg % nt : wg / kt), k0 = PW_K * (int64_t)(p.ldb ? wg / nt : wg % kt);
-  const int row = threadIdx.x >> 4, piece = threadIdx.x & 15;
-  const int64_t n = n0 + row, k = k0 + 16 * piece;
-  const bool live = n < N && k < K;
-  uint32_t code[2] = {0u, 0u};
-  float c = 0.0f;
-  if (live) {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.w.codes + (n * K + k) / 2);
-    code[0] = src[0];
-    code[1] = src[1];
-    const int64_t blk = (n * K + k) >> 6;
-    c = DQ ? __builtin_fmaf(e4m3_decode(p.w.qc.absmax_q[blk]), p.w.qc.dq_scale[blk >> 8], *p.w.qc.dq_mean)
-           : p.w.qc.absmax[blk];
-  }
-  if (threadIdx.x < 256) sPair[threadIdx.x] = f32x2_t{p.lv.q[threadIdx.x >> 4], p.lv.q[threadIdx.x & 15]};
-  __syncthreads();
-  u32x4_t o[2];
-#pragma unroll
-  for (int b = 0; b < 8; ++b) {
-    const f32x2_t q = sPair[(code[b >> 2] >> (8 * (b & 3))) & 0xFFu];
-    o[b >> 2][b & 3] = pack_bf16x2(q.x * c, q.y * c);
-  }
+  const float mean = DQ ? *p.w.qc.dq_mean : 0.0f;
   if (!p.ldb) {
-    if (live) {
-      u32x4_t* dst = reinterpret_cast<u32x4_t*>(p.wd + n * K + k);
-      dst[0] = o[0];
-      dst[1] = o[1];
+    const int64_t e0 = (int64_t)wg * (PW_FLAT * 1024 * 16) + threadIdx.x * 16, last = N * K - 16;
+    RawCodes raw[PW_FLAT];
+#pragma unroll
+    for (int u = 0; u < PW_FLAT; ++u) raw[u] = load_codes<DQ>(p.w, min(e0 + u * 1024 * 16, last));
+    if (threadIdx.x < 256) sPair[threadIdx.x] = f32x2_t{p.lv.q[threadIdx.x >> 4], p.lv.q[threadIdx.x & 15]};
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < PW_FLAT; ++u) {
+      const int64_t e = e0 + u * 1024 * 16;
+      u32x4_t o[2];
+      decode16<DQ>(raw[u], mean, sPair, o);
+      if (e <= last) {
+        u32x4_t* dst = reinterpret_cast<u32x4_t*>(p.wd + e);
+        dst[0] = o[0];
+        dst[1] = o[1];
+      }
     }
     return;
   }
+  // transposed: row tiles inner, so that neighbours write the same lines of W'^T
+  const unsigned nt = (unsigned)((N + PW_T - 1) / PW_T);
+  const int64_t n0 = PW_T * (int64_t)(wg % nt), k0 = PW_T * (int64_t)(wg / nt);
+  const int row = threadIdx.x >> 3, piece = threadIdx.x & 7;
+  const int64_t n = n0 + row, k = k0 + 16 * piece;
+  const bool live = n < N && k < K;
+  const RawCodes raw = load_codes<DQ>(p.w, live ? n * K + k : 0);
+  if (threadIdx.x < 256) sPair[threadIdx.x] = f32x2_t{p.lv.q[threadIdx.x >> 4], p.lv.q[threadIdx.x & 15]};
+  __syncthreads();
+  u32x4_t o[2];
+  decode16<DQ>(raw, mean, sPair, o);
   if (!live) o[0] = o[1] = u32x4_t{0u, 0u, 0u, 0u};
   u32x4_t* st = reinterpret_cast<u32x4_t*>(sW + row * PW_PITCH + 16 * piece);
   st[0] = o[0];
   st[1] = o[1];
   __syncthreads();
-  // wave w: columns 16 w of the tile; lane (li, lg): column li, rows 32 h + 8 lg + [0, 8)
+  // wave w: columns 16 (w % 8), rows 64 (w / 8) of the tile; lane (li, lg):
+  // column li, rows 32 h + 8 lg + [0, 8)
   typedef __bf16 v4b __attribute__((ext_vector_type(4)));
   typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
   typedef __attribute__((address_space(3))) v4b* lds_p;
   const int wave = threadIdx.x >> 6, li = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
-  const int64_t kk = k0 + 16 * wave + li;
+  const int64_t kk = k0 + 16 * (wave & 7) + li;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint16_t* src = sW + (32 * h + 8 * lg + (li >> 2)) * PW_PITCH + 16 * wave + 4 * (li & 3);
+    const int r0 = 64 * (wave >> 3) + 32 * h + 8 * lg;
+    const uint16_t* src = sW + (r0 + (li >> 2)) * PW_PITCH + 16 * (wave & 7) + 4 * (li & 3);
     const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)src));
     const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)(src + 4 * PW_PITCH)));
-    if (kk < K) *reinterpret_cast<u32x4_t*>(p.wd + kk * p.ldb + n0 + 32 * h + 8 * lg) = u32x4_t{a[0], a[1], b[0], b[1]};
+    if (kk < K && n0 + r0 < p.ldb)   // ldb covers N in whole runs of 64
+      *reinterpret_cast<u32x4_t*>(p.wd + kk * p.ldb + n0 + r0) = u32x4_t{a[0], a[1], b[0], b[1]};
   }
 }
 
@@ -234,6 +268,7 @@ __device__ __forceinline__ void prep_adapter(const PrepJob& p, unsigned a, unsig
 __global__ __launch_bounds__(1024) void k_adapter_prep(PrepJob p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char prep_lds[];
   unsigned wg = blockIdx.x;
+  if (wg == 0 && threadIdx.x < 8 && p.zeros) p.zeros[threadIdx.x] = 0;
   if (wg < p.route_wgs) {
     route_tokens(p.route, reinterpret_cast<int32_t*>(prep_lds));
     return;
@@ -245,7 +280,7 @@ __global__ __launch_bounds__(1024) void k_adapter_prep(PrepJob p) {
     return;
   }
   wg -= p.weight_wgs;
-  prep_adapter(p, wg / p.per_adapter, wg % p.per_adapter, prep_lds);
+  if (p.per_adapter) prep_adapter(p, wg / p.per_adapter, wg % p.per_adapter, prep_lds);
 }
 
 // Item b of the segments [off[a], off[a + 1]), a < nseg, cut into pieces of
@@ -306,21 +341,33 @@ __device__ __forceinline__ void split3(float v, uint16_t (&o)[3]) {
   }
 }
 
+// t[row][j] = x of the token at sorted position pos: kept as given, and as the terms of s_a x.
+__device__ __forceinline__ void put_t(const DownJob& jb, const AdapterView& v, const Route& rt, const lq_adapter& ad,
+                                      int64_t pos, int j, float x) {
+  const int r8 = (ad.r + 7) & ~7;
+  if (jb.save && j < v.r_max) jb.save[(int64_t)rt.perm[pos] * v.r_max + j] = x;
+  if (j < r8) {
+    uint16_t o[3];
+    split3(ad.scale * x, o);
+    uint16_t* d = jb.terms + pos * 3 * v.rs + j;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) d[k * r8] = o[k];
+  }
+}
+
 // ===========================================================================
-// Row form: 16 routed tokens of one adapter per workgroup; its W waves take
+// Row form, few tokens: 16 routed tokens of one adapter per workgroup; its W waves take
 // contiguous runs of 64-column blocks, MFMA 16x16x32 with tokens as rows and
 // the adapter's rows as columns, both straight from memory into registers, a
 // wave's next U blocks loading while the current ones are multiplied. The
 // waves' partial sums meet in LDS and are added in wave order.
 // ===========================================================================
 template <int JT, int W, int U>
-__global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt,
-                                                         uint16_t* zeros) {
+__global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt) {
   __shared__ f32x4_t part[W][JT][64];
   const DownJob jb = blockIdx.y ? j1 : j0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 8) zeros[threadIdx.x] = 0;
   Item it;
   if (!find_item(rt.off, v.n + 1, 16, (int)blockIdx.x, it)) return;
   if (it.seg == v.n) {   // tokens without an adapter
@@ -331,17 +378,7 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
   }
   const lq_adapter ad = v.tab[it.seg];
   const int r = min(ad.r, 16 * JT), r8 = (r + 7) & ~7;
-  auto put = [&](int row, int j, float x) {   // x = t[row][j]
-    const int64_t pos = it.start + row;
-    if (jb.save && j < v.r_max) jb.save[(int64_t)rt.perm[pos] * v.r_max + j] = x;
-    if (j < r8) {
-      uint16_t o[3];
-      split3(ad.scale * x, o);
-      uint16_t* d = jb.terms + pos * 3 * v.rs + j;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) d[k * r8] = o[k];
-    }
-  };
+  auto put = [&](int row, int j, float x) { put_t(jb, v, rt, ad, it.start + row, j, x); };
   if (!jb.Q) {
     for (int i = threadIdx.x; i < it.count * r8; i += 64 * W) {
       const int row = i / r8, j = i - row * r8;
@@ -415,6 +452,129 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
 }
 
 // ===========================================================================
+// Row form, many tokens: 64 routed tokens of one adapter x BN of its rows per
+// workgroup (a fourth of the reads of the adapter that 16 tokens cost), over a
+// share of the columns; tiles through a ring of four LDS buffers filled by
+// memory-to-LDS loads three 64-wide steps ahead. The shares' sums, float32 in
+// sorted order [shares][M][rs], are joined by k_adapter_down_join, which also
+// turns a given t into terms.
+// ===========================================================================
+constexpr int DT_M = 64, DT_K = 64, DT_RING = 4;
+
+__device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+template <int BN>
+__global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt,
+                                                            const uint16_t* zeros) {
+  constexpr int CT = BN / 16, QW = BN >= 32 ? BN / 32 : 1;
+  struct __attribute__((aligned(16))) Lds {
+    uint16_t x[DT_RING][DT_M * DT_K];
+    uint16_t w[DT_RING][(BN < 32 ? 32 : BN) * DT_K];
+  };
+  __shared__ Lds lds;
+  const DownJob jb = blockIdx.z ? j1 : j0;
+  if (!jb.Q) return;
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  Item it;
+  if (!find_item(rt.off, v.n, DT_M, (int)blockIdx.x, it)) return;
+  const lq_adapter ad = v.tab[it.seg];
+  const int r = min(ad.r, BN);
+  const int64_t C = jb.C;
+  const uint16_t* R = jb.rbase ? jb.rbase + C * ad.row8 : ad.A;
+  const int all = (int)((C + DT_K - 1) / DT_K), per = (all + gridDim.y - 1) / gridDim.y;
+  const int s0 = min(all, (int)blockIdx.y * per), s1 = min(all, s0 + per);
+  // a load instruction of a wave fills 8 rows of 128 bytes: lane l row l / 8,
+  // slot l % 8 with chunk slot ^ (row % 8)
+  const int sub = lane >> 3, ch = (lane & 7) ^ sub;
+  const uint16_t *px[2], *pw[QW];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    px[q] = jb.Q + (int64_t)rt.perm[it.start + min((wave * 2 + q) * 8 + sub, it.count - 1)] * C + 8 * ch;
+#pragma unroll
+  for (int q = 0; q < QW; ++q) pw[q] = R + (int64_t)min((wave * QW + q) * 8 + sub, r - 1) * C + 8 * ch;
+  auto load = [&](int s) {   // step s into its buffer; past the end zeros (the count of outstanding loads stays)
+    const int buf = (s - s0) % DT_RING;
+    const int64_t k0 = (int64_t)s * DT_K;
+    const bool ok = s < s1 && k0 + 8 * ch + 8 <= C;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) load_lds16(ok ? px[q] + k0 : zeros, lds.x[buf] + (wave * 2 + q) * 8 * DT_K);
+#pragma unroll
+    for (int q = 0; q < QW; ++q) load_lds16(ok ? pw[q] + k0 : zeros, lds.w[buf] + (wave * QW + q) * 8 * DT_K);
+  };
+  f32x4_t acc[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < DT_RING - 1; ++k) load(s0 + k);
+  const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
+  for (int s = s0; s < s1; ++s) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((DT_RING - 2) * (2 + QW)) : "memory");   // this wave's share of step s
+    asm volatile("s_barrier" ::: "memory");                                            // everyone's; s - 1 is read
+    load(s + DT_RING - 1);
+    const int buf = (s - s0) % DT_RING;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const u32x4_t a = ld16(lds.x[buf] + (16 * wave + li) * DT_K + slot[u]);
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(ld16(lds.w[buf] + (16 * c + li) * DT_K + slot[u])),
+                                                         acc[c], 0, 0, 0);
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // before the workgroup's LDS is given up
+  // lane: tokens 16 wave + 4 lg + e, row 16 c + li of the adapter
+  float* part = jb.part + (int64_t)blockIdx.y * M * v.rs;
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = 16 * wave + 4 * lg + e, j = 16 * c + li;
+      if (row < it.count && j < r) part[(int64_t)(it.start + row) * v.rs + j] = acc[c][e];
+    }
+}
+
+__global__ __launch_bounds__(256) void k_adapter_down_join(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt,
+                                                           int shares) {
+  const DownJob jb = blockIdx.y ? j1 : j0;
+  const int64_t total = M * v.rs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t pos = i / v.rs;
+    const int j = (int)(i - pos * v.rs), a = rt.sid[pos];
+    if (a >= v.n) {   // a token without an adapter
+      if (jb.save && j < v.r_max) jb.save[(int64_t)rt.perm[pos] * v.r_max + j] = 0.0f;
+      continue;
+    }
+    const lq_adapter ad = v.tab[a];
+    float x = 0.0f;
+    if (j < ad.r) {
+      if (jb.Q) {
+        x = jb.part[i];
+        for (int k = 1; k < shares; ++k) x += jb.part[k * total + i];
+      } else {
+        x = jb.given[(int64_t)rt.perm[pos] * v.r_max + j];
+      }
+    }
+    put_t(jb, v, rt, ad, pos, j, x);
+  }
+}
+
+// The tiled form pays once the tokens fill it: at 2048 tokens of rank 16 the
+// two took 10.5 us alike, at 4096 tokens of rank 64 45 against 23 us.
+bool down_tiled(int64_t M, int32_t rs) { return M * rs >= 65536; }
+
+// Shares of the columns: two workgroups per CU, at least 8 steps each.
+int down_shares(int64_t M, int64_t C) {
+  const int64_t tiles = (M + DT_M - 1) / DT_M, steps = (C + DT_K - 1) / DT_K;
+  int s = 1;
+  while (s < 16 && tiles * s * 2 <= 512 && steps / (s * 2) >= 8) s *= 2;
+  return s;
+}
+
+// ===========================================================================
 // Column form: out_a[j][c] = sum_m (s_a P)[m][j] Q[m][c] over a's tokens. One
 // workgroup per 256 columns (64 a wave) and run of at most `rows` sorted
 // positions; 32 tokens per step. P comes as three bfloat16 terms, so the
@@ -439,7 +599,7 @@ __device__ __forceinline__ u32x4_t tr_frag(const uint16_t* base, int pitch, int 
 }
 
 template <int JT>
-__global__ __launch_bounds__(256) void k_adapter_col(ColReq q0, ColReq q1, unsigned tiles0, int rows, AdapterView v,
+__global__ __launch_bounds__(256, 2) void k_adapter_col(ColReq q0, ColReq q1, unsigned tiles0, int rows, AdapterView v,
                                                      Route rt) {
   constexpr int PP = 16 * JT + 16;
   constexpr int PQ = (3 * 32 * 2 * JT + 255) / 256;   // 16-byte pieces of P per thread
@@ -466,25 +626,24 @@ __global__ __launch_bounds__(256) void k_adapter_col(ColReq q0, ColReq q1, unsig
   };
   auto load = [&](int mb) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      xq[u] = ld16(rq.Q + (int64_t)tok[u] * C + (qin ? c0 + qc : 0));
-      if (!qin || mb + qr + 8 * u >= it.count) xq[u] = u32x4_t{0u, 0u, 0u, 0u};
-    }
+    for (int u = 0; u < 4; ++u) xq[u] = ld16(rq.Q + (int64_t)tok[u] * C + (qin ? c0 + qc : 0));
 #pragma unroll
     for (int k = 0; k < PQ; ++k) {
       const int i = threadIdx.x + 256 * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, term = min(i / (64 * JT), 2);
-      const bool ok = mb + row < it.count && 8 * c8 < r8;
-      xp[k] = ld16(rq.terms + (int64_t)(it.start + min(mb + row, it.count - 1)) * 3 * v.rs + (ok ? term * r8 + 8 * c8 : 0));
-      if (!ok) xp[k] = u32x4_t{0u, 0u, 0u, 0u};
+      xp[k] = ld16(rq.terms + (int64_t)(it.start + min(mb + row, it.count - 1)) * 3 * v.rs +
+                   (8 * c8 < r8 ? term * r8 + 8 * c8 : 0));
     }
   };
-  auto store = [&](int b) {
+  auto store = [&](int mb, int b) {
+    const u32x4_t none = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int u = 0; u < 4; ++u) *reinterpret_cast<u32x4_t*>(sQ[b] + (qr + 8 * u) * CQ_PITCH + qc) = xq[u];
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<u32x4_t*>(sQ[b] + (qr + 8 * u) * CQ_PITCH + qc) = qin && mb + qr + 8 * u < it.count ? xq[u] : none;
 #pragma unroll
     for (int k = 0; k < PQ; ++k) {
       const int i = threadIdx.x + 256 * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, term = i / (64 * JT);
-      if (term < 3) *reinterpret_cast<u32x4_t*>(sP[b] + (32 * term + row) * PP + 8 * c8) = xp[k];
+      if (term < 3)
+        *reinterpret_cast<u32x4_t*>(sP[b] + (32 * term + row) * PP + 8 * c8) = mb + row < it.count && 8 * c8 < r8 ? xp[k] : none;
     }
   };
   f32x4_t acc[JT][4];
@@ -495,38 +654,47 @@ __global__ __launch_bounds__(256) void k_adapter_col(ColReq q0, ColReq q1, unsig
   tokens(0);
   load(0);
   tokens(32);
-  int b = 0;
-  for (int mb = 0; mb < it.count; mb += 32, b ^= 1) {
-    store(b);
-    __syncthreads();
-    if (mb + 32 < it.count) {
-      load(mb + 32);
-      tokens(mb + 64);
+  for (int mb = 0; mb < it.count; mb += 64) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int m = mb + 32 * b;
+      if (m >= it.count) break;
+      store(m, b);
+      __syncthreads();
+      load(m + 32);
+      tokens(m + 64);
+      u32x4_t fq[4];
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) fq[ct] = tr_frag(sQ[b] + 64 * wave + 16 * ct, CQ_PITCH, li, lg);
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+#pragma unroll
+        for (int jt = 0; jt < JT; ++jt) {
+          const u32x4_t a = tr_frag(sP[b] + 32 * t * PP + 16 * jt, PP, li, lg);
+#pragma unroll
+          for (int ct = 0; ct < 4; ++ct)
+            acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(fq[ct]), acc[jt][ct], 0, 0, 0);
+        }
     }
-    u32x4_t fq[4];
-#pragma unroll
-    for (int ct = 0; ct < 4; ++ct) fq[ct] = tr_frag(sQ[b] + 64 * wave + 16 * ct, CQ_PITCH, li, lg);
-#pragma unroll
-    for (int t = 0; t < 3; ++t)
-#pragma unroll
-      for (int jt = 0; jt < JT; ++jt) {
-        const u32x4_t a = tr_frag(sP[b] + 32 * t * PP + 16 * jt, PP, li, lg);
-#pragma unroll
-        for (int ct = 0; ct < 4; ++ct)
-          acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(fq[ct]), acc[jt][ct], 0, 0, 0);
-      }
   }
-  // lane: column li of each tile, rows j = 4 lg + e
+  // lane: column li of each tile, rows j = 4 lg + e. Partial sums lie as
+  // [slot][rs][C] (16 lanes 64 bytes in a row; [C][rs] measured slower).
+  const bool vec = rq.transposed && it.slot < 0 && r % 4 == 0 && (reinterpret_cast<uintptr_t>(rq.out) & 15) == 0;
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
     for (int ct = 0; ct < 4; ++ct) {
       const int64_t c = c0 + 64 * wave + 16 * ct + li;
-      if (c >= C) continue;
+      const int j0 = 16 * jt + 4 * lg;
+      if (c >= C || j0 >= r) continue;
+      if (vec) {   // C * row and c * r are multiples of 4
+        *reinterpret_cast<f32x4_t*>(rq.out + C * ad.row + c * r + j0) = acc[jt][ct];
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int j = 16 * jt + 4 * lg + e;
-        if (j >= r) continue;
+        const int j = j0 + e;
+        if (j >= r) break;
         if (it.slot >= 0) rq.part[((int64_t)it.slot * v.rs + j) * C + c] = acc[jt][ct][e];
         else if (rq.transposed) rq.out[C * ad.row + c * r + j] = acc[jt][ct][e];
         else rq.out[(ad.row + (int64_t)j) * C + c] = acc[jt][ct][e];
@@ -549,13 +717,35 @@ __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1
   const int runs = (rt.off[a + 1] - rt.off[a] + rows - 1) / rows;
   if (runs == 1) return;
   const lq_adapter ad = v.tab[a];
-  const int64_t n0 = ad.r * q0.C, n1 = nreq > 1 ? ad.r * q1.C : 0;
+  // four values a thread: of one row (C % 8 == 0), or of four rows where the
+  // output is transposed (then consecutive threads still read consecutive columns)
+  const int rq = (ad.r + 3) / 4;
+  const int64_t n0 = q0.transposed ? rq * q0.C : ad.r * q0.C / 4;
+  const int64_t n1 = nreq > 1 ? (q1.transposed ? rq * q1.C : ad.r * q1.C / 4) : 0;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n0 + n1; i += (int64_t)gridDim.x * 256) {
     const ColReq& q = i < n0 ? q0 : q1;
-    const int64_t e = i < n0 ? i : i - n0, j = e / q.C, c = e % q.C;
-    float sum = 0.0f;
-    for (int k = 0; k < runs; ++k) sum += q.part[((int64_t)(before + k) * v.rs + j) * q.C + c];
-    q.out[q.C * ad.row + (q.transposed ? c * ad.r + j : e)] = sum;
+    const int64_t e = i < n0 ? i : i - n0;
+    if (q.transposed) {
+      const int64_t c = e % q.C;
+      const int j = 4 * (int)(e / q.C);
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int k = 0; k < runs; ++k) {
+        const float* p = q.part + ((int64_t)(before + k) * v.rs + j) * q.C + c;   // rs rows: a multiple of 8
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sum[u] += p[u * q.C];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j + u < ad.r) q.out[q.C * ad.row + c * ad.r + j + u] = sum[u];
+    } else {
+      const int64_t j = 4 * e / q.C, c = 4 * e % q.C;
+      f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int k = 0; k < runs; ++k)
+        sum += *reinterpret_cast<const f32x4_t*>(q.part + ((int64_t)(before + k) * v.rs + j) * q.C + c);
+      float* o = q.out + (q.C * (ad.row + j) + c);   // 4-byte aligned
+#pragma unroll
+      for (int u = 0; u < 4; ++u) o[u] = sum[u];
+    }
   }
 }
 
@@ -563,7 +753,7 @@ __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1
 // the chip, but runs of at least 256 tokens so that the partial sums stay few.
 int col_rows(int64_t M, int64_t cols) {
   const int64_t tiles = (cols + CQ_COLS - 1) / CQ_COLS;
-  int64_t rows = M * tiles / 384 / 32 * 32;
+  int64_t rows = M * tiles / 448 / 32 * 32;
   return (int)std::max<int64_t>(256, std::min<int64_t>(rows, 4096));
 }
 
@@ -571,7 +761,7 @@ int col_rows(int64_t M, int64_t cols) {
 
 hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, const QWeight& w, uint16_t* wd,
                                int64_t ldb, const AdapterView& v, uint16_t* at, uint16_t* bt, uint16_t* bp,
-                               hipStream_t s) {
+                               uint16_t* zeros, hipStream_t s) {
   LQ_DASSERT(!wd || w.format == LQ_FMT_NF4);
   PrepJob p{};
   size_t lds = 0;
@@ -586,31 +776,57 @@ hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, co
   p.wd = wd;
   p.ldb = ldb;
   if (wd) {
-    p.weight_wgs = (unsigned)(((w.N + 63) / 64) * ((w.K + PW_K - 1) / PW_K));
-    lds = std::max(lds, 256 * sizeof(f32x2_t) + (ldb ? (size_t)64 * PW_PITCH * 2 : 0));
+    const int64_t flat = PW_FLAT * 1024 * 16;
+    p.weight_wgs = (unsigned)(ldb ? ((w.N + PW_T - 1) / PW_T) * ((w.K + PW_T - 1) / PW_T) : (w.N * w.K + flat - 1) / flat);
+    lds = std::max(lds, 256 * sizeof(f32x2_t) + (ldb ? (size_t)PW_T * PW_PITCH * 2 : 0));
   }
   p.v = v;
   p.at = at;
   p.bt = bt;
   p.bp = bp;
+  p.zeros = zeros;
   p.at_wgs = at ? (unsigned)((w.K + RL_C - 1) / RL_C) : 0;
   p.b_wgs = bt || bp ? (unsigned)((w.N + RL_C - 1) / RL_C) : 0;
   p.per_adapter = p.at_wgs + p.b_wgs;
   if (p.per_adapter) lds = std::max(lds, (size_t)RL_C * (v.rs + 2) * 2);
-  const int64_t grid = (int64_t)p.route_wgs + p.weight_wgs + (int64_t)v.n * p.per_adapter;
+  const int64_t grid = std::max<int64_t>(1, (int64_t)p.route_wgs + p.weight_wgs + (int64_t)v.n * p.per_adapter);
   LQ_DASSERT(grid < (int64_t(1) << 31) && lds <= 65536);
-  if (grid == 0) return hipSuccess;
   hipLaunchKernelGGL(k_adapter_prep, dim3((unsigned)grid), dim3(1024), lds, s, p);
   return hipGetLastError();
 }
 
+size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs) {
+  return down_tiled(M, rs) ? (size_t)down_shares(M, C) * M * rs : 0;
+}
+
 hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
-                               uint16_t* zeros, hipStream_t s) {
+                               const uint16_t* zeros, hipStream_t s) {
   if (njobs < 1 || njobs > 2) return hipErrorInvalidValue;
   const DownJob j0 = jobs[0], j1 = jobs[njobs - 1];
+  if (down_tiled(M, v.rs)) {
+    int shares = 1;
+    int64_t C = 0;
+    for (int i = 0; i < njobs; ++i)
+      if (jobs[i].Q) C = C ? std::min(C, jobs[i].C) : jobs[i].C;   // both jobs' workspaces hold these shares
+    if (C) {
+      shares = down_shares(M, C);
+      const dim3 grid((unsigned)((M + DT_M - 1) / DT_M + std::min<int64_t>(v.n, M)), (unsigned)shares, (unsigned)njobs);
+#define LQ_AT(BN) hipLaunchKernelGGL(k_adapter_down_tiles<BN>, grid, dim3(256), 0, s, j0, j1, M, v, rt, zeros)
+      if (v.r_max <= 16) LQ_AT(16);
+      else if (v.r_max <= 32) LQ_AT(32);
+      else if (v.r_max <= 64) LQ_AT(64);
+      else LQ_AT(128);
+#undef LQ_AT
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    const unsigned gx = (unsigned)std::min<int64_t>((M * v.rs + 255) / 256, 8192);
+    hipLaunchKernelGGL(k_adapter_down_join, dim3(gx, (unsigned)njobs), dim3(256), 0, s, j0, j1, M, v, rt, shares);
+    return hipGetLastError();
+  }
   // one item per 16 tokens, and one more per adapter (or none) for its remainder
   const dim3 grid((unsigned)((M + 15) / 16 + std::min<int64_t>(v.n + 1, M)), (unsigned)njobs);
-#define LQ_AD(JT, W, U) hipLaunchKernelGGL((k_adapter_down<JT, W, U>), grid, dim3(64 * W), 0, s, j0, j1, M, v, rt, zeros)
+#define LQ_AD(JT, W, U) hipLaunchKernelGGL((k_adapter_down<JT, W, U>), grid, dim3(64 * W), 0, s, j0, j1, M, v, rt)
   if (v.r_max <= 16) LQ_AD(1, 16, 2);
   else if (v.r_max <= 32) LQ_AD(2, 8, 2);
   else if (v.r_max <= 64) LQ_AD(4, 8, 1);

@@ -54,6 +54,7 @@ size_t bytes16(size_t elems) { return align_up(elems * sizeof(uint16_t)); }
 size_t forward_ws(const QWeight& q, int64_t M, const AdapterView& v, const lq_adapter_set* set) {
   if (adapter_decode_supported(q, M)) return align_up(adapter_decode_ws_bytes(q, M, v));
   return align_up(route_bytes(M, v.n)) + bytes16(terms_elems(M, v)) + bytes16((size_t)q.N * q.K) + bytes16(8) +
+         align_up(adapter_down_ws_floats(M, q.K, v.rs) * sizeof(float)) +
          (any_odd_rank(set) ? bytes16((size_t)sum_r8(set) * q.N) : 0);
 }
 
@@ -64,7 +65,9 @@ size_t backward_ws(const QWeight& q, int64_t M, const AdapterView& v, int64_t r8
          bytes16((size_t)r8 * q.N) + (q.format == LQ_FMT_NF4 ? 0 : bytes16((size_t)q.N * q.K)) +
          bytes16((size_t)q.K * ldb_of(q.N)) +
          align_up(adapter_col_ws_floats(M, q.K, v.rs) * sizeof(float)) +
-         align_up(adapter_col_ws_floats(M, q.N, v.rs) * sizeof(float)) + bytes16(8);
+         align_up(adapter_col_ws_floats(M, q.N, v.rs) * sizeof(float)) + bytes16(8) +
+         align_up(adapter_down_ws_floats(M, q.K, v.rs) * sizeof(float)) +
+         align_up(adapter_down_ws_floats(M, q.N, v.rs) * sizeof(float));
 }
 
 }  // namespace
@@ -88,7 +91,7 @@ int lq_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_t* route, s
   QWeight none{};
   const AdapterView v{nullptr, n, 0, 0};
   return launch_status(launch_adapter_prep(ids, M, route, none, nullptr, 0, v, nullptr, nullptr, nullptr,
-                                           (hipStream_t)stream));
+                                           nullptr, (hipStream_t)stream));
 }
 
 size_t lq_adapters_forward_workspace(const lq_qweight* w, int64_t M, const lq_adapter_set* set) {
@@ -122,15 +125,17 @@ int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const
   uint16_t* terms = cv.take<uint16_t>(terms_elems(M, v));
   uint16_t* wd = cv.take<uint16_t>((size_t)q.N * q.K);
   uint16_t* zeros = cv.take<uint16_t>(8);
+  float* part = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs));
   uint16_t* bp = any_odd_rank(set) ? cv.take<uint16_t>((size_t)sum_r8(set) * q.N) : nullptr;
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
 
   const bool nf4 = q.format == LQ_FMT_NF4;
-  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, nf4 ? wd : nullptr, 0, v, nullptr, nullptr, bp, s);
+  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, nf4 ? wd : nullptr, 0, v, nullptr, nullptr, bp,
+                                     zeros, s);
   if (e == hipSuccess && !nf4) e = launch_dequant(q, wd, s);
   if (e != hipSuccess) return LQ_ERR_LAUNCH;
   const Route rt = route_view(route ? route : rws, M, v.n);
-  const DownJob job{X, q.K, nullptr, nullptr, terms, t_save};
+  const DownJob job{X, q.K, nullptr, nullptr, terms, t_save, part};
   if ((e = launch_adapter_down(&job, 1, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   const AdapterGemm g{X, M, q.N, q.K, wd, q.K, terms, v, bp, 0, rt, H, h_dtype == LQ_F32 ? 1 : 0, zeros};
   return launch_status(launch_adapter_gemm(g, s));
@@ -173,18 +178,20 @@ int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t*
   float* part_a = cv.take<float>(adapter_col_ws_floats(M, q.K, v.rs));
   float* part_b = cv.take<float>(adapter_col_ws_floats(M, q.N, v.rs));
   uint16_t* zeros = cv.take<uint16_t>(8);
+  float* down_t = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs));
+  float* down_u = cv.take<float>(adapter_down_ws_floats(M, q.N, v.rs));
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
   if (!grad_X && !dA && !dB) return LQ_OK;
 
   const bool need_u = grad_X || dA, nf4 = q.format == LQ_FMT_NF4;
   hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, grad_X && nf4 ? wt : nullptr, ldb, v,
-                                     grad_X ? at : nullptr, need_u ? bt : nullptr, nullptr, s);
+                                     grad_X ? at : nullptr, need_u ? bt : nullptr, nullptr, zeros, s);
   if (e != hipSuccess) return LQ_ERR_LAUNCH;
   const Route rt = route_view(route ? route : rws, M, v.n);
   DownJob jobs[2];
   int nj = 0;
-  if (need_u) jobs[nj++] = DownJob{G, q.N, bt, nullptr, u, nullptr};
-  if (dB) jobs[nj++] = DownJob{t_saved ? nullptr : X, q.K, nullptr, t_saved, t, nullptr};
+  if (need_u) jobs[nj++] = DownJob{G, q.N, bt, nullptr, u, nullptr, down_u};
+  if (dB) jobs[nj++] = DownJob{t_saved ? nullptr : X, q.K, nullptr, t_saved, t, nullptr, down_t};
   if (nj && (e = launch_adapter_down(jobs, nj, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   ColReq cols[2];
   int nc = 0;
