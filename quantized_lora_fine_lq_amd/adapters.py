@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 from typing import Optional, Sequence, Tuple
 
-from . import (LQ_BF16, LQ_F32, QWeight, _check, _contig_cuda, _dtype_code, _ptr, _stream, _torch, c_f32, c_i32, c_i64,
+from . import (LQ_BF16, LQ_F32, QWeight, _check, _contig_cuda, _dtype_code, _ptr, _torch, c_f32, c_i32, c_i64,
                c_sz, c_vp, lib, QW_P)
 
 LQ_ADAPTERS_MAX = 1000
@@ -111,32 +111,29 @@ class AdapterSet:
         return out
 
 
-def _check_ids(ids, M, device):
-    torch = _torch()
-    _contig_cuda(ids, "ids")
-    if ids.dtype != torch.int32 or tuple(ids.shape) != (M,) or ids.device != device:
-        raise ValueError(f"ids must be int32 [{M}] on the tokens' device")
+# The smallest calls run for ten microseconds, so these helpers cost as little
+# as they can: one condition each, the words only on failure; and the stream's
+# handle by device index instead of a Stream object (2 us).
+def _stream(dev):
+    return _torch()._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _check_tokens(x, name, cols, device):
-    torch = _torch()
-    _contig_cuda(x, name)
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != cols or x.device != device:
-        raise ValueError(f"{name} must be bfloat16 [tokens, {cols}] on the weight's device")
+def _tokens(torch, x, name, cols, device):
+    if not (x.is_cuda and x.dtype is torch.bfloat16 and x.dim() == 2 and x.size(1) == cols and x.is_contiguous()
+            and x.device == device):
+        raise ValueError(f"{name} must be contiguous bfloat16 [tokens, {cols}] on the weight's device")
 
 
-def _check_set(qw, adapters):
-    if (adapters.N, adapters.K) != (qw.N, qw.K) or adapters.device != qw.device:
+def _tokens_args(torch, M, qw, adapters, ids, route, device):
+    if adapters.N != qw.N or adapters.K != qw.K or adapters.device != device:
         raise ValueError(f"the adapters belong to a [{adapters.N}, {adapters.K}] weight on {adapters.device}")
-
-
-def _check_route(route, ids, n):
-    torch = _torch()
-    if route is not None:
-        _contig_cuda(route, "route")
-        if route.dtype != torch.int32 or route.device != ids.device or \
-                4 * route.numel() < lib.lq_adapter_route_bytes(ids.numel(), n):
-            raise ValueError("route is not one of these ids and this many adapters")
+    if not (ids.is_cuda and ids.dtype is torch.int32 and ids.dim() == 1 and ids.size(0) == M and ids.is_contiguous()
+            and ids.device == device):
+        raise ValueError(f"ids must be contiguous int32 [{M}] on the tokens' device")
+    if route is not None and not (
+            route.is_cuda and route.dtype is torch.int32 and route.is_contiguous() and route.device == device
+            and 4 * route.numel() >= lib.lq_adapter_route_bytes(M, adapters.n)):
+        raise ValueError("route is not one of these ids and this many adapters")
 
 
 def adapter_route(ids, n: int):
@@ -157,21 +154,23 @@ def adapters_forward(qw: QWeight, X, adapters: AdapterSet, ids, out_dtype=None, 
     """H[m] = W' X[m] + (alpha_a / r_a) B_a A_a X[m] with a = ids[m] (outside
     [0, n): the base weight alone). Returns (H [M, N], t [M, r_max] f32 or None)."""
     torch = _torch()
-    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is None:
+        out_dtype = torch.bfloat16
+    f32 = out_dtype is torch.float32
+    if not f32 and out_dtype is not torch.bfloat16:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    _check_tokens(X, "X", qw.K, qw.device)
-    M = X.shape[0]
-    _check_set(qw, adapters)
-    _check_ids(ids, M, X.device)
-    _check_route(route, ids, adapters.n)
-    H = torch.empty(M, qw.N, dtype=out_dtype, device=X.device)
-    t = torch.empty(M, adapters.r_max, dtype=torch.float32, device=X.device) if save_t else None
-    ws_bytes = lib.lq_adapters_forward_workspace(qw.ref(), M, adapters.ref())
-    ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=X.device)
-    h_code = LQ_F32 if out_dtype == torch.float32 else LQ_BF16
-    _check(lib.lq_adapters_forward(qw.ref(), _ptr(X), M, adapters.ref(), _ptr(ids), _ptr(route), _ptr(H), h_code,
-                                   _ptr(t), _ptr(ws), ws_bytes, _stream(X.device)), "lq_adapters_forward")
+    dev = qw.device
+    _tokens(torch, X, "X", qw.K, dev)
+    M = X.size(0)
+    _tokens_args(torch, M, qw, adapters, ids, route, dev)
+    empty, w, s = torch.empty, qw.ref(), adapters.ref()
+    H = empty((M, qw.N), dtype=out_dtype, device=dev)
+    t = empty((M, adapters.r_max), dtype=torch.float32, device=dev) if save_t else None
+    ws_bytes = lib.lq_adapters_forward_workspace(w, M, s)
+    ws = empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
+    _check(lib.lq_adapters_forward(w, X.data_ptr(), M, s, ids.data_ptr(), None if route is None else route.data_ptr(),
+                                   H.data_ptr(), LQ_F32 if f32 else LQ_BF16, t.data_ptr() if save_t else None,
+                                   ws.data_ptr(), ws_bytes, _stream(dev)), "lq_adapters_forward")
     return H, t
 
 
@@ -181,28 +180,30 @@ def adapters_backward(qw: QWeight, X, G, adapters: AdapterSet, ids, t=None, need
     ranks]), each None if not needed; adapters.split(dA, dB) gives them by
     adapter. t: the forward's, or None to form it again from X."""
     torch = _torch()
-    _check_tokens(G, "G", qw.N, qw.device)
-    M, dev = G.shape[0], G.device
-    _check_set(qw, adapters)
+    dev = qw.device
+    _tokens(torch, G, "G", qw.N, dev)
+    M = G.size(0)
     if X is not None:
-        _check_tokens(X, "X", qw.K, dev)
-        if X.shape[0] != M:
+        _tokens(torch, X, "X", qw.K, dev)
+        if X.size(0) != M:
             raise ValueError("X and G differ in their tokens")
-    _check_ids(ids, M, dev)
-    _check_route(route, ids, adapters.n)
-    if t is not None:
-        _contig_cuda(t, "t")
-        if t.dtype != torch.float32 or tuple(t.shape) != (M, adapters.r_max) or t.device != dev:
-            raise ValueError(f"t must be float32 [{M}, {adapters.r_max}] on the tokens' device")
-    gx = torch.empty(M, qw.K, dtype=torch.bfloat16, device=dev) if need_grad_x else None
-    dA = torch.empty(adapters.r_sum, qw.K, dtype=torch.float32, device=dev) if need_dA else None
-    dB = torch.empty(qw.N * adapters.r_sum, dtype=torch.float32, device=dev) if need_dB else None
-    ws_bytes = lib.lq_adapters_backward_workspace(qw.ref(), M, adapters.ref())
-    ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-    _check(lib.lq_adapters_backward(qw.ref(), _ptr(X), _ptr(G), M, adapters.ref(), _ptr(ids), _ptr(route), _ptr(t),
-                                    _ptr(gx), _ptr(dA), _ptr(dB), _ptr(ws), ws_bytes, _stream(dev)),
-           "lq_adapters_backward")
+    _tokens_args(torch, M, qw, adapters, ids, route, dev)
+    if t is not None and not (t.is_cuda and t.dtype is torch.float32 and t.shape == (M, adapters.r_max)
+                              and t.is_contiguous() and t.device == dev):
+        raise ValueError(f"t must be contiguous float32 [{M}, {adapters.r_max}] on the tokens' device")
+    empty, w, s, f32 = torch.empty, qw.ref(), adapters.ref(), torch.float32
+    gx = empty((M, qw.K), dtype=torch.bfloat16, device=dev) if need_grad_x else None
+    dA = empty((adapters.r_sum, qw.K), dtype=f32, device=dev) if need_dA else None
+    dB = empty((qw.N * adapters.r_sum,), dtype=f32, device=dev) if need_dB else None
+    ws_bytes = lib.lq_adapters_backward_workspace(w, M, s)
+    ws = empty((max(ws_bytes, 1),), dtype=torch.uint8, device=dev)
+    _check(lib.lq_adapters_backward(w, _at(X), G.data_ptr(), M, s, ids.data_ptr(), _at(route), _at(t), _at(gx), _at(dA),
+                                    _at(dB), ws.data_ptr(), ws_bytes, _stream(dev)), "lq_adapters_backward")
     return gx, dA, dB
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 class GradList:
@@ -219,7 +220,10 @@ class GradList:
         if len(groups) != len(self.tensors):
             raise ValueError("groups must have one entry per tensor")
         self.n_groups = max(groups, default=0) + 1 if n_groups is None else int(n_groups)
-        self.device = self.tensors[0].device if self.tensors else torch.device("cuda" if device is None else device)
+        if self.tensors:
+            self.device = self.tensors[0].device
+        else:   # as tensors name it, with its index
+            self.device = torch.empty(0, device="cuda" if device is None else device).device
         arr = (lq_grad_tensor * max(len(self.tensors), 1))()
         for i, (t, g) in enumerate(zip(self.tensors, groups)):
             _contig_cuda(t, f"gradient {i}")
@@ -233,22 +237,22 @@ class GradList:
                                       ctypes.byref(self.desc)), "lq_grad_list_build")
         self._dev = host.to(self.device)
         self.desc.dev = self._dev.data_ptr()
+        self._ws_bytes = lib.lq_grad_norm_workspace(self.ref())
 
     def ref(self):
         return ctypes.byref(self.desc)
 
-
-def _norm_buffers(grads: GradList):
-    torch = _torch()
-    norms = torch.empty(grads.n_groups, dtype=torch.float32, device=grads.device)
-    ws_bytes = lib.lq_grad_norm_workspace(grads.ref())
-    return norms, torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=grads.device), ws_bytes
+    def _buffers(self):
+        torch = _torch()
+        norms = torch.empty((self.n_groups,), dtype=torch.float32, device=self.device)
+        return norms, torch.empty((max(self._ws_bytes, 1),), dtype=torch.uint8, device=self.device)
 
 
 def grad_norm(grads: GradList):
     """The L2 norm of each group's gradients (f32 [n_groups])."""
-    norms, ws, ws_bytes = _norm_buffers(grads)
-    _check(lib.lq_grad_norm(grads.ref(), _ptr(norms), _ptr(ws), ws_bytes, _stream(grads.device)), "lq_grad_norm")
+    norms, ws = grads._buffers()
+    _check(lib.lq_grad_norm(grads.ref(), norms.data_ptr(), ws.data_ptr(), grads._ws_bytes, _stream(grads.device)),
+           "lq_grad_norm")
     return norms
 
 
@@ -257,10 +261,11 @@ def clip_grad_norm(grads: GradList, max_norm: float, out: Optional[GradList] = N
     or into `out` (a list of the same sizes, types and groups). Returns the
     norms before clipping (f32 [n_groups]); a group whose norm is not finite
     shows there."""
-    out = grads if out is None else out
-    if out.device != grads.device:
+    if out is None:
+        out = grads
+    elif out.device != grads.device:
         raise ValueError("the lists are on different devices")
-    norms, ws, ws_bytes = _norm_buffers(grads)
-    _check(lib.lq_clip_grad_norm(grads.ref(), out.ref(), float(max_norm), float(eps), _ptr(norms), _ptr(ws), ws_bytes,
-                                 _stream(grads.device)), "lq_clip_grad_norm")
+    norms, ws = grads._buffers()
+    _check(lib.lq_clip_grad_norm(grads.ref(), out.ref(), float(max_norm), float(eps), norms.data_ptr(), ws.data_ptr(),
+                                 grads._ws_bytes, _stream(grads.device)), "lq_clip_grad_norm")
     return norms

@@ -15,11 +15,6 @@ namespace {
 
 __device__ __forceinline__ u32x4_t ld16(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int read_lane(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
-__device__ __forceinline__ uint64_t read_lane(uint64_t v, int l) {
-  return (uint64_t)(uint32_t)read_lane((int)(uint32_t)v, l) | ((uint64_t)(uint32_t)read_lane((int)(uint32_t)(v >> 32), l) << 32);
-}
-__device__ __forceinline__ int first_bit(uint64_t m) { return uniform(__ffsll((unsigned long long)m) - 1); }
 // set bits of m below the lane
 __device__ __forceinline__ int bits_below(uint64_t m) {
   return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
@@ -32,6 +27,50 @@ __device__ __forceinline__ int lane_key(const int32_t* ids, int M, int n) {
   const int id = lane < M ? ids[lane] : -1;
   return (uint32_t)id < (uint32_t)n ? id : -1;
 }
+
+// The adapters' part as steps of 32 contraction columns (4 runs of 8; TERMS
+// copies of an adapter's runs), dealt to the waves in turn. Lane l holds the
+// adapter of token l; the first token of each adapter in use leads it, and the
+// leaders' step counts, summed over the lanes, number the steps. The launch
+// that forms t writes the steps out for the projection (DcRecord), whose waves
+// then start from one uniform load instead of a chain of them.
+struct DcSteps {
+  lq_adapter ad;     // the lane's token's adapter (leaders' entries are used)
+  uint64_t same;     // its tokens
+  int first, count;  // its steps (0 unless the lane leads)
+  int total;
+};
+__device__ __forceinline__ DcSteps dc_steps(const lq_adapter& ad, int key, int terms) {
+  DcSteps st;
+  st.ad = ad;
+  // the tokens of the lane's adapter, from one ballot per bit of the key
+  uint64_t peers = __ballot(key >= 0);
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {
+    const uint64_t one = __ballot((key >> b) & 1);
+    peers &= ((key >> b) & 1) ? one : ~one;
+  }
+  st.same = peers;
+  const bool leads = key >= 0 && bits_below(peers) == 0;
+  st.count = leads ? (terms * ((st.ad.r + 7) >> 3) + 3) >> 2 : 0;   // at most 12
+  st.first = 0;
+  st.total = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {   // the sum over the lanes below, bit by bit
+    const uint64_t one = __ballot((st.count >> b) & 1);
+    st.first += bits_below(one) << b;
+    st.total += __popcll(one) << b;
+  }
+  return st;
+}
+
+struct DcRecord {
+  uint64_t B, same;    // B_a, its tokens
+  float scale;
+  int32_t r, run0;     // first of the step's 4 runs
+  int32_t total;       // steps in all (every record)
+};
+constexpr int DC_RECORDS = 64 * 12;
 
 // ===========================================================================
 // t = A_a x: one workgroup per adapter in use (workgroup b takes the b-th in
@@ -50,11 +89,21 @@ template <int JT, int W>
 __global__ __launch_bounds__(64 * W) void k_decode_down(const uint16_t* __restrict__ X, int M, int64_t K,
                                                         AdapterView v, const int32_t* __restrict__ ids,
                                                         float* __restrict__ t, u32x4_t* __restrict__ xp, int TT,
-                                                        int wgs) {
+                                                        int wgs, DcRecord* __restrict__ records, int terms) {
   __shared__ f32x4_t part[W][JT][64];
-  if ((int)blockIdx.x >= wgs) {
-    const int workers = ((int)gridDim.x - wgs) * (int)gridDim.y * 64 * W;
-    int i = (((int)blockIdx.x - wgs) * (int)gridDim.y + (int)blockIdx.y) * 64 * W + (int)threadIdx.x;
+  if ((int)blockIdx.x == wgs) {   // the steps, by the lanes that lead an adapter
+    if (blockIdx.y || threadIdx.x >= 64) return;
+    const int key = lane_key(ids, M, v.n);
+    const DcSteps st = dc_steps(v.tab[max(key, 0)], key, terms);
+    for (int k = 0; k < st.count; ++k)
+      records[st.first + k] = DcRecord{(uint64_t)reinterpret_cast<uintptr_t>(st.ad.B), st.same, st.ad.scale, st.ad.r, 4 * k,
+                                       st.total};
+    if (st.total == 0 && threadIdx.x == 0) records[0].total = 0;
+    return;
+  }
+  if ((int)blockIdx.x > wgs) {
+    const int workers = ((int)gridDim.x - wgs - 1) * (int)gridDim.y * 64 * W;
+    int i = (((int)blockIdx.x - wgs - 1) * (int)gridDim.y + (int)blockIdx.y) * 64 * W + (int)threadIdx.x;
     for (; i < xp_units(K, TT); i += workers) {
       const int ln = i & 63, u = (i >> 6) & 3, tt = (i >> 8) % TT, s = (i >> 8) / TT;
       const int64_t k = 128 * (int64_t)s + 32 * (ln >> 4) + 8 * u;
@@ -106,12 +155,12 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(const uint16_t* __restri
       u32x4_t x[UB][2], w[UB][2][JT];
 #pragma unroll
       for (int u = 0; u < UB; ++u) {
-        const int64_t c = 64 * (int64_t)min(b + W * u, blocks - 1) + 16 * lg;
+        const int64_t c = 64 * (int64_t)min(b + W * u, blocks - 1) + 8 * lg;   // 64 bytes of each row a load
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          x[u][h] = ld16(q + c + 8 * h);
+          x[u][h] = ld16(q + c + 32 * h);
 #pragma unroll
-          for (int jt = 0; jt < JT; ++jt) w[u][h][jt] = ld16(rr[jt] + c + 8 * h);
+          for (int jt = 0; jt < JT; ++jt) w[u][h][jt] = ld16(rr[jt] + c + 32 * h);
         }
       }
 #pragma unroll
@@ -156,12 +205,12 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(const uint16_t* __restri
 // (2 KB) two thirds of the lookups' cycles were bank conflicts.
 // ===========================================================================
 struct DecodeParams {
-  const uint16_t* X;
-  const u32x4_t* xp;   // X in fragment order (more than one token tile)
+  const u32x4_t* xp;   // X in fragment order
+  const DcRecord* records;
   int M;
   const int32_t* ids;
   AdapterView v;
-  const float* t;      // [parts][M, rs], or null: formed here (few ranks in use)
+  const float* t;      // [parts][M, rs]
   int parts;
   float* t_out;        // [M, r_max], or null
   void* out;
@@ -170,14 +219,13 @@ struct DecodeParams {
 };
 
 constexpr int DC_PAIRS = 256 * 32;   // f32x2_t, 64 KB
-constexpr int DC_TR = 32;            // largest sum of ranks, each rounded up to 16, whose t the kernel forms itself
+constexpr int DC_PARTS = 8;           // most column parts of t
 
-template <int RG, int XT, int AT>
+template <int RG>
 struct DcStage {
   u32x4_t code[RG];
-  u32x4_t x[XT][4];   // one token tile: its X ahead with the codes
-  u32x4_t a[AT][4];   // and, where the kernel forms t, 16 rows of A each
-  int bl;             // the lane's 64-block (the last one where that lies past the row)
+  u32x4_t x[4];   // one token tile: its X ahead with the codes
+  int bl;         // the lane's 64-block (the last one where that lies past the row)
 };
 
 __device__ __forceinline__ float term_of(float v, int t) {
@@ -187,55 +235,20 @@ __device__ __forceinline__ float term_of(float v, int t) {
   return t == 1 ? mid : v - hi - mid;
 }
 
-// floats of LDS after the pair table: constants, then the partial sums of t or
-// of one token tile
+// floats of LDS after the pair table: constants, then the partial sums of one
+// token tile
 template <int RG, int W>
 __host__ __device__ constexpr int dc_floats(int nb) {
   const int c = (16 * RG * (nb + 1) + 3) / 4 * 4, red = W * RG * 272;
   return c > red ? c : red;
 }
-size_t dc_lds_bytes(int rg, int tt, int w, int nb, int rs, bool tk) {
+size_t dc_lds_bytes(int rg, int tt, int w, int nb, int rs) {
   const int c = (16 * rg * (nb + 1) + 3) / 4 * 4, red = w * rg * 272;
   return DC_PAIRS * sizeof(f32x2_t) +
-         4 * (size_t)((c > red ? c : red) + (tk ? 16 * DC_TR + DC_TR / 16 * w * 256 : 16 * tt * rs));
+         4 * (size_t)((c > red ? c : red) + 16 * tt * rs);
 }
 
-// The adapters' part as steps of 32 contraction columns (4 runs of 8; TERMS
-// copies of an adapter's runs), dealt to the waves in turn. Lane l holds the
-// adapter of token l; the first token of each adapter in use leads it, and the
-// leaders' step counts, summed over the lanes, number the steps.
-struct DcSteps {
-  lq_adapter ad;     // the lane's token's adapter (leaders' entries are used)
-  uint64_t same;     // its tokens
-  int first, count;  // its steps (0 unless the lane leads)
-  int total;
-};
-template <int TERMS>
-__device__ __forceinline__ DcSteps dc_steps(const lq_adapter& ad, int key) {
-  DcSteps st;
-  st.ad = ad;
-  // the tokens of the lane's adapter, from one ballot per bit of the key
-  uint64_t peers = __ballot(key >= 0);
-#pragma unroll
-  for (int b = 0; b < 10; ++b) {
-    const uint64_t one = __ballot((key >> b) & 1);
-    peers &= ((key >> b) & 1) ? one : ~one;
-  }
-  st.same = peers;
-  const bool leads = key >= 0 && bits_below(peers) == 0;
-  st.count = leads ? (TERMS * ((st.ad.r + 7) >> 3) + 3) >> 2 : 0;   // at most 12
-  st.first = 0;
-  st.total = 0;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {   // the sum over the lanes below, bit by bit
-    const uint64_t one = __ballot((st.count >> b) & 1);
-    st.first += bits_below(one) << b;
-    st.total += __popcll(one) << b;
-  }
-  return st;
-}
-
-// Step k as every lane needs it, with the weight-side operand loaded.
+// A step as every lane needs it, with the weight-side operand loaded.
 template <int RG>
 struct DcStep {
   u32x4_t w[RG];
@@ -245,14 +258,13 @@ struct DcStep {
   bool live;
 };
 template <int RG, int TERMS>
-__device__ __forceinline__ void dc_step(const DcSteps& st, int k, int64_t n0, int64_t N, DcStep<RG>& o) {
+__device__ __forceinline__ void dc_step(const DcRecord& rec, int64_t n0, int64_t N, DcStep<RG>& o) {
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int l = first_bit(__ballot(k >= st.first && k < st.first + st.count));
-  const uint16_t* B = reinterpret_cast<const uint16_t*>(read_lane((uint64_t)reinterpret_cast<uintptr_t>(st.ad.B), l));
-  const int r = read_lane(st.ad.r, l), runs = (r + 7) >> 3;
-  const int run = 4 * (k - read_lane(st.first, l)) + lg;
-  o.scale = __int_as_float(read_lane(__float_as_int(st.ad.scale), l));
-  o.same = read_lane(st.same, l);
+  const uint16_t* B = reinterpret_cast<const uint16_t*>(rec.B);
+  const int r = rec.r, runs = (r + 7) >> 3;
+  const int run = rec.run0 + lg;
+  o.scale = rec.scale;
+  o.same = rec.same;
   o.live = run < TERMS * runs;
   o.term = o.live ? run / runs : 0;
   o.j0 = o.live ? 8 * (run - o.term * runs) : 0;
@@ -299,13 +311,11 @@ __device__ __forceinline__ void dc_apply(const DcStep<RG>& o, const float* sT, i
   }
 }
 
-template <int RG, int TT, int W, bool DQ, bool OUT_F32, int TA>
+template <int RG, int TT, int W, bool DQ, bool OUT_F32>
 __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dc_lds[];
   constexpr int TERMS = OUT_F32 ? 3 : 2;
   constexpr bool XA = TT == 1;   // X is loaded a stage ahead, with the codes
-  constexpr bool TK = TA > 0;    // t formed here, TA groups of 16 rows of A
-  constexpr int XT = 1, AT = TK ? TA : 1;
   f32x2_t* sPair = reinterpret_cast<f32x2_t*>(dc_lds);
   float* sC = reinterpret_cast<float*>(dc_lds + DC_PAIRS * sizeof(f32x2_t));
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -313,35 +323,24 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
   const int64_t N = p.w.N, K = p.w.K;
   const int64_t n0 = (int64_t)blockIdx.x * 16 * RG;
   const int nb = (int)(K / 64), pitch = nb + 1, ns = (nb + 1) / 2;
-  const int tstride = TK ? DC_TR : p.v.rs;
-  float* sT = sC + dc_floats<RG, W>(nb);                          // t [16 TT][tstride]
-  f32x4_t* sP = reinterpret_cast<f32x4_t*>(sT + 16 * DC_TR);      // TK: the waves' sums of t [TA][W][64]
+  float* sT = sC + dc_floats<RG, W>(nb);   // t [M][rs]
 
-  const int key = lane_key(p.ids, p.M, p.v.n);   // the first load of a chain: id, table entry, A and B
   const uint8_t* crow[RG];
 #pragma unroll
   for (int g = 0; g < RG; ++g) crow[g] = p.w.codes + min(n0 + 16 * g + li, N - 1) * (K / 2) + 16 * (lg & 1);
-  const uint16_t* xrow = p.X + (int64_t)min(li, p.M - 1) * K + 32 * (lg & 1);   // TT == 1
-  const uint16_t* arow[AT];
-  auto load = [&](int s, DcStage<RG, XT, AT>& st) {
-    const int bl = 2 * min(s, ns - 1) + (lg >> 1);
-    st.bl = min(bl, nb - 1);
+  auto load = [&](int s, DcStage<RG>& st) {
+    const int ss = min(s, ns - 1);
+    st.bl = min(2 * ss + (lg >> 1), nb - 1);
 #pragma unroll
     for (int g = 0; g < RG; ++g) st.code[g] = ld16(crow[g] + (int64_t)st.bl * 32);
     if constexpr (XA)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) st.x[0][u] = ld16(xrow + (int64_t)st.bl * 64 + 8 * u);
+      for (int u = 0; u < 4; ++u) st.x[u] = p.xp[((int64_t)ss * 4 + u) * 64 + lane];
   };
-  auto load_a = [&](DcStage<RG, XT, AT>& st) {
-#pragma unroll
-    for (int j = 0; j < AT; ++j)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) st.a[j][u] = ld16(arow[j] + (int64_t)st.bl * 64 + 8 * u);
-  };
+  DcStage<RG> s0, s1;
+  load(wave, s0);
+  load(wave + W, s1);
 
-  // Loads return in order, so a chain (id, table entry, then A and B) that
-  // started behind the codes would wait for them at every link: the pair table
-  // covers the ids' latency, and the codes follow the entries' load.
   // The pair table: lane l of a wave writes slot l % 32 of entries e + l / 32
 #pragma unroll
   for (int k = 0; k < 128 / W; ++k) {
@@ -349,41 +348,28 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
     const float first = p.lv.q[e >> 4], lo = p.lv.q[e & 15], hi = p.lv.q[(e & 15) + 1];
     sPair[32 * e + lane] = f32x2_t{first, lane < 32 ? lo : hi};
   }
-  const lq_adapter mine = p.v.tab[max(key, 0)];
-  DcStage<RG, XT, AT> s0, s1;
-  load(wave, s0);
-  load(wave + W, s1);
-  const DcSteps steps = dc_steps<TERMS>(mine, key);
-  if constexpr (TK) {
-    // row li of the j-th 16 rows in use, adapter after adapter (any valid row past the last)
-    uint64_t left = __ballot(steps.count > 0);
-#pragma unroll
-    for (int j = 0; j < AT; ++j) arow[j] = p.X + 32 * (lg & 1);
-    for (int jt = 0; left; left &= left - 1) {
-      const int l = first_bit(left);
-      const uint16_t* A = reinterpret_cast<const uint16_t*>(read_lane((uint64_t)reinterpret_cast<uintptr_t>(steps.ad.A), l));
-      const int r = read_lane(steps.ad.r, l);
-      for (int j0 = 0; j0 < r; j0 += 16, ++jt) {
-#pragma unroll
-        for (int j = 0; j < AT; ++j)
-          if (j == jt) arow[j] = A + (int64_t)min(j0 + li, r - 1) * K + 32 * (lg & 1);
-      }
-    }
-    load_a(s0);
-    load_a(s1);
-  }
+  const int nsteps = p.records[0].total;
   DcStep<RG> step;
   const float mean = DQ ? *p.w.qc.dq_mean : 0.0f;
-  if (DQ && nb % 16 == 0) {
-    const int cpr = nb / 16;
-    for (int i = threadIdx.x; i < 16 * RG * cpr; i += 64 * W) {
-      const int rr = i / cpr, cb = i - rr * cpr;
-      const int64_t blk = min(n0 + rr, N - 1) * nb + 16 * cb;
-      const u32x4_t q8 = ld16(p.w.qc.absmax_q + blk);
-      const float s2 = p.w.qc.dq_scale[blk >> 8];
+  // the rows' constants, four a thread: thread t row t % (16 RG)
+  if (nb % 4 == 0) {
+    const int rr = threadIdx.x % (16 * RG);
+    const int64_t b0 = min(n0 + rr, N - 1) * nb;
+#pragma unroll 2
+    for (int c = 4 * (threadIdx.x / (16 * RG)); c < nb; c += 4 * (64 * W / (16 * RG))) {
+      const int64_t blk = b0 + c;   // a multiple of 4: one second-level scale
+      f32x4_t v;
+      if constexpr (DQ) {
+        const uint32_t q8 = *reinterpret_cast<const uint32_t*>(p.w.qc.absmax_q + blk);
+        const float s2 = p.w.qc.dq_scale[blk >> 8];
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        sC[rr * pitch + 16 * cb + e] = __builtin_fmaf(e4m3_decode((q8[e >> 2] >> (8 * (e & 3))) & 0xFFu), s2, mean);
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(e4m3_decode((q8 >> (8 * e)) & 0xFFu), s2, mean);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = p.w.qc.absmax[blk + e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sC[rr * pitch + c + e] = v[e];
     }
   } else {
     for (int i = threadIdx.x; i < 16 * RG * nb; i += 64 * W) {
@@ -393,24 +379,20 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
                                : p.w.qc.absmax[blk];
     }
   }
-  if (wave < steps.total) dc_step<RG, TERMS>(steps, wave, n0, N, step);
-  if constexpr (!TK) {
-    // t: its parts added (in order), tokens without an adapter and the columns past a rank 0
+  if (wave < nsteps) dc_step<RG, TERMS>(p.records[wave], n0, N, step);
+  {
+    // t: its parts added in order (rows of tokens without an adapter hold
+    // anything: no step takes them)
     const int nt = p.M * p.v.rs;
     for (int i0 = 0; i0 < nt; i0 += 64 * W) {
-      const int i = min(i0 + (int)threadIdx.x, nt - 1), m = i / p.v.rs;
-      float part[8];
+      const int i = min(i0 + (int)threadIdx.x, nt - 1);
+      float part[DC_PARTS];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) part[k] = p.t[(int64_t)min(k, p.parts - 1) * nt + i];
+      for (int k = 0; k < DC_PARTS; ++k) part[k] = p.t[(int64_t)min(k, p.parts - 1) * nt + i];
       float sum = part[0];
 #pragma unroll
-      for (int k = 1; k < 8; ++k) sum += k < p.parts ? part[k] : 0.0f;
-      if (__shfl(key, m) < 0) sum = 0.0f;
-      if (i0 + (int)threadIdx.x < nt) {
-        sT[i] = sum;
-        const int j = i - m * p.v.rs;
-        if (blockIdx.x == 0 && p.t_out && j < p.v.r_max) p.t_out[m * p.v.r_max + j] = sum;
-      }
+      for (int k = 1; k < DC_PARTS; ++k) sum += k < p.parts ? part[k] : 0.0f;
+      if (i0 + (int)threadIdx.x < nt) sT[i] = sum;
     }
   }
   __syncthreads();
@@ -420,17 +402,16 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
   for (int g = 0; g < RG; ++g)
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) acc[g][tt] = zero4();
-  f32x4_t tacc[AT];
-#pragma unroll
-  for (int j = 0; j < AT; ++j) tacc[j] = zero4();
-  auto lora = [&]() {
-    for (int k = wave; k < steps.total; k += W) {
-      const DcStep<RG> cur = step;
-      if (k + W < steps.total) dc_step<RG, TERMS>(steps, k + W, n0, N, step);   // the next one's loads
-      dc_apply<RG, TT>(cur, sT, tstride, p.M, acc);
+  for (int k = wave; k < nsteps; k += W) {
+    const DcStep<RG> cur = step;
+    if (k + W < nsteps) dc_step<RG, TERMS>(p.records[k + W], n0, N, step);   // the next one's loads
+    dc_apply<RG, TT>(cur, sT, p.v.rs, p.M, acc);
+  }
+  if (p.t_out)   // workgroup b: tokens b, b + the grid, ...
+    for (int m = blockIdx.x; m < p.M; m += gridDim.x) {
+      const bool has = (uint32_t)p.ids[m] < (uint32_t)p.v.n;
+      for (int j = threadIdx.x; j < p.v.r_max; j += 64 * W) p.t_out[m * p.v.r_max + j] = has ? sT[m * p.v.rs + j] : 0.0f;
     }
-  };
-  if constexpr (!TK) lora();
 
   const uint32_t slot = 8 * (lane & 31);
   constexpr int GB = RG < 2 ? RG : 2;   // row groups per batch of lookups
@@ -438,11 +419,11 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       if (s + half * W >= ns) break;
-      DcStage<RG, XT, AT>& st = half ? s1 : s0;
+      DcStage<RG>& st = half ? s1 : s0;
       u32x4_t x[TT][4];
       if constexpr (XA) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[0][u] = st.x[0][u];
+        for (int u = 0; u < 4; ++u) x[0][u] = st.x[u];
       } else {
         const u32x4_t* xs = p.xp + (int64_t)(s + half * W) * (TT * 256) + lane;
 #pragma unroll
@@ -450,29 +431,14 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
 #pragma unroll
           for (int tt = 0; tt < TT; ++tt) x[tt][u] = xs[(tt * 4 + u) * 64];
       }
-      // K / 64 odd: the last stage's second block lies past the row and adds
-      // zeros (its X too: 0 times an infinity is not 0; XPack holds zeros there)
-      if ((nb & 1) && s + half * W == ns - 1) {
-        if constexpr (XA)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (lg >= 2) x[0][u] = u32x4_t{0u, 0u, 0u, 0u};
-            if constexpr (TK)
-#pragma unroll
-              for (int j = 0; j < AT; ++j)
-                if (lg >= 2) st.a[j][u] = u32x4_t{0u, 0u, 0u, 0u};
-          }
-      }
+      // (K / 64 odd: the last stage's second block lies past the row, where
+      // XPack holds zeros)
       float cp[RG];
 #pragma unroll
       for (int g = 0; g < RG; ++g) cp[g] = sC[(16 * g + li) * pitch + st.bl];
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if constexpr (TK)
-#pragma unroll
-          for (int j = 0; j < AT; ++j)   // tokens as rows, rows of A as columns
-            tacc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[0][u]), as_bf16x8(st.a[j][u]), tacc[j], 0, 0, 0);
 #pragma unroll
         for (int g0 = 0; g0 < RG; g0 += GB) {
           f32x2_t q[GB][4];
@@ -498,37 +464,8 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
         }
       }
       load(s + (2 + half) * W, st);
-      if constexpr (TK) load_a(st);
     }
   }
-  if constexpr (TK) {
-    // t: the waves' sums in order, an adapter's columns at its tokens' rows, from column 0
-#pragma unroll
-    for (int j = 0; j < AT; ++j) sP[(j * W + wave) * 64 + lane] = tacc[j];
-    __syncthreads();
-    for (int i0 = 0; i0 < p.M * DC_TR; i0 += 64 * W) {
-      const int i = min(i0 + (int)threadIdx.x, p.M * DC_TR - 1), m = i / DC_TR, j = i % DC_TR;
-      const int mk = __shfl(key, m);
-      float sum = 0.0f;
-      uint64_t left = __ballot(steps.count > 0);
-      for (int jt = 0; left; left &= left - 1) {
-        const int l = first_bit(left);
-        const int r = read_lane(steps.ad.r, l);
-        if (mk == read_lane(key, l) && j < r) {
-#pragma unroll
-          for (int w = 0; w < W; ++w) sum += sP[((jt + (j >> 4)) * W + w) * 64 + 16 * (m >> 2) + (j & 15)][m & 3];
-        }
-        jt += (r + 15) >> 4;
-      }
-      if (i0 + (int)threadIdx.x < p.M * DC_TR) {
-        sT[i] = sum;
-        if (blockIdx.x == 0 && p.t_out && j < p.v.r_max) p.t_out[m * p.v.r_max + j] = sum;
-      }
-    }
-    __syncthreads();
-    lora();
-  }
-
   // the waves' sums, one token tile at a time, over the constants' space. A lane
   // holds token li, rows 4 lg + [0, 4) of each row group; lane l of a group lies
   // at 16-byte slot l + l / 16 of 68, so that the readers (consecutive threads:
@@ -571,15 +508,15 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
   }
 }
 
-template <int RG, int TT, int W, int TK>
+template <int RG, int TT, int W>
 hipError_t launch_rg(const DecodeParams& p, bool f32, hipStream_t s) {
   const dim3 grid((unsigned)((p.w.N + 16 * RG - 1) / (16 * RG))), block(64 * W);
-  const size_t lds = dc_lds_bytes(RG, TT, W, (int)(p.w.K / 64), p.v.rs, TK > 0);
+  const size_t lds = dc_lds_bytes(RG, TT, W, (int)(p.w.K / 64), p.v.rs);
   const bool dq = p.w.qc.absmax == nullptr;
-  if (dq && f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, true, TK>), grid, block, lds, s, p);
-  else if (dq) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, false, TK>), grid, block, lds, s, p);
-  else if (f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, true, TK>), grid, block, lds, s, p);
-  else hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, false, TK>), grid, block, lds, s, p);
+  if (dq && f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, true>), grid, block, lds, s, p);
+  else if (dq) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, false>), grid, block, lds, s, p);
+  else if (f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, true>), grid, block, lds, s, p);
+  else hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, false>), grid, block, lds, s, p);
   return hipGetLastError();
 }
 
@@ -589,12 +526,12 @@ constexpr size_t kLdsBytes = 160 * 1024;
 // Row groups per workgroup, one workgroup per CU (the pair table takes 64 KB
 // of LDS): the shortest queue of the longest CU, a workgroup costing its row
 // groups and about two more for its start and its X.
-int decode_rg(int64_t N, int64_t K, int tt, int rs, bool tk) {
+int decode_rg(int64_t N, int64_t K, int tt, int rs) {
   const int64_t groups = (N + 15) / 16;
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int rg = 1; rg <= 4; rg *= 2) {
-    if (dc_lds_bytes(rg, tt, rg == 1 && tt == 1 && !tk ? 16 : 8, (int)(K / 64), rs, tk) > kLdsBytes) break;
+    if (dc_lds_bytes(rg, tt, 8, (int)(K / 64), rs) > kLdsBytes) break;
     const int64_t sets = (groups + rg - 1) / rg, c = (sets + kCus - 1) / kCus * (rg + 2);
     if (c <= cost) {
       cost = c;
@@ -611,68 +548,56 @@ int decode_rg(int64_t N, int64_t K, int tt, int rs, bool tk) {
 bool adapter_decode_supported(const QWeight& w, int64_t M) {
   return w.format == LQ_FMT_NF4 && M <= 64 && w.K <= 49152;
 }
-static bool adapter_decode_forms_t(int64_t M, const AdapterView& v) {
-  return M <= 16 && std::min<int64_t>(M, v.n) * ((v.r_max + 15) / 16 * 16) <= DC_TR;
-}
-
-// Token tiles of the projection, and the workspace: t's parts, and X in
-// fragment order for more than one tile.
+// Token tiles of the projection, and the workspace: t's parts, the steps, and
+// X in fragment order.
 static int token_tiles(int64_t M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
 static int adapter_decode_parts(const QWeight& w, int64_t M, const AdapterView& v);
 static size_t t_bytes(const QWeight& w, int64_t M, const AdapterView& v) {
   return ((size_t)adapter_decode_parts(w, M, v) * M * v.rs * sizeof(float) + 255) / 256 * 256;
 }
 size_t adapter_decode_ws_bytes(const QWeight& w, int64_t M, const AdapterView& v) {
-  const int tt = token_tiles(M);
-  return t_bytes(w, M, v) + (tt > 1 ? (size_t)((w.K + 127) / 128) * tt * 256 * 16 : 0);
+  return t_bytes(w, M, v) + DC_RECORDS * sizeof(DcRecord) + (size_t)((w.K + 127) / 128) * token_tiles(M) * 256 * 16;
 }
 
 // Column parts of t: with few adapters the columns are shared by several
 // workgroups, at least eight 64-column blocks each.
 static int adapter_decode_parts(const QWeight& w, int64_t M, const AdapterView& v) {
-  if (adapter_decode_forms_t(M, v)) return 1;
   const int64_t wgs = std::min<int64_t>(M, v.n);
   int parts = 1;
-  while (parts < 8 && wgs * parts * 2 <= kCus && w.K / 64 / (parts * 2) >= 8) parts *= 2;
+  while (parts < DC_PARTS && wgs * parts * 2 <= kCus && w.K / 64 / (parts * 2) >= 8) parts *= 2;
   return parts;
 }
 
 hipError_t launch_adapter_decode(const QWeight& w, const uint16_t* X, int64_t M, const int32_t* ids,
                                  const AdapterView& v, void* ws, float* t_save, void* H, bool f32, hipStream_t s) {
   if (!adapter_decode_supported(w, M)) return hipErrorInvalidValue;
-  const bool tk = adapter_decode_forms_t(M, v);
   const int parts = adapter_decode_parts(w, M, v), tt = token_tiles(M);
   float* t_ws = reinterpret_cast<float*>(ws);
-  u32x4_t* xp = reinterpret_cast<u32x4_t*>(reinterpret_cast<char*>(ws) + t_bytes(w, M, v));
-  DecodeParams p{X, xp, (int)M, ids, v, tk ? nullptr : t_ws, parts, t_save, H, w, tables().lv};
-  if (!tk) {
-    const int wgs = (int)std::min<int64_t>(M, v.n);
-    const dim3 grid((unsigned)(wgs + (tt > 1 ? std::max(1, 64 / parts) : 0)), (unsigned)parts);
-    const int jt = (v.r_max + 15) / 16;
-#define LQ_DD(JT, W) hipLaunchKernelGGL((k_decode_down<JT, W>), grid, dim3(64 * W), 0, s, X, (int)M, w.K, v, ids, t_ws, xp, tt, wgs)
-    if (jt <= 1) LQ_DD(1, 16);
-    else if (jt <= 2) LQ_DD(2, 16);
-    else if (jt <= 4) LQ_DD(4, 8);
-    else LQ_DD(8, 8);
+  DcRecord* records = reinterpret_cast<DcRecord*>(reinterpret_cast<char*>(ws) + t_bytes(w, M, v));
+  u32x4_t* xp = reinterpret_cast<u32x4_t*>(records + DC_RECORDS);
+  const int wgs = (int)std::min<int64_t>(M, v.n);
+  const dim3 grid((unsigned)(wgs + 1 + std::max(1, 16 * tt / parts)), (unsigned)parts);
+  const int jt = (v.r_max + 15) / 16;
+#define LQ_DD(JT, W)                                                                                                 \
+  hipLaunchKernelGGL((k_decode_down<JT, W>), grid, dim3(64 * W), 0, s, X, (int)M, w.K, v, ids, t_ws, xp, tt, wgs, records, \
+                     f32 ? 3 : 2)
+  if (jt <= 1) LQ_DD(1, 16);
+  else if (jt <= 2) LQ_DD(2, 16);
+  else if (jt <= 4) LQ_DD(4, 8);
+  else LQ_DD(8, 8);
 #undef LQ_DD
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  const int rg = decode_rg(w.N, w.K, tt, v.rs, tk);
-  if (tk) {
-    const bool one = std::min<int64_t>(M, v.n) * ((v.r_max + 15) / 16) == 1;
-    if (rg == 4) return one ? launch_rg<4, 1, 8, 1>(p, f32, s) : launch_rg<4, 1, 8, 2>(p, f32, s);
-    if (rg == 2) return one ? launch_rg<2, 1, 8, 1>(p, f32, s) : launch_rg<2, 1, 8, 2>(p, f32, s);
-    return one ? launch_rg<1, 1, 8, 1>(p, f32, s) : launch_rg<1, 1, 8, 2>(p, f32, s);
-  }
-#define LQ_RG(TT)                                              \
-  do {                                                         \
-    if (rg == 4) return launch_rg<4, TT, 8, 0>(p, f32, s); \
-    if (rg == 2) return launch_rg<2, TT, 8, 0>(p, f32, s); \
-    return launch_rg<1, TT, TT == 1 ? 16 : 8, 0>(p, f32, s); \
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const DecodeParams p{xp, records, (int)M, ids, v, t_ws, parts, t_save, H, w, tables().lv};
+  const int rg = decode_rg(w.N, w.K, tt, v.rs);
+#define LQ_RG(TT)                                    \
+  do {                                               \
+    if (rg == 4) return launch_rg<4, TT, 8>(p, f32, s); \
+    if (rg == 2) return launch_rg<2, TT, 8>(p, f32, s); \
+    return launch_rg<1, TT, 8>(p, f32, s);           \
   } while (0)
-  if (M <= 16) LQ_RG(1);
-  if (M <= 32) LQ_RG(2);
+  if (tt == 1) LQ_RG(1);
+  if (tt == 2) LQ_RG(2);
   LQ_RG(4);
 #undef LQ_RG
 }

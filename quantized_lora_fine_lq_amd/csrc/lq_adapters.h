@@ -96,8 +96,8 @@ hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s);
 // [N, K] -> [K, ldb] bf16 (zero columns from N to ldb)
 hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out, hipStream_t s);
 
-// Decode sizes (NF4, M <= 64): the whole forward without a route, in one or
-// two launches.
+// Decode sizes (NF4, M <= 64): the whole forward without a route, in two
+// launches.
 bool adapter_decode_supported(const QWeight& w, int64_t M);
 size_t adapter_decode_ws_bytes(const QWeight& w, int64_t M, const AdapterView& v);
 hipError_t launch_adapter_decode(const QWeight& w, const uint16_t* X, int64_t M, const int32_t* ids,
