@@ -67,10 +67,12 @@ __device__ __forceinline__ DcSteps dc_steps(const lq_adapter& ad, int key, int t
 struct DcRecord {
   uint64_t B, same;    // B_a, its tokens
   float scale;
-  int32_t r, run0;     // first of the step's 4 runs
+  int32_t r;
+  uint32_t runs;       // byte q, run q of the step: rank / 8, term << 4, 64 where it is one of the adapter's
   int32_t total;       // steps in all (every record)
 };
-constexpr int DC_RECORDS = 64 * 12;
+constexpr int DC_PAD = 64;                        // no token's steps past the last: the projection asks for them too
+constexpr int DC_RECORDS = 64 * 12 + DC_PAD;
 
 // ===========================================================================
 // t = A_a x: one workgroup per adapter in use (workgroup b takes the b-th in
@@ -95,10 +97,19 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(const uint16_t* __restri
     if (blockIdx.y || threadIdx.x >= 64) return;
     const int key = lane_key(ids, M, v.n);
     const DcSteps st = dc_steps(v.tab[max(key, 0)], key, terms);
-    for (int k = 0; k < st.count; ++k)
-      records[st.first + k] = DcRecord{(uint64_t)reinterpret_cast<uintptr_t>(st.ad.B), st.same, st.ad.scale, st.ad.r, 4 * k,
+    const int runs = (st.ad.r + 7) >> 3;
+    for (int k = 0, term = 0, run = 0; k < st.count; ++k) {
+      uint32_t packed = 0;
+      for (int q = 0; q < 4; ++q) {
+        if (term < terms) packed |= (uint32_t)(run | term << 4 | 64) << (8 * q);
+        if (++run == runs) run = 0, ++term;
+      }
+      records[st.first + k] = DcRecord{(uint64_t)reinterpret_cast<uintptr_t>(st.ad.B), st.same, st.ad.scale, st.ad.r, packed,
                                        st.total};
-    if (st.total == 0 && threadIdx.x == 0) records[0].total = 0;
+    }
+    const lq_adapter any = v.tab[0];
+    if (threadIdx.x < DC_PAD)
+      records[st.total + threadIdx.x] = DcRecord{(uint64_t)reinterpret_cast<uintptr_t>(any.B), 0, 0.0f, any.r, 0, st.total};
     return;
   }
   if ((int)blockIdx.x > wgs) {
@@ -199,10 +210,20 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(const uint16_t* __restri
 // li, decodes them into the A operand of four MFMA 16x16x32, and multiplies TT
 // tiles of 16 tokens; X comes from the L2.
 //
-// A code byte becomes two levels through an LDS table of level pairs, held
-// once per bank pair: entry e of slot s at 8 (32 e + s), and lane l reads slot
-// l % 32, so no two lanes of a half wave ever meet in a bank. With one copy
-// (2 KB) two thirds of the lookups' cycles were bank conflicts.
+// A code byte becomes two levels through an LDS table of level pairs in 16
+// copies: entry e of copy s at 8 (16 e + s), and lane l reads copy l % 16. With
+// one copy (2 KB) two thirds of the lookups' cycles were bank conflicts; with
+// 32 none were, but the table (64 KB) left room for one workgroup per CU, which
+// then started, waited and finished with nothing beside it.
+//
+// Four row groups run in workgroups of four waves, two of them per CU, fewer in
+// workgroups of eight. Measured, 64 tokens, N = 28672, K = 8192, 32 adapters of
+// rank 8 to 32: 71 us, that is 1.7 TB/s of codes, the launch before it 13. A
+// workgroup's 60 us are 9 of start, 10 of the adapters' part (B is read from
+// memory, 34 MB in all) and 38 of the stages, whose lookups and products wait
+// for one another at two waves a SIMD: 64 tokens' sums and X take 128 registers.
+// 16 tokens, N = K = 4096: 7.9 us after 5.6; one token: 7.5 after 4.4 (forming
+// t in the projection instead took 14.0 in all).
 // ===========================================================================
 struct DecodeParams {
   const u32x4_t* xp;   // X in fragment order
@@ -218,8 +239,10 @@ struct DecodeParams {
   Nf4Levels lv;
 };
 
-constexpr int DC_PAIRS = 256 * 32;   // f32x2_t, 64 KB
+constexpr int DC_PAIRS = 256 * 16;   // f32x2_t, 32 KB
 constexpr int DC_PARTS = 8;           // most column parts of t
+
+constexpr int kXcds = 8;
 
 template <int RG>
 struct DcStage {
@@ -228,13 +251,6 @@ struct DcStage {
   int bl;         // the lane's 64-block (the last one where that lies past the row)
 };
 
-__device__ __forceinline__ float term_of(float v, int t) {
-  const float hi = bf16lo_to_f32(pack_bf16x2(v, 0.0f));
-  if (t == 0) return hi;
-  const float mid = bf16lo_to_f32(pack_bf16x2(v - hi, 0.0f));
-  return t == 1 ? mid : v - hi - mid;
-}
-
 // floats of LDS after the pair table: constants, then the partial sums of one
 // token tile
 template <int RG, int W>
@@ -242,10 +258,17 @@ __host__ __device__ constexpr int dc_floats(int nb) {
   const int c = (16 * RG * (nb + 1) + 3) / 4 * 4, red = W * RG * 272;
   return c > red ? c : red;
 }
-size_t dc_lds_bytes(int rg, int tt, int w, int nb, int rs) {
+size_t dc_lds_bytes(int rg, int tt, int w, int nb, int rs, int terms) {
   const int c = (16 * rg * (nb + 1) + 3) / 4 * 4, red = w * rg * 272;
   return DC_PAIRS * sizeof(f32x2_t) +
-         4 * (size_t)((c > red ? c : red) + 16 * tt * rs);
+         4 * (size_t)(c > red ? c : red) + 2 * (size_t)(16 * tt * rs * terms);
+}
+
+__device__ __forceinline__ DcRecord of_lane(const DcRecord& x, int l) {
+  auto u = [&](uint32_t w) { return (uint32_t)__builtin_amdgcn_readlane((int)w, l); };
+  return DcRecord{u((uint32_t)x.B) | (uint64_t)u((uint32_t)(x.B >> 32)) << 32,
+                  u((uint32_t)x.same) | (uint64_t)u((uint32_t)(x.same >> 32)) << 32,
+                  __uint_as_float(u(__float_as_uint(x.scale))), (int)u((uint32_t)x.r), u(x.runs), (int)u((uint32_t)x.total)};
 }
 
 // A step as every lane needs it, with the weight-side operand loaded.
@@ -257,20 +280,19 @@ struct DcStep {
   int term, j0;
   bool live;
 };
-template <int RG, int TERMS>
-__device__ __forceinline__ void dc_step(const DcRecord& rec, int64_t n0, int64_t N, DcStep<RG>& o) {
-  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+template <int RG>
+__device__ __forceinline__ void dc_step(const DcRecord& rec, const int64_t (&row)[RG], DcStep<RG>& o) {
   const uint16_t* B = reinterpret_cast<const uint16_t*>(rec.B);
-  const int r = rec.r, runs = (r + 7) >> 3;
-  const int run = rec.run0 + lg;
+  const int r = rec.r;
+  const uint32_t run = rec.runs >> (threadIdx.x >> 1 & 24);   // the lane's: byte lane / 16
   o.scale = rec.scale;
   o.same = rec.same;
-  o.live = run < TERMS * runs;
-  o.term = o.live ? run / runs : 0;
-  o.j0 = o.live ? 8 * (run - o.term * runs) : 0;
+  o.live = run & 64;
+  o.term = (run >> 4) & 3;
+  o.j0 = 8 * (run & 15);
 #pragma unroll
   for (int g = 0; g < RG; ++g) {
-    const uint16_t* b = B + min(n0 + 16 * g + li, N - 1) * r;
+    const uint16_t* b = B + row[g] * r;
     if (r % 8 == 0) {
       o.w[g] = ld16(b + o.j0);
     } else {
@@ -281,38 +303,32 @@ __device__ __forceinline__ void dc_step(const DcRecord& rec, int64_t n0, int64_t
         o.w[g][e] = (j < r ? x : 0u) | ((j + 1 < r ? y : 0u) << 16);
       }
     }
+    if (!o.live) o.w[g] = u32x4_t{0u, 0u, 0u, 0u};
   }
 }
 // Adds step o: each product goes to its own tokens' columns alone.
-template <int RG, int TT>
-__device__ __forceinline__ void dc_apply(const DcStep<RG>& o, const float* sT, int tstride, int M, f32x4_t (&acc)[RG][TT]) {
+template <int RG, int TT, int TERMS>
+__device__ __forceinline__ void dc_apply(const DcStep<RG>& o, const uint16_t* sT, int rs, int M, f32x4_t (&acc)[RG][TT]) {
   const int lane = threadIdx.x & 63, li = lane & 15;
+  const u32x4_t none = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int tt = 0; tt < TT; ++tt) {
     if (!((o.same >> (16 * tt)) & 0xFFFF)) continue;
     const int m = 16 * tt + li;
     const bool mine = (o.same >> m) & 1;
-    const float* tr = sT + min(m, M - 1) * tstride + o.j0;
-    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(tr), y = *reinterpret_cast<const f32x4_t*>(tr + 4);
-    u32x4_t tv;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      tv[e] = pack_bf16x2(term_of(o.scale * x[2 * e], o.term), term_of(o.scale * x[2 * e + 1], o.term));
-      tv[2 + e] = pack_bf16x2(term_of(o.scale * y[2 * e], o.term), term_of(o.scale * y[2 * e + 1], o.term));
-    }
-    const u32x4_t none = {0u, 0u, 0u, 0u};
+    u32x4_t tv = *reinterpret_cast<const u32x4_t*>(sT + (min(m, M - 1) * TERMS + o.term) * rs + o.j0);
     if (!o.live) tv = none;
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
-      const f32x4_t d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(o.live ? o.w[g] : none), as_bf16x8(tv), zero4(), 0, 0, 0);
+      const f32x4_t d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(o.w[g]), as_bf16x8(tv), zero4(), 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[g][tt][e] += mine ? d[e] : 0.0f;
+      for (int e = 0; e < 4; ++e) acc[g][tt][e] = __builtin_fmaf(o.scale, mine ? d[e] : 0.0f, acc[g][tt][e]);
     }
   }
 }
 
 template <int RG, int TT, int W, bool DQ, bool OUT_F32>
-__global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) void k_decode_nf4(DecodeParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dc_lds[];
   constexpr int TERMS = OUT_F32 ? 3 : 2;
   constexpr bool XA = TT == 1;   // X is loaded a stage ahead, with the codes
@@ -323,13 +339,21 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
   const int64_t N = p.w.N, K = p.w.K;
   const int64_t n0 = (int64_t)blockIdx.x * 16 * RG;
   const int nb = (int)(K / 64), pitch = nb + 1, ns = (nb + 1) / 2;
-  float* sT = sC + dc_floats<RG, W>(nb);   // t [M][rs]
+  uint16_t* sT = reinterpret_cast<uint16_t*>(sC + dc_floats<RG, W>(nb));   // t's bf16 terms [M][TERMS][rs]
 
   const uint8_t* crow[RG];
 #pragma unroll
   for (int g = 0; g < RG; ++g) crow[g] = p.w.codes + min(n0 + 16 * g + li, N - 1) * (K / 2) + 16 * (lg & 1);
+  // The stages in an order rotated by workgroup: rows lie a power of two apart in
+  // the common sizes, so workgroups in step would all read from the same few
+  // channels of the L2.
+  const int rot = (int)((blockIdx.x / kXcds * 4) % ns);
+  auto place = [&](int s) {
+    const int at = min(s, ns - 1) + rot;
+    return at < ns ? at : at - ns;
+  };
   auto load = [&](int s, DcStage<RG>& st) {
-    const int ss = min(s, ns - 1);
+    const int ss = place(s);
     st.bl = min(2 * ss + (lg >> 1), nb - 1);
 #pragma unroll
     for (int g = 0; g < RG; ++g) st.code[g] = ld16(crow[g] + (int64_t)st.bl * 32);
@@ -337,25 +361,53 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) st.x[u] = p.xp[((int64_t)ss * 4 + u) * 64 + lane];
   };
+  // Several token tiles: each sub-step's X is refilled for the wave's next stage
+  // as soon as it is used. Loads return in order, so X asked for when needed
+  // would wait for the codes asked for before it, from memory.
+  u32x4_t x[TT][4];
+  auto load_x = [&](int s, int u) {
+    const u32x4_t* xs = p.xp + (int64_t)place(s) * (TT * 256) + lane;
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) x[tt][u] = xs[(tt * 4 + u) * 64];
+  };
+  // Everything that the start waits for is asked for before any of it is used:
+  // the first codes, and B of the wave's first DEEP steps (a step is a round
+  // trip to memory).
+  constexpr int DEEP = RG == 4 ? 4 : 1;   // (few row groups: 16 tokens' steps are one or two a wave)
+  static_assert(W * 2 * DEEP <= DC_PAD, "the steps asked for end within the padding");
+  int64_t row[RG];
+#pragma unroll
+  for (int g = 0; g < RG; ++g) row[g] = min(n0 + 16 * g + li, N - 1);
+  DcStep<RG> steps[DEEP];
   DcStage<RG> s0, s1;
   load(wave, s0);
-  load(wave + W, s1);
+  if constexpr (XA) load(wave + W, s1);
+  // Lane l keeps the record of the wave's step 64 c + l.
+  DcRecord rec;
+  auto load_records = [&](int i) {
+    const u32x4_t* at = reinterpret_cast<const u32x4_t*>(p.records + min(wave + W * (i + lane), DC_RECORDS - 1));
+    const u32x4_t a = at[0], b = at[1];
+    rec = DcRecord{a[0] | (uint64_t)a[1] << 32, a[2] | (uint64_t)a[3] << 32, __uint_as_float(b[0]), (int)b[1], b[2], (int)b[3]};
+  };
+  auto ask = [&](int i, DcStep<RG>& o) { dc_step<RG>(of_lane(rec, i & 63), row, o); };
+  load_records(0);
+#pragma unroll
+  for (int d = 0; d < DEEP; ++d) ask(d, steps[d]);
+  const int nsteps = of_lane(rec, 0).total;
 
   // The pair table: lane l of a wave writes slot l % 32 of entries e + l / 32
+  const float level = p.lv.q[lane & 15], second = __shfl(level, 4 * (wave & 3) + (lane >> 4));
 #pragma unroll
-  for (int k = 0; k < 128 / W; ++k) {
-    const int e = 2 * (wave + W * k);   // even: e and e + 1 share their first level
-    const float first = p.lv.q[e >> 4], lo = p.lv.q[e & 15], hi = p.lv.q[(e & 15) + 1];
-    sPair[32 * e + lane] = f32x2_t{first, lane < 32 ? lo : hi};
+  for (int k = 0; k < 64 / W; ++k) {
+    const int e = 4 * (wave + W * k);   // e .. e + 3: one first level
+    sPair[16 * e + lane] = f32x2_t{__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(level), e >> 4)), second};
   }
-  const int nsteps = p.records[0].total;
-  DcStep<RG> step;
   const float mean = DQ ? *p.w.qc.dq_mean : 0.0f;
   // the rows' constants, four a thread: thread t row t % (16 RG)
   if (nb % 4 == 0) {
     const int rr = threadIdx.x % (16 * RG);
     const int64_t b0 = min(n0 + rr, N - 1) * nb;
-#pragma unroll 2
+#pragma unroll 4
     for (int c = 4 * (threadIdx.x / (16 * RG)); c < nb; c += 4 * (64 * W / (16 * RG))) {
       const int64_t blk = b0 + c;   // a multiple of 4: one second-level scale
       f32x4_t v;
@@ -379,20 +431,40 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
                                : p.w.qc.absmax[blk];
     }
   }
-  if (wave < nsteps) dc_step<RG, TERMS>(p.records[wave], n0, N, step);
   {
-    // t: its parts added in order (rows of tokens without an adapter hold
-    // anything: no step takes them)
-    const int nt = p.M * p.v.rs;
-    for (int i0 = 0; i0 < nt; i0 += 64 * W) {
-      const int i = min(i0 + (int)threadIdx.x, nt - 1);
-      float part[DC_PARTS];
+    // t: its parts added in order, and split into bf16 terms whose sum is t to
+    // 16 bits more than H keeps (rows of tokens without an adapter hold
+    // anything: no step takes them). Token m's t is saved by workgroup m % grid.
+    const int quads = p.v.rs / 4, nq = p.M * quads, nt = p.M * p.v.rs;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < nq; i += 64 * W) {
+      f32x4_t part[DC_PARTS];
 #pragma unroll
-      for (int k = 0; k < DC_PARTS; ++k) part[k] = p.t[(int64_t)min(k, p.parts - 1) * nt + i];
-      float sum = part[0];
+      for (int k = 0; k < DC_PARTS; ++k)
+        part[k] = *reinterpret_cast<const f32x4_t*>(p.t + (int64_t)min(k, p.parts - 1) * nt + 4 * i);
+      f32x4_t sum = part[0];
 #pragma unroll
-      for (int k = 1; k < DC_PARTS; ++k) sum += k < p.parts ? part[k] : 0.0f;
-      if (i0 + (int)threadIdx.x < nt) sT[i] = sum;
+      for (int k = 1; k < DC_PARTS; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += k < p.parts ? part[k][e] : 0.0f;
+      const int m = (uint32_t)i / (uint32_t)quads, j = 4 * (i - m * quads);
+      if (p.t_out && m % gridDim.x == blockIdx.x) {
+        const bool has = (uint32_t)p.ids[m] < (uint32_t)p.v.n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < p.v.r_max) p.t_out[m * p.v.r_max + j + e] = has ? sum[e] : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < TERMS; ++q) {
+        uint2 bits;
+        bits.x = pack_bf16x2(sum[0], sum[1]);
+        bits.y = pack_bf16x2(sum[2], sum[3]);
+        *reinterpret_cast<uint2*>(sT + (m * TERMS + q) * p.v.rs + j) = bits;
+        sum[0] -= bf16lo_to_f32(bits.x);
+        sum[1] -= bf16hi_to_f32(bits.x);
+        sum[2] -= bf16lo_to_f32(bits.y);
+        sum[3] -= bf16hi_to_f32(bits.y);
+      }
     }
   }
   __syncthreads();
@@ -402,70 +474,69 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
   for (int g = 0; g < RG; ++g)
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) acc[g][tt] = zero4();
-  for (int k = wave; k < nsteps; k += W) {
-    const DcStep<RG> cur = step;
-    if (k + W < nsteps) dc_step<RG, TERMS>(p.records[k + W], n0, N, step);   // the next one's loads
-    dc_apply<RG, TT>(cur, sT, p.v.rs, p.M, acc);
-  }
-  if (p.t_out)   // workgroup b: tokens b, b + the grid, ...
-    for (int m = blockIdx.x; m < p.M; m += gridDim.x) {
-      const bool has = (uint32_t)p.ids[m] < (uint32_t)p.v.n;
-      for (int j = threadIdx.x; j < p.v.r_max; j += 64 * W) p.t_out[m * p.v.r_max + j] = has ? sT[m * p.v.rs + j] : 0.0f;
+  for (int i = 0; wave + W * i < nsteps; i += DEEP) {
+    if (((i + DEEP) & 63) == 0) load_records(i + DEEP);
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+      dc_apply<RG, TT, TERMS>(steps[d], sT, p.v.rs, p.M, acc);
+      ask(i + DEEP + d, steps[d]);
     }
-
-  const uint32_t slot = 8 * (lane & 31);
+  }
+  if constexpr (!XA) {   // in the loop's order
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_x(wave, u);
+    load(wave + W, s1);
+  }
+  const uint32_t slot = 8 * (lane & 15);
   constexpr int GB = RG < 2 ? RG : 2;   // row groups per batch of lookups
-  for (int s = wave; s < ns; s += 2 * W) {
+  auto stage = [&](int s, DcStage<RG>& st) {
+    if constexpr (XA)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (s + half * W >= ns) break;
-      DcStage<RG>& st = half ? s1 : s0;
-      u32x4_t x[TT][4];
-      if constexpr (XA) {
+      for (int u = 0; u < 4; ++u) x[0][u] = st.x[u];
+    // (K / 64 odd: the last stage's second block lies past the row, where
+    // XPack holds zeros)
+    float cp[RG];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[0][u] = st.x[u];
-      } else {
-        const u32x4_t* xs = p.xp + (int64_t)(s + half * W) * (TT * 256) + lane;
+    for (int g = 0; g < RG; ++g) cp[g] = sC[(16 * g + li) * pitch + st.bl];
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u) {
 #pragma unroll
-          for (int tt = 0; tt < TT; ++tt) x[tt][u] = xs[(tt * 4 + u) * 64];
-      }
-      // (K / 64 odd: the last stage's second block lies past the row, where
-      // XPack holds zeros)
-      float cp[RG];
+      for (int g0 = 0; g0 < RG; g0 += GB) {
+        f32x2_t q[GB][4];
 #pragma unroll
-      for (int g = 0; g < RG; ++g) cp[g] = sC[(16 * g + li) * pitch + st.bl];
-      __builtin_amdgcn_sched_barrier(0);
+        for (int g = 0; g < GB; ++g)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-#pragma unroll
-        for (int g0 = 0; g0 < RG; g0 += GB) {
-          f32x2_t q[GB][4];
-#pragma unroll
-          for (int g = 0; g < GB; ++g)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              // address: byte 0 the slot, byte 1 the code byte
-              const uint32_t at = __builtin_amdgcn_perm(st.code[g0 + g][u], slot, 0x0C0C0400u + (b << 8));
-              q[g][b] = *reinterpret_cast<const f32x2_t*>(dc_lds + at);
-            }
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int g = 0; g < GB; ++g) {
-            u32x4_t wv;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) wv[b] = pack_bf16x2(q[g][b].x * cp[g0 + g], q[g][b].y * cp[g0 + g]);
-#pragma unroll
-            for (int tt = 0; tt < TT; ++tt)
-              acc[g0 + g][tt] =
-                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wv), as_bf16x8(x[tt][u]), acc[g0 + g][tt], 0, 0, 0);
+          for (int b = 0; b < 4; ++b) {
+            // (the table lies at LDS address 0: the kernel has no other static LDS)
+            const uint32_t c = st.code[g0 + g][u];
+            const uint32_t at = ((b ? c >> (8 * b - 7) : c << 7) & 0x7F80u) | slot;
+            q[g][b] = *reinterpret_cast<const __attribute__((address_space(3))) f32x2_t*>(at);
           }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int g = 0; g < GB; ++g) {
+          u32x4_t wv;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) wv[b] = pack_bf16x2(q[g][b].x * cp[g0 + g], q[g][b].y * cp[g0 + g]);
+#pragma unroll
+          for (int tt = 0; tt < TT; ++tt)
+            acc[g0 + g][tt] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wv), as_bf16x8(x[tt][u]), acc[g0 + g][tt], 0, 0, 0);
         }
       }
-      load(s + (2 + half) * W, st);
+      if constexpr (!XA) load_x(s + W, u);
     }
+    load(s + 2 * W, st);
+  };
+  // Pairs of stages without a way out between them: a path that skipped the
+  // second would make every wait at the top one for all loads in flight.
+  int s = wave;
+  for (; s + W < ns; s += 2 * W) {
+    stage(s, s0);
+    stage(s + W, s1);
   }
+  if (s < ns) stage(s, s0);
   // the waves' sums, one token tile at a time, over the constants' space. A lane
   // holds token li, rows 4 lg + [0, 4) of each row group; lane l of a group lies
   // at 16-byte slot l + l / 16 of 68, so that the readers (consecutive threads:
@@ -511,7 +582,7 @@ __global__ __launch_bounds__(64 * W) void k_decode_nf4(DecodeParams p) {
 template <int RG, int TT, int W>
 hipError_t launch_rg(const DecodeParams& p, bool f32, hipStream_t s) {
   const dim3 grid((unsigned)((p.w.N + 16 * RG - 1) / (16 * RG))), block(64 * W);
-  const size_t lds = dc_lds_bytes(RG, TT, W, (int)(p.w.K / 64), p.v.rs);
+  const size_t lds = dc_lds_bytes(RG, TT, W, (int)(p.w.K / 64), p.v.rs, f32 ? 3 : 2);
   const bool dq = p.w.qc.absmax == nullptr;
   if (dq && f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, true>), grid, block, lds, s, p);
   else if (dq) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, false>), grid, block, lds, s, p);
@@ -523,15 +594,17 @@ hipError_t launch_rg(const DecodeParams& p, bool f32, hipStream_t s) {
 constexpr int kCus = 256;
 constexpr size_t kLdsBytes = 160 * 1024;
 
-// Row groups per workgroup, one workgroup per CU (the pair table takes 64 KB
-// of LDS): the shortest queue of the longest CU, a workgroup costing its row
-// groups and about two more for its start and its X.
-int decode_rg(int64_t N, int64_t K, int tt, int rs) {
+// Row groups per workgroup: the shortest queue of the longest CU, a workgroup
+// costing its row groups and about two more for its start and its X. Four need
+// the LDS of two workgroups (K up to some 10000).
+int decode_rg(int64_t N, int64_t K, int tt, int rs, int terms) {
   const int64_t groups = (N + 15) / 16;
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int rg = 1; rg <= 4; rg *= 2) {
-    if (dc_lds_bytes(rg, tt, 8, (int)(K / 64), rs) > kLdsBytes) break;
+    const size_t lds = rg == 4 ? 2 * dc_lds_bytes(rg, tt, 4, (int)(K / 64), rs, terms)
+                               : dc_lds_bytes(rg, tt, 8, (int)(K / 64), rs, terms);
+    if (lds > kLdsBytes) break;
     const int64_t sets = (groups + rg - 1) / rg, c = (sets + kCus - 1) / kCus * (rg + 2);
     if (c <= cost) {
       cost = c;
@@ -544,7 +617,7 @@ int decode_rg(int64_t N, int64_t K, int tt, int rs) {
 }  // namespace
 
 // NF4, at most 64 tokens, and one row group's constants within the LDS that the
-// tables (64 KB) and t (at most 32 KB) leave.
+// table (32 KB) and t's terms (at most 48 KB) leave.
 bool adapter_decode_supported(const QWeight& w, int64_t M) {
   return w.format == LQ_FMT_NF4 && M <= 64 && w.K <= 49152;
 }
@@ -589,10 +662,10 @@ hipError_t launch_adapter_decode(const QWeight& w, const uint16_t* X, int64_t M,
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const DecodeParams p{xp, records, (int)M, ids, v, t_ws, parts, t_save, H, w, tables().lv};
-  const int rg = decode_rg(w.N, w.K, tt, v.rs);
+  const int rg = decode_rg(w.N, w.K, tt, v.rs, f32 ? 3 : 2);
 #define LQ_RG(TT)                                    \
   do {                                               \
-    if (rg == 4) return launch_rg<4, TT, 8>(p, f32, s); \
+    if (rg == 4) return launch_rg<4, TT, 4>(p, f32, s); \
     if (rg == 2) return launch_rg<2, TT, 8>(p, f32, s); \
     return launch_rg<1, TT, 8>(p, f32, s);           \
   } while (0)
