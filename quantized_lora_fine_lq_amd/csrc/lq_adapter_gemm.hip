@@ -141,6 +141,16 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
 #pragma unroll
     for (int q = 0; q < QY; ++q) py[i][q] = p.Bt + min(n0 + yrow(i, q) + sub, p.Ncols - 1) * p.ldb + 8 * ch;
   const int nk = (int)((p.Kc + GK - 1) / GK);
+  // Each XCD begins at an eighth of its own of the contraction (whole steps
+  // only): in step, all eight would ask for the same columns, whose rows lie a
+  // power of two apart, of the same memory channels. 2 to 4 % of the kernel's
+  // time; a place of its own per tile costs the tiles of an XCD the weight rows
+  // and tokens that they share in its L2 (2048 tokens: 72 -> 90 us).
+  const int rot = p.Kc % GK ? 0 : (int)(xcd * nk / 8);
+  auto column = [&](int it) {   // first column of step it
+    const int at = it + rot;
+    return (int64_t)(at < nk ? at : at - nk) * GK;
+  };
 
   // The adapters' part: an adapter's [hi | mid (| lo)] columns of the terms
   // against as many copies of Lb, in steps of 64 (columns past the last are
@@ -174,7 +184,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   typedef std::integral_constant<bool, false> Any;
   auto load_x = [&](auto plain, int it, int i, int buf) {
     if (plain.value || it < nk) {
-      const int64_t k0 = (int64_t)it * GK;
+      const int64_t k0 = column(it);
       const bool ok = plain.value || !BWD || k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (0 * NaN is not 0)
 #pragma unroll
       for (int q = 0; q < QX; ++q) load_lds16(ok ? px[i][q] + k0 : p.zeros, lds.x[buf] + xrow(i, q) * GK);
@@ -184,7 +194,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   };
   auto load_y = [&](auto plain, int it, int i, int buf) {
     if (plain.value || it < nk) {
-      const int64_t k0 = (int64_t)it * GK;
+      const int64_t k0 = column(it);
 #pragma unroll
       for (int q = 0; q < QY; ++q) load_lds16(py[i][q] + k0, lds.y[buf] + yrow(i, q) * GK);
     } else {
