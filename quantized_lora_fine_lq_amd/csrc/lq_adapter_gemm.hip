@@ -382,25 +382,42 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   }
 }
 
-// Few tokens or a small weight: tiles of 64 positions x 64 weight rows, 4 waves
-// of 32 x 32, so that the tiles cover the chip; a ring of four LDS buffers (64
-// KB: two workgroups per CU), loads three steps ahead, one barrier a step. The
-// adapters' steps follow the base contraction's in the same ring: of a tile of
-// one adapter they accumulate, of one with several each goes to its own
-// tokens' columns alone.
+// Few tokens or a small weight: tiles of 64 positions x 64 weight rows, four
+// waves of 32 x 32, so that the tiles cover the chip. Steps pass through a ring
+// of four LDS buffers (64 KB) with loads three ahead and one barrier a step. A
+// step's chain (barrier, loads, fragment reads, eight MFMA) needs a second wave
+// per SIMD beside it: past 256 tiles another workgroup's; up to 256 the
+// workgroup has a second group of waves that takes every other step through a
+// ring of its own, and the two sums meet at the end. (A ring of eight buffers
+// instead did not shorten the chain.) Measured, N = K = 4096: 250 tokens 20 us
+// (one group: 27), 500 tokens 30 (two groups: 37).
+//
+// The adapters' steps follow the base contraction's in the same rings, from a
+// table made at the start; the products of each go to its own tokens' columns
+// alone.
 constexpr int SM = 64, SN = 64, S_THREADS = 256, S_RING = 4;
+constexpr int S_STEPS = SM * 6;   // an adapter per token, 3 terms of rank 128
 
-template <bool OUT_F32, bool BWD>
-__global__ __launch_bounds__(S_THREADS, 2) void k_adapter_gemm_small(AdapterGemm p) {
+struct SmallStep {
+  const uint16_t* base;    // Lb
+  int runs, live, first;   // of Lb: runs of 8 columns; of all terms; the step's first
+  int lo, hi;              // its positions of the tile
+};
+
+template <int GROUPS, bool OUT_F32, bool BWD>
+__global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(AdapterGemm p) {
   constexpr int TERMS = OUT_F32 ? 3 : 2;
   struct __attribute__((aligned(16))) Lds {
-    uint16_t x[S_RING][SM * GK];
-    uint16_t y[S_RING][SN * GK];
+    uint16_t x[GROUPS][S_RING][SM * GK];
+    uint16_t y[GROUPS][S_RING][SN * GK];
+    SmallStep steps[S_STEPS];
+    int total;
   };
   __shared__ Lds lds;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int group = wave >> 2, w4 = wave & 3;
   const int li = lane & 15, lg = lane >> 4;
-  const int wn = wave & 1, wm = wave >> 1;
+  const int wn = w4 & 1, wm = w4 >> 1;
   const int64_t tiles_m = (p.M + SM - 1) / SM, tiles_n = (p.Ncols + SN - 1) / SN;
   const int64_t total = tiles_m * tiles_n;
   const int64_t xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
@@ -412,7 +429,7 @@ __global__ __launch_bounds__(S_THREADS, 2) void k_adapter_gemm_small(AdapterGemm
   int64_t ny[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int row = (wave * 2 + q) * 8 + sub;
+    const int row = (w4 * 2 + q) * 8 + sub;
     const int64_t pos = min(m0 + row, p.M - 1);
     px[q] = p.A + (int64_t)p.rt.perm[pos] * p.Kc + 8 * ch;
     pt[q] = p.terms + pos * 3 * p.v.rs;
@@ -420,33 +437,63 @@ __global__ __launch_bounds__(S_THREADS, 2) void k_adapter_gemm_small(AdapterGemm
     py[q] = p.Bt + ny[q] * p.ldb + 8 * ch;
   }
   const int nk = (int)((p.Kc + GK - 1) / GK);
-  Adapter src = adapter_at<TERMS>(p, m0, mend);   // the adapter whose steps are loaded next
-  int kt = 0;
-  // the next step of the sequence (base contraction, then adapter after
-  // adapter) into buffer buf; past the end zeros
+  int steps = 0;   // of both parts, once the table is there
+  uint16_t(*const rx)[SM * GK] = lds.x[group];
+  uint16_t(*const ry)[SN * GK] = lds.y[group];
+  // step it of the sequence into the group's buffer buf; past the end zeros
   auto load = [&](int it, int buf) {
     if (it < nk) {
       const int64_t k0 = (int64_t)it * GK;
       const bool ok = !BWD || k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (0 * NaN is not 0)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        load_lds16(ok ? px[q] + k0 : p.zeros, lds.x[buf] + (wave * 2 + q) * 8 * GK);
-        load_lds16(py[q] + k0, lds.y[buf] + (wave * 2 + q) * 8 * GK);
+        load_lds16(ok ? px[q] + k0 : p.zeros, rx[buf] + (w4 * 2 + q) * 8 * GK);
+        load_lds16(py[q] + k0, ry[buf] + (w4 * 2 + q) * 8 * GK);
       }
       return;
     }
-    const int c = 8 * kt + ch;
+    SmallStep st{nullptr, 1, 0, 0, 0, 0};
+    if (it < steps) st = lds.steps[it - nk];
+    const int c = st.first + ch;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      load_lds16(c < src.live ? pt[q] + 8 * c : p.zeros, lds.x[buf] + (wave * 2 + q) * 8 * GK);
-      load_lds16(c < src.live ? src.base + ny[q] * src.stride + 8 * (c % src.runs) : p.zeros,
-                 lds.y[buf] + (wave * 2 + q) * 8 * GK);
-    }
-    if (src.steps && ++kt >= src.steps) {
-      src = adapter_at<TERMS>(p, src.hi, mend);
-      kt = 0;
+      load_lds16(c < st.live ? pt[q] + 8 * c : p.zeros, rx[buf] + (w4 * 2 + q) * 8 * GK);
+      load_lds16(c < st.live ? st.base + (ny[q] * st.runs + c % st.runs) * 8 : p.zeros, ry[buf] + (w4 * 2 + q) * 8 * GK);
     }
   };
+  auto prime = [&]() {
+#pragma unroll
+    for (int i = 0; i < S_RING - 1; ++i) load(GROUPS * i + group, i);
+  };
+  const bool early = nk >= GROUPS * (S_RING - 1);   // the first loads need no table
+  if (early) prime();
+  if (wave == 4 * GROUPS - 1) {
+    // Lane l: position l of the tile. Equal adapters lie side by side; the
+    // first position of each writes its steps, numbered by a sum over the
+    // lanes below, bit by bit.
+    const bool valid = m0 + lane < mend;
+    const int a = valid ? p.rt.sid[m0 + lane] : -1, before = __shfl_up(a, 1);
+    const uint64_t starts = __ballot(lane == 0 || a != before);
+    const bool leads = valid && a < p.v.n && ((starts >> lane) & 1);
+    const lq_adapter ad = p.v.tab[leads ? a : 0];
+    const int runs = (ad.r + 7) >> 3, live = TERMS * runs, count = leads ? (live + 7) >> 3 : 0;
+    int first = 0, sum = 0;
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {
+      const uint64_t one = __ballot((count >> b) & 1);
+      first += (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(one >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)one, 0)) << b;
+      sum += __popcll(one) << b;
+    }
+    const uint64_t above = lane < 63 ? starts >> (lane + 1) : 0;
+    const int hi = above ? lane + __ffsll((unsigned long long)above) : SM;
+    const uint16_t* base = !p.lt_all && ad.r % 8 == 0 ? ad.B : p.lt + p.Ncols * ad.row8;
+    for (int k = 0; k < count; ++k) lds.steps[first + k] = SmallStep{base, runs, live, 8 * k, lane, hi};
+    if (lane == 0) lds.total = sum;
+  }
+  __syncthreads();
+  steps = nk + uniform(lds.total);
+  if (!early) prime();
+
   f32x4_t acc[2][2];
 #pragma unroll
   for (int c = 0; c < 2; ++c)
@@ -455,24 +502,18 @@ __global__ __launch_bounds__(S_THREADS, 2) void k_adapter_gemm_small(AdapterGemm
   const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
   const int ox = (wm * 32 + li) * GK, oy = (wn * 32 + li) * GK;
   u32x4_t fx[2][2], fy[2][2];
-  auto read = [&](int buf) {
+  auto turn = [&](int i) {   // the group's step i is in LDS, and step i - 1 read by everyone
+    wait_vm<(S_RING - 2) * 4>();
+    barrier();
+    load(GROUPS * (i + S_RING - 1) + group, (i + S_RING - 1) % S_RING);
+    const int buf = i % S_RING;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        fx[u][i] = ld16(lds.x[buf] + ox + 16 * i * GK + slot[u]);
-        fy[u][i] = ld16(lds.y[buf] + oy + 16 * i * GK + slot[u]);
+      for (int k = 0; k < 2; ++k) {
+        fx[u][k] = ld16(rx[buf] + ox + 16 * k * GK + slot[u]);
+        fy[u][k] = ld16(ry[buf] + oy + 16 * k * GK + slot[u]);
       }
-  };
-  Adapter cur = src;   // the adapter whose steps are multiplied next
-#pragma unroll
-  for (int it = 0; it < S_RING - 1; ++it) load(it, it);
-  int it = 0;
-  auto turn = [&]() {   // step it is in LDS, and step it - 1 read by everyone
-    wait_vm<(S_RING - 2) * 4>();
-    barrier();
-    load(it + S_RING - 1, (it + S_RING - 1) % S_RING);
-    read(it % S_RING);
   };
   auto multiply = [&]() {
 #pragma unroll
@@ -483,20 +524,22 @@ __global__ __launch_bounds__(S_THREADS, 2) void k_adapter_gemm_small(AdapterGemm
         for (int r = 0; r < 2; ++r)
           acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fy[u][c]), as_bf16x8(fx[u][r]), acc[c][r], 0, 0, 0);
   };
-  const bool whole = cur.steps && cur.hi == mend;
-  const int last = nk + (whole ? cur.steps : 0);
-  for (; it < last; ++it) {
-    turn();
+  int i = 0;
+  for (; GROUPS * (i + 1) <= nk; ++i) {
+    turn(i);
     multiply();
   }
-  if (!whole) {
-    int k = 0;
-    for (; cur.steps; ++it) {
-      turn();
+  for (; GROUPS * i < steps; ++i) {   // the same count for both groups
+    turn(i);
+    const int it = GROUPS * i + group;
+    if (it < nk) {
+      multiply();
+    } else if (it < steps) {
+      const int lo = lds.steps[it - nk].lo, hi = lds.steps[it - nk].hi;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int64_t pos = m0 + wm * 32 + 16 * r + li;
-        const bool mine = pos >= cur.lo && pos < cur.hi;
+        const int pos = wm * 32 + 16 * r + li;
+        const bool mine = pos >= lo && pos < hi;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           f32x4_t d = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -507,20 +550,30 @@ __global__ __launch_bounds__(S_THREADS, 2) void k_adapter_gemm_small(AdapterGemm
           for (int e = 0; e < 4; ++e) acc[c][r][e] += mine ? d[e] : 0.0f;
         }
       }
-      if (++k >= cur.steps) {
-        cur = adapter_at<TERMS>(p, cur.hi, mend);
-        k = 0;
-      }
     }
   }
-  wait_vm<0>();   // the loads past the last step, before the workgroup's LDS is given up
+  wait_vm<0>();   // the loads past the last step
+  if constexpr (GROUPS == 2) {   // group g finishes the weight rows of c = g, group 0's sum first
+    __syncthreads();
+    f32x4_t* sum = reinterpret_cast<f32x4_t*>(lds.x) + 128 * w4 + lane;   // [group][w4][r][lane]
+#pragma unroll
+    for (int r = 0; r < 2; ++r) sum[512 * group + 64 * r] = group ? acc[0][r] : acc[1][r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const f32x4_t other = sum[512 * (1 - group) + 64 * r];
+      if (group) acc[1][r] = other + acc[1][r];
+      else acc[0][r] = acc[0][r] + other;
+    }
+  }
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int64_t pos = m0 + wm * 32 + 16 * r + li;
     if (pos >= p.M) continue;
     const int64_t row = (int64_t)p.rt.perm[pos] * p.Ncols;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) store4<OUT_F32>(p, row, n0 + wn * 32 + 16 * c + 4 * lg, acc[c][r]);
+    for (int c = 0; c < 2; ++c)
+      if (GROUPS == 1 || c == group) store4<OUT_F32>(p, row, n0 + wn * 32 + 16 * c + 4 * lg, acc[c][r]);
   }
 }
 
@@ -558,13 +611,13 @@ hipError_t launch_tile(const AdapterGemm& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_small(const AdapterGemm& g, hipStream_t s) {
-  const int64_t tiles = ((g.M + SM - 1) / SM) * ((g.Ncols + SN - 1) / SN);
+template <int GROUPS>
+hipError_t launch_small(const AdapterGemm& g, int64_t tiles, hipStream_t s) {
   LQ_DASSERT(tiles > 0 && tiles < (int64_t(1) << 31));
-  const dim3 grid((unsigned)tiles), block(S_THREADS);
-  if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm_small<false, true>), grid, block, 0, s, g);
-  else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm_small<true, false>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((k_adapter_gemm_small<false, false>), grid, block, 0, s, g);
+  const dim3 grid((unsigned)tiles), block(S_THREADS * GROUPS);
+  if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, true>), grid, block, 0, s, g);
+  else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, true, false>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, false>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 
@@ -572,15 +625,16 @@ hipError_t launch_small(const AdapterGemm& g, hipStream_t s) {
 
 hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s) {
   LQ_DASSERT(g.M > 0 && g.Ncols > 0 && g.Kc > 0 && g.Kc % 8 == 0 && g.ldb % 64 == 0 && g.ldb >= g.Kc);
-  // Rounds of a chip full of tiles times a tile's time per step: 1.7 us
-  // (256 x 256), 1.05 (256 x 128) and, with two workgroups per CU, 0.3 (64 x 64)
-  // as measured over K = 4096.
-  auto cost = [&](int64_t m, int64_t n, int64_t slots, double us) {
-    const int64_t tiles = ((g.M + m - 1) / m) * ((g.Ncols + n - 1) / n);
-    return (double)((tiles + slots - 1) / slots) * us;
-  };
-  const double c256 = cost(256, 256, 256, 1.7), c128 = cost(256, 128, 256, 1.05), c64 = cost(64, 64, 512, 0.3);
-  if (c64 < c128 && c64 < c256) return launch_small(g, s);
+  // Rounds of a chip full of tiles times a tile's time per step, in us as
+  // measured over K = 4096: 1.7 (256 x 256), 1.05 (256 x 128) and for 64 x 64,
+  // two workgroups per CU, 0.3 where the tiles number more than the CUs. (Fewer
+  // of them always win: 0.2.)
+  auto tiles = [&](int64_t m, int64_t n) { return ((g.M + m - 1) / m) * ((g.Ncols + n - 1) / n); };
+  auto cost = [&](int64_t count, int64_t slots, double us) { return (double)((count + slots - 1) / slots) * us; };
+  const int64_t small = tiles(SM, SN);
+  const double c256 = cost(tiles(256, 256), 256, 1.7), c128 = cost(tiles(256, 128), 256, 1.05), c64 = cost(small, 512, 0.3);
+  if (small <= 256) return launch_small<2>(g, small, s);
+  if (c64 < c128 && c64 < c256) return launch_small<1>(g, small, s);
   return c256 <= c128 ? launch_tile<256>(g, s) : launch_tile<128>(g, s);
 }
 

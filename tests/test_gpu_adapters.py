@@ -198,6 +198,25 @@ def test_large_forward(lq, torch, case, out):
     assert ((H.double() - ref).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("ranks,ids", [([16, 8, 7], "runs"), ([128] * 200, "mixed"), ([3, 64] * 20, "mixed")], ids=str)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_more_small_tiles_than_compute_units(lq, torch, ranks, ids, out):
+    """Tiles of 64 x 64, one group of waves each; an adapter to nearly every token of a tile."""
+    L = Layer(lq, torch, 1037, 192, 1999, ranks, ids)
+    H, _ = lq.adapters_forward(L.qw, L.X, L.set, L.ids_dev, out_dtype=torch.float32 if out == "f32" else torch.bfloat16)
+    (ref, mag, lora), _, _, _ = reference64(torch, L)
+    bound = (192 + 3 * max(ranks) + 8) * U * (mag + lora) + 192 * U * lora
+    if out == "bf16":
+        bound += 2.0 ** -16 * lora + 2.0 ** -8 * ref.abs() + 2.0 ** -130
+    assert ((H.double() - ref).abs() <= bound).all()
+    if out == "bf16":
+        B = Layer(lq, torch, 200, 1088, 1999, ranks, ids)
+        gx = lq.adapters_backward(B.qw, B.X, B.G, B.set, B.ids_dev, need_dA=False, need_dB=False)[0]
+        _, (ref, mag, lora), _, _ = reference64(torch, B)
+        bound = (200 + 3 * max(ranks) + 8) * U * (mag + lora) + 200 * U * lora + 2.0 ** -16 * lora + 2.0 ** -8 * ref.abs()
+        assert ((gx.double() - ref).abs() <= bound + 2.0 ** -130).all()
+
+
 # the backward's result is [M, K], its contraction N: the same tiles with N and K exchanged
 @pytest.mark.parametrize("case", [(200, 4096, 2047, [16, 8, 64, 24], "runs", "nf4_dq"),
                                   (64, 4096, 1800, [16] * 9, "mixed", "codebook"),
