@@ -10,6 +10,11 @@ Two layers, both argument marshalling only:
   current stream are the only things taken from PyTorch) and call the same
   entry points. All arithmetic runs in the library's HIP kernels.
 
+Many adapters over one projection, and the clipping of their gradients
+(include/lq_adapters.h), are in ``adapters.py`` and exported here too:
+``AdapterSet``, ``adapter_route``, ``adapters_forward``,
+``adapters_backward``, ``GradList``, ``grad_norm``, ``clip_grad_norm``.
+
 Importing fails loudly if liblq.so has not been built
 (``python quantized_lora_fine_lq_amd/build.py``).
 """

@@ -22,6 +22,8 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // group its place among the group's equal ids from ballots (one per bit of
 // the id). Bound by the latency of its few dependent passes; the first
 // RT_KEEP groups of a wave keep their ids in registers between the passes.
+// About 4 us at 250 tokens; in a call that decodes a weight too it runs beside
+// that (k_adapter_prep) and costs nothing of its own.
 // ===========================================================================
 constexpr int RT_WAVES = 16, RT_KEEP = 4;
 
@@ -117,7 +119,9 @@ __device__ __forceinline__ void route_tokens(const RouteJob& jb, int32_t* cnt) {
 // Preparation, one launch: workgroup 0 builds the route, the others decode the
 // NF4 weight (as it lies, or transposed for the backward) and re-lay the
 // adapters; none of it depends on the rest. Bound by writing the bfloat16
-// weight.
+// weight: 4096 x 4096 10 us as it lies and 14 transposed (4.2 and 3.0 TB/s of
+// codes and weight together), 11008 x 4096 25 and 43 us; the transposing form
+// also writes the adapters' copies.
 // ===========================================================================
 constexpr int PW_T = 128;                 // transposed: tiles of PW_T weight rows x PW_T columns
 constexpr int PW_PITCH = PW_T + 16;       // bf16 per LDS row: the transposing reads of 4 rows hit distinct banks
@@ -360,7 +364,9 @@ __device__ __forceinline__ void put_t(const DownJob& jb, const AdapterView& v, c
 // contiguous runs of 64-column blocks, MFMA 16x16x32 with tokens as rows and
 // the adapter's rows as columns, both straight from memory into registers, a
 // wave's next U blocks loading while the current ones are multiplied. The
-// waves' partial sums meet in LDS and are added in wave order.
+// waves' partial sums meet in LDS and are added in wave order. Bound by the
+// count of its 16-byte load instructions, which scattered rows make slow: 10 us
+// at 250 to 2048 tokens of rank 16, K = 4096; 6 at 300 tokens, K = 1024.
 // ===========================================================================
 template <int JT, int W, int U>
 __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt) {
@@ -457,7 +463,9 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
 // share of the columns; tiles through a ring of four LDS buffers filled by
 // memory-to-LDS loads three 64-wide steps ahead. The shares' sums, float32 in
 // sorted order [shares][M][rs], are joined by k_adapter_down_join, which also
-// turns a given t into terms.
+// turns a given t into terms. 4096 tokens of rank 64, K = 4096: 19 + 6 us for
+// 34 MB of X (7 us at the rate of a large copy); 1999 tokens of rank 8 to 64:
+// 8.6 + 5.
 // ===========================================================================
 constexpr int DT_M = 64, DT_K = 64, DT_RING = 4;
 
@@ -583,7 +591,11 @@ int down_shares(int64_t M, int64_t C) {
 // (the next step's loads are in flight while one is multiplied), and are read
 // transposed (ds_read_b64_tr_b16: the 16 lanes of a group point at 4 rows of 16
 // elements, lane l gets column l of the 4 rows). Tokens past the segment are
-// zero in both, so no neighbour's infinity or NaN enters.
+// zero in both, so no neighbour's infinity or NaN enters. Bound by the chain of
+// a step (stage, barrier, transposed reads) at one or two workgroups per CU:
+// dA and dB of 2048 tokens of rank 16, N = K = 4096, 12.7 us for 34 MB; of 4096
+// tokens of rank 64, N = 4096, K = 11008, 55 for 124 MB. Two steps in flight
+// instead of one did not change that.
 // ===========================================================================
 constexpr int CQ_COLS = 256, CQ_PITCH = CQ_COLS + 16;
 
@@ -703,7 +715,8 @@ __global__ __launch_bounds__(256, 2) void k_adapter_col(ColReq q0, ColReq q1, un
 }
 
 // Joins the runs of adapters with more than one, in order, and writes the zero
-// gradients of adapters without tokens.
+// gradients of adapters without tokens. 7 us at 2048 tokens of rank 16, 16 at
+// 4096 of rank 64 (four partial sums a thread at a time).
 __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1, int nreq, int rows, AdapterView v,
                                                             Route rt) {
   const int a = blockIdx.y, lane = threadIdx.x & 63;

@@ -8,6 +8,15 @@
 // underflows for |x| outside about 1e-19 .. 1e19, and float64 has room for any
 // float32 gradient; the additions are few against the memory traffic that
 // bounds both passes. All sums run in a fixed order.
+//
+// The squares of a group must all be known before its first product, so large
+// gradients are read twice: two launches, the second from the last slot to the
+// first, which finds some of what the first read last in the 256 MB cache.
+// Every workgroup of the second adds its group's slot sums itself (a third
+// launch would cost about as much as they do). 16-byte vectors, eight in flight
+// per lane. Measured, float32 from one list to another: 640 MB (224 x 32 layers'
+// tensors in 4 groups) 140 + 245 us, 4.6 and 5.2 TB/s; 5 MB 4.4 + 6.6 us,
+// latency; 19.6 MB of bfloat16 at odd addresses 6.6 + 8.8 us.
 #include "lq_adapters.h"
 #include "lq_device.h"
 
