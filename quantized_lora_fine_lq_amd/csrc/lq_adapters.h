@@ -52,8 +52,8 @@ hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const 
 
 // Preparation, one launch of independent parts, each left out where its
 // pointer is null: 16 zero bytes (read by the other kernels in place of what
-// lies past an end); the route of ids; an NF4 weight decoded to wd (W' [N, K], or
-// with ldb W'^T [K, ldb], zero columns from N on); the adapters re-laid for the
+// lies past an end); the route of ids; the weight decoded to wd (W' [N, K], or,
+// NF4 with ldb, W'^T [K, ldb], zero columns from N on); the adapters re-laid for the
 // matrix kernels: at = A^T [K, r8] at K * row8_a, bt = B^T [r, N] at N *
 // row8_a, bp = B [N, r8] at N * row8_a of the adapters whose rank is not a
 // multiple of 8 (zero columns past r_a).

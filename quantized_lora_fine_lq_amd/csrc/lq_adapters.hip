@@ -117,15 +117,18 @@ __device__ __forceinline__ void route_tokens(const RouteJob& jb, int32_t* cnt) {
 
 // ===========================================================================
 // Preparation, one launch: workgroup 0 builds the route, the others decode the
-// NF4 weight (as it lies, or transposed for the backward) and re-lay the
+// weight (as it lies; NF4 transposed for the backward) and re-lay the
 // adapters; none of it depends on the rest. Bound by writing the bfloat16
 // weight: 4096 x 4096 10 us as it lies and 14 transposed (4.2 and 3.0 TB/s of
 // codes and weight together), 11008 x 4096 25 and 43 us; the transposing form
-// also writes the adapters' copies.
+// also writes the adapters' copies. Codebook 4096 x 4096: 16 us, of which about
+// half is the chain from a row's width and offset to its first planes (a
+// workgroup per row and a launch after the route's took 4 + 18).
 // ===========================================================================
 constexpr int PW_T = 128;                 // transposed: tiles of PW_T weight rows x PW_T columns
 constexpr int PW_PITCH = PW_T + 16;       // bf16 per LDS row: the transposing reads of 4 rows hit distinct banks
 constexpr int PW_FLAT = 4;                // as it lies: pieces of 16 codes per thread, all in flight together
+constexpr int PC_ROWS = 8;                // codebook: rows per workgroup, two per 256 threads, their loads together
 constexpr int RL_C = 128;                 // re-laid per workgroup: RL_C rows of A^T or B
 
 struct PrepJob {
@@ -230,6 +233,70 @@ __device__ __forceinline__ void prep_weight(const PrepJob& p, unsigned wg, unsig
   }
 }
 
+// Codebook rows: 16 codes a thread, two bytes of each of the row's bit planes.
+// The row's levels become a table of 256 pairs whose index interleaves the bits
+// of two adjacent codes, so that a pair is one 2-bit field of each plane.
+template <bool DQ>
+__device__ __forceinline__ void prep_codebook(const PrepJob& p, unsigned wg, unsigned char* lds) {
+  const int64_t N = p.w.N, K = p.w.K;
+  const int part = threadIdx.x >> 8, th = threadIdx.x & 255;
+  f32x2_t* sPair = reinterpret_cast<f32x2_t*>(lds) + 512 * part;   // of the part's two rows
+  const float mean = DQ ? *p.w.qc.dq_mean : 0.0f;
+  int64_t row[2];
+  int bits[2];
+  const uint8_t* src[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    row[u] = min((int64_t)wg * PC_ROWS + 2 * part + u, N - 1);   // past the last row: decoded, not stored
+    bits[u] = min(max((int)p.w.row_bits[row[u]], 1), 4);
+    src[u] = p.w.codes + p.w.row_offset[row[u]];
+    uint32_t f = 0, g = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      f |= ((th >> (2 * b)) & 1u) << b;
+      g |= ((th >> (2 * b + 1)) & 1u) << b;
+    }
+    sPair[256 * u + th] = f32x2_t{p.w.levels[row[u] * 16 + f], p.w.levels[row[u] * 16 + g]};
+  }
+  __syncthreads();
+  for (int64_t i = th; i < K / 16; i += 256) {
+    const int64_t blk = i >> 2;
+    uint32_t plane[2][4], q8[2];
+    float c[2], s2[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* at = src[u] + blk * 8 * bits[u] + 2 * (i & 3);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) plane[u][b] = b < bits[u] ? at[8 * b] | (uint32_t)at[8 * b + 1] << 8 : 0u;
+      const int64_t cb = row[u] * (K / 64) + blk;
+      if (DQ) {
+        q8[u] = p.w.qc.absmax_q[cb];
+        s2[u] = p.w.qc.dq_scale[cb >> 8];
+      } else {
+        c[u] = p.w.qc.absmax[cb];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float cp = DQ ? __builtin_fmaf(e4m3_decode(q8[u]), s2[u], mean) : c[u];
+      u32x4_t o[2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t idx = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) idx |= ((plane[u][b] >> (2 * e)) & 3u) << (2 * b);
+        const f32x2_t q = sPair[256 * u + idx];
+        o[e >> 2][e & 3] = pack_bf16x2(q.x * cp, q.y * cp);
+      }
+      if ((int64_t)wg * PC_ROWS + 2 * part + u < N) {
+        u32x4_t* dst = reinterpret_cast<u32x4_t*>(p.wd + row[u] * K + 16 * i);
+        dst[0] = o[0];
+        dst[1] = o[1];
+      }
+    }
+  }
+}
+
 // at[k][j] = A[j][k], bp[n][j] = B[n][j] (j < r8, zero past r), bt[j][n] = B[n][j],
 // through an LDS tile of RL_C rows (k or n) x r8.
 __device__ __forceinline__ void prep_adapter(const PrepJob& p, unsigned a, unsigned wg, unsigned char* lds) {
@@ -279,8 +346,13 @@ __global__ __launch_bounds__(1024) void k_adapter_prep(PrepJob p) {
   }
   wg -= p.route_wgs;
   if (wg < p.weight_wgs) {
-    if (p.w.qc.absmax) prep_weight<false>(p, wg, prep_lds);
-    else prep_weight<true>(p, wg, prep_lds);
+    if (p.w.format == LQ_FMT_CODEBOOK) {
+      if (p.w.qc.absmax) prep_codebook<false>(p, wg, prep_lds);
+      else prep_codebook<true>(p, wg, prep_lds);
+    } else {
+      if (p.w.qc.absmax) prep_weight<false>(p, wg, prep_lds);
+      else prep_weight<true>(p, wg, prep_lds);
+    }
     return;
   }
   wg -= p.weight_wgs;
@@ -775,7 +847,7 @@ int col_rows(int64_t M, int64_t cols) {
 hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, const QWeight& w, uint16_t* wd,
                                int64_t ldb, const AdapterView& v, uint16_t* at, uint16_t* bt, uint16_t* bp,
                                uint16_t* zeros, hipStream_t s) {
-  LQ_DASSERT(!wd || w.format == LQ_FMT_NF4);
+  LQ_DASSERT(!wd || w.format == LQ_FMT_NF4 || !ldb);
   PrepJob p{};
   size_t lds = 0;
   if (route) {
@@ -790,8 +862,13 @@ hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, co
   p.ldb = ldb;
   if (wd) {
     const int64_t flat = PW_FLAT * 1024 * 16;
-    p.weight_wgs = (unsigned)(ldb ? ((w.N + PW_T - 1) / PW_T) * ((w.K + PW_T - 1) / PW_T) : (w.N * w.K + flat - 1) / flat);
-    lds = std::max(lds, 256 * sizeof(f32x2_t) + (ldb ? (size_t)PW_T * PW_PITCH * 2 : 0));
+    if (w.format == LQ_FMT_CODEBOOK) {
+      p.weight_wgs = (unsigned)((w.N + PC_ROWS - 1) / PC_ROWS);
+      lds = std::max(lds, (size_t)PC_ROWS * 256 * sizeof(f32x2_t));
+    } else {
+      p.weight_wgs = (unsigned)(ldb ? ((w.N + PW_T - 1) / PW_T) * ((w.K + PW_T - 1) / PW_T) : (w.N * w.K + flat - 1) / flat);
+      lds = std::max(lds, 256 * sizeof(f32x2_t) + (ldb ? (size_t)PW_T * PW_PITCH * 2 : 0));
+    }
   }
   p.v = v;
   p.at = at;

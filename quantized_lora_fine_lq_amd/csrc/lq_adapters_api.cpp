@@ -129,10 +129,7 @@ int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const
   uint16_t* bp = any_odd_rank(set) ? cv.take<uint16_t>((size_t)sum_r8(set) * q.N) : nullptr;
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
 
-  const bool nf4 = q.format == LQ_FMT_NF4;
-  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, nf4 ? wd : nullptr, 0, v, nullptr, nullptr, bp,
-                                     zeros, s);
-  if (e == hipSuccess && !nf4) e = launch_dequant(q, wd, s);
+  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, wd, 0, v, nullptr, nullptr, bp, zeros, s);
   if (e != hipSuccess) return LQ_ERR_LAUNCH;
   const Route rt = route_view(route ? route : rws, M, v.n);
   const DownJob job{X, q.K, nullptr, nullptr, terms, t_save, part};
@@ -184,8 +181,8 @@ int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t*
   if (!grad_X && !dA && !dB) return LQ_OK;
 
   const bool need_u = grad_X || dA, nf4 = q.format == LQ_FMT_NF4;
-  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, grad_X && nf4 ? wt : nullptr, ldb, v,
-                                     grad_X ? at : nullptr, need_u ? bt : nullptr, nullptr, zeros, s);
+  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, !grad_X ? nullptr : nf4 ? wt : wd, nf4 ? ldb : 0,
+                                     v, grad_X ? at : nullptr, need_u ? bt : nullptr, nullptr, zeros, s);
   if (e != hipSuccess) return LQ_ERR_LAUNCH;
   const Route rt = route_view(route ? route : rws, M, v.n);
   DownJob jobs[2];
@@ -199,10 +196,7 @@ int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t*
   if (dA) cols[nc++] = ColReq{u, X, q.K, dA, 0, part_a};
   if (nc && (e = launch_adapter_col(cols, nc, M, v, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   if (!grad_X) return LQ_OK;
-  if (!nf4) {
-    if ((e = launch_dequant(q, wd, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-    if ((e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  }
+  if (!nf4 && (e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   const AdapterGemm g{G, M, q.K, q.N, wt, ldb, u, v, at, 1, rt, grad_X, 0, zeros};
   return launch_status(launch_adapter_gemm(g, s));
 }
