@@ -659,12 +659,14 @@ int down_shares(int64_t M, int64_t C) {
 // workgroup per 256 columns (64 a wave) and run of at most `rows` sorted
 // positions; 32 tokens per step. P comes as three bfloat16 terms, so the
 // products carry float32 P on the bf16 matrix cores; all three go into the same
-// accumulators. P and Q tiles lie in LDS with tokens as rows, double buffered
-// (the next step's loads are in flight while one is multiplied), and are read
-// transposed (ds_read_b64_tr_b16: the 16 lanes of a group point at 4 rows of 16
-// elements, lane l gets column l of the 4 rows). Tokens past the segment are
-// zero in both, so no neighbour's infinity or NaN enters. Bound by the chain of
-// a step (stage, barrier, transposed reads) at one or two workgroups per CU:
+// accumulators. P and Q tiles lie in LDS with tokens as rows (the next step's
+// loads are in flight while one is multiplied; two buffers up to rank 32, above
+// it one and a second barrier, so that three workgroups fit a CU: rank 64 59 ->
+// 55 us, rank 16 with one buffer 12.8 -> 13.4), and are read transposed
+// (ds_read_b64_tr_b16: the 16 lanes of a group point at 4 rows of 16 elements,
+// lane l gets column l of the 4 rows). Tokens past the segment are zero in
+// both, so no neighbour's infinity or NaN enters. Bound by the chain of
+// a step (stage, barrier, transposed reads) at three workgroups per CU:
 // dA and dB of 2048 tokens of rank 16, N = K = 4096, 12.7 us for 34 MB; of 4096
 // tokens of rank 64, N = 4096, K = 11008, 55 for 124 MB. Two steps in flight
 // instead of one did not change that.
@@ -682,13 +684,18 @@ __device__ __forceinline__ u32x4_t tr_frag(const uint16_t* base, int pitch, int 
   return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
 }
 
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 template <int JT>
-__global__ __launch_bounds__(256, 2) void k_adapter_col(ColReq q0, ColReq q1, unsigned tiles0, int rows, AdapterView v,
+__global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0, ColReq q1, unsigned tiles0, int rows, AdapterView v,
                                                      Route rt) {
   constexpr int PP = 16 * JT + 16;
+  constexpr int BUFS = JT <= 2 ? 2 : 1;
   constexpr int PQ = (3 * 32 * 2 * JT + 255) / 256;   // 16-byte pieces of P per thread
-  __shared__ __attribute__((aligned(16))) uint16_t sQ[2][32 * CQ_PITCH];
-  __shared__ __attribute__((aligned(16))) uint16_t sP[2][3 * 32 * PP];
+  __shared__ __attribute__((aligned(16))) uint16_t sQ[BUFS][32 * CQ_PITCH];
+  __shared__ __attribute__((aligned(16))) uint16_t sP[BUFS][3 * 32 * PP];
   const bool second = blockIdx.x >= tiles0;
   const ColReq rq = second ? q1 : q0;
   Item it;
@@ -738,27 +745,30 @@ __global__ __launch_bounds__(256, 2) void k_adapter_col(ColReq q0, ColReq q1, un
   tokens(0);
   load(0);
   tokens(32);
-  for (int mb = 0; mb < it.count; mb += 64) {
+  auto step = [&](int m, int b) {
+    store(m, b);
+    __syncthreads();
+    load(m + 32);
+    tokens(m + 64);
+    u32x4_t fq[4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int m = mb + 32 * b;
-      if (m >= it.count) break;
-      store(m, b);
-      __syncthreads();
-      load(m + 32);
-      tokens(m + 64);
-      u32x4_t fq[4];
+    for (int ct = 0; ct < 4; ++ct) fq[ct] = tr_frag(sQ[b] + 64 * wave + 16 * ct, CQ_PITCH, li, lg);
 #pragma unroll
-      for (int ct = 0; ct < 4; ++ct) fq[ct] = tr_frag(sQ[b] + 64 * wave + 16 * ct, CQ_PITCH, li, lg);
+    for (int t = 0; t < 3; ++t)
 #pragma unroll
-      for (int t = 0; t < 3; ++t)
+      for (int jt = 0; jt < JT; ++jt) {
+        const u32x4_t a = tr_frag(sP[b] + 32 * t * PP + 16 * jt, PP, li, lg);
 #pragma unroll
-        for (int jt = 0; jt < JT; ++jt) {
-          const u32x4_t a = tr_frag(sP[b] + 32 * t * PP + 16 * jt, PP, li, lg);
-#pragma unroll
-          for (int ct = 0; ct < 4; ++ct)
-            acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(fq[ct]), acc[jt][ct], 0, 0, 0);
-        }
+        for (int ct = 0; ct < 4; ++ct)
+          acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(fq[ct]), acc[jt][ct], 0, 0, 0);
+      }
+  };
+  for (int m = 0; m < it.count; m += 32 * BUFS) {
+    step(m, 0);
+    if constexpr (BUFS == 2) {
+      if (m + 32 < it.count) step(m + 32, 1);
+    } else {
+      lds_barrier();   // read by everyone; the next step's loads stay in flight
     }
   }
   // lane: column li of each tile, rows j = 4 lg + e. Partial sums lie as
