@@ -78,8 +78,9 @@ size_t lq_adapters_forward_workspace(const lq_qweight* w, int64_t M, const lq_ad
 /*
  * Forward of M tokens, each with its own adapter.
  *   X      [M, K] bf16;  ids [M] int32 (4-byte aligned)
- *   route  lq_adapter_route's output for these ids and set->n, or NULL: built
- *          in the workspace when the call needs it
+ *   route  lq_adapter_route's output for these ids (so this M) and set->n, or
+ *          NULL: built in the workspace when the call needs it. Its contents
+ *          are not checked: one of another M or n sends the kernels out of range
  *   H      [M, N] of h_dtype (LQ_BF16 or LQ_F32), written
  *   t_save [M, r_max] float32, written if not NULL: t in its token's first r_a
  *          columns, 0 in the others and for tokens without an adapter

@@ -131,15 +131,19 @@ def _tokens_args(torch, M, qw, adapters, ids, route, device):
     if not (ids.is_cuda and ids.dtype is torch.int32 and ids.dim() == 1 and ids.size(0) == M and ids.is_contiguous()
             and ids.device == device):
         raise ValueError(f"ids must be contiguous int32 [{M}] on the tokens' device")
+    # a route of other sizes has its arrays elsewhere, and positions past this call's tokens
     if route is not None and not (
-            route.is_cuda and route.dtype is torch.int32 and route.is_contiguous() and route.device == device
+            getattr(route, "lq_route_of", None) == (M, adapters.n) and route.device == device
+            and route.dtype is torch.int32 and route.is_contiguous()
             and 4 * route.numel() >= lib.lq_adapter_route_bytes(M, adapters.n)):
-        raise ValueError("route is not one of these ids and this many adapters")
+        raise ValueError(f"route must be adapter_route's, of {M} ids and {adapters.n} adapters")
 
 
 def adapter_route(ids, n: int):
     """Tokens sorted by adapter (int32 buffer) for ids int32 [M] and sets of n
-    adapters; pass it to the calls of every projection of the step."""
+    adapters; pass it to the calls of every projection of the step. The buffer
+    carries (M, n) as lq_route_of: the calls take it for these sizes alone, and
+    no copy of it."""
     torch = _torch()
     _contig_cuda(ids, "ids")
     if ids.dtype != torch.int32 or ids.dim() != 1:
@@ -148,6 +152,7 @@ def adapter_route(ids, n: int):
     size = lib.lq_adapter_route_bytes(M, n)
     route = torch.empty(max(size // 4, 1), dtype=torch.int32, device=ids.device)
     _check(lib.lq_adapter_route(_ptr(ids), M, n, _ptr(route), size, _stream(ids.device)), "lq_adapter_route")
+    route.lq_route_of = (M, n)
     return route
 
 

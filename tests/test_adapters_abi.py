@@ -255,3 +255,87 @@ def test_oracle_clip():
     assert np.allclose(out[0], [3.0 / (5 + 1e-6), 0]) and np.allclose(out[1], 4.0 / (5 + 1e-6))
     norms, out = oad.clip(x, [0, 0, 0], 1, 1e4, 1e-6)
     assert all(np.array_equal(a, b) for a, b in zip(x, out))
+
+
+# ---- routes that are not the call's: refused by the helpers before any launch ----
+class FakeTensor:
+    """As much of a device tensor as the helpers look at; never dereferenced."""
+    is_cuda, device = True, "cuda:0"
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype = tuple(shape), dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def size(self, i):
+        return self.shape[i]
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+
+class Launched(Exception):
+    pass
+
+
+@pytest.fixture
+def host_only(lq, ad, monkeypatch):
+    """The helpers over fake tensors; the entry points that would launch raise Launched (adapter_route's returns)."""
+    import types
+
+    import torch
+
+    def launch(*args):
+        raise Launched
+    stub = types.SimpleNamespace(int32=torch.int32, float32=torch.float32, bfloat16=torch.bfloat16, uint8=torch.uint8,
+                                 empty=lambda n, dtype, device: FakeTensor((n,), dtype),
+                                 empty_strided=lambda shape, stride, dtype, device: FakeTensor(shape, dtype))
+    library = types.SimpleNamespace(**{name: getattr(lq.lib, name) for name in ad.SIGNATURES})
+    library.lq_adapter_route = lambda *args: lq.LQ_OK
+    library.lq_adapters_forward = library.lq_adapters_backward = launch
+    monkeypatch.setattr(ad, "_torch", lambda: stub)
+    monkeypatch.setattr(ad, "lib", library)
+    monkeypatch.setattr(ad, "_stream", lambda dev: None)
+    N, K, ranks = 128, 256, [8, 16, 5, 4]
+    desc, c_set = nf4(lq, N, K), make_set(ad, ranks)
+    qw = types.SimpleNamespace(N=N, K=K, device="cuda:0", ref=lambda: ctypes.byref(desc))
+    adapters = types.SimpleNamespace(N=N, K=K, device="cuda:0", n=len(ranks), r_max=16, r_sum=33,
+                                     ref=lambda: ctypes.byref(c_set))
+
+    def call(which, M, route):
+        ids, X = FakeTensor((M,), torch.int32), FakeTensor((M, K), torch.bfloat16)
+        if which == "forward":
+            ad.adapters_forward(qw, X, adapters, ids, route=route)
+        else:
+            ad.adapters_backward(qw, X, FakeTensor((M, N), torch.bfloat16), adapters, ids, route=route)
+    return types.SimpleNamespace(call=call, ids=lambda M: FakeTensor((M,), torch.int32), ad=ad, lib=lq.lib,
+                                 buffer=lambda words: FakeTensor((words,), torch.int32))
+
+
+@pytest.mark.parametrize("which", ["forward", "backward"])
+def test_a_route_of_other_tokens_or_adapters_is_refused(host_only, which):
+    """Such a route's positions lie elsewhere in the buffer, and its tokens past the call's: read as this call's it
+    would send the kernels out of range."""
+    h = host_only
+    for M in (1, 70, 128):                        # its own
+        with pytest.raises(Launched):
+            h.call(which, M, h.ad.adapter_route(h.ids(M), 4))
+        with pytest.raises(Launched):
+            h.call(which, M, None)
+    for M, tokens, n in [(70, 128, 4),            # the last, shorter batch with the route of a full one
+                         (70, 72, 4), (70, 71, 4), (70, 69, 4), (128, 70, 4),
+                         (70, 70, 6), (70, 70, 3), (70, 70, 1000)]:
+        if (tokens, n) in ((72, 4), (71, 4), (70, 6)):     # padded to the same size
+            assert h.lib.lq_adapter_route_bytes(tokens, n) == h.lib.lq_adapter_route_bytes(M, 4)
+        with pytest.raises(ValueError):
+            h.call(which, M, h.ad.adapter_route(h.ids(tokens), n))
+    # a buffer that no adapter_route call wrote
+    with pytest.raises(ValueError):
+        h.call(which, 70, h.buffer(h.lib.lq_adapter_route_bytes(70, 4) // 4))

@@ -602,3 +602,17 @@ def test_example(torch):
     first, last, h, want = mod.run()
     assert all(l < 0.2 * f for f, l in zip(first, last))
     assert torch.allclose(h[-1], want[-1], rtol=1e-4, atol=1e-4)     # no adapter: the frozen projection
+
+
+def test_a_route_of_another_batch_is_refused(lq, torch):
+    """The last, shorter batch with a full one's route, and a route of another number of adapters."""
+    L = Layer(lq, torch, 72, 128, 70, [8, 4, 16, 5])
+    full = torch.zeros(128, dtype=torch.int32, device="cuda")
+    own = lq.adapter_route(L.ids_dev, 4)
+    for route in (lq.adapter_route(full, 4), lq.adapter_route(L.ids_dev, 6), lq.adapter_route(full[:72], 4), own.clone()):
+        with pytest.raises(ValueError):
+            lq.adapters_forward(L.qw, L.X, L.set, L.ids_dev, route=route)
+        with pytest.raises(ValueError):
+            lq.adapters_backward(L.qw, L.X, L.G, L.set, L.ids_dev, route=route)
+    check_forward(lq, torch, L, route=own)
+    check_backward(lq, torch, L, route=own)
