@@ -324,7 +324,10 @@ __device__ __forceinline__ void dc_apply(const DcStep<RG>& o, const uint16_t* sT
     for (int g = 0; g < RG; ++g) {
       const f32x4_t d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(o.w[g]), as_bf16x8(tv), zero4(), 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[g][tt][e] = __builtin_fmaf(o.scale, mine ? d[e] : 0.0f, acc[g][tt][e]);
+      for (int e = 0; e < 4; ++e) {   // selected last: a scale that is not finite makes NaN of 0, too
+        const float with = __builtin_fmaf(o.scale, d[e], acc[g][tt][e]);
+        acc[g][tt][e] = mine ? with : acc[g][tt][e];
+      }
     }
   }
 }

@@ -616,3 +616,29 @@ def test_a_route_of_another_batch_is_refused(lq, torch):
             lq.adapters_backward(L.qw, L.X, L.G, L.set, L.ids_dev, route=route)
     check_forward(lq, torch, L, route=own)
     check_backward(lq, torch, L, route=own)
+
+
+def with_alpha(lq, L, a, alpha):
+    """L's adapters with another alpha for adapter a."""
+    return lq.AdapterSet([(A, B, alpha if i == a else al) for i, (A, B, al) in enumerate(L.adapters)])
+
+
+@pytest.mark.parametrize("M", [3, 16, 50, 64, 100, 300])
+@pytest.mark.parametrize("alpha", [float("inf"), -float("inf"), float("nan")])
+def test_a_scale_that_is_not_finite_stays_with_its_tokens(lq, torch, M, alpha):
+    L = Layer(lq, torch, 136, 128, M, [16, 8, 12], ids=np.arange(M) % 4 - 1)
+    bad = with_alpha(lq, L, 1, alpha)
+    mine = torch.from_numpy(L.ids == 1).cuda()
+    for dt in (torch.float32, torch.bfloat16):
+        H0, t0 = lq.adapters_forward(L.qw, L.X, L.set, L.ids_dev, out_dtype=dt)
+        H1, t1 = lq.adapters_forward(L.qw, L.X, bad, L.ids_dev, out_dtype=dt)
+        assert torch.equal(t0, t1)                       # t is not scaled
+        assert torch.equal(H0[~mine], H1[~mine])
+        assert not torch.isfinite(H1[mine]).any()
+    gx0, dA0, dB0 = lq.adapters_backward(L.qw, L.X, L.G, L.set, L.ids_dev)
+    gx1, dA1, dB1 = lq.adapters_backward(L.qw, L.X, L.G, bad, L.ids_dev)
+    assert torch.equal(gx0[~mine], gx1[~mine]) and not torch.isfinite(gx1[mine]).any()
+    p0, p1 = L.set.split(dA0, dB0), bad.split(dA1, dB1)
+    for a in (0, 2):
+        assert torch.equal(p0[a][0], p1[a][0]) and torch.equal(p0[a][1], p1[a][1])
+    assert not torch.isfinite(p1[1][0]).any() and not torch.isfinite(p1[1][1]).any()
