@@ -85,7 +85,10 @@ size_t lq_adapters_forward_workspace(const lq_qweight* w, int64_t M, const lq_ad
  *   t_save [M, r_max] float32, written if not NULL: t in its token's first r_a
  *          columns, 0 in the others and for tokens without an adapter
  * An adapter's values and its scale reach only its own tokens' outputs, also
- * where they are infinite or NaN. Errors: as lq_qlora_forward and lq_check_adapters.
+ * where they are infinite or NaN. An infinite t gives infinities by the
+ * equation; t's products with an infinite B are formed in parts, and give an
+ * infinity or NaN (likewise in the backward: an infinite u, and the infinities
+ * of A in grad_X, of X in dA, of G in dB). Errors: as lq_qlora_forward and lq_check_adapters.
  */
 int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const lq_adapter_set* set,
                         const int32_t* ids, const int32_t* route, void* H, int32_t h_dtype, float* t_save,

@@ -437,9 +437,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
     }
   }
   {
-    // t: its parts added in order, and split into bf16 terms whose sum is t to
-    // 16 bits more than H keeps (rows of tokens without an adapter hold
-    // anything: no step takes them). Token m's t is saved by workgroup m % grid.
+    // t: its parts added in order, and split into bf16 terms: two keep 16 bits
+    // of it, 8 more than a bf16 H, three all 24 (rows of tokens without an
+    // adapter hold anything: no step takes them). Token m's t is saved by workgroup m % grid.
     const int quads = p.v.rs / 4, nq = p.M * quads, nt = p.M * p.v.rs;
 #pragma unroll 2
     for (int i = threadIdx.x; i < nq; i += 64 * W) {
@@ -459,16 +459,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
         for (int e = 0; e < 4; ++e)
           if (j + e < p.v.r_max) p.t_out[m * p.v.r_max + j + e] = has ? sum[e] : 0.0f;
       }
+      float v[4] = {sum[0], sum[1], sum[2], sum[3]};
 #pragma unroll
       for (int q = 0; q < TERMS; ++q) {
-        uint2 bits;
-        bits.x = pack_bf16x2(sum[0], sum[1]);
-        bits.y = pack_bf16x2(sum[2], sum[3]);
+        const uint2 bits = {take_bf16_terms(v[0], v[1]), take_bf16_terms(v[2], v[3])};
         *reinterpret_cast<uint2*>(sT + (m * TERMS + q) * p.v.rs + j) = bits;
-        sum[0] -= bf16lo_to_f32(bits.x);
-        sum[1] -= bf16hi_to_f32(bits.x);
-        sum[2] -= bf16lo_to_f32(bits.y);
-        sum[3] -= bf16hi_to_f32(bits.y);
       }
     }
   }

@@ -27,7 +27,9 @@ struct AdapterView {
 };
 
 // s_a t and s_a u travel between the kernels as three bfloat16 terms, hi + mid
-// + lo = the float32 value exactly (3 x 8 significand bits), in sorted order:
+// + lo = the float32 value exactly (3 x 8 significand bits; short of it only
+// where a term falls below bfloat16's range), an infinity or NaN as three
+// copies of itself, in sorted order:
 // row p holds the token of sorted position p, its hi terms in columns [0, r8),
 // mid in [r8, 2 r8), lo in [2 r8, 3 r8) with r8 = r_a rounded up to a multiple
 // of 8 (zero columns past r_a); row stride 3 rs. Rows of tokens without an

@@ -411,9 +411,8 @@ __device__ __forceinline__ bool find_item(const int32_t* __restrict__ off, int n
 __device__ __forceinline__ void split3(float v, uint16_t (&o)[3]) {
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    const uint32_t b = pack_bf16x2(v, 0.0f) & 0xFFFFu;
-    o[k] = (uint16_t)b;
-    v -= bf16lo_to_f32(b);
+    float none = 0.0f;
+    o[k] = (uint16_t)take_bf16_terms(v, none);
   }
 }
 

@@ -26,6 +26,22 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float bf16lo_to_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi_to_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+// Takes the next bfloat16 term (the nearest) off each of lo and hi: a finite
+// float32 is the sum of three. One past the largest bfloat16 gives that; an
+// infinity or NaN gives itself and stays, so that all of its terms are alike and
+// their products with one value add up to an infinity, not to inf - inf.
+__device__ __forceinline__ uint32_t take_bf16_terms(float& lo, float& hi) {
+  uint32_t w = pack_bf16x2(lo, hi);
+  if ((__float_as_uint(lo) & 0x7FFFFFFFu) < 0x7F800000u) {
+    if ((w & 0x7FFFu) == 0x7F80u) w -= 1u;
+    lo -= bf16lo_to_f32(w);
+  }
+  if ((__float_as_uint(hi) & 0x7FFFFFFFu) < 0x7F800000u) {
+    if ((w & 0x7FFF0000u) == 0x7F800000u) w -= 0x10000u;
+    hi -= bf16hi_to_f32(w);
+  }
+  return w;
+}
 
 __device__ __forceinline__ bf16x8_t as_bf16x8(u32x4_t v) { return __builtin_bit_cast(bf16x8_t, v); }
 

@@ -642,3 +642,54 @@ def test_a_scale_that_is_not_finite_stays_with_its_tokens(lq, torch, M, alpha):
     for a in (0, 2):
         assert torch.equal(p0[a][0], p1[a][0]) and torch.equal(p0[a][1], p1[a][1])
     assert not torch.isfinite(p1[1][0]).any() and not torch.isfinite(p1[1][1]).any()
+
+
+@pytest.mark.parametrize("M", [4, 16, 50, 64, 100, 300, 4100])
+def test_an_infinite_t_or_u_stays_infinite(lq, torch, M):
+    """An infinity in a row of A makes t infinite there, and an infinity in a row of B makes u infinite: the
+    results are infinities of the definition's sign, not NaN. One token has the adapter, so that no sum mixes signs."""
+    K, N = 128, 136
+    ids = np.arange(M) % 3 - 1
+    ids[ids == 1] = 2
+    ids[M // 2] = 1
+    for which in ("t", "u"):
+        L = Layer(lq, torch, N, K, M, [16, 8, 12], ids=ids)
+        assert bool((L.X != 0).all()) and bool((L.G != 0).all())
+        A, B, _ = L.adapters[1]
+        (A if which == "t" else B)[3, 5] = float("inf")
+        L.host[1] = (f64(A), f64(B), L.host[1][2])
+        if which == "t":
+            ref = oad.forward(L.Wd, f64(L.X), L.host, ids)
+            for dt in (torch.float32, torch.bfloat16):
+                H, t = lq.adapters_forward(L.qw, L.X, L.set, L.ids_dev, out_dtype=dt)
+                assert np.isinf(ref[1][M // 2, 3]) and np.isinf(ref[0][M // 2]).all()
+                assert f64(t)[M // 2, 3] == ref[1][M // 2, 3] and np.array_equal(f64(H)[M // 2], ref[0][M // 2])
+                assert torch.isfinite(H[L.ids_dev != 1]).all()
+            for saved in (None, t):
+                _, _, dB = lq.adapters_backward(L.qw, L.X, L.G, L.set, L.ids_dev, t=saved)
+                got, want = f64(L.set.split(torch.empty(36, K), dB)[1][1]), oad.backward(L.Wd, f64(L.X), f64(L.G), L.host, ids)[0][2][1]
+                assert np.isinf(want[:, 3]).all() and np.array_equal(got[:, 3], want[:, 3])
+                assert np.isfinite(np.delete(got, 3, 1)).all()
+        else:
+            gx, dA, _ = lq.adapters_backward(L.qw, L.X, L.G, L.set, L.ids_dev)
+            rX, rA, _ = oad.backward(L.Wd, f64(L.X), f64(L.G), L.host, ids)[0]
+            assert np.isinf(rX[M // 2]).all() and np.array_equal(f64(gx)[M // 2], rX[M // 2])
+            assert torch.isfinite(gx[L.ids_dev != 1]).all()
+            got = f64(dA[16:24])
+            assert np.isinf(rA[1][5]).all() and np.array_equal(got[5], rA[1][5])
+            assert np.isfinite(np.delete(got, 5, 0)).all()
+
+
+@pytest.mark.parametrize("M", [3, 70])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_a_finite_t_past_the_largest_bfloat16(lq, torch, M, out):
+    """t = 2^128 (1 - 2^-10): a float32 value that rounds to an infinite bfloat16."""
+    L = Layer(lq, torch, 72, 64, M, [8], ids=np.zeros(M, dtype=int))
+    A, B, _ = L.adapters[0]
+    A.zero_(), L.X.zero_(), B.fill_(2.0 ** -64)
+    L.X[:, 0], A[0, 0] = (2 - 2.0 ** -7) * 2.0 ** 63, 2.0 ** 64
+    L.X[:, 1], A[0, 1] = 1.5 * 2.0 ** 60, 2.0 ** 59
+    L.set = lq.AdapterSet([(A, B, 8.0)])
+    L.host = [(f64(A), f64(B), 1.0)]
+    _, t = check_forward(lq, torch, L, out)
+    assert (f64(t)[:, 0] == 2.0 ** 128 * (1 - 2.0 ** -10)).all() and torch.isinf(t[:, 0].to(torch.bfloat16)).all()
