@@ -30,6 +30,12 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
 }
 __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+// At most `n` loads outstanding and no reads of LDS, then the barrier: past it
+// a buffer that everyone has read may be refilled.
+template <int n>
+__device__ __forceinline__ void ring_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(n) : "memory");
+}
 
 // The adapter of the sorted positions from pos on, inside a tile that ends at
 // mend: its columns are steps of 64 (8 runs of 8) of TERMS copies of Lb.
@@ -307,7 +313,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
     load_x(Any(), 1, 0, 1);
     load_y(Any(), 1, 0, 1);
     load_y(Any(), 1, 1, 1);
-    wait_vm<10>();
+    ring_barrier<10>();
   } else {
     load_x(Any(), 0, 0, 0);
     load_y(Any(), 0, 0, 0);
@@ -315,9 +321,8 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
     load_x(Any(), 1, 0, 1);
     load_y(Any(), 1, 0, 1);
     load_y(Any(), 1, 1, 1);
-    wait_vm<QX + 2 * QY>();
+    ring_barrier<QX + 2 * QY>();
   }
-  barrier();
   if (late) barrier();
   const int nplain = nk - 3;   // steps that load whole steps of the contraction: without a branch
   while (it < nplain) step(Plain());
@@ -333,7 +338,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   if (!whole.steps && next.steps) {
     Adapter cur = next;
     int kt = 0;
-    barrier();   // everyone has read the last step
+    ring_barrier<0>();   // everyone has read the last step
     lora_x(cur, 0, 0, 0);
     if constexpr (XP == 2) lora_x(cur, 0, 1, 0);
     lora_y(cur, 0, 0, 0);
@@ -344,8 +349,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
         cur = adapter_at<TERMS>(p, cur.hi, mend);
         kt = 0;
       }
-      wait_vm<0>();
-      barrier();   // this step has landed, and the other buffer is read
+      ring_barrier<0>();   // this step has landed, and the other buffer is read
       if (cur.steps) {
         lora_x(cur, kt, 0, b ^ 1);
         if constexpr (XP == 2) lora_x(cur, kt, 1, b ^ 1);
@@ -511,8 +515,7 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
   const int ox = (wm * 32 + li) * GK, oy = (wn * 32 + li) * GK;
   u32x4_t fx[2][2], fy[2][2];
   auto turn = [&](int i) {   // the group's step i is in LDS, and step i - 1 read by everyone
-    wait_vm<(S_RING - 2) * 4>();
-    barrier();
+    ring_barrier<(S_RING - 2) * 4>();
     load(GROUPS * (i + S_RING - 1) + group, (i + S_RING - 1) % S_RING);
     const int buf = i % S_RING;
 #pragma unroll
@@ -562,7 +565,7 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
   }
   wait_vm<0>();   // the loads past the last step
   if constexpr (GROUPS == 2) {   // group g finishes the weight rows of c = g, group 0's sum first
-    __syncthreads();
+    ring_barrier<0>();   // the tiles are read: the sums take their place
     f32x4_t* sum = reinterpret_cast<f32x4_t*>(lds.x) + 128 * w4 + lane;   // [group][w4][r][lane]
 #pragma unroll
     for (int r = 0; r < 2; ++r) sum[512 * group + 64 * r] = group ? acc[0][r] : acc[1][r];

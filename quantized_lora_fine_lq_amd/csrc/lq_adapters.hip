@@ -591,8 +591,8 @@ __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJob j0, DownJob 
   for (int k = 0; k < DT_RING - 1; ++k) load(s0 + k);
   const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
   for (int s = s0; s < s1; ++s) {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((DT_RING - 2) * (2 + QW)) : "memory");   // this wave's share of step s
-    asm volatile("s_barrier" ::: "memory");                                            // everyone's; s - 1 is read
+    // this wave's share of step s is there and its reads of s - 1 are done; then everyone's
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((DT_RING - 2) * (2 + QW)) : "memory");
     load(s + DT_RING - 1);
     const int buf = (s - s0) % DT_RING;
 #pragma unroll
