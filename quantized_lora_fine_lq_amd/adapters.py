@@ -79,6 +79,9 @@ class AdapterSet:
         if not 1 <= len(self.adapters) <= LQ_ADAPTERS_MAX:
             raise ValueError(f"a set has 1 to {LQ_ADAPTERS_MAX} adapters")
         self.n = len(self.adapters)
+        for a, (A, B, _) in enumerate(self.adapters):
+            if A.dim() != 2 or B.dim() != 2 or A.shape[0] < 1:
+                raise ValueError(f"adapter {a}: A and B must be matrices of a rank of at least 1")
         self.K, self.N = self.adapters[0][0].shape[1], self.adapters[0][1].shape[0]
         self.device = self.adapters[0][0].device
         self._host = (lq_adapter * self.n)()

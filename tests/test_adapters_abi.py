@@ -339,3 +339,14 @@ def test_a_route_of_other_tokens_or_adapters_is_refused(host_only, which):
     # a buffer that no adapter_route call wrote
     with pytest.raises(ValueError):
         h.call(which, 70, h.buffer(h.lib.lq_adapter_route_bytes(70, 4) // 4))
+
+
+def test_adapters_that_are_no_matrices_are_refused_in_words(ad):
+    import torch
+    m = lambda *shape: FakeTensor(shape, torch.bfloat16)
+    ok = (m(8, 256), m(128, 8), 1.0)
+    for bad in [(m(0, 256), m(128, 0), 1.0), (m(256), m(128, 8), 1.0), (m(8, 256), m(128), 1.0),
+                (m(1, 8, 256), m(128, 8), 1.0), (m(), m(128, 8), 1.0)]:
+        for adapters in ([bad], [ok, bad]):
+            with pytest.raises(ValueError):
+                ad.AdapterSet(adapters)
