@@ -693,3 +693,65 @@ def test_a_finite_t_past_the_largest_bfloat16(lq, torch, M, out):
     L.host = [(f64(A), f64(B), 1.0)]
     _, t = check_forward(lq, torch, L, out)
     assert (f64(t)[:, 0] == 2.0 ** 128 * (1 - 2.0 ** -10)).all() and torch.isinf(t[:, 0].to(torch.bfloat16)).all()
+
+
+SHARES = [
+    # N, K, M, ranks, ids, out: row products in column shares (tiles of 16, 32, 64 and 128 of the adapter's rows), K % 128
+    (72, 1088, 4100, [16, 8, 5], "mixed", "bf16"),
+    (136, 2048, 4099, [16, 16, 3], "runs", "f32"),
+    (200, 1536, 2049, [32, 7], "runs", "bf16"),
+    (64, 4160, 1031, [64, 24, 9], "mixed", "f32"),
+    (80, 1024, 515, [128, 1], "runs", "f32"),
+    # tiles of 256 x 256 with more steps of the contraction than the loads run ahead; K % 64 == 0, begun at an eighth per XCD
+    (8184, 1024, 4001, [16, 40, 7], "mixed", "bf16"),
+    (8184, 1024, 4001, [16, 40, 7], "mixed", "f32"),
+    (8192, 576, 4096, [64], "runs", "bf16"),
+    # tiles of 256 x 128 likewise
+    # tiles of 256 x 128 likewise, N % 4
+    (4090, 1088, 2047, [16, 8, 64, 24], "runs", "bf16"),
+    (4090, 1088, 2047, [16, 8, 64, 24], "mixed", "f32"),
+]
+
+
+@pytest.mark.parametrize("case", SHARES, ids=str)
+def test_forward_long_contraction(lq, torch, case):
+    N, K, M, ranks, ids, out = case
+    L = Layer(lq, torch, N, K, M, ranks, ids)
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    H, t = lq.adapters_forward(L.qw, L.X, L.set, L.ids_dev, out_dtype=dt)
+    (ref, mag, lora), _, _, _ = reference64(torch, L)
+    bound = (K + 3 * max(ranks) + 8) * U * (mag + lora) + K * U * lora
+    if out == "bf16":
+        bound += 2.0 ** -16 * lora + 2.0 ** -8 * ref.abs() + 2.0 ** -130
+    assert ((H.double() - ref).abs() <= bound).all()
+    X = L.X.double()
+    for a, (A, _, _) in enumerate(L.adapters):
+        m, r = (L.ids_dev == a).nonzero()[:, 0], A.shape[0]
+        want, tmag = X[m] @ A.double().T, X[m].abs() @ A.double().abs().T
+        assert ((t[m, :r].double() - want).abs() <= (K + 8) * U * tmag).all()
+        assert not t[m, r:].any()
+    assert not t[L.ids_dev < 0].any()
+    again = lq.adapters_forward(L.qw, L.X, L.set, L.ids_dev, out_dtype=dt)
+    assert torch.equal(again[0], H) and torch.equal(again[1], t)
+
+
+@pytest.mark.parametrize("case", [
+    # N, K, M, ranks, ids, weight: u and t in column shares of their own lengths
+    (1024, 1088, 2051, [32, 16, 7], "runs", "nf4_dq"),
+    (2056, 1024, 4100, [16, 5], "mixed", "nf4_f32"),
+    (1032, 3136, 1033, [64, 24], "runs", "codebook"),
+    (1024, 8192, 4001, [16, 40], "mixed", "nf4_dq"),      # tiles of 256 x 256, begun at an eighth per XCD
+], ids=str)
+@pytest.mark.parametrize("saved", [False, True])
+def test_backward_long_contraction(lq, torch, case, saved):
+    N, K, M, ranks, ids, weight = case
+    L = Layer(lq, torch, N, K, M, ranks, ids, weight)
+    t = lq.adapters_forward(L.qw, L.X, L.set, L.ids_dev)[1] if saved else None
+    gx, dA, dB = lq.adapters_backward(L.qw, L.X, L.G, L.set, L.ids_dev, t=t)
+    _, (ref, mag, lora), rA, rB = reference64(torch, L, t)
+    bound = (N + 3 * max(ranks) + 8) * U * (mag + lora) + N * U * lora + 2.0 ** -16 * lora + 2.0 ** -8 * ref.abs()
+    assert ((gx.double() - ref).abs() <= bound + 2.0 ** -130).all()
+    for a, (da, db) in enumerate(L.set.split(dA, dB)):
+        tokens = int((L.ids == a).sum())
+        assert ((da.double() - rA[a][0]).abs() <= (3 * tokens + N + 16) * U * rA[a][1]).all()
+        assert ((db.double() - rB[a][0]).abs() <= (3 * tokens + (0 if saved else K) + 16) * U * rB[a][1]).all()
