@@ -7,13 +7,26 @@ from there on. So before such a barrier the wave waits for its own reads of LDS
 leaving it to where the compiler puts the products that use the fragments. (At
 a barrier of its own the compiler keeps account of them.)
 """
+import importlib.util
 import os
 import re
 import subprocess
 
 import pytest
 
-import quantized_lora_fine_lq_amd.build as build
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _build_module():
+    # by path: importing the package would load the library, and with it a HIP
+    # runtime, before the GPU tests of the same run load torch's
+    spec = importlib.util.spec_from_file_location("lq_build", os.path.join(ROOT, "quantized_lora_fine_lq_amd", "build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+build = _build_module()
 
 KERNELS = {"lq_adapters.hip": ["k_adapter_down_tiles"],
            "lq_adapter_gemm.hip": ["k_adapter_gemm_small", "k_adapter_gemm"]}
