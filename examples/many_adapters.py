@@ -57,7 +57,8 @@ def run(steps: int = 60, lr: float = 0.02, max_norm: float = 1.0, seed: int = 0)
         _, dA, dB = lq.adapters_backward(qw, X, G, adapters, ids, t=t, need_grad_x=False, route=route)
         grads = adapters.split(dA, dB)
         flat = [g for ab in grads for g in ab]
-        lq.clip_grad_norm(lq.GradList(flat, [a for a in range(n) for _ in range(2)]), max_norm)   # by job
+        # by job; a list a step, since adapters_backward returns new tensors
+        lq.clip_grad_norm(lq.GradList(flat, [a for a in range(n) for _ in range(2)]), max_norm)
         for a, ab in enumerate(grads):                       # Adam, into the masters and the kernels' copies
             for k, g in enumerate(ab):
                 m, v = moments[a][2 * k], moments[a][2 * k + 1]

@@ -72,7 +72,9 @@ size_t lq_adapter_route_bytes(int64_t M, int32_t n);
  */
 int lq_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_t* route, size_t bytes, void* stream);
 
-/* Workspace bytes of lq_adapters_forward (0 for an invalid argument). */
+/* Workspace bytes of lq_adapters_forward (0 for an invalid argument): up to 64
+ * tokens of an NF4 weight with K <= 49152 about the size of X and t; otherwise
+ * above all the weight in bfloat16, 2 N K bytes. */
 size_t lq_adapters_forward_workspace(const lq_qweight* w, int64_t M, const lq_adapter_set* set);
 
 /*
@@ -94,7 +96,9 @@ int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const
                         const int32_t* ids, const int32_t* route, void* H, int32_t h_dtype, float* t_save,
                         void* workspace, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of lq_adapters_backward (0 for an invalid argument). */
+/* Workspace bytes of lq_adapters_backward (0 for an invalid argument): above all
+ * the transposed weight in bfloat16, 2 N K bytes, twice that for a codebook
+ * weight. */
 size_t lq_adapters_backward_workspace(const lq_qweight* w, int64_t M, const lq_adapter_set* set);
 
 /*

@@ -219,7 +219,11 @@ class GradList:
     """Gradient tensors (contiguous, f32 / bf16 / f16, any element alignment)
     prepared for grad_norm and clip_grad_norm; groups[i] is the group whose
     norm tensor i counts in (default: one group for all). Keeps the tensors;
-    their values may change between calls, their addresses may not."""
+    their values may change between calls, their addresses may not. Building a
+    list walks its tensors on the host and copies a table to the device, for
+    which the host waits (44 us for 14 tensors, 2.3 ms for 1792): keep it where
+    the gradients stay in place. adapters_backward returns new tensors every
+    time; lq_adapters_backward itself writes where its caller says."""
 
     def __init__(self, tensors: Sequence, groups: Optional[Sequence[int]] = None, n_groups: Optional[int] = None,
                  device=None):

@@ -23,7 +23,6 @@ __device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
-
 // Wait until at most `n` of the wave's memory operations are outstanding.
 template <int n>
 __device__ __forceinline__ void wait_vm() {
@@ -101,10 +100,10 @@ __device__ __forceinline__ void store4(const AdapterGemm& p, int64_t row, int64_
 // read the part, which puts five to seven quadrants between a load and its
 // use. BN = 128: waves 4 x 2 of 64 x 64, two halves a step, three buffers.
 //
-// Measured: 4096 tokens, 4096 -> 11008, rank 64: 324 to 383 us with the clock,
-// 0.98 to 1.16 PFLOP/s; 1999 tokens, 4096 -> 4096: 70.6 us, 0.96 PFLOP/s;
-// backward of 2048 tokens 69.3. The library's plain product reaches 0.87 to
-// 1.09 PFLOP/s at such sizes and 1.38 at 8192^3. Bound by the matrix cores'
+// Measured: 4096 tokens, 4096 -> 11008, rank 64: 325 to 394 us with the clock,
+// 0.95 to 1.15 PFLOP/s; 1999 tokens, 4096 -> 4096: 71 us, 0.95 PFLOP/s;
+// backward of 2048 tokens 70. The library's plain product reaches 0.87 PFLOP/s
+// at the first size, 1.09 at 2048 tokens and 1.38 at 8192^3. Bound by the matrix cores'
 // issue and the clock they leave; what the slots lose is the edges (a last
 // round that is not full, the start of a tile) and, where a tile's tokens
 // belong to several adapters, their steps at its end.
@@ -401,8 +400,9 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
 // per SIMD beside it: past 256 tiles another workgroup's; up to 256 the
 // workgroup has a second group of waves that takes every other step through a
 // ring of its own, and the two sums meet at the end. (A ring of eight buffers
-// instead did not shorten the chain.) Measured, N = K = 4096: 250 tokens 20 us
-// (one group: 27), 500 tokens 30 (two groups: 37).
+// instead did not shorten the chain.) Measured, N = K = 4096, 8 adapters of rank
+// 16, bfloat16: 250 tokens 21 us (one group: 25), 500 tokens 31 (two groups:
+// 38); 250 tokens of 20 adapters in float32 24.
 //
 // The adapters' steps follow the base contraction's in the same rings, from a
 // table made at the start; the products of each go to its own tokens' columns
