@@ -13,7 +13,9 @@ Two layers, both argument marshalling only:
 Many adapters over one projection, and the clipping of their gradients
 (include/lq_adapters.h), are in ``adapters.py`` and exported here too:
 ``AdapterSet``, ``adapter_route``, ``adapters_forward``,
-``adapters_backward``, ``GradList``, ``grad_norm``, ``clip_grad_norm``.
+``adapters_backward``, ``GradList``, ``grad_norm``, ``clip_grad_norm``. So is
+dropout without a stored mask (include/lq_dropout.h, ``dropouts.py``):
+``dropout_key``, ``Dropout``, ``dropout``.
 
 Importing fails loudly if liblq.so has not been built
 (``python quantized_lora_fine_lq_amd/build.py``).
@@ -538,3 +540,5 @@ def quantize_codebook(W, row_bits, thresholds, blocksize: int = 64):
 # many adapters over one projection, gradient norms and clipping
 from .adapters import (AdapterSet, GradList, adapter_route, adapters_backward, adapters_forward,  # noqa: E402
                        clip_grad_norm, grad_norm)
+# dropout from a counter-based generator
+from .dropouts import Dropout, dropout, dropout_key  # noqa: E402

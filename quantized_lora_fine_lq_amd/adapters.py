@@ -159,9 +159,16 @@ def adapter_route(ids, n: int):
     return route
 
 
-def adapters_forward(qw: QWeight, X, adapters: AdapterSet, ids, out_dtype=None, save_t: bool = True, route=None):
+def _drop_args(drop, device):
+    if drop.device != device:
+        raise ValueError("the dropout key is on another device")
+
+
+def adapters_forward(qw: QWeight, X, adapters: AdapterSet, ids, out_dtype=None, save_t: bool = True, route=None,
+                     dropout=None):
     """H[m] = W' X[m] + (alpha_a / r_a) B_a A_a X[m] with a = ids[m] (outside
-    [0, n): the base weight alone). Returns (H [M, N], t [M, r_max] f32 or None)."""
+    [0, n): the base weight alone). Returns (H [M, N], t [M, r_max] f32 or None).
+    dropout (a Dropout): the adapters see dropout(X) in place of X."""
     torch = _torch()
     if out_dtype is None:
         out_dtype = torch.bfloat16
@@ -175,6 +182,14 @@ def adapters_forward(qw: QWeight, X, adapters: AdapterSet, ids, out_dtype=None, 
     N, r, w, s, empty = qw.N, adapters.r_max, qw.ref(), adapters.ref(), torch.empty_strided
     H = empty((M, N), (N, 1), dtype=out_dtype, device=dev)
     t = empty((M, r), (r, 1), dtype=torch.float32, device=dev) if save_t else None
+    if dropout is not None:
+        _drop_args(dropout, dev)
+        ws_bytes = lib.lq_adapters_forward_dropout_workspace(w, M, s)
+        ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
+        _check(lib.lq_adapters_forward_dropout(w, X.data_ptr(), M, s, ids.data_ptr(), _at(route), dropout.ref(),
+                                               H.data_ptr(), LQ_F32 if f32 else LQ_BF16, _at(t), ws.data_ptr(),
+                                               ws_bytes, _stream(dev)), "lq_adapters_forward_dropout")
+        return H, t
     ws_bytes = lib.lq_adapters_forward_workspace(w, M, s)
     ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
     _check(lib.lq_adapters_forward(w, X.data_ptr(), M, s, ids.data_ptr(), None if route is None else route.data_ptr(),
@@ -184,10 +199,11 @@ def adapters_forward(qw: QWeight, X, adapters: AdapterSet, ids, out_dtype=None, 
 
 
 def adapters_backward(qw: QWeight, X, G, adapters: AdapterSet, ids, t=None, need_grad_x: bool = True,
-                      need_dA: bool = True, need_dB: bool = True, route=None):
+                      need_dA: bool = True, need_dB: bool = True, route=None, dropout=None):
     """Returns (grad_X bf16 [M, K], dA f32 [sum of ranks, K], dB f32 [N * sum of
     ranks]), each None if not needed; adapters.split(dA, dB) gives them by
-    adapter. t: the forward's, or None to form it again from X."""
+    adapter. t: the forward's, or None to form it again from X. dropout: the
+    forward's, on the key as it stood there."""
     torch = _torch()
     dev = qw.device
     _tokens(torch, G, "G", qw.N, dev)
@@ -204,6 +220,14 @@ def adapters_backward(qw: QWeight, X, G, adapters: AdapterSet, ids, t=None, need
     gx = empty((M, K), (K, 1), dtype=torch.bfloat16, device=dev) if need_grad_x else None
     dA = empty((adapters.r_sum, K), (K, 1), dtype=f32, device=dev) if need_dA else None
     dB = empty((qw.N * adapters.r_sum,), (1,), dtype=f32, device=dev) if need_dB else None
+    if dropout is not None:
+        _drop_args(dropout, dev)
+        ws_bytes = lib.lq_adapters_backward_dropout_workspace(w, M, s)
+        ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
+        _check(lib.lq_adapters_backward_dropout(w, _at(X), G.data_ptr(), M, s, ids.data_ptr(), _at(route),
+                                                dropout.ref(), _at(t), _at(gx), _at(dA), _at(dB), ws.data_ptr(),
+                                                ws_bytes, _stream(dev)), "lq_adapters_backward_dropout")
+        return gx, dA, dB
     ws_bytes = lib.lq_adapters_backward_workspace(w, M, s)
     ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
     _check(lib.lq_adapters_backward(w, _at(X), G.data_ptr(), M, s, ids.data_ptr(), _at(route), _at(t), _at(gx), _at(dA),

@@ -61,6 +61,52 @@ __device__ __forceinline__ Adapter adapter_at(const AdapterGemm& p, int64_t pos,
   return s;
 }
 
+// Which of a lane's outputs dropout keeps: of the token at position pw + 16 rt +
+// li, output cw + 16 ct + 4 lg + e, bit 8 ct + 4 (rt % 2) + e of word rt / 2. A
+// generator block spans the 4 outputs of two lanes, 16 apart: for tokens rt and
+// rt + 1 the even one runs the first's block, the odd one the second's, and they
+// exchange halves. Past the last position: any bits. One block after the other:
+// the accumulators leave few registers.
+template <int RT>
+struct Kept {
+  uint32_t w[RT / 2];
+};
+template <int CT, int RT>
+__device__ __forceinline__ Kept<RT> kept_outputs(const DropView& d, const int32_t* perm, int64_t M, int64_t ncols,
+                                                 int64_t pw, int64_t cw) {
+  static_assert(CT <= 4, "eight bits a tile of 16 outputs");
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const DropGen g = drop_gen(d);
+  const bool odd = lg & 1;
+  int32_t token[RT / 2];
+#pragma unroll
+  for (int k = 0; k < RT / 2; ++k) token[k] = perm[min(pw + 16 * (2 * k + odd) + li, M - 1)];
+  Kept<RT> keep;
+#pragma unroll
+  for (int k = 0; k < RT / 2; ++k) {
+    const int64_t first = token[k] * (ncols / 8) + (cw >> 3) + (lg >> 1);
+    uint32_t word = 0;
+#pragma unroll 1
+    for (int ct = 0; ct < CT; ++ct) {
+      const u32x4_t b = drop_bits(g, (uint64_t)(first + 2 * ct));
+      const uint32_t o0 = __shfl_xor(odd ? b[0] : b[2], 16), o1 = __shfl_xor(odd ? b[1] : b[3], 16);
+      const uint32_t w[4] = {odd ? o0 : b[0], odd ? o1 : b[1], odd ? b[2] : o0, odd ? b[3] : o1};
+      uint32_t eight = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) eight |= (uint32_t)(((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) >= d.T) << e;
+      word |= eight << (8 * ct);
+    }
+    keep.w[k] = word;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  return keep;
+}
+
+// v where bit `at` of keep is set, else +0 (also of an infinity or NaN).
+__device__ __forceinline__ float kept_value(float v, uint32_t keep, int at) {
+  return __uint_as_float(__float_as_uint(v) & (uint32_t)__builtin_amdgcn_sbfe((int)keep, (uint32_t)at, 1u));
+}
+
 // A lane's 4 consecutive outputs c .. c + 3 of one token.
 template <bool OUT_F32>
 __device__ __forceinline__ void store4(const AdapterGemm& p, int64_t row, int64_t c, const f32x4_t& v) {
@@ -107,7 +153,10 @@ __device__ __forceinline__ void store4(const AdapterGemm& p, int64_t row, int64_
 // issue and the clock they leave; what the slots lose is the edges (a last
 // round that is not full, the start of a tile) and, where a tile's tokens
 // belong to several adapters, their steps at its end.
-template <int BN, bool OUT_F32, bool BWD>
+//
+// DROP (grad_X behind dropout): the adapters' part is always formed apart, after
+// the main loop, and added where the generator keeps the output.
+template <int BN, bool OUT_F32, bool BWD, bool DROP>
 __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   constexpr bool BIG = BN == 256;
   constexpr int WN = BIG ? 4 : 2, WM = 8 / WN;         // waves over weight rows, tokens
@@ -201,6 +250,9 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
       const bool ok = plain.value || !BWD || k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (0 * NaN is not 0)
 #pragma unroll
       for (int q = 0; q < QX; ++q) load_lds16(ok ? px[i][q] + k0 : p.zeros, lds.x[buf] + xrow(i, q) * GK);
+    } else if constexpr (DROP) {
+#pragma unroll
+      for (int q = 0; q < QX; ++q) load_lds16(p.zeros, lds.x[buf] + xrow(i, q) * GK);
     } else {
       lora_x(whole, it - nk, i, buf);
     }
@@ -210,6 +262,9 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
       const int64_t k0 = column(it);
 #pragma unroll
       for (int q = 0; q < QY; ++q) load_lds16(py[i][q] + k0, lds.y[buf] + yrow(i, q) * GK);
+    } else if constexpr (DROP) {
+#pragma unroll
+      for (int q = 0; q < QY; ++q) load_lds16(p.zeros, lds.y[buf] + yrow(i, q) * GK);
     } else {
       lora_y(whole, it - nk, i, buf);
     }
@@ -262,7 +317,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
 
   const bool late = wave >= 4;   // the group that works one slot behind
   Adapter next = adapter_at<TERMS>(p, m0, mend);
-  if (next.steps && next.hi == mend) whole = next;
+  if (!DROP && next.steps && next.hi == mend) whole = next;
   const int nsteps = nk + whole.steps;
   int it = 0, buf = 0;
   auto step = [&](auto plain) {
@@ -334,14 +389,19 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   // A tile of several adapters: one after the other, each one's products formed
   // apart and added to its own tokens' columns alone, so that an adapter's
   // infinities and NaN stay with its tokens.
-  if (!whole.steps && next.steps) {
+  // (DROP: without the branch, across which the compiler would hold the sums twice.)
+  if (DROP || (!whole.steps && next.steps)) {
+    Kept<RT> keep{};
+    if constexpr (DROP) keep = kept_outputs<CT, RT>(p.drop, p.rt.perm, p.M, p.Ncols, pw, cw);
     Adapter cur = next;
     int kt = 0;
     ring_barrier<0>();   // everyone has read the last step
-    lora_x(cur, 0, 0, 0);
-    if constexpr (XP == 2) lora_x(cur, 0, 1, 0);
-    lora_y(cur, 0, 0, 0);
-    lora_y(cur, 0, 1, 0);
+    if (!DROP || cur.steps) {
+      lora_x(cur, 0, 0, 0);
+      if constexpr (XP == 2) lora_x(cur, 0, 1, 0);
+      lora_y(cur, 0, 0, 0);
+      lora_y(cur, 0, 1, 0);
+    }
     for (int b = 0; cur.steps; b ^= 1) {
       const int64_t lo = cur.lo, hi = cur.hi;
       if (++kt >= cur.steps) {
@@ -364,6 +424,9 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
         for (int r = 0; r < 4; ++r) {
           const int64_t pos = pw + 16 * (xi * 4 + r) + li;
           const bool mine = pos >= lo && pos < hi;
+          if constexpr (DROP)   // or each bit's mask would be formed before the loop and held
+#pragma unroll
+            for (uint32_t& w : keep.w) asm volatile("" : "+v"(w));
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
             f32x4_t d = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -372,7 +435,11 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
               d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fy[c / (CT / 2)][u][c % (CT / 2)]), as_bf16x8(fx[u][r]),
                                                           d, 0, 0, 0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[c][xi * 4 + r][e] += mine ? d[e] : 0.0f;
+            for (int e = 0; e < 4; ++e) {
+              const int rt = xi * 4 + r;
+              const float add = DROP ? kept_value(d[e], keep.w[rt / 2], 8 * c + 4 * (rt % 2) + e) : d[e];
+              acc[c][xi * 4 + r][e] += mine ? add : 0.0f;
+            }
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -416,7 +483,7 @@ struct SmallStep {
   int lo, hi;              // its positions of the tile
 };
 
-template <int GROUPS, bool OUT_F32, bool BWD>
+template <int GROUPS, bool OUT_F32, bool BWD, bool DROP>
 __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(AdapterGemm p) {
   constexpr int TERMS = OUT_F32 ? 3 : 2;
   struct __attribute__((aligned(16))) Lds {
@@ -535,6 +602,8 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
         for (int r = 0; r < 2; ++r)
           acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fy[u][c]), as_bf16x8(fx[u][r]), acc[c][r], 0, 0, 0);
   };
+  uint32_t keep = 0;
+  if (DROP && steps > nk) keep = kept_outputs<2, 2>(p.drop, p.rt.perm, p.M, p.Ncols, m0 + wm * 32, n0 + wn * 32).w[0];
   int i = 0;
   for (; GROUPS * (i + 1) <= nk; ++i) {
     turn(i);
@@ -558,7 +627,10 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
           for (int u = 0; u < 2; ++u)
             d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fy[u][c]), as_bf16x8(fx[u][r]), d, 0, 0, 0);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[c][r][e] += mine ? d[e] : 0.0f;
+          for (int e = 0; e < 4; ++e) {
+            const float add = DROP ? kept_value(d[e], keep, 8 * c + 4 * r + e) : d[e];
+            acc[c][r][e] += mine ? add : 0.0f;
+          }
         }
       }
     }
@@ -616,9 +688,10 @@ hipError_t launch_tile(const AdapterGemm& g, hipStream_t s) {
   const int64_t tiles = ((g.M + GM - 1) / GM) * ((g.Ncols + BN - 1) / BN);
   LQ_DASSERT(tiles > 0 && tiles < (int64_t(1) << 31));
   const dim3 grid((unsigned)tiles), block(G_THREADS);
-  if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm<BN, false, true>), grid, block, 0, s, g);
-  else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm<BN, true, false>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((k_adapter_gemm<BN, false, false>), grid, block, 0, s, g);
+  if (g.lt_all && g.drop.T) hipLaunchKernelGGL((k_adapter_gemm<BN, false, true, true>), grid, block, 0, s, g);
+  else if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm<BN, false, true, false>), grid, block, 0, s, g);
+  else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm<BN, true, false, false>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((k_adapter_gemm<BN, false, false, false>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 
@@ -626,9 +699,10 @@ template <int GROUPS>
 hipError_t launch_small(const AdapterGemm& g, int64_t tiles, hipStream_t s) {
   LQ_DASSERT(tiles > 0 && tiles < (int64_t(1) << 31));
   const dim3 grid((unsigned)tiles), block(S_THREADS * GROUPS);
-  if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, true>), grid, block, 0, s, g);
-  else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, true, false>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, false>), grid, block, 0, s, g);
+  if (g.lt_all && g.drop.T) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, true, true>), grid, block, 0, s, g);
+  else if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, true, false>), grid, block, 0, s, g);
+  else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, true, false, false>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, false, false>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 

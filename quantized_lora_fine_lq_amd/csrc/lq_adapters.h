@@ -2,6 +2,7 @@
 #pragma once
 
 #include "../../include/lq_adapters.h"
+#include "lq_dropout.h"
 #include "lq_internal.h"
 
 namespace lq {
@@ -37,8 +38,9 @@ struct AdapterView {
 // result and three for a float32 one.
 inline size_t terms_elems(int64_t M, const AdapterView& v) { return (size_t)M * 3 * v.rs; }
 
-// Row form over routed tokens: t[m][j] = sum_c Q[m][c] R_a[j][c], j < r_a, as
-// terms of s_a t; or, with Q null, the terms of a given t.
+// Row form over routed tokens: t[m][j] = post * sum_c Q[m][c] R_a[j][c], j < r_a,
+// Q's dropped elements left out, as terms of s_a t; or, with Q null, the terms
+// of a given t.
 struct DownJob {
   const uint16_t* Q;       // [M, C] bf16, or null
   int64_t C;               // C % 8 == 0
@@ -47,6 +49,8 @@ struct DownJob {
   uint16_t* terms;
   float* save;             // t [M, r_max] or null (zero past r_a and for tokens without an adapter)
   float* part;             // adapter_down_ws_floats(M, C, rs)
+  DropView drop;           // element m C + c of Q
+  float post;              // 1 for a given t
 };
 size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs);
 hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
@@ -72,6 +76,7 @@ struct ColReq {
   float* out;
   int transposed;
   float* part;             // adapter_col_ws_floats
+  DropView drop;           // element m C + c of Q is left out
 };
 size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs);
 hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const AdapterView& v, const Route& rt,
@@ -93,6 +98,7 @@ struct AdapterGemm {
   void* out;               // [M, Ncols] bf16 or float32
   int out_f32;
   const uint16_t* zeros;   // 16 zero bytes
+  DropView drop;           // lt_all: element m Ncols + c of the adapters' part is left out
 };
 hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s);
 // [N, K] -> [K, ldb] bf16 (zero columns from N to ldb)

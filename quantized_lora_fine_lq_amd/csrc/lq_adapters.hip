@@ -439,7 +439,7 @@ __device__ __forceinline__ void put_t(const DownJob& jb, const AdapterView& v, c
 // count of its 16-byte load instructions, which scattered rows make slow: 10 us
 // at 250 to 2048 tokens of rank 16, K = 4096; 6 at 300 tokens, K = 1024.
 // ===========================================================================
-template <int JT, int W, int U>
+template <int JT, int W, int U, bool DROP>
 __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt) {
   __shared__ f32x4_t part[W][JT][64];
   const DownJob jb = blockIdx.y ? j1 : j0;
@@ -455,7 +455,7 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
   }
   const lq_adapter ad = v.tab[it.seg];
   const int r = min(ad.r, 16 * JT), r8 = (r + 7) & ~7;
-  auto put = [&](int row, int j, float x) { put_t(jb, v, rt, ad, it.start + row, j, x); };
+  auto put = [&](int row, int j, float x) { put_t(jb, v, rt, ad, it.start + row, j, jb.post * x); };
   if (!jb.Q) {
     for (int i = threadIdx.x; i < it.count * r8; i += 64 * W) {
       const int row = i / r8, j = i - row * r8;
@@ -465,7 +465,11 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
   }
   const int64_t C = jb.C;
   const uint16_t* R = jb.rbase ? jb.rbase + C * ad.row8 : ad.A;
-  const uint16_t* q = jb.Q + (int64_t)rt.perm[it.start + min(li, it.count - 1)] * C;
+  const int64_t token = rt.perm[it.start + min(li, it.count - 1)];
+  const uint16_t* q = jb.Q + token * C;
+  const bool drops = DROP && jb.drop.T;
+  DropGen gen{};
+  if (drops) gen = drop_gen(jb.drop);
   const uint16_t* rr[JT];
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt) rr[jt] = R + (int64_t)min(16 * jt + li, r - 1) * C;
@@ -495,23 +499,26 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1,
         }
       }
   };
-  auto mul = [&](const Set& s) {
+  auto mul = [&](int b, const Set& s) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        u32x4_t a = s.a[u][h];
+        if (drops) a = drop_16bit(a, drop_bits(gen, (uint64_t)(token * (C / 8) + 8 * (int64_t)(b + u) + 4 * h + lg)), jb.drop.T);
 #pragma unroll
         for (int jt = 0; jt < JT; ++jt)
-          acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(s.a[u][h]), as_bf16x8(s.w[u][h][jt]), acc[jt], 0, 0, 0);
+          acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(s.w[u][h][jt]), acc[jt], 0, 0, 0);
+      }
   };
   Set s0, s1;
   if (b0 < b1) load(b0, s0);
   for (int b = b0; b < b1; b += 2 * U) {
     if (b + U < b1) load(b + U, s1);
-    mul(s0);
+    mul(b, s0);
     if (b + U >= b1) break;
     if (b + 2 * U < b1) load(b + 2 * U, s0);
-    mul(s1);
+    mul(b + U, s1);
   }
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt) part[wave][jt][lane] = acc[jt];
@@ -545,7 +552,7 @@ __device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
-template <int BN>
+template <int BN, bool DROP>
 __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt,
                                                             const uint16_t* zeros) {
   constexpr int CT = BN / 16, QW = BN >= 32 ? BN / 32 : 1;
@@ -590,14 +597,26 @@ __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJob j0, DownJob 
 #pragma unroll
   for (int k = 0; k < DT_RING - 1; ++k) load(s0 + k);
   const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
+  const bool drops = DROP && jb.drop.T;
+  DropGen gen{};
+  int64_t block = 0;   // of the generator: the lane's token and first column
+  if (drops) {
+    gen = drop_gen(jb.drop);
+    block = rt.perm[it.start + min(16 * wave + li, it.count - 1)] * (C / 8) + lg;
+  }
   for (int s = s0; s < s1; ++s) {
+    u32x4_t bits[2];   // before the wait: the generator's rounds run while the tile travels
+    if (drops)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) bits[u] = drop_bits(gen, (uint64_t)(block + 8 * (int64_t)s + 4 * u));
     // this wave's share of step s is there and its reads of s - 1 are done; then everyone's
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((DT_RING - 2) * (2 + QW)) : "memory");
     load(s + DT_RING - 1);
     const int buf = (s - s0) % DT_RING;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const u32x4_t a = ld16(lds.x[buf] + (16 * wave + li) * DT_K + slot[u]);
+      u32x4_t a = ld16(lds.x[buf] + (16 * wave + li) * DT_K + slot[u]);
+      if (drops) a = drop_16bit(a, bits[u], jb.drop.T);
 #pragma unroll
       for (int c = 0; c < CT; ++c)
         acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(ld16(lds.w[buf] + (16 * c + li) * DT_K + slot[u])),
@@ -633,6 +652,7 @@ __global__ __launch_bounds__(256) void k_adapter_down_join(DownJob j0, DownJob j
       if (jb.Q) {
         x = jb.part[i];
         for (int k = 1; k < shares; ++k) x += jb.part[k * total + i];
+        x *= jb.post;
       } else {
         x = jb.given[(int64_t)rt.perm[pos] * v.r_max + j];
       }
@@ -687,7 +707,7 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <int JT>
+template <int JT, bool DROP>
 __global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0, ColReq q1, unsigned tiles0, int rows, AdapterView v,
                                                      Route rt) {
   constexpr int PP = 16 * JT + 16;
@@ -708,15 +728,21 @@ __global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0,
   // of (term, token) of P
   const int qc = 8 * (threadIdx.x & 31), qr = threadIdx.x >> 5;
   const bool qin = c0 + qc + 8 <= C;
+  const bool drops = DROP && rq.drop.T;
+  DropGen gen{};
+  if (drops) gen = drop_gen(rq.drop);
   u32x4_t xq[4], xp[PQ];
-  int tok[4];
+  int tok[4], of[4];   // tokens to load next, and those in xq
   auto tokens = [&](int mb) {   // of the step's rows (a valid one past the end)
 #pragma unroll
     for (int u = 0; u < 4; ++u) tok[u] = rt.perm[it.start + min(mb + qr + 8 * u, it.count - 1)];
   };
   auto load = [&](int mb) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) xq[u] = ld16(rq.Q + (int64_t)tok[u] * C + (qin ? c0 + qc : 0));
+    for (int u = 0; u < 4; ++u) {
+      xq[u] = ld16(rq.Q + (int64_t)tok[u] * C + (qin ? c0 + qc : 0));
+      of[u] = tok[u];
+    }
 #pragma unroll
     for (int k = 0; k < PQ; ++k) {
       const int i = threadIdx.x + 256 * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, term = min(i / (64 * JT), 2);
@@ -726,6 +752,10 @@ __global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0,
   };
   auto store = [&](int mb, int b) {
     const u32x4_t none = {0u, 0u, 0u, 0u};
+    if (drops)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        xq[u] = drop_16bit(xq[u], drop_bits(gen, (uint64_t)(of[u] * (C / 8) + (c0 + qc) / 8)), rq.drop.T);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       *reinterpret_cast<u32x4_t*>(sQ[b] + (qr + 8 * u) * CQ_PITCH + qc) = qin && mb + qr + 8 * u < it.count ? xq[u] : none;
@@ -902,6 +932,7 @@ hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const 
                                const uint16_t* zeros, hipStream_t s) {
   if (njobs < 1 || njobs > 2) return hipErrorInvalidValue;
   const DownJob j0 = jobs[0], j1 = jobs[njobs - 1];
+  const bool drops = j0.drop.T || j1.drop.T;
   if (down_tiled(M, v.rs)) {
     int shares = 1;
     int64_t C = 0;
@@ -910,7 +941,11 @@ hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const 
     if (C) {
       shares = down_shares(M, C);
       const dim3 grid((unsigned)((M + DT_M - 1) / DT_M + std::min<int64_t>(v.n, M)), (unsigned)shares, (unsigned)njobs);
-#define LQ_AT(BN) hipLaunchKernelGGL(k_adapter_down_tiles<BN>, grid, dim3(256), 0, s, j0, j1, M, v, rt, zeros)
+#define LQ_AT(BN)                                                                                               \
+  do {                                                                                                          \
+    if (drops) hipLaunchKernelGGL((k_adapter_down_tiles<BN, true>), grid, dim3(256), 0, s, j0, j1, M, v, rt, zeros); \
+    else hipLaunchKernelGGL((k_adapter_down_tiles<BN, false>), grid, dim3(256), 0, s, j0, j1, M, v, rt, zeros);      \
+  } while (0)
       if (v.r_max <= 16) LQ_AT(16);
       else if (v.r_max <= 32) LQ_AT(32);
       else if (v.r_max <= 64) LQ_AT(64);
@@ -925,7 +960,11 @@ hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const 
   }
   // one item per 16 tokens, and one more per adapter (or none) for its remainder
   const dim3 grid((unsigned)((M + 15) / 16 + std::min<int64_t>(v.n + 1, M)), (unsigned)njobs);
-#define LQ_AD(JT, W, U) hipLaunchKernelGGL((k_adapter_down<JT, W, U>), grid, dim3(64 * W), 0, s, j0, j1, M, v, rt)
+#define LQ_AD(JT, W, U)                                                                                        \
+  do {                                                                                                         \
+    if (drops) hipLaunchKernelGGL((k_adapter_down<JT, W, U, true>), grid, dim3(64 * W), 0, s, j0, j1, M, v, rt); \
+    else hipLaunchKernelGGL((k_adapter_down<JT, W, U, false>), grid, dim3(64 * W), 0, s, j0, j1, M, v, rt);      \
+  } while (0)
   if (v.r_max <= 16) LQ_AD(1, 16, 2);
   else if (v.r_max <= 32) LQ_AD(2, 8, 2);
   else if (v.r_max <= 64) LQ_AD(4, 8, 1);
@@ -944,12 +983,17 @@ hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Ada
                               hipStream_t s) {
   if (nreq < 1 || nreq > 2) return hipErrorInvalidValue;
   const ColReq q0 = reqs[0], q1 = reqs[nreq - 1];
+  const bool drops = q0.drop.T || q1.drop.T;
   const int rows = col_rows(M, q0.C + (nreq > 1 ? q1.C : 0));
   const unsigned t0 = (unsigned)((q0.C + CQ_COLS - 1) / CQ_COLS);
   const unsigned t1 = nreq > 1 ? (unsigned)((q1.C + CQ_COLS - 1) / CQ_COLS) : 0u;
   const dim3 grid(t0 + t1, (unsigned)((M + rows - 1) / rows + std::min<int64_t>(v.n, M)));
   switch ((v.r_max + 15) / 16) {
-#define LQ_AC(JT) case JT: hipLaunchKernelGGL(k_adapter_col<JT>, grid, dim3(256), 0, s, q0, q1, t0, rows, v, rt); break;
+#define LQ_AC(JT)                                                                                                    \
+  case JT:                                                                                                           \
+    if (drops) hipLaunchKernelGGL((k_adapter_col<JT, true>), grid, dim3(256), 0, s, q0, q1, t0, rows, v, rt);        \
+    else hipLaunchKernelGGL((k_adapter_col<JT, false>), grid, dim3(256), 0, s, q0, q1, t0, rows, v, rt);             \
+    break;
     LQ_AC(1) LQ_AC(2) LQ_AC(3) LQ_AC(4) LQ_AC(5) LQ_AC(6) LQ_AC(7) LQ_AC(8)
 #undef LQ_AC
     default: return hipErrorInvalidValue;

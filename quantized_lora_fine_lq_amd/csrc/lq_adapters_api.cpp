@@ -51,8 +51,8 @@ size_t bytes16(size_t elems) { return align_up(elems * sizeof(uint16_t)); }
 
 // route, terms of t, W', zeros, B of ranks that are no multiple of 8; at
 // decode sizes what that path keeps
-size_t forward_ws(const QWeight& q, int64_t M, const AdapterView& v, const lq_adapter_set* set) {
-  if (adapter_decode_supported(q, M)) return align_up(adapter_decode_ws_bytes(q, M, v));
+size_t forward_ws(const QWeight& q, int64_t M, const AdapterView& v, const lq_adapter_set* set, bool drops) {
+  if (!drops && adapter_decode_supported(q, M)) return align_up(adapter_decode_ws_bytes(q, M, v));
   return align_up(route_bytes(M, v.n)) + bytes16(terms_elems(M, v)) + bytes16((size_t)q.N * q.K) + bytes16(8) +
          align_up(adapter_down_ws_floats(M, q.K, v.rs) * sizeof(float)) +
          (any_odd_rank(set) ? bytes16((size_t)sum_r8(set) * q.N) : 0);
@@ -68,6 +68,110 @@ size_t backward_ws(const QWeight& q, int64_t M, const AdapterView& v, int64_t r8
          align_up(adapter_col_ws_floats(M, q.N, v.rs) * sizeof(float)) + bytes16(8) +
          align_up(adapter_down_ws_floats(M, q.K, v.rs) * sizeof(float)) +
          align_up(adapter_down_ws_floats(M, q.N, v.rs) * sizeof(float));
+}
+
+// The generator counts a tensor's elements up to 2^47.
+bool drop_fits(int64_t M, int64_t K) { return K < (int64_t(1) << 47) / M; }
+
+// The forward; d null: without dropout. Decode sizes with dropout run as larger ones.
+int run_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const lq_adapter_set* set, const int32_t* ids,
+                const int32_t* route, const lq_dropout* d, void* H, int32_t h_dtype, float* t_save, void* workspace,
+                size_t ws_bytes, void* stream) {
+  QWeight q;
+  AdapterView v;
+  DropView drop;
+  float factor;
+  int st = check_qweight(w, &q);
+  if (st != LQ_OK) return st;
+  if ((st = check_set(set, q.N, q.K, &v)) != LQ_OK) return st;
+  if ((st = drop_view(d, &drop, &factor)) != LQ_OK) return st;
+  if (!X || !ids || !H) return LQ_ERR_ARG;
+  if (!al(X, kVec) || !al(ids, 4) || !al(route, kVec) || !al(H, h_dtype == LQ_F32 ? 4 : kVec) || !al(t_save, 4) ||
+      !al(workspace, kVec))
+    return LQ_ERR_ARG;
+  if (!valid_M(M) || (d && !drop_fits(M, q.K))) return LQ_ERR_SHAPE;
+  if (h_dtype != LQ_BF16 && h_dtype != LQ_F32) return LQ_ERR_UNSUPPORTED;
+  if (!workspace || ws_bytes < forward_ws(q, M, v, set, d != nullptr)) return LQ_ERR_WORKSPACE;
+  hipStream_t s = (hipStream_t)stream;
+  if ((st = debug_check_weight(q, s)) != LQ_OK) return st;
+  Carver cv(workspace, ws_bytes);
+  if (!d && adapter_decode_supported(q, M))
+    return launch_status(launch_adapter_decode(q, X, M, ids, v, workspace, t_save, H, h_dtype == LQ_F32, s));
+  int32_t* rws = cv.take<int32_t>(route_words(M, v.n));
+  uint16_t* terms = cv.take<uint16_t>(terms_elems(M, v));
+  uint16_t* wd = cv.take<uint16_t>((size_t)q.N * q.K);
+  uint16_t* zeros = cv.take<uint16_t>(8);
+  float* part = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs));
+  uint16_t* bp = any_odd_rank(set) ? cv.take<uint16_t>((size_t)sum_r8(set) * q.N) : nullptr;
+  if (!cv.ok()) return LQ_ERR_WORKSPACE;
+
+  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, wd, 0, v, nullptr, nullptr, bp, zeros, s);
+  if (e != hipSuccess) return LQ_ERR_LAUNCH;
+  const Route rt = route_view(route ? route : rws, M, v.n);
+  const DownJob job{X, q.K, nullptr, nullptr, terms, t_save, part, drop, factor};
+  if ((e = launch_adapter_down(&job, 1, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  const AdapterGemm g{X, M, q.N, q.K, wd, q.K, terms, v, bp, 0, rt, H, h_dtype == LQ_F32 ? 1 : 0, zeros, DropView{}};
+  return launch_status(launch_adapter_gemm(g, s));
+}
+
+int run_backward(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int64_t M, const lq_adapter_set* set,
+                 const int32_t* ids, const int32_t* route, const lq_dropout* d, const float* t_saved,
+                 uint16_t* grad_X, float* dA, float* dB, void* workspace, size_t ws_bytes, void* stream) {
+  QWeight q;
+  AdapterView v;
+  DropView drop;
+  float factor;
+  int st = check_qweight(w, &q);
+  if (st != LQ_OK) return st;
+  if ((st = check_set(set, q.N, q.K, &v)) != LQ_OK) return st;
+  if ((st = drop_view(d, &drop, &factor)) != LQ_OK) return st;
+  const bool need_t = dB && !t_saved;
+  if (!G || !ids || ((dA || need_t) && !X)) return LQ_ERR_ARG;
+  if (!al(X, kVec) || !al(G, kVec) || !al(ids, 4) || !al(route, kVec) || !al(t_saved, 4) || !al(grad_X, kVec) ||
+      !al(dA, 4) || !al(dB, 4) || !al(workspace, kVec))
+    return LQ_ERR_ARG;
+  if (!valid_M(M) || q.N % 8 != 0 || (d && !drop_fits(M, q.K))) return LQ_ERR_SHAPE;
+  const int64_t r8 = sum_r8(set);
+  if (!workspace || ws_bytes < backward_ws(q, M, v, r8)) return LQ_ERR_WORKSPACE;
+  hipStream_t s = (hipStream_t)stream;
+  if ((st = debug_check_weight(q, s)) != LQ_OK) return st;
+  Carver cv(workspace, ws_bytes);
+  int32_t* rws = cv.take<int32_t>(route_words(M, v.n));
+  uint16_t* u = cv.take<uint16_t>(terms_elems(M, v));
+  uint16_t* t = cv.take<uint16_t>(terms_elems(M, v));
+  uint16_t* at = cv.take<uint16_t>((size_t)r8 * q.K);
+  uint16_t* bt = cv.take<uint16_t>((size_t)r8 * q.N);
+  uint16_t* wd = q.format == LQ_FMT_NF4 ? nullptr : cv.take<uint16_t>((size_t)q.N * q.K);
+  const int64_t ldb = ldb_of(q.N);
+  uint16_t* wt = cv.take<uint16_t>((size_t)q.K * ldb);
+  float* part_a = cv.take<float>(adapter_col_ws_floats(M, q.K, v.rs));
+  float* part_b = cv.take<float>(adapter_col_ws_floats(M, q.N, v.rs));
+  uint16_t* zeros = cv.take<uint16_t>(8);
+  float* down_t = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs));
+  float* down_u = cv.take<float>(adapter_down_ws_floats(M, q.N, v.rs));
+  if (!cv.ok()) return LQ_ERR_WORKSPACE;
+  if (!grad_X && !dA && !dB) return LQ_OK;
+
+  const bool need_u = grad_X || dA, nf4 = q.format == LQ_FMT_NF4;
+  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, !grad_X ? nullptr : nf4 ? wt : wd, nf4 ? ldb : 0,
+                                     v, grad_X ? at : nullptr, need_u ? bt : nullptr, nullptr, zeros, s);
+  if (e != hipSuccess) return LQ_ERR_LAUNCH;
+  const Route rt = route_view(route ? route : rws, M, v.n);
+  DownJob jobs[2];
+  int nj = 0;
+  if (need_u) jobs[nj++] = DownJob{G, q.N, bt, nullptr, u, nullptr, down_u, DropView{}, factor};
+  if (dB) jobs[nj++] = DownJob{t_saved ? nullptr : X, q.K, nullptr, t_saved, t, nullptr, down_t,
+                                t_saved ? DropView{} : drop, t_saved ? 1.0f : factor};
+  if (nj && (e = launch_adapter_down(jobs, nj, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  ColReq cols[2];
+  int nc = 0;
+  if (dB) cols[nc++] = ColReq{t, G, q.N, dB, 1, part_b, DropView{}};
+  if (dA) cols[nc++] = ColReq{u, X, q.K, dA, 0, part_a, drop};
+  if (nc && (e = launch_adapter_col(cols, nc, M, v, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  if (!grad_X) return LQ_OK;
+  if (!nf4 && (e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  const AdapterGemm g{G, M, q.K, q.N, wt, ldb, u, v, at, 1, rt, grad_X, 0, zeros, drop};
+  return launch_status(launch_adapter_gemm(g, s));
 }
 
 }  // namespace
@@ -98,44 +202,13 @@ size_t lq_adapters_forward_workspace(const lq_qweight* w, int64_t M, const lq_ad
   QWeight q;
   AdapterView v;
   if (check_qweight(w, &q) != LQ_OK || !valid_M(M) || check_set(set, q.N, q.K, &v) != LQ_OK) return 0;
-  return forward_ws(q, M, v, set);
+  return forward_ws(q, M, v, set, false);
 }
 
 int lq_adapters_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const lq_adapter_set* set,
                         const int32_t* ids, const int32_t* route, void* H, int32_t h_dtype, float* t_save,
                         void* workspace, size_t ws_bytes, void* stream) {
-  QWeight q;
-  AdapterView v;
-  int st = check_qweight(w, &q);
-  if (st != LQ_OK) return st;
-  if ((st = check_set(set, q.N, q.K, &v)) != LQ_OK) return st;
-  if (!X || !ids || !H) return LQ_ERR_ARG;
-  if (!al(X, kVec) || !al(ids, 4) || !al(route, kVec) || !al(H, h_dtype == LQ_F32 ? 4 : kVec) || !al(t_save, 4) ||
-      !al(workspace, kVec))
-    return LQ_ERR_ARG;
-  if (!valid_M(M)) return LQ_ERR_SHAPE;
-  if (h_dtype != LQ_BF16 && h_dtype != LQ_F32) return LQ_ERR_UNSUPPORTED;
-  if (!workspace || ws_bytes < forward_ws(q, M, v, set)) return LQ_ERR_WORKSPACE;
-  hipStream_t s = (hipStream_t)stream;
-  if ((st = debug_check_weight(q, s)) != LQ_OK) return st;
-  Carver cv(workspace, ws_bytes);
-  if (adapter_decode_supported(q, M))
-    return launch_status(launch_adapter_decode(q, X, M, ids, v, workspace, t_save, H, h_dtype == LQ_F32, s));
-  int32_t* rws = cv.take<int32_t>(route_words(M, v.n));
-  uint16_t* terms = cv.take<uint16_t>(terms_elems(M, v));
-  uint16_t* wd = cv.take<uint16_t>((size_t)q.N * q.K);
-  uint16_t* zeros = cv.take<uint16_t>(8);
-  float* part = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs));
-  uint16_t* bp = any_odd_rank(set) ? cv.take<uint16_t>((size_t)sum_r8(set) * q.N) : nullptr;
-  if (!cv.ok()) return LQ_ERR_WORKSPACE;
-
-  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, wd, 0, v, nullptr, nullptr, bp, zeros, s);
-  if (e != hipSuccess) return LQ_ERR_LAUNCH;
-  const Route rt = route_view(route ? route : rws, M, v.n);
-  const DownJob job{X, q.K, nullptr, nullptr, terms, t_save, part};
-  if ((e = launch_adapter_down(&job, 1, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  const AdapterGemm g{X, M, q.N, q.K, wd, q.K, terms, v, bp, 0, rt, H, h_dtype == LQ_F32 ? 1 : 0, zeros};
-  return launch_status(launch_adapter_gemm(g, s));
+  return run_forward(w, X, M, set, ids, route, nullptr, H, h_dtype, t_save, workspace, ws_bytes, stream);
 }
 
 size_t lq_adapters_backward_workspace(const lq_qweight* w, int64_t M, const lq_adapter_set* set) {
@@ -148,57 +221,50 @@ size_t lq_adapters_backward_workspace(const lq_qweight* w, int64_t M, const lq_a
 int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int64_t M,
                          const lq_adapter_set* set, const int32_t* ids, const int32_t* route, const float* t_saved,
                          uint16_t* grad_X, float* dA, float* dB, void* workspace, size_t ws_bytes, void* stream) {
+  return run_backward(w, X, G, M, set, ids, route, nullptr, t_saved, grad_X, dA, dB, workspace, ws_bytes, stream);
+}
+
+// ---- dropout --------------------------------------------------------------------
+int lq_dropout_apply(const lq_dropout* d, const void* x, int64_t numel, int32_t dtype, void* out, void* stream) {
+  DropView drop;
+  float factor;
+  if (!d) return LQ_ERR_ARG;
+  const int st = drop_view(d, &drop, &factor);
+  if (st != LQ_OK) return st;
+  if (dtype != LQ_F32 && dtype != LQ_BF16 && dtype != LQ_F16) return LQ_ERR_ARG;
+  if (numel < 0 || numel >= (int64_t(1) << 47)) return LQ_ERR_SHAPE;
+  if (numel == 0) return LQ_OK;
+  const uintptr_t size = dtype == LQ_F32 ? 4 : 2;
+  if (!x || !out || !al(x, size) || !al(out, size)) return LQ_ERR_ARG;
+  return launch_status(launch_dropout(drop, factor, x, numel, dtype, out, (hipStream_t)stream));
+}
+
+size_t lq_adapters_forward_dropout_workspace(const lq_qweight* w, int64_t M, const lq_adapter_set* set) {
   QWeight q;
   AdapterView v;
-  int st = check_qweight(w, &q);
-  if (st != LQ_OK) return st;
-  if ((st = check_set(set, q.N, q.K, &v)) != LQ_OK) return st;
-  const bool need_t = dB && !t_saved;
-  if (!G || !ids || ((dA || need_t) && !X)) return LQ_ERR_ARG;
-  if (!al(X, kVec) || !al(G, kVec) || !al(ids, 4) || !al(route, kVec) || !al(t_saved, 4) || !al(grad_X, kVec) ||
-      !al(dA, 4) || !al(dB, 4) || !al(workspace, kVec))
-    return LQ_ERR_ARG;
-  if (!valid_M(M) || q.N % 8 != 0) return LQ_ERR_SHAPE;
-  const int64_t r8 = sum_r8(set);
-  if (!workspace || ws_bytes < backward_ws(q, M, v, r8)) return LQ_ERR_WORKSPACE;
-  hipStream_t s = (hipStream_t)stream;
-  if ((st = debug_check_weight(q, s)) != LQ_OK) return st;
-  Carver cv(workspace, ws_bytes);
-  int32_t* rws = cv.take<int32_t>(route_words(M, v.n));
-  uint16_t* u = cv.take<uint16_t>(terms_elems(M, v));
-  uint16_t* t = cv.take<uint16_t>(terms_elems(M, v));
-  uint16_t* at = cv.take<uint16_t>((size_t)r8 * q.K);
-  uint16_t* bt = cv.take<uint16_t>((size_t)r8 * q.N);
-  uint16_t* wd = q.format == LQ_FMT_NF4 ? nullptr : cv.take<uint16_t>((size_t)q.N * q.K);
-  const int64_t ldb = ldb_of(q.N);
-  uint16_t* wt = cv.take<uint16_t>((size_t)q.K * ldb);
-  float* part_a = cv.take<float>(adapter_col_ws_floats(M, q.K, v.rs));
-  float* part_b = cv.take<float>(adapter_col_ws_floats(M, q.N, v.rs));
-  uint16_t* zeros = cv.take<uint16_t>(8);
-  float* down_t = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs));
-  float* down_u = cv.take<float>(adapter_down_ws_floats(M, q.N, v.rs));
-  if (!cv.ok()) return LQ_ERR_WORKSPACE;
-  if (!grad_X && !dA && !dB) return LQ_OK;
+  if (check_qweight(w, &q) != LQ_OK || !valid_M(M) || check_set(set, q.N, q.K, &v) != LQ_OK || !drop_fits(M, q.K)) return 0;
+  return forward_ws(q, M, v, set, true);
+}
 
-  const bool need_u = grad_X || dA, nf4 = q.format == LQ_FMT_NF4;
-  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, !grad_X ? nullptr : nf4 ? wt : wd, nf4 ? ldb : 0,
-                                     v, grad_X ? at : nullptr, need_u ? bt : nullptr, nullptr, zeros, s);
-  if (e != hipSuccess) return LQ_ERR_LAUNCH;
-  const Route rt = route_view(route ? route : rws, M, v.n);
-  DownJob jobs[2];
-  int nj = 0;
-  if (need_u) jobs[nj++] = DownJob{G, q.N, bt, nullptr, u, nullptr, down_u};
-  if (dB) jobs[nj++] = DownJob{t_saved ? nullptr : X, q.K, nullptr, t_saved, t, nullptr, down_t};
-  if (nj && (e = launch_adapter_down(jobs, nj, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  ColReq cols[2];
-  int nc = 0;
-  if (dB) cols[nc++] = ColReq{t, G, q.N, dB, 1, part_b};
-  if (dA) cols[nc++] = ColReq{u, X, q.K, dA, 0, part_a};
-  if (nc && (e = launch_adapter_col(cols, nc, M, v, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  if (!grad_X) return LQ_OK;
-  if (!nf4 && (e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  const AdapterGemm g{G, M, q.K, q.N, wt, ldb, u, v, at, 1, rt, grad_X, 0, zeros};
-  return launch_status(launch_adapter_gemm(g, s));
+int lq_adapters_forward_dropout(const lq_qweight* w, const uint16_t* X, int64_t M, const lq_adapter_set* set,
+                                const int32_t* ids, const int32_t* route, const lq_dropout* d, void* H,
+                                int32_t h_dtype, float* t_save, void* workspace, size_t ws_bytes, void* stream) {
+  if (!d) return LQ_ERR_ARG;
+  return run_forward(w, X, M, set, ids, route, d, H, h_dtype, t_save, workspace, ws_bytes, stream);
+}
+
+size_t lq_adapters_backward_dropout_workspace(const lq_qweight* w, int64_t M, const lq_adapter_set* set) {
+  QWeight q;
+  if (check_qweight(w, &q) != LQ_OK || !valid_M(M) || !drop_fits(M, q.K)) return 0;
+  return lq_adapters_backward_workspace(w, M, set);
+}
+
+int lq_adapters_backward_dropout(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int64_t M,
+                                 const lq_adapter_set* set, const int32_t* ids, const int32_t* route,
+                                 const lq_dropout* d, const float* t_saved, uint16_t* grad_X, float* dA, float* dB,
+                                 void* workspace, size_t ws_bytes, void* stream) {
+  if (!d) return LQ_ERR_ARG;
+  return run_backward(w, X, G, M, set, ids, route, d, t_saved, grad_X, dA, dB, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"
