@@ -15,7 +15,9 @@ Many adapters over one projection, and the clipping of their gradients
 ``AdapterSet``, ``adapter_route``, ``adapters_forward``,
 ``adapters_backward``, ``GradList``, ``grad_norm``, ``clip_grad_norm``. So is
 dropout without a stored mask (include/lq_dropout.h, ``dropouts.py``):
-``dropout_key``, ``Dropout``, ``dropout``.
+``dropout_key``, ``Dropout``, ``dropout``; and the gated pair of projections of
+an MLP (include/lq_gated.h, ``gated.py``): ``GatedPair``, ``gated_forward``,
+``gated_backward``, ``GatedSaved``, ``GatedGrads``.
 
 Importing fails loudly if liblq.so has not been built
 (``python quantized_lora_fine_lq_amd/build.py``).
@@ -542,3 +544,5 @@ from .adapters import (AdapterSet, GradList, adapter_route, adapters_backward, a
                        clip_grad_norm, grad_norm)
 # dropout from a counter-based generator
 from .dropouts import Dropout, dropout, dropout_key  # noqa: E402
+# the gated pair of an MLP
+from .gated import GatedGrads, GatedPair, GatedSaved, gated_backward, gated_forward  # noqa: E402

@@ -21,7 +21,8 @@ LIB = os.path.join(LIB_DIR, "liblq.so")
 LIB_DEBUG = os.path.join(LIB_DIR, "liblq_debug.so")
 SOURCES = ["lq_tables.cpp", "lq_api.cpp", "lq_codec.hip", "lq_gemm.hip", "lq_lloyd.hip", "lq_lowrank.hip",
            "lq_noalloc.hip", "lq_adapters_api.cpp", "lq_adapters.hip", "lq_adapter_decode.hip",
-           "lq_adapter_gemm.hip", "lq_gradclip.hip", "lq_dropout.hip"]
+           "lq_adapter_gemm.hip", "lq_gradclip.hip", "lq_dropout.hip",
+           "lq_gated_api.cpp", "lq_gated.hip"]
 ARCH = os.environ.get("LQ_OFFLOAD_ARCH", "gfx950")
 
 

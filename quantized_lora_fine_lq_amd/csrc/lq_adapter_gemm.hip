@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "lq_act.h"
 #include "lq_adapters.h"
 #include "lq_device.h"
 
@@ -36,24 +37,35 @@ __device__ __forceinline__ void ring_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(n) : "memory");
 }
 
+// yes ? a : b as a selection: a is formed either way, or the compiler would
+// branch around each address of a step.
+__device__ __forceinline__ const uint16_t* chosen(bool yes, const uint16_t* a, const uint16_t* b) {
+  asm("" : "+v"(a));
+  return yes ? a : b;
+}
+
 // The adapter of the sorted positions from pos on, inside a tile that ends at
-// mend: its columns are steps of 64 (8 runs of 8) of TERMS copies of Lb.
+// mend: its columns are steps of 64 (8 runs of 8) of TERMS copies of Lb. Of a
+// pair of sets, side 1's adapters follow side 0's, of the same positions from m0.
 struct Adapter {
   int64_t lo, hi;          // its positions inside the tile
   const uint16_t* base;    // Lb
   int stride, runs;        // of Lb: elements a row, runs of 8 columns
   int live, steps;         // runs of all terms, steps of 8 of them (0: no adapter)
+  int side;
+  const uint16_t* terms;   // the side's
+  int pitch;               // of its rows
 };
 template <int TERMS>
-__device__ __forceinline__ Adapter adapter_at(const AdapterGemm& p, int64_t pos, int64_t mend) {
-  Adapter s{pos, mend, nullptr, 8, 1, 0, 0};
+__device__ __forceinline__ Adapter adapter_at(const AdapterGemm& p, int side, int64_t pos, int64_t mend) {
+  Adapter s{pos, mend, nullptr, 8, 1, 0, 0, side, side ? p.s[1].terms : p.s[0].terms, 3 * (side ? p.s[1].v.rs : p.s[0].v.rs)};
   if (pos >= mend) return s;
   const int a = uniform(p.rt.sid[pos]);
-  if (a >= p.v.n) return s;
+  if (a >= p.s[0].v.n) return s;
   s.hi = min((int64_t)uniform(p.rt.off[a + 1]), mend);
-  const lq_adapter ad = p.v.tab[a];
+  const lq_adapter ad = (side ? p.s[1].v.tab : p.s[0].v.tab)[a];
   const int r8 = (ad.r + 7) & ~7;
-  s.base = !p.lt_all && ad.r % 8 == 0 ? ad.B : p.lt + p.Ncols * ad.row8;
+  s.base = !p.lt_all && ad.r % 8 == 0 ? ad.B : (side ? p.s[1].lt : p.s[0].lt) + p.Ncols * ad.row8;
   s.stride = r8;
   s.runs = r8 >> 3;
   s.live = TERMS * s.runs;
@@ -109,26 +121,44 @@ __device__ __forceinline__ float kept_value(float v, uint32_t keep, int at) {
 
 // A lane's 4 consecutive outputs c .. c + 3 of one token.
 template <bool OUT_F32>
-__device__ __forceinline__ void store4(const AdapterGemm& p, int64_t row, int64_t c, const f32x4_t& v) {
+__device__ __forceinline__ void store4(const AdapterGemm& p, void* out, int64_t row, int64_t c, const f32x4_t& v) {
   if (p.Ncols % 4 == 0) {
     if (c >= p.Ncols) return;
     if (OUT_F32) {
-      float* o = reinterpret_cast<float*>(p.out) + row + c;   // 4-byte aligned
+      float* o = reinterpret_cast<float*>(out) + row + c;   // 4-byte aligned
       o[0] = v[0]; o[1] = v[1]; o[2] = v[2]; o[3] = v[3];
     } else {
       uint2 o;
       o.x = pack_bf16x2(v[0], v[1]);
       o.y = pack_bf16x2(v[2], v[3]);
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + row + c) = o;
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + row + c) = o;
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (c + e >= p.Ncols) break;
-      if (OUT_F32) reinterpret_cast<float*>(p.out)[row + c + e] = v[e];
-      else reinterpret_cast<uint16_t*>(p.out)[row + c + e] = (uint16_t)(pack_bf16x2(v[e], 0.f) & 0xFFFFu);
+      if (OUT_F32) reinterpret_cast<float*>(out)[row + c + e] = v[e];
+      else reinterpret_cast<uint16_t*>(out)[row + c + e] = (uint16_t)(pack_bf16x2(v[e], 0.f) & 0xFFFFu);
     }
   }
+}
+
+// The same lane's 4 outputs of a gated pair from g and u.
+template <bool OUT_F32, int ACT>
+__device__ __forceinline__ void store_gated4(const AdapterGemm& p, int64_t row, int64_t c, const f32x4_t& g, const f32x4_t& u) {
+  f32x4_t h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = act_value<ACT>(g[e]) * u[e];
+  store4<OUT_F32>(p, p.out, row, c, h);
+  if (p.g_out) store4<false>(p, p.g_out, row, c, g);
+  if (p.u_out) store4<false>(p, p.u_out, row, c, u);
+}
+// act as a constant, for code that unrolls over many outputs.
+template <class F>
+__device__ __forceinline__ void with_act(int act, const F& f) {
+  if (act == LQ_SILU) f(std::integral_constant<int, LQ_SILU>());
+  else if (act == LQ_GELU) f(std::integral_constant<int, LQ_GELU>());
+  else f(std::integral_constant<int, LQ_GELU_TANH>());
 }
 
 // Tile 256 positions x BN weight rows, 64-wide steps, 8 waves in two groups of
@@ -156,9 +186,14 @@ __device__ __forceinline__ void store4(const AdapterGemm& p, int64_t row, int64_
 //
 // DROP (grad_X behind dropout): the adapters' part is always formed apart, after
 // the main loop, and added where the generator keeps the output.
-template <int BN, bool OUT_F32, bool BWD, bool DROP>
+//
+// GATED: a wave's 64 weight rows are 32 of the gate (part 0) and the same 32 of
+// up (part 1), so that a lane ends with g and u of the same outputs; the tile is
+// BN / 2 outputs wide. TWO and GATED also form the adapters' part apart.
+template <int BN, bool OUT_F32, bool BWD, bool DROP, int MODE>
 __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
-  constexpr bool BIG = BN == 256;
+  constexpr bool BIG = BN == 256, GATED = MODE == GEMM_GATED, APART = DROP || MODE != GEMM_ONE;
+  constexpr int NT = GATED ? BN / 2 : BN;              // outputs per tile
   constexpr int WN = BIG ? 4 : 2, WM = 8 / WN;         // waves over weight rows, tokens
   constexpr int CT = BN / WN / 16, RT = GM / WM / 16;  // 16 x 16 tiles per wave
   constexpr int RING = BIG ? 2 : 3;
@@ -172,36 +207,40 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
   const int wn = wave % WN, wm = wave / WN;
-  const int64_t tiles_m = (p.M + GM - 1) / GM, tiles_n = (p.Ncols + BN - 1) / BN;
+  const int64_t tiles_m = (p.M + GM - 1) / GM, tiles_n = (p.Ncols + NT - 1) / NT;
   const int64_t total = tiles_m * tiles_n;
   // XCD x (workgroups x, x + 8, ...) takes a contiguous range of tiles, the
   // token tiles inner
   const int64_t xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
   const int64_t t = xcd * per + min(xcd, rem) + blockIdx.x / 8;
-  const int64_t m0 = t % tiles_m * GM, n0 = t / tiles_m * BN;
+  const int64_t m0 = t % tiles_m * GM, n0 = t / tiles_m * NT;
 
   // A load instruction of a wave fills 8 LDS rows (lane l: row l / 8, slot
   // l % 8). Part i of the token tile: rows 64 i .. of every wave's 128 (all
   // rows for BN = 128); part i of the weight tile: rows 16 CT / 2 i .. of every
   // wave's 16 CT.
   const int sub = lane >> 3, ch = (lane & 7) ^ sub;
-  auto xrow = [&](int part, int q) {   // first tile row of the wave's q-th load
+  auto xrow = [&](int part, int q) __attribute__((always_inline)) {   // first tile row of the wave's q-th load
     const int k = wave * QX + q;       // 8-row groups 0 .. 8 QX - 1 of the part
     return BIG ? (k >> 3) * 128 + part * 64 + (k & 7) * 8 : k * 8;
   };
-  auto yrow = [&](int part, int q) {
+  auto yrow = [&](int part, int q) __attribute__((always_inline)) {
     const int k = wave * QY + q, per_wave = 16 * CT / 2 / 8;
     return (k / per_wave) * 16 * CT + part * 8 * CT + (k % per_wave) * 8;
+  };
+  auto wrow = [&](int part, int q) __attribute__((always_inline)) {   // row of its weight that the lane loads there
+    const int k = wave * QY + q, per_wave = 16 * CT / 2 / 8;
+    return min(n0 + (GATED ? (k / per_wave) * 8 * CT + (k % per_wave) * 8 : yrow(part, q)) + sub, p.Ncols - 1);
   };
   const uint16_t *px[XP][QX], *py[2][QY];
 #pragma unroll
   for (int i = 0; i < XP; ++i)
 #pragma unroll
-    for (int q = 0; q < QX; ++q) px[i][q] = p.A + (int64_t)p.rt.perm[min(m0 + xrow(i, q) + sub, p.M - 1)] * p.Kc + 8 * ch;
+    for (int q = 0; q < QX; ++q) px[i][q] = p.A + (int64_t)p.rt.perm[min(m0 + xrow(i, q) + sub, p.M - 1)] * p.lda + 8 * ch;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int q = 0; q < QY; ++q) py[i][q] = p.Bt + min(n0 + yrow(i, q) + sub, p.Ncols - 1) * p.ldb + 8 * ch;
+    for (int q = 0; q < QY; ++q) py[i][q] = (GATED && i ? p.Bt2 : p.Bt) + wrow(i, q) * p.ldb + 8 * ch;
   const int nk = (int)((p.Kc + GK - 1) / GK);
   // Each XCD begins at an eighth of its own of the contraction (whole steps
   // only): in step, all eight would ask for the same columns, whose rows lie a
@@ -209,7 +248,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   // time; a place of its own per tile costs the tiles of an XCD the weight rows
   // and tokens that they share in its L2 (2048 tokens: 72 -> 90 us).
   const int rot = p.Kc % GK ? 0 : (int)(xcd * nk / 8);
-  auto column = [&](int it) {   // first column of step it
+  auto column = [&](int it) __attribute__((always_inline)) {   // first column of step it
     const int at = it + rot;
     return (int64_t)(at < nk ? at : at - nk) * GK;
   };
@@ -220,53 +259,44 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   // the end of the contraction, steps nk .. nk + nl - 1 of the main loop.
   constexpr int TERMS = OUT_F32 ? 3 : 2;
   const int64_t mend = min(m0 + GM, p.M);
-  auto lora_x = [&](const Adapter& s, int kt, int i, int buf) {
+  auto lora_x = [&](const Adapter& s, int kt, int i, int q) __attribute__((always_inline)) {   // the lane's 16 bytes of load q
     const int c = 8 * kt + ch;   // this lane's run of 8 columns
-#pragma unroll
-    for (int q = 0; q < QX; ++q) {
-      const int64_t pos = min(m0 + xrow(i, q) + sub, p.M - 1);
-      load_lds16(c < s.live ? p.terms + pos * 3 * p.v.rs + 8 * c : p.zeros, lds.x[buf] + xrow(i, q) * GK);
-    }
+    const int64_t pos = min(m0 + xrow(i, q) + sub, p.M - 1);
+    return chosen(c < s.live, s.terms + pos * s.pitch + 8 * c, p.zeros);
   };
-  auto lora_y = [&](const Adapter& s, int kt, int i, int buf) {
+  auto lora_y = [&](const Adapter& s, int kt, int i, int q) __attribute__((always_inline)) {
     const int c = 8 * kt + ch;
-#pragma unroll
-    for (int q = 0; q < QY; ++q) {
-      const int64_t n = min(n0 + yrow(i, q) + sub, p.Ncols - 1);
-      load_lds16(c < s.live ? s.base + n * s.stride + 8 * (c % s.runs) : p.zeros, lds.y[buf] + yrow(i, q) * GK);
-    }
+    return chosen(c < s.live, s.base + wrow(i, q) * s.stride + 8 * (c % s.runs), p.zeros);
   };
 
   // Part i of step it into its buffer; Plain: a whole step of the base
   // contraction. Past the last step zeros, into a buffer that nobody reads any
   // more: the count of outstanding loads, on which the waits rely, stays the
   // same.
-  Adapter whole{0, 0, nullptr, 8, 1, 0, 0};   // the tile's one adapter, if it has one
+  Adapter whole{0, 0, nullptr, 8, 1, 0, 0, 0, nullptr, 0};   // the tile's one adapter, if it has one
   typedef std::integral_constant<bool, true> Plain;
   typedef std::integral_constant<bool, false> Any;
-  auto load_x = [&](auto plain, int it, int i, int buf) {
-    if (plain.value || it < nk) {
-      const int64_t k0 = column(it);
-      const bool ok = plain.value || !BWD || k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (0 * NaN is not 0)
+  auto load_x = [&](auto plain, int it, int i, int buf) __attribute__((always_inline)) {
+    const bool base = plain.value || it < nk;
+    const int64_t k0 = base ? column(it) : 0;
+    const bool ok = plain.value || !BWD || k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (0 * NaN is not 0)
 #pragma unroll
-      for (int q = 0; q < QX; ++q) load_lds16(ok ? px[i][q] + k0 : p.zeros, lds.x[buf] + xrow(i, q) * GK);
-    } else if constexpr (DROP) {
-#pragma unroll
-      for (int q = 0; q < QX; ++q) load_lds16(p.zeros, lds.x[buf] + xrow(i, q) * GK);
-    } else {
-      lora_x(whole, it - nk, i, buf);
+    for (int q = 0; q < QX; ++q) {
+      const uint16_t* src = p.zeros;
+      if (base) src = ok ? px[i][q] + k0 : p.zeros;
+      else if (!APART) src = lora_x(whole, it - nk, i, q);
+      load_lds16(src, lds.x[buf] + xrow(i, q) * GK);
     }
   };
-  auto load_y = [&](auto plain, int it, int i, int buf) {
-    if (plain.value || it < nk) {
-      const int64_t k0 = column(it);
+  auto load_y = [&](auto plain, int it, int i, int buf) __attribute__((always_inline)) {
+    const bool base = plain.value || it < nk;
+    const int64_t k0 = base ? column(it) : 0;
 #pragma unroll
-      for (int q = 0; q < QY; ++q) load_lds16(py[i][q] + k0, lds.y[buf] + yrow(i, q) * GK);
-    } else if constexpr (DROP) {
-#pragma unroll
-      for (int q = 0; q < QY; ++q) load_lds16(p.zeros, lds.y[buf] + yrow(i, q) * GK);
-    } else {
-      lora_y(whole, it - nk, i, buf);
+    for (int q = 0; q < QY; ++q) {
+      const uint16_t* src = p.zeros;
+      if (base) src = py[i][q] + k0;
+      else if (!APART) src = lora_y(whole, it - nk, i, q);
+      load_lds16(src, lds.y[buf] + yrow(i, q) * GK);
     }
   };
 
@@ -278,7 +308,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   u32x4_t fx[2][4], fy[2][2][CT / 2];   // [k half][tile], weight side [part][k half][tile]
   const int slot0 = 8 * (lg ^ (li & 7)), slot1 = 8 * ((4 + lg) ^ (li & 7));
   const int ox = (wm * 16 * RT + li) * GK, oy = (wn * 16 * CT + li) * GK;
-  auto read_x = [&](int i, int buf) {
+  auto read_x = [&](int i, int buf) __attribute__((always_inline)) {
     const uint16_t* b = lds.x[buf] + ox + i * 64 * GK;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -286,7 +316,7 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
       fx[1][r] = ld16(b + 16 * r * GK + slot1);
     }
   };
-  auto read_y = [&](int i, int buf) {
+  auto read_y = [&](int i, int buf) __attribute__((always_inline)) {
     const uint16_t* b = lds.y[buf] + oy + i * 8 * CT * GK;
 #pragma unroll
     for (int c = 0; c < CT / 2; ++c) {
@@ -294,12 +324,12 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
       fy[i][1][c] = ld16(b + 16 * c * GK + slot1);
     }
   };
-  auto end_memory = [&]() {   // the fragments have arrived: a part may be refilled after the barrier
+  auto end_memory = [&]() __attribute__((always_inline)) {   // the fragments have arrived: a part may be refilled after the barrier
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto multiply = [&](int xi, int yi) {
+  auto multiply = [&](int xi, int yi) __attribute__((always_inline)) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -316,11 +346,16 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   };
 
   const bool late = wave >= 4;   // the group that works one slot behind
-  Adapter next = adapter_at<TERMS>(p, m0, mend);
-  if (!DROP && next.steps && next.hi == mend) whole = next;
+  Adapter next = adapter_at<TERMS>(p, 0, m0, mend);
+  if constexpr (!APART) {
+    const bool one = next.steps && next.hi == mend;
+    whole = next;
+    whole.steps = one ? next.steps : 0;
+    whole.live = one ? next.live : 0;
+  }
   const int nsteps = nk + whole.steps;
   int it = 0, buf = 0;
-  auto step = [&](auto plain) {
+  auto step = [&](auto plain) __attribute__((always_inline)) {
     if constexpr (BIG) {
       read_x(0, buf);
       read_y(0, buf);
@@ -384,39 +419,51 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   if (!late) barrier();   // as many barriers as the other group
   wait_vm<0>();           // the loads past the last step, before the workgroup's LDS is given up
 
-  const int64_t pw = m0 + wm * 16 * RT, cw = n0 + wn * 16 * CT;
+  const int64_t pw = m0 + wm * 16 * RT, cw = n0 + wn * (GATED ? 8 : 16) * CT;
 
-  // A tile of several adapters: one after the other, each one's products formed
-  // apart and added to its own tokens' columns alone, so that an adapter's
-  // infinities and NaN stay with its tokens.
-  // (DROP: without the branch, across which the compiler would hold the sums twice.)
-  if (DROP || (!whole.steps && next.steps)) {
-    Kept<RT> keep{};
-    if constexpr (DROP) keep = kept_outputs<CT, RT>(p.drop, p.rt.perm, p.M, p.Ncols, pw, cw);
+  // A tile of several adapters (APART: of any): one after the other, each one's
+  // products formed apart and added to its own tokens' columns alone, so that an
+  // adapter's infinities and NaN stay with its tokens (GATED: and with its own
+  // side's weight rows). APART: without a branch around it, and in one loop for
+  // both sides: the compiler would hold the sums twice.
+  if (APART || (!whole.steps && next.steps)) {
+    Kept<RT> keep0{}, keep1{};
+    if constexpr (DROP) keep0 = kept_outputs<CT, RT>(p.s[0].drop, p.rt.perm, p.M, p.Ncols, pw, cw);
+    if constexpr (DROP && MODE == GEMM_TWO) keep1 = kept_outputs<CT, RT>(p.s[1].drop, p.rt.perm, p.M, p.Ncols, pw, cw);
     Adapter cur = next;
     int kt = 0;
+    auto load = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < XP; ++i)
+#pragma unroll
+        for (int q = 0; q < QX; ++q) load_lds16(lora_x(cur, kt, i, q), lds.x[b] + xrow(i, q) * GK);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < QY; ++q) load_lds16(lora_y(cur, kt, i, q), lds.y[b] + yrow(i, q) * GK);
+    };
     ring_barrier<0>();   // everyone has read the last step
-    if (!DROP || cur.steps) {
-      lora_x(cur, 0, 0, 0);
-      if constexpr (XP == 2) lora_x(cur, 0, 1, 0);
-      lora_y(cur, 0, 0, 0);
-      lora_y(cur, 0, 1, 0);
-    }
-    for (int b = 0; cur.steps; b ^= 1) {
-      const int64_t lo = cur.lo, hi = cur.hi;
+    load(0);   // (APART: of a tile without adapters a step of zeros, no token's)
+    int b = 0;
+    do {
+      const int64_t lo = cur.lo, hi = !APART || cur.steps ? cur.hi : cur.lo;
+      const int side = cur.side;
       if (++kt >= cur.steps) {
-        cur = adapter_at<TERMS>(p, cur.hi, mend);
+        cur = adapter_at<TERMS>(p, side, cur.hi, mend);
+        if (MODE != GEMM_ONE && !cur.steps && !side) cur = adapter_at<TERMS>(p, 1, m0, mend);
         kt = 0;
       }
       ring_barrier<0>();   // this step has landed, and the other buffer is read
-      if (cur.steps) {
-        lora_x(cur, kt, 0, b ^ 1);
-        if constexpr (XP == 2) lora_x(cur, kt, 1, b ^ 1);
-        lora_y(cur, kt, 0, b ^ 1);
-        lora_y(cur, kt, 1, b ^ 1);
-      }
+      if (cur.steps) load(b ^ 1);
       read_y(0, b);
       read_y(1, b);
+      Kept<RT> keep = keep0;
+      if constexpr (DROP && MODE == GEMM_TWO)
+#pragma unroll
+        for (int i = 0; i < RT / 2; ++i) keep.w[i] = side ? keep1.w[i] : keep0.w[i];
+      if constexpr (DROP)   // or each bit's mask would be formed before the loop and held
+#pragma unroll
+        for (uint32_t& w : keep.w) asm volatile("" : "+v"(w));
 #pragma unroll
       for (int xi = 0; xi < XP; ++xi) {
         read_x(xi, b);
@@ -424,9 +471,6 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
         for (int r = 0; r < 4; ++r) {
           const int64_t pos = pw + 16 * (xi * 4 + r) + li;
           const bool mine = pos >= lo && pos < hi;
-          if constexpr (DROP)   // or each bit's mask would be formed before the loop and held
-#pragma unroll
-            for (uint32_t& w : keep.w) asm volatile("" : "+v"(w));
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
             f32x4_t d = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -438,24 +482,37 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
             for (int e = 0; e < 4; ++e) {
               const int rt = xi * 4 + r;
               const float add = DROP ? kept_value(d[e], keep.w[rt / 2], 8 * c + 4 * (rt % 2) + e) : d[e];
-              acc[c][xi * 4 + r][e] += mine ? add : 0.0f;
+              acc[c][xi * 4 + r][e] += mine && (!GATED || side == c / (CT / 2)) ? add : 0.0f;
             }
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-    }
+      b ^= 1;
+    } while (cur.steps);
   }
 
   // lane: token position pw + 16 rt + li, outputs cw + 16 ct + 4 lg + [0, 4)
+  if constexpr (GATED) {
+    with_act(p.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int64_t pos = pw + 16 * rt + li;
-    if (pos >= p.M) continue;
-    const int64_t row = (int64_t)p.rt.perm[pos] * p.Ncols;
+      for (int rt = 0; rt < RT; ++rt) {
+        const int64_t pos = pw + 16 * rt + li;
+        if (pos >= p.M) continue;
+        const int64_t row = (int64_t)p.rt.perm[pos] * p.Ncols;
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      store4<OUT_F32>(p, row, cw + 16 * ct + 4 * lg, acc[ct][rt]);
+        for (int ct = 0; ct < CT / 2; ++ct)
+          store_gated4<OUT_F32, decltype(act)::value>(p, row, cw + 16 * ct + 4 * lg, acc[ct][rt], acc[ct + CT / 2][rt]);
+      }
+    });
+  } else {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int64_t pos = pw + 16 * rt + li;
+      if (pos >= p.M) continue;
+      const int64_t row = (int64_t)p.rt.perm[pos] * p.Ncols;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) store4<OUT_F32>(p, p.out, row, cw + 16 * ct + 4 * lg, acc[ct][rt]);
     }
   }
 }
@@ -475,21 +532,24 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
 // table made at the start; the products of each go to its own tokens' columns
 // alone.
 constexpr int SM = 64, SN = 64, S_THREADS = 256, S_RING = 4;
-constexpr int S_STEPS = SM * 6;   // an adapter per token, 3 terms of rank 128
+constexpr int S_STEPS = SM * 6;   // of a side: an adapter per token, 3 terms of rank 128
 
 struct SmallStep {
-  const uint16_t* base;    // Lb
-  int runs, live, first;   // of Lb: runs of 8 columns; of all terms; the step's first
-  int lo, hi;              // its positions of the tile
+  const uint16_t* base;           // Lb
+  uint8_t runs, live, first;      // of Lb: runs of 8 columns; of all terms; the step's first
+  uint8_t lo, hi;                 // its positions of the tile
+  uint8_t side;
 };
 
-template <int GROUPS, bool OUT_F32, bool BWD, bool DROP>
+template <int GROUPS, bool OUT_F32, bool BWD, bool DROP, int MODE>
 __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(AdapterGemm p) {
-  constexpr int TERMS = OUT_F32 ? 3 : 2;
+  constexpr int TERMS = OUT_F32 ? 3 : 2, SIDES = MODE == GEMM_ONE ? 1 : 2;
+  constexpr bool GATED = MODE == GEMM_GATED;   // c = 0: gate, c = 1: up
+  constexpr int NT = GATED ? SN / 2 : SN;      // outputs per tile
   struct __attribute__((aligned(16))) Lds {
     uint16_t x[GROUPS][S_RING][SM * GK];
     uint16_t y[GROUPS][S_RING][SN * GK];
-    SmallStep steps[S_STEPS];
+    SmallStep steps[SIDES * S_STEPS];
     int total;
   };
   __shared__ Lds lds;
@@ -497,23 +557,25 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
   const int group = wave >> 2, w4 = wave & 3;
   const int li = lane & 15, lg = lane >> 4;
   const int wn = w4 & 1, wm = w4 >> 1;
-  const int64_t tiles_m = (p.M + SM - 1) / SM, tiles_n = (p.Ncols + SN - 1) / SN;
+  const int64_t tiles_m = (p.M + SM - 1) / SM, tiles_n = (p.Ncols + NT - 1) / NT;
   const int64_t total = tiles_m * tiles_n;
   const int64_t xcd = blockIdx.x % 8, per = total / 8, rem = total % 8;
   const int64_t t = xcd * per + min(xcd, rem) + blockIdx.x / 8;
-  const int64_t m0 = t % tiles_m * SM, n0 = t / tiles_m * SN, mend = min(m0 + SM, p.M);
+  const int64_t m0 = t % tiles_m * SM, n0 = t / tiles_m * NT, mend = min(m0 + SM, p.M);
 
   const int sub = lane >> 3, ch = (lane & 7) ^ sub;
-  const uint16_t *px[2], *py[2], *pt[2];
+  const uint16_t *px[2], *py[2], *pt[SIDES][2];
   int64_t ny[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int row = (w4 * 2 + q) * 8 + sub;
     const int64_t pos = min(m0 + row, p.M - 1);
-    px[q] = p.A + (int64_t)p.rt.perm[pos] * p.Kc + 8 * ch;
-    pt[q] = p.terms + pos * 3 * p.v.rs;
-    ny[q] = min(n0 + row, p.Ncols - 1);
-    py[q] = p.Bt + ny[q] * p.ldb + 8 * ch;
+    px[q] = p.A + (int64_t)p.rt.perm[pos] * p.lda + 8 * ch;
+#pragma unroll
+    for (int sd = 0; sd < SIDES; ++sd) pt[sd][q] = p.s[sd].terms + pos * 3 * p.s[sd].v.rs;
+    // GATED: row 32 wn + 16 c + i of the tile is row 16 wn + i of weight c
+    ny[q] = min(n0 + (GATED ? (row >> 5) * 16 + (row & 15) : row), p.Ncols - 1);
+    py[q] = (GATED && (w4 & 1) ? p.Bt2 : p.Bt) + ny[q] * p.ldb + 8 * ch;
   }
   const int nk = (int)((p.Kc + GK - 1) / GK);
   int steps = 0;   // of both parts, once the table is there
@@ -531,12 +593,14 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
       }
       return;
     }
-    SmallStep st{nullptr, 1, 0, 0, 0, 0};
+    SmallStep st{nullptr, 1, 0, 0, 0, 0, 0};
     if (it < steps) st = lds.steps[it - nk];
     const int c = st.first + ch;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      load_lds16(c < st.live ? pt[q] + 8 * c : p.zeros, rx[buf] + (w4 * 2 + q) * 8 * GK);
+      const uint16_t *const t0 = pt[0][q], *const t1 = pt[SIDES - 1][q];
+      load_lds16(c < st.live ? (SIDES == 2 && st.side ? t1 : t0) + 8 * c : p.zeros,
+                 rx[buf] + (w4 * 2 + q) * 8 * GK);
       load_lds16(c < st.live ? st.base + (ny[q] * st.runs + c % st.runs) * 8 : p.zeros, ry[buf] + (w4 * 2 + q) * 8 * GK);
     }
   };
@@ -553,21 +617,27 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
     const bool valid = m0 + lane < mend;
     const int a = valid ? p.rt.sid[m0 + lane] : -1, before = __shfl_up(a, 1);
     const uint64_t starts = __ballot(lane == 0 || a != before);
-    const bool leads = valid && a < p.v.n && ((starts >> lane) & 1);
-    const lq_adapter ad = p.v.tab[leads ? a : 0];
-    const int runs = (ad.r + 7) >> 3, live = TERMS * runs, count = leads ? (live + 7) >> 3 : 0;
-    int first = 0, sum = 0;
-#pragma unroll
-    for (int b = 0; b < 3; ++b) {
-      const uint64_t one = __ballot((count >> b) & 1);
-      first += (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(one >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)one, 0)) << b;
-      sum += __popcll(one) << b;
-    }
+    const bool leads = valid && a < p.s[0].v.n && ((starts >> lane) & 1);
     const uint64_t above = lane < 63 ? starts >> (lane + 1) : 0;
     const int hi = above ? lane + __ffsll((unsigned long long)above) : SM;
-    const uint16_t* base = !p.lt_all && ad.r % 8 == 0 ? ad.B : p.lt + p.Ncols * ad.row8;
-    for (int k = 0; k < count; ++k) lds.steps[first + k] = SmallStep{base, runs, live, 8 * k, lane, hi};
-    if (lane == 0) lds.total = sum;
+    int total = 0;
+    auto list = [&](const lq_adapter* tab, const uint16_t* lt, int side) {
+      const lq_adapter ad = tab[leads ? a : 0];
+      const int runs = (ad.r + 7) >> 3, live = TERMS * runs, count = leads ? (live + 7) >> 3 : 0;
+      int first = total;
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        const uint64_t one = __ballot((count >> b) & 1);
+        first += (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(one >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)one, 0)) << b;
+        total += __popcll(one) << b;
+      }
+      const uint16_t* base = !p.lt_all && ad.r % 8 == 0 ? ad.B : lt + p.Ncols * ad.row8;
+      for (int k = 0; k < count; ++k)
+        lds.steps[first + k] = SmallStep{base, (uint8_t)runs, (uint8_t)live, (uint8_t)(8 * k), (uint8_t)lane, (uint8_t)hi, (uint8_t)side};
+    };
+    if (MODE == GEMM_ONE || p.s[0].v.n) list(p.s[0].v.tab, p.s[0].lt, 0);   // (a pair may be without sets)
+    if (MODE != GEMM_ONE && p.s[0].v.n) list(p.s[1].v.tab, p.s[1].lt, 1);
+    if (lane == 0) lds.total = total;
   }
   __syncthreads();
   steps = nk + uniform(lds.total);
@@ -602,8 +672,13 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
         for (int r = 0; r < 2; ++r)
           acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fy[u][c]), as_bf16x8(fx[u][r]), acc[c][r], 0, 0, 0);
   };
-  uint32_t keep = 0;
-  if (DROP && steps > nk) keep = kept_outputs<2, 2>(p.drop, p.rt.perm, p.M, p.Ncols, m0 + wm * 32, n0 + wn * 32).w[0];
+  uint32_t keep[SIDES];
+#pragma unroll
+  for (int sd = 0; sd < SIDES; ++sd) {
+    keep[sd] = ~0u;
+    if (DROP && steps > nk)
+      keep[sd] = kept_outputs<2, 2>(p.s[sd].drop, p.rt.perm, p.M, p.Ncols, m0 + wm * 32, n0 + wn * 32).w[0];
+  }
   int i = 0;
   for (; GROUPS * (i + 1) <= nk; ++i) {
     turn(i);
@@ -616,6 +691,8 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
       multiply();
     } else if (it < steps) {
       const int lo = lds.steps[it - nk].lo, hi = lds.steps[it - nk].hi;
+      const int side = SIDES == 2 ? uniform(lds.steps[it - nk].side) : 0;
+      const uint32_t keep0 = keep[0], keep1 = keep[SIDES - 1], kept = SIDES == 2 && side ? keep1 : keep0;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int pos = wm * 32 + 16 * r + li;
@@ -628,25 +705,31 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
             d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(fy[u][c]), as_bf16x8(fx[u][r]), d, 0, 0, 0);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float add = DROP ? kept_value(d[e], keep, 8 * c + 4 * r + e) : d[e];
-            acc[c][r][e] += mine ? add : 0.0f;
+            const float add = DROP ? kept_value(d[e], kept, 8 * c + 4 * r + e) : d[e];
+            acc[c][r][e] += mine && (!GATED || side == c) ? add : 0.0f;
           }
         }
       }
     }
   }
   wait_vm<0>();   // the loads past the last step
-  if constexpr (GROUPS == 2) {   // group g finishes the weight rows of c = g, group 0's sum first
+  if constexpr (GROUPS == 2) {   // group g finishes the weight rows of c = g (GATED: the tokens of r = g), group 0's sum first
     ring_barrier<0>();   // the tiles are read: the sums take their place
-    f32x4_t* sum = reinterpret_cast<f32x4_t*>(lds.x) + 128 * w4 + lane;   // [group][w4][r][lane]
+    f32x4_t* sum = reinterpret_cast<f32x4_t*>(lds.x) + 128 * w4 + lane;   // [group][w4][k][lane]
 #pragma unroll
-    for (int r = 0; r < 2; ++r) sum[512 * group + 64 * r] = group ? acc[0][r] : acc[1][r];
+    for (int k = 0; k < 2; ++k)
+      sum[512 * group + 64 * k] = GATED ? (group ? acc[k][0] : acc[k][1]) : (group ? acc[0][k] : acc[1][k]);
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const f32x4_t other = sum[512 * (1 - group) + 64 * r];
-      if (group) acc[1][r] = other + acc[1][r];
-      else acc[0][r] = acc[0][r] + other;
+    for (int k = 0; k < 2; ++k) {
+      const f32x4_t other = sum[512 * (1 - group) + 64 * k];
+      if (GATED) {
+        if (group) acc[k][1] = other + acc[k][1];
+        else acc[k][0] = acc[k][0] + other;
+      } else {
+        if (group) acc[1][k] = other + acc[1][k];
+        else acc[0][k] = acc[0][k] + other;
+      }
     }
   }
 #pragma unroll
@@ -654,13 +737,20 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
     const int64_t pos = m0 + wm * 32 + 16 * r + li;
     if (pos >= p.M) continue;
     const int64_t row = (int64_t)p.rt.perm[pos] * p.Ncols;
+    if constexpr (GATED) {
+      if (GROUPS == 1 || r == group)
+        with_act(p.act, [&](auto act) __attribute__((always_inline)) {
+          store_gated4<OUT_F32, decltype(act)::value>(p, row, n0 + wn * 16 + 4 * lg, acc[0][r], acc[1][r]);
+        });
+    } else {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (GROUPS == 1 || c == group) store4<OUT_F32>(p, row, n0 + wn * 32 + 16 * c + 4 * lg, acc[c][r]);
+      for (int c = 0; c < 2; ++c)
+        if (GROUPS == 1 || c == group) store4<OUT_F32>(p, p.out, row, n0 + wn * 32 + 16 * c + 4 * lg, acc[c][r]);
+    }
   }
 }
 
-// 64 x 64 tiles through LDS; columns N .. ldb of the output are zero.
+// 64 x 64 tiles through LDS; columns past N, up to a multiple of 64, are zero.
 __global__ __launch_bounds__(256) void k_transpose_weight(const uint16_t* __restrict__ w, int64_t N, int64_t K,
                                                           int64_t ldb, uint16_t* __restrict__ out) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];   // [n][k]
@@ -679,19 +769,32 @@ __global__ __launch_bounds__(256) void k_transpose_weight(const uint16_t* __rest
     u32x4_t v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = (uint32_t)tile[c + 2 * e][k] | ((uint32_t)tile[c + 2 * e + 1][k] << 16);
-    *reinterpret_cast<u32x4_t*>(out + (k0 + k) * ldb + n0 + c) = v;   // ldb % 64 == 0 covers the tile
+    *reinterpret_cast<u32x4_t*>(out + (k0 + k) * ldb + n0 + c) = v;   // the row stride covers the tile
   }
 }
 
+#define LQ_GEMM_MODES(KERNEL, SIZE)                                                                                \
+  do {                                                                                                             \
+    const bool drops = g.s[0].drop.T || g.s[1].drop.T;                                                             \
+    if (g.mode == GEMM_GATED && g.out_f32) hipLaunchKernelGGL((KERNEL<SIZE, true, false, false, GEMM_GATED>), grid, block, 0, s, g); \
+    else if (g.mode == GEMM_GATED) hipLaunchKernelGGL((KERNEL<SIZE, false, false, false, GEMM_GATED>), grid, block, 0, s, g); \
+    else if (g.mode == GEMM_TWO && drops) hipLaunchKernelGGL((KERNEL<SIZE, false, true, true, GEMM_TWO>), grid, block, 0, s, g); \
+    else if (g.mode == GEMM_TWO) hipLaunchKernelGGL((KERNEL<SIZE, false, true, false, GEMM_TWO>), grid, block, 0, s, g); \
+    else if (g.lt_all && drops) hipLaunchKernelGGL((KERNEL<SIZE, false, true, true, GEMM_ONE>), grid, block, 0, s, g); \
+    else if (g.lt_all) hipLaunchKernelGGL((KERNEL<SIZE, false, true, false, GEMM_ONE>), grid, block, 0, s, g);      \
+    else if (g.out_f32) hipLaunchKernelGGL((KERNEL<SIZE, true, false, false, GEMM_ONE>), grid, block, 0, s, g);     \
+    else hipLaunchKernelGGL((KERNEL<SIZE, false, false, false, GEMM_ONE>), grid, block, 0, s, g);                   \
+  } while (0)
+
+// Weight rows per output of a tile: a gated tile's are shared by two weights.
+int64_t tile_cols(const AdapterGemm& g, int64_t bn) { return g.mode == GEMM_GATED ? bn / 2 : bn; }
+
 template <int BN>
 hipError_t launch_tile(const AdapterGemm& g, hipStream_t s) {
-  const int64_t tiles = ((g.M + GM - 1) / GM) * ((g.Ncols + BN - 1) / BN);
+  const int64_t cols = tile_cols(g, BN), tiles = ((g.M + GM - 1) / GM) * ((g.Ncols + cols - 1) / cols);
   LQ_DASSERT(tiles > 0 && tiles < (int64_t(1) << 31));
   const dim3 grid((unsigned)tiles), block(G_THREADS);
-  if (g.lt_all && g.drop.T) hipLaunchKernelGGL((k_adapter_gemm<BN, false, true, true>), grid, block, 0, s, g);
-  else if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm<BN, false, true, false>), grid, block, 0, s, g);
-  else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm<BN, true, false, false>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((k_adapter_gemm<BN, false, false, false>), grid, block, 0, s, g);
+  LQ_GEMM_MODES(k_adapter_gemm, BN);
   return hipGetLastError();
 }
 
@@ -699,22 +802,24 @@ template <int GROUPS>
 hipError_t launch_small(const AdapterGemm& g, int64_t tiles, hipStream_t s) {
   LQ_DASSERT(tiles > 0 && tiles < (int64_t(1) << 31));
   const dim3 grid((unsigned)tiles), block(S_THREADS * GROUPS);
-  if (g.lt_all && g.drop.T) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, true, true>), grid, block, 0, s, g);
-  else if (g.lt_all) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, true, false>), grid, block, 0, s, g);
-  else if (g.out_f32) hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, true, false, false>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((k_adapter_gemm_small<GROUPS, false, false, false>), grid, block, 0, s, g);
+  LQ_GEMM_MODES(k_adapter_gemm_small, GROUPS);
   return hipGetLastError();
 }
+#undef LQ_GEMM_MODES
 
 }  // namespace
 
 hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s) {
-  LQ_DASSERT(g.M > 0 && g.Ncols > 0 && g.Kc > 0 && g.Kc % 8 == 0 && g.ldb % 64 == 0 && g.ldb >= g.Kc);
+  LQ_DASSERT(g.M > 0 && g.Ncols > 0 && g.Kc > 0 && g.Kc % 8 == 0 && g.ldb % 64 == 0 && g.ldb >= g.Kc && g.lda >= g.Kc);
+  LQ_DASSERT(g.mode == GEMM_ONE || g.Kc % 64 == 0);
   // Rounds of a chip full of tiles times a tile's time per step, in us as
   // measured over K = 4096: 1.7 (256 x 256), 1.05 (256 x 128) and for 64 x 64,
   // two workgroups per CU, 0.3 where the tiles number more than the CUs. (Fewer
   // of them always win: 0.2.)
-  auto tiles = [&](int64_t m, int64_t n) { return ((g.M + m - 1) / m) * ((g.Ncols + n - 1) / n); };
+  auto tiles = [&](int64_t m, int64_t n) {
+    const int64_t cols = tile_cols(g, n);
+    return ((g.M + m - 1) / m) * ((g.Ncols + cols - 1) / cols);
+  };
   auto cost = [&](int64_t count, int64_t slots, double us) { return (double)((count + slots - 1) / slots) * us; };
   const int64_t small = tiles(SM, SN);
   const double c256 = cost(tiles(256, 256), 256, 1.7), c128 = cost(tiles(256, 128), 256, 1.05), c64 = cost(small, 512, 0.3);
@@ -725,8 +830,8 @@ hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s) {
 
 hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out,
                                    hipStream_t s) {
-  LQ_DASSERT(K % 64 == 0 && ldb % 64 == 0 && ldb >= N && ldb < N + 64);
-  hipLaunchKernelGGL(k_transpose_weight, dim3((unsigned)(ldb / 64), (unsigned)(K / 64)), dim3(256), 0, s, w, N, K, ldb,
+  LQ_DASSERT(K % 64 == 0 && ldb % 64 == 0 && ldb >= N);
+  hipLaunchKernelGGL(k_transpose_weight, dim3((unsigned)((N + 63) / 64), (unsigned)(K / 64)), dim3(256), 0, s, w, N, K, ldb,
                      out);
   return hipGetLastError();
 }

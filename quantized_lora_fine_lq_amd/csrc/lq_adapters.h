@@ -51,15 +51,24 @@ struct DownJob {
   float* part;             // adapter_down_ws_floats(M, C, rs)
   DropView drop;           // element m C + c of Q
   float post;              // 1 for a given t
+  AdapterView v;           // sets of one n
+  int shares;              // of the columns, joined in order (the launcher's)
+};
+constexpr int kDownJobs = 4;
+struct DownJobs {
+  DownJob j[kDownJobs];
 };
 size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs);
-hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
-                               const uint16_t* zeros, hipStream_t s);
+hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const Route& rt, const uint16_t* zeros,
+                               hipStream_t s);
+// The last part alone: `shares` partial sums of each job (or a given t) to terms.
+hipError_t launch_adapter_join(const DownJob* jobs, int njobs, int64_t M, const Route& rt, hipStream_t s);
 
 // Preparation, one launch of independent parts, each left out where its
 // pointer is null: 16 zero bytes (read by the other kernels in place of what
-// lies past an end); the route of ids; the weight decoded to wd (W' [N, K], or,
-// NF4 with ldb, W'^T [K, ldb], zero columns from N on); the adapters re-laid for the
+// lies past an end); the route of ids (ids null with a route: all tokens without
+// an adapter); the weight decoded to wd (W' [N, K], or, NF4 with ldb, W'^T [K, N
+// rounded up to a multiple of 64] of row stride ldb, zero columns past N); the adapters re-laid for the
 // matrix kernels: at = A^T [K, r8] at K * row8_a, bt = B^T [r, N] at N *
 // row8_a, bp = B [N, r8] at N * row8_a of the adapters whose rank is not a
 // multiple of 8 (zero columns past r_a).
@@ -77,31 +86,46 @@ struct ColReq {
   int transposed;
   float* part;             // adapter_col_ws_floats
   DropView drop;           // element m C + c of Q is left out
+  AdapterView v;           // sets of one n
 };
 size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs);
-hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const AdapterView& v, const Route& rt,
-                              hipStream_t s);
+hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Route& rt, hipStream_t s);
+// Its second part: joins the runs of `rows` positions of adapters with more than
+// one, and writes the zeros of adapters without tokens.
+hipError_t launch_adapter_col_reduce(const ColReq* reqs, int nreq, int rows, const Route& rt, hipStream_t s);
 
 // out[token][c] = sum_k A[token][k] Bt[c][k] + sum_j (s_a L)[token][j] Lb_a(c, j)
 // over the sorted positions; Lb_a(c, j): row c of lt + Ncols * row8_a
 // [Ncols, r8]; of B_a itself where lt_all is 0 and r_a % 8 == 0.
-struct AdapterGemm {
-  const uint16_t* A;       // [M, Kc]
-  int64_t M, Ncols, Kc;
-  const uint16_t* Bt;      // [Ncols, ldb], ldb % 64 == 0, zero from Kc to ldb
-  int64_t ldb;
+struct GemmSide {
   const uint16_t* terms;   // of s_a L
   AdapterView v;
   const uint16_t* lt;
+  DropView drop;           // lt_all: element m Ncols + c of this side's part is left out
+};
+// GEMM_ONE: side 0. GEMM_TWO (lt_all): the parts of both sides. GEMM_GATED (not
+// lt_all): two products of the same A, side 0 with Bt (g), side 1 with Bt2 (u);
+// out = act(g) u, and g and u themselves in bf16 where wanted.
+enum GemmMode { GEMM_ONE, GEMM_TWO, GEMM_GATED };
+struct AdapterGemm {
+  const uint16_t* A;       // [M, lda]
+  int64_t M, Ncols, Kc;
+  int64_t lda;
+  const uint16_t* Bt;      // [Ncols, ldb], ldb % 64 == 0, zero from Kc to ldb
+  int64_t ldb;
+  GemmSide s[2];
   int lt_all;
   Route rt;
   void* out;               // [M, Ncols] bf16 or float32
   int out_f32;
   const uint16_t* zeros;   // 16 zero bytes
-  DropView drop;           // lt_all: element m Ncols + c of the adapters' part is left out
+  int mode;
+  const uint16_t* Bt2;
+  int act;
+  uint16_t *g_out, *u_out; // [M, Ncols] or null
 };
 hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s);
-// [N, K] -> [K, ldb] bf16 (zero columns from N to ldb)
+// [N, K] -> [K, N rounded up to a multiple of 64] bf16 of row stride ldb (zero columns past N)
 hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out, hipStream_t s);
 
 // Decode sizes (NF4, M <= 64): the whole forward without a route, in two
@@ -110,6 +134,24 @@ bool adapter_decode_supported(const QWeight& w, int64_t M);
 size_t adapter_decode_ws_bytes(const QWeight& w, int64_t M, const AdapterView& v);
 hipError_t launch_adapter_decode(const QWeight& w, const uint16_t* X, int64_t M, const int32_t* ids,
                                  const AdapterView& v, void* ws, float* t_save, void* H, bool f32, hipStream_t s);
+
+// ---- the gated pair ----------------------------------------------------------
+// dg = G u act'(g), du = G act(g) of M tokens, formed from G, g, u [M, N] bf16.
+struct GatedGrad {
+  const uint16_t *G, *g, *u;
+  int64_t N;               // N % 8 == 0
+  int act;
+};
+// u_g = B_g^T dg and u_u = B_u^T du as partial sums [shares][M][rs] of each side
+// (bt: B^T [r, N] at N * row8_a; v.n == 0: of neither), and dg, du in bfloat16 as
+// D [M, 2 Np], Np = N rounded up to a multiple of 64, zero between (null: not wanted).
+size_t gated_down_ws_floats(int64_t M, int64_t N, int32_t rs);
+int gated_down_shares(int64_t M, int64_t N);
+hipError_t launch_gated_down(const GatedGrad& gr, int64_t M, const AdapterView (&v)[2], const uint16_t* const (&bt)[2],
+                             float* const (&part)[2], uint16_t* D, const Route& rt, hipStream_t s);
+// dB of both sides: requests as launch_adapter_col's (transposed), Q in place of
+// side 0's dg, side 1's du; a null out: not wanted.
+hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t M, const Route& rt, hipStream_t s);
 
 // ---- gradient lists ----------------------------------------------------------
 struct GradPiece {

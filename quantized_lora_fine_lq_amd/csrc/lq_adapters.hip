@@ -7,12 +7,10 @@
 
 #include "lq_adapters.h"
 #include "lq_device.h"
+#include "lq_route.h"
 
 namespace lq {
 namespace {
-
-__device__ __forceinline__ u32x4_t ld16(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // ===========================================================================
 // Route: a stable counting sort of the tokens by adapter, by one workgroup.
@@ -28,7 +26,7 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 constexpr int RT_WAVES = 16, RT_KEEP = 4;
 
 struct RouteJob {
-  const int32_t* ids;   // null: no route wanted
+  const int32_t* ids;   // null: no token has an adapter
   int64_t M;
   int32_t n;
   int32_t *off, *perm, *sid;
@@ -44,14 +42,14 @@ __device__ __forceinline__ void route_tokens(const RouteJob& jb, int32_t* cnt) {
   const int64_t m0 = min(M, wave * per), m1 = min(M, m0 + per);
   int keep[RT_KEEP];
 #pragma unroll
-  for (int g = 0; g < RT_KEEP; ++g) keep[g] = jb.ids[min(m0 + 64 * g + lane, M - 1)];
+  for (int g = 0; g < RT_KEEP; ++g) keep[g] = jb.ids ? jb.ids[min(m0 + 64 * g + lane, M - 1)] : -1;
   for (int i = threadIdx.x; i < RT_WAVES * keys; i += 64 * RT_WAVES) cnt[i] = 0;
   __syncthreads();
   auto key_of = [&](int id) { return (uint32_t)id < (uint32_t)n ? id : n; };
 #pragma unroll
   for (int g = 0; g < RT_KEEP; ++g)
     if (m0 + 64 * g + lane < m1) atomicAdd(&cnt[wave * keys + key_of(keep[g])], 1);
-  for (int64_t m = m0 + 64 * RT_KEEP + lane; m < m1; m += 64) atomicAdd(&cnt[wave * keys + key_of(jb.ids[m])], 1);
+  for (int64_t m = m0 + 64 * RT_KEEP + lane; m < m1; m += 64) atomicAdd(&cnt[wave * keys + key_of(jb.ids ? jb.ids[m] : -1)], 1);
   __syncthreads();
   // totals per key (thread k; keys <= 1024), waves' counts to exclusive sums
   const int k = threadIdx.x;
@@ -112,7 +110,7 @@ __device__ __forceinline__ void route_tokens(const RouteJob& jb, int32_t* cnt) {
 #pragma unroll
   for (int g = 0; g < RT_KEEP; ++g)
     if (m0 + 64 * g < m1) place(m0 + 64 * g, keep[g]);
-  for (int64_t g = m0 + 64 * RT_KEEP; g < m1; g += 64) place(g, g + lane < m1 ? jb.ids[g + lane] : 0);
+  for (int64_t g = m0 + 64 * RT_KEEP; g < m1; g += 64) place(g, g + lane < m1 && jb.ids ? jb.ids[g + lane] : -1);
 }
 
 // ===========================================================================
@@ -137,6 +135,7 @@ struct PrepJob {
   Nf4Levels lv;
   uint16_t* wd;          // W' [N, K], or transposed [K, ldb] (zero columns past N); null: not wanted
   int64_t ldb;           // 0: not transposed
+  int64_t wcols;         // columns written of the transposed rows
   AdapterView v;
   uint16_t *at, *bt, *bp;
   uint16_t* zeros;       // 16 bytes, cleared
@@ -228,7 +227,7 @@ __device__ __forceinline__ void prep_weight(const PrepJob& p, unsigned wg, unsig
     const uint16_t* src = sW + (r0 + (li >> 2)) * PW_PITCH + 16 * (wave & 7) + 4 * (li & 3);
     const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)src));
     const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)(src + 4 * PW_PITCH)));
-    if (kk < K && n0 + r0 < p.ldb)   // ldb covers N in whole runs of 64
+    if (kk < K && n0 + r0 < p.wcols)   // N in whole runs of 64
       *reinterpret_cast<u32x4_t*>(p.wd + kk * p.ldb + n0 + r0) = u32x4_t{a[0], a[1], b[0], b[1]};
   }
 }
@@ -359,54 +358,6 @@ __global__ __launch_bounds__(1024) void k_adapter_prep(PrepJob p) {
   if (p.per_adapter) prep_adapter(p, wg / p.per_adapter, wg % p.per_adapter, prep_lds);
 }
 
-// Item b of the segments [off[a], off[a + 1]), a < nseg, cut into pieces of
-// `rows` sorted positions: its segment, first position and row count. With
-// slot: the index of the piece among those of segments with more than one, or
-// -1. Every wave finds the item for itself (uniform results); false past the
-// last item.
-struct Item {
-  int seg, start, count, slot;
-};
-__device__ __forceinline__ bool find_item(const int32_t* __restrict__ off, int nseg, int rows, int b, Item& it) {
-  const int lane = threadIdx.x & 63;
-  int base = 0, sbase = 0;
-  for (int a0 = 0; a0 < nseg; a0 += 64) {
-    const int a = a0 + lane;
-    int lo = 0, len = 0;
-    if (a < nseg) {
-      lo = off[a];
-      len = off[a + 1] - lo;
-    }
-    const int c = (len + rows - 1) / rows, cs = c > 1 ? c : 0;
-    int inc = c, incs = cs;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int o = __shfl_up(inc, d), os = __shfl_up(incs, d);
-      if (lane >= d) {
-        inc += o;
-        incs += os;
-      }
-    }
-    const int first = base + inc - c;
-    const uint64_t hit = __ballot(b >= first && b < first + c);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      const int k = b - __shfl(first, l);
-      const int s = __shfl(lo, l) + k * rows;
-      const int e = __shfl(lo + len, l);
-      const int sl = __shfl(cs > 0 ? sbase + incs - cs : -1, l);
-      it.seg = uniform(a0 + l);
-      it.start = uniform(s);
-      it.count = uniform(min(rows, e - s));
-      it.slot = uniform(sl < 0 ? -1 : sl + k);
-      return true;
-    }
-    base += uniform(__shfl(inc, 63));
-    sbase += uniform(__shfl(incs, 63));
-  }
-  return false;
-}
-
 // The three bfloat16 terms of v.
 __device__ __forceinline__ void split3(float v, uint16_t (&o)[3]) {
 #pragma unroll
@@ -440,9 +391,10 @@ __device__ __forceinline__ void put_t(const DownJob& jb, const AdapterView& v, c
 // at 250 to 2048 tokens of rank 16, K = 4096; 6 at 300 tokens, K = 1024.
 // ===========================================================================
 template <int JT, int W, int U, bool DROP>
-__global__ __launch_bounds__(64 * W) void k_adapter_down(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt) {
+__global__ __launch_bounds__(64 * W) void k_adapter_down(DownJobs jobs, int64_t M, Route rt) {
   __shared__ f32x4_t part[W][JT][64];
-  const DownJob jb = blockIdx.y ? j1 : j0;
+  const DownJob jb = jobs.j[blockIdx.y];
+  const AdapterView& v = jb.v;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
   Item it;
@@ -553,15 +505,15 @@ __device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
 }
 
 template <int BN, bool DROP>
-__global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt,
-                                                            const uint16_t* zeros) {
+__global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJobs jobs, int64_t M, Route rt, const uint16_t* zeros) {
   constexpr int CT = BN / 16, QW = BN >= 32 ? BN / 32 : 1;
   struct __attribute__((aligned(16))) Lds {
     uint16_t x[DT_RING][DT_M * DT_K];
     uint16_t w[DT_RING][(BN < 32 ? 32 : BN) * DT_K];
   };
   __shared__ Lds lds;
-  const DownJob jb = blockIdx.z ? j1 : j0;
+  const DownJob jb = jobs.j[blockIdx.z];
+  const AdapterView& v = jb.v;
   if (!jb.Q) return;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
@@ -635,9 +587,9 @@ __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJob j0, DownJob 
     }
 }
 
-__global__ __launch_bounds__(256) void k_adapter_down_join(DownJob j0, DownJob j1, int64_t M, AdapterView v, Route rt,
-                                                           int shares) {
-  const DownJob jb = blockIdx.y ? j1 : j0;
+__global__ __launch_bounds__(256) void k_adapter_down_join(DownJobs jobs, int64_t M, Route rt) {
+  const DownJob jb = jobs.j[blockIdx.y];
+  const AdapterView& v = jb.v;
   const int64_t total = M * v.rs;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t pos = i / v.rs;
@@ -651,7 +603,7 @@ __global__ __launch_bounds__(256) void k_adapter_down_join(DownJob j0, DownJob j
     if (j < ad.r) {
       if (jb.Q) {
         x = jb.part[i];
-        for (int k = 1; k < shares; ++k) x += jb.part[k * total + i];
+        for (int k = 1; k < jb.shares; ++k) x += jb.part[k * total + i];
         x *= jb.post;
       } else {
         x = jb.given[(int64_t)rt.perm[pos] * v.r_max + j];
@@ -692,24 +644,8 @@ int down_shares(int64_t M, int64_t C) {
 // ===========================================================================
 constexpr int CQ_COLS = 256, CQ_PITCH = CQ_COLS + 16;
 
-// lane's 8 values k = 8 lg + [0, 8) of column li, from rows of `pitch` elements
-__device__ __forceinline__ u32x4_t tr_frag(const uint16_t* base, int pitch, int li, int lg) {
-  typedef __bf16 v4b __attribute__((ext_vector_type(4)));
-  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-  typedef __attribute__((address_space(3))) v4b* lds_p;
-  const uint16_t* p = base + (8 * lg + (li >> 2)) * pitch + 4 * (li & 3);
-  const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)p));
-  const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)(p + 4 * pitch)));
-  return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-}
-
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 template <int JT, bool DROP>
-__global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0, ColReq q1, unsigned tiles0, int rows, AdapterView v,
-                                                     Route rt) {
+__global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0, ColReq q1, unsigned tiles0, int rows, Route rt) {
   constexpr int PP = 16 * JT + 16;
   constexpr int BUFS = JT <= 2 ? 2 : 1;
   constexpr int PQ = (3 * 32 * 2 * JT + 255) / 256;   // 16-byte pieces of P per thread
@@ -717,6 +653,7 @@ __global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0,
   __shared__ __attribute__((aligned(16))) uint16_t sP[BUFS][3 * 32 * PP];
   const bool second = blockIdx.x >= tiles0;
   const ColReq rq = second ? q1 : q0;
+  const AdapterView& v = rq.v;
   Item it;
   if (!find_item(rt.off, v.n, rows, (int)blockIdx.y, it)) return;
   const lq_adapter ad = v.tab[it.seg];
@@ -828,8 +765,7 @@ __global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0,
 // Joins the runs of adapters with more than one, in order, and writes the zero
 // gradients of adapters without tokens. 7 us at 2048 tokens of rank 16, 16 at
 // 4096 of rank 64 (four partial sums a thread at a time).
-__global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1, int nreq, int rows, AdapterView v,
-                                                            Route rt) {
+__global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1, int nreq, int rows, Route rt) {
   const int a = blockIdx.y, lane = threadIdx.x & 63;
   int before = 0;   // slots of the adapters before a
   for (int b = lane; b < a; b += 64) {
@@ -840,21 +776,23 @@ __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1
   for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
   const int runs = (rt.off[a + 1] - rt.off[a] + rows - 1) / rows;
   if (runs == 1) return;
-  const lq_adapter ad = v.tab[a];
   // four values a thread: of one row (C % 8 == 0), or of four rows where the
   // output is transposed (then consecutive threads still read consecutive columns)
-  const int rq = (ad.r + 3) / 4;
-  const int64_t n0 = q0.transposed ? rq * q0.C : ad.r * q0.C / 4;
-  const int64_t n1 = nreq > 1 ? (q1.transposed ? rq * q1.C : ad.r * q1.C / 4) : 0;
+  auto count = [&](const ColReq& q) {
+    const int r = q.v.tab[a].r;
+    return q.transposed ? (r + 3) / 4 * q.C : r * q.C / 4;
+  };
+  const int64_t n0 = count(q0), n1 = nreq > 1 ? count(q1) : 0;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n0 + n1; i += (int64_t)gridDim.x * 256) {
     const ColReq& q = i < n0 ? q0 : q1;
+    const lq_adapter ad = q.v.tab[a];
     const int64_t e = i < n0 ? i : i - n0;
     if (q.transposed) {
       const int64_t c = e % q.C;
       const int j = 4 * (int)(e / q.C);
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int k = 0; k < runs; ++k) {
-        const float* p = q.part + ((int64_t)(before + k) * v.rs + j) * q.C + c;   // rs rows: a multiple of 8
+        const float* p = q.part + ((int64_t)(before + k) * q.v.rs + j) * q.C + c;   // rs rows: a multiple of 8
 #pragma unroll
         for (int u = 0; u < 4; ++u) sum[u] += p[u * q.C];
       }
@@ -865,7 +803,7 @@ __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1
       const int64_t j = 4 * e / q.C, c = 4 * e % q.C;
       f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int k = 0; k < runs; ++k)
-        sum += *reinterpret_cast<const f32x4_t*>(q.part + ((int64_t)(before + k) * v.rs + j) * q.C + c);
+        sum += *reinterpret_cast<const f32x4_t*>(q.part + ((int64_t)(before + k) * q.v.rs + j) * q.C + c);
       float* o = q.out + (q.C * (ad.row + j) + c);   // 4-byte aligned
 #pragma unroll
       for (int u = 0; u < 4; ++u) o[u] = sum[u];
@@ -899,6 +837,7 @@ hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, co
   p.lv = tables().lv;
   p.wd = wd;
   p.ldb = ldb;
+  p.wcols = (w.N + 63) / 64 * 64;
   if (wd) {
     const int64_t flat = PW_FLAT * 1024 * 16;
     if (w.format == LQ_FMT_CODEBOOK) {
@@ -928,46 +867,76 @@ size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs) {
   return down_tiled(M, rs) ? (size_t)down_shares(M, C) * M * rs : 0;
 }
 
-hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const AdapterView& v, const Route& rt,
-                               const uint16_t* zeros, hipStream_t s) {
-  if (njobs < 1 || njobs > 2) return hipErrorInvalidValue;
-  const DownJob j0 = jobs[0], j1 = jobs[njobs - 1];
-  const bool drops = j0.drop.T || j1.drop.T;
-  if (down_tiled(M, v.rs)) {
-    int shares = 1;
+hipError_t launch_adapter_join(const DownJob* jobs, int njobs, int64_t M, const Route& rt, hipStream_t s) {
+  if (njobs < 1 || njobs > kDownJobs) return hipErrorInvalidValue;
+  DownJobs all{};
+  int32_t rs = 0;
+  for (int i = 0; i < njobs; ++i) {
+    all.j[i] = jobs[i];
+    rs = std::max(rs, jobs[i].v.rs);
+  }
+  const unsigned gx = (unsigned)std::min<int64_t>((M * rs + 255) / 256, 8192);
+  hipLaunchKernelGGL(k_adapter_down_join, dim3(gx, (unsigned)njobs), dim3(256), 0, s, all, M, rt);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const Route& rt, const uint16_t* zeros,
+                               hipStream_t s) {
+  if (njobs < 1 || njobs > kDownJobs) return hipErrorInvalidValue;
+  DownJobs all{};
+  bool drops = false, tiled = false;
+  int32_t r_max = 0;
+  const int32_t n = jobs[0].v.n;
+  for (int i = 0; i < njobs; ++i) {
+    all.j[i] = jobs[i];
+    drops |= jobs[i].drop.T != 0;
+    r_max = std::max(r_max, jobs[i].v.r_max);
+    tiled |= down_tiled(M, jobs[i].v.rs);
+  }
+  // jobs of one form each: of sets whose ranks differ, some may be tiled
+  if (tiled)
+    for (int i = 0; i < njobs; ++i)
+      if (!down_tiled(M, jobs[i].v.rs)) {
+        if (njobs == 1) return hipErrorInvalidValue;
+        DownJob a[kDownJobs], b[kDownJobs];
+        int na = 0, nb = 0;
+        for (int k = 0; k < njobs; ++k) (down_tiled(M, jobs[k].v.rs) ? a[na++] : b[nb++]) = jobs[k];
+        const hipError_t e = launch_adapter_down(a, na, M, rt, zeros, s);
+        return e != hipSuccess ? e : launch_adapter_down(b, nb, M, rt, zeros, s);
+      }
+  if (tiled) {
     int64_t C = 0;
     for (int i = 0; i < njobs; ++i)
-      if (jobs[i].Q) C = C ? std::min(C, jobs[i].C) : jobs[i].C;   // both jobs' workspaces hold these shares
+      if (jobs[i].Q) C = C ? std::min(C, jobs[i].C) : jobs[i].C;   // all jobs' workspaces hold these shares
+    const int shares = C ? down_shares(M, C) : 1;
+    for (int i = 0; i < njobs; ++i) all.j[i].shares = shares;
     if (C) {
-      shares = down_shares(M, C);
-      const dim3 grid((unsigned)((M + DT_M - 1) / DT_M + std::min<int64_t>(v.n, M)), (unsigned)shares, (unsigned)njobs);
-#define LQ_AT(BN)                                                                                               \
-  do {                                                                                                          \
-    if (drops) hipLaunchKernelGGL((k_adapter_down_tiles<BN, true>), grid, dim3(256), 0, s, j0, j1, M, v, rt, zeros); \
-    else hipLaunchKernelGGL((k_adapter_down_tiles<BN, false>), grid, dim3(256), 0, s, j0, j1, M, v, rt, zeros);      \
+      const dim3 grid((unsigned)((M + DT_M - 1) / DT_M + std::min<int64_t>(n, M)), (unsigned)shares, (unsigned)njobs);
+#define LQ_AT(BN)                                                                                      \
+  do {                                                                                                 \
+    if (drops) hipLaunchKernelGGL((k_adapter_down_tiles<BN, true>), grid, dim3(256), 0, s, all, M, rt, zeros); \
+    else hipLaunchKernelGGL((k_adapter_down_tiles<BN, false>), grid, dim3(256), 0, s, all, M, rt, zeros);      \
   } while (0)
-      if (v.r_max <= 16) LQ_AT(16);
-      else if (v.r_max <= 32) LQ_AT(32);
-      else if (v.r_max <= 64) LQ_AT(64);
+      if (r_max <= 16) LQ_AT(16);
+      else if (r_max <= 32) LQ_AT(32);
+      else if (r_max <= 64) LQ_AT(64);
       else LQ_AT(128);
 #undef LQ_AT
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    const unsigned gx = (unsigned)std::min<int64_t>((M * v.rs + 255) / 256, 8192);
-    hipLaunchKernelGGL(k_adapter_down_join, dim3(gx, (unsigned)njobs), dim3(256), 0, s, j0, j1, M, v, rt, shares);
-    return hipGetLastError();
+    return launch_adapter_join(all.j, njobs, M, rt, s);
   }
   // one item per 16 tokens, and one more per adapter (or none) for its remainder
-  const dim3 grid((unsigned)((M + 15) / 16 + std::min<int64_t>(v.n + 1, M)), (unsigned)njobs);
-#define LQ_AD(JT, W, U)                                                                                        \
-  do {                                                                                                         \
-    if (drops) hipLaunchKernelGGL((k_adapter_down<JT, W, U, true>), grid, dim3(64 * W), 0, s, j0, j1, M, v, rt); \
-    else hipLaunchKernelGGL((k_adapter_down<JT, W, U, false>), grid, dim3(64 * W), 0, s, j0, j1, M, v, rt);      \
+  const dim3 grid((unsigned)((M + 15) / 16 + std::min<int64_t>(n + 1, M)), (unsigned)njobs);
+#define LQ_AD(JT, W, U)                                                                              \
+  do {                                                                                               \
+    if (drops) hipLaunchKernelGGL((k_adapter_down<JT, W, U, true>), grid, dim3(64 * W), 0, s, all, M, rt); \
+    else hipLaunchKernelGGL((k_adapter_down<JT, W, U, false>), grid, dim3(64 * W), 0, s, all, M, rt);      \
   } while (0)
-  if (v.r_max <= 16) LQ_AD(1, 16, 2);
-  else if (v.r_max <= 32) LQ_AD(2, 8, 2);
-  else if (v.r_max <= 64) LQ_AD(4, 8, 1);
+  if (r_max <= 16) LQ_AD(1, 16, 2);
+  else if (r_max <= 32) LQ_AD(2, 8, 2);
+  else if (r_max <= 64) LQ_AD(4, 8, 1);
   else LQ_AD(8, 8, 1);
 #undef LQ_AD
   return hipGetLastError();
@@ -979,30 +948,36 @@ size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs) {
   return (size_t)(2 * ((M + rows - 1) / rows)) * rs * C;
 }
 
-hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const AdapterView& v, const Route& rt,
-                              hipStream_t s) {
+hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Route& rt, hipStream_t s) {
   if (nreq < 1 || nreq > 2) return hipErrorInvalidValue;
   const ColReq q0 = reqs[0], q1 = reqs[nreq - 1];
   const bool drops = q0.drop.T || q1.drop.T;
   const int rows = col_rows(M, q0.C + (nreq > 1 ? q1.C : 0));
   const unsigned t0 = (unsigned)((q0.C + CQ_COLS - 1) / CQ_COLS);
   const unsigned t1 = nreq > 1 ? (unsigned)((q1.C + CQ_COLS - 1) / CQ_COLS) : 0u;
-  const dim3 grid(t0 + t1, (unsigned)((M + rows - 1) / rows + std::min<int64_t>(v.n, M)));
-  switch ((v.r_max + 15) / 16) {
-#define LQ_AC(JT)                                                                                                    \
-  case JT:                                                                                                           \
-    if (drops) hipLaunchKernelGGL((k_adapter_col<JT, true>), grid, dim3(256), 0, s, q0, q1, t0, rows, v, rt);        \
-    else hipLaunchKernelGGL((k_adapter_col<JT, false>), grid, dim3(256), 0, s, q0, q1, t0, rows, v, rt);             \
+  const dim3 grid(t0 + t1, (unsigned)((M + rows - 1) / rows + std::min<int64_t>(q0.v.n, M)));
+  switch ((std::max(q0.v.r_max, q1.v.r_max) + 15) / 16) {
+#define LQ_AC(JT)                                                                                                  \
+  case JT:                                                                                                         \
+    if (drops) hipLaunchKernelGGL((k_adapter_col<JT, true>), grid, dim3(256), 0, s, q0, q1, t0, rows, rt);         \
+    else hipLaunchKernelGGL((k_adapter_col<JT, false>), grid, dim3(256), 0, s, q0, q1, t0, rows, rt);              \
     break;
     LQ_AC(1) LQ_AC(2) LQ_AC(3) LQ_AC(4) LQ_AC(5) LQ_AC(6) LQ_AC(7) LQ_AC(8)
 #undef LQ_AC
     default: return hipErrorInvalidValue;
   }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t most = (int64_t)v.r_max * (q0.C + (nreq > 1 ? q1.C : 0));
-  const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 255) / 256, std::max(32, 4096 / v.n)));
-  hipLaunchKernelGGL(k_adapter_col_reduce, dim3(gx, (unsigned)v.n), dim3(256), 0, s, q0, q1, nreq, rows, v, rt);
+  return launch_adapter_col_reduce(reqs, nreq, rows, rt, s);
+}
+
+hipError_t launch_adapter_col_reduce(const ColReq* reqs, int nreq, int rows, const Route& rt, hipStream_t s) {
+  if (nreq < 1 || nreq > 2) return hipErrorInvalidValue;
+  const ColReq q0 = reqs[0], q1 = reqs[nreq - 1];
+  const int64_t most = q0.v.r_max * q0.C + (nreq > 1 ? q1.v.r_max * q1.C : 0);
+  const unsigned gx =
+      (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 255) / 256, std::max(32, 4096 / q0.v.n)));
+  hipLaunchKernelGGL(k_adapter_col_reduce, dim3(gx, (unsigned)q0.v.n), dim3(256), 0, s, q0, q1, nreq, rows, rt);
   return hipGetLastError();
 }
 

@@ -6,11 +6,9 @@
 #include <vector>
 
 #include "lq_adapters.h"
-#include "lq_host.h"
+#include "lq_adapters_host.h"
 
-namespace {
-
-using namespace lq;
+namespace lq {
 
 int check_set(const lq_adapter_set* set, int64_t N, int64_t K, AdapterView* v) {
   if (!set || !set->host || !set->dev || !al(set->dev, 8)) return LQ_ERR_ARG;
@@ -30,24 +28,11 @@ int check_set(const lq_adapter_set* set, int64_t N, int64_t K, AdapterView* v) {
   return LQ_OK;
 }
 
-int64_t sum_r8(const lq_adapter_set* set) {
-  const lq_adapter& last = set->host[set->n - 1];
-  return (int64_t)last.row8 + (last.r + 7) / 8 * 8;
-}
+}  // namespace lq
 
-bool valid_M(int64_t M) { return M >= 1 && M < (int64_t(1) << 31); }
+namespace {
 
-size_t route_bytes(int64_t M, int32_t n) { return (size_t)route_words(M, n) * sizeof(int32_t); }
-
-int64_t ldb_of(int64_t n) { return (n + 63) / 64 * 64; }
-
-bool any_odd_rank(const lq_adapter_set* set) {
-  for (int32_t a = 0; a < set->n; ++a)
-    if (set->host[a].r % 8) return true;
-  return false;
-}
-
-size_t bytes16(size_t elems) { return align_up(elems * sizeof(uint16_t)); }
+using namespace lq;
 
 // route, terms of t, W', zeros, B of ranks that are no multiple of 8; at
 // decode sizes what that path keeps
@@ -69,9 +54,6 @@ size_t backward_ws(const QWeight& q, int64_t M, const AdapterView& v, int64_t r8
          align_up(adapter_down_ws_floats(M, q.K, v.rs) * sizeof(float)) +
          align_up(adapter_down_ws_floats(M, q.N, v.rs) * sizeof(float));
 }
-
-// The generator counts a tensor's elements up to 2^47.
-bool drop_fits(int64_t M, int64_t K) { return K < (int64_t(1) << 47) / M; }
 
 // The forward; d null: without dropout. Decode sizes with dropout run as larger ones.
 int run_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const lq_adapter_set* set, const int32_t* ids,
@@ -108,9 +90,10 @@ int run_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const lq_adap
   hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, wd, 0, v, nullptr, nullptr, bp, zeros, s);
   if (e != hipSuccess) return LQ_ERR_LAUNCH;
   const Route rt = route_view(route ? route : rws, M, v.n);
-  const DownJob job{X, q.K, nullptr, nullptr, terms, t_save, part, drop, factor};
-  if ((e = launch_adapter_down(&job, 1, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  const AdapterGemm g{X, M, q.N, q.K, wd, q.K, terms, v, bp, 0, rt, H, h_dtype == LQ_F32 ? 1 : 0, zeros, DropView{}};
+  const DownJob job{X, q.K, nullptr, nullptr, terms, t_save, part, drop, factor, v, 1};
+  if ((e = launch_adapter_down(&job, 1, M, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  const AdapterGemm g{X,  M, q.N, q.K, q.K, wd, q.K, {{terms, v, bp, DropView{}}, {}}, 0, rt, H,
+                      h_dtype == LQ_F32 ? 1 : 0, zeros, GEMM_ONE, nullptr, 0, nullptr, nullptr};
   return launch_status(launch_adapter_gemm(g, s));
 }
 
@@ -159,18 +142,19 @@ int run_backward(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int6
   const Route rt = route_view(route ? route : rws, M, v.n);
   DownJob jobs[2];
   int nj = 0;
-  if (need_u) jobs[nj++] = DownJob{G, q.N, bt, nullptr, u, nullptr, down_u, DropView{}, factor};
+  if (need_u) jobs[nj++] = DownJob{G, q.N, bt, nullptr, u, nullptr, down_u, DropView{}, factor, v, 1};
   if (dB) jobs[nj++] = DownJob{t_saved ? nullptr : X, q.K, nullptr, t_saved, t, nullptr, down_t,
-                                t_saved ? DropView{} : drop, t_saved ? 1.0f : factor};
-  if (nj && (e = launch_adapter_down(jobs, nj, M, v, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+                                t_saved ? DropView{} : drop, t_saved ? 1.0f : factor, v, 1};
+  if (nj && (e = launch_adapter_down(jobs, nj, M, rt, zeros, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   ColReq cols[2];
   int nc = 0;
-  if (dB) cols[nc++] = ColReq{t, G, q.N, dB, 1, part_b, DropView{}};
-  if (dA) cols[nc++] = ColReq{u, X, q.K, dA, 0, part_a, drop};
-  if (nc && (e = launch_adapter_col(cols, nc, M, v, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  if (dB) cols[nc++] = ColReq{t, G, q.N, dB, 1, part_b, DropView{}, v};
+  if (dA) cols[nc++] = ColReq{u, X, q.K, dA, 0, part_a, drop, v};
+  if (nc && (e = launch_adapter_col(cols, nc, M, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   if (!grad_X) return LQ_OK;
   if (!nf4 && (e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
-  const AdapterGemm g{G, M, q.K, q.N, wt, ldb, u, v, at, 1, rt, grad_X, 0, zeros, drop};
+  const AdapterGemm g{G,  M, q.K, q.N, q.N, wt, ldb, {{u, v, at, drop}, {}}, 1, rt, grad_X,
+                      0,  zeros, GEMM_ONE, nullptr, 0, nullptr, nullptr};
   return launch_status(launch_adapter_gemm(g, s));
 }
 

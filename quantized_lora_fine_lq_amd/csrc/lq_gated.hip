@@ -1,0 +1,361 @@
+// The gated pair's backward between its two ends: from G, g and u the gradients
+//   dg = G u act'(g),  du = G act(g)
+// and their skinny products with the adapters, u_g = B_g^T dg, u_u = B_u^T du,
+// dB_g = s dg^T t_g, dB_u = s du^T t_u.
+//
+// dg and du are formed again where they are used, from the three bfloat16
+// tensors: that is 6 bytes an element read against 12 if their three bfloat16
+// terms were kept. They enter the adapters' products as those terms (all 24
+// bits, since dA and dB are float32); grad_X's large product takes the first
+// term alone, its bfloat16 rounding, whose error is that of the rounded result.
+#include <algorithm>
+
+#include "lq_act.h"
+#include "lq_adapters.h"
+#include "lq_device.h"
+#include "lq_route.h"
+
+namespace lq {
+namespace {
+
+// 8 elements' dg and du.
+template <int ACT>
+__device__ __forceinline__ void gate_grads(u32x4_t G, u32x4_t g, u32x4_t u, float (&dg)[8], float (&du)[8]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t Gw = G[w], gw = g[w], uw = u[w];
+    const ActPair a0 = act_pair<ACT>(bf16lo_to_f32(gw)), a1 = act_pair<ACT>(bf16hi_to_f32(gw));
+    const float G0 = bf16lo_to_f32(Gw), G1 = bf16hi_to_f32(Gw);
+    dg[2 * w] = G0 * bf16lo_to_f32(uw) * a0.slope;
+    dg[2 * w + 1] = G1 * bf16hi_to_f32(uw) * a1.slope;
+    du[2 * w] = G0 * a0.value;
+    du[2 * w + 1] = G1 * a1.value;
+  }
+}
+// The next bfloat16 term of 8 values.
+__device__ __forceinline__ u32x4_t take8(float (&v)[8]) {
+  return u32x4_t{take_bf16_terms(v[0], v[1]), take_bf16_terms(v[2], v[3]), take_bf16_terms(v[4], v[5]),
+                 take_bf16_terms(v[6], v[7])};
+}
+
+// ===========================================================================
+// Row form: 64 routed tokens of one adapter (or of none: D alone) per workgroup
+// and share of the columns, 16 a wave, in steps of 64 columns. A lane forms dg
+// and du of 8 columns of a token in registers, which is the matrix product's
+// operand; B^T's rows pass through LDS, double buffered, loaded a step ahead.
+// ===========================================================================
+constexpr int GD_M = 64, GD_K = 64;
+
+struct GatedDown {
+  GatedGrad gr;
+  AdapterView v[2];
+  const uint16_t* bt[2];
+  float* part[2];
+  uint16_t* D;
+  int64_t Np;
+};
+
+template <int JT, int ACT>
+__global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Route rt) {
+  constexpr int ROWS = 16 * JT;
+  __shared__ __attribute__((aligned(16))) uint16_t sW[2][2][ROWS * GD_K];   // [buffer][side]
+  Item it;
+  if (!find_item(rt.off, p.v[0].n + 1, GD_M, (int)blockIdx.x, it)) return;
+  const bool has = it.seg < p.v[0].n;
+  const int64_t N = p.gr.N;
+  int r[2] = {1, 1};
+  const uint16_t* bt[2] = {nullptr, nullptr};
+  if (has) {
+#pragma unroll
+    for (int sd = 0; sd < 2; ++sd) {
+      const lq_adapter ad = p.v[sd].tab[it.seg];
+      r[sd] = min(ad.r, ROWS);
+      bt[sd] = p.bt[sd] + N * ad.row8;
+    }
+  }
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  const int all = (int)(p.Np / GD_K), per = (all + gridDim.y - 1) / gridDim.y;
+  const int s0 = min(all, (int)blockIdx.y * per), s1 = min(all, s0 + per);
+  const int row = 16 * wave + li;
+  const bool live = row < it.count;
+  const int64_t token = rt.perm[it.start + min(row, it.count - 1)];
+  const uint16_t *pG = p.gr.G + token * N, *pg = p.gr.g + token * N, *pu = p.gr.u + token * N;
+  struct Q {
+    u32x4_t G[2], g[2], u[2];
+  };
+  Q q;
+  u32x4_t w[JT];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t c = GD_K * (int64_t)s + 32 * h + 8 * lg;
+      const bool ok = c < N;   // N % 8 == 0
+      const int64_t o = ok ? c : 0;
+      q.G[h] = ld16(pG + o);
+      q.g[h] = ld16(pg + o);
+      q.u[h] = ld16(pu + o);
+      if (!ok) q.G[h] = q.g[h] = q.u[h] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+    if (!has) return;
+#pragma unroll
+    for (int k = 0; k < JT; ++k) {
+      const int i = threadIdx.x + 256 * k, sd = i / (8 * ROWS), j = (i >> 3) % ROWS;
+      const int64_t c = GD_K * (int64_t)s + 8 * (i & 7);
+      w[k] = ld16((sd ? bt[1] : bt[0]) + min(j, (sd ? r[1] : r[0]) - 1) * N + (c < N ? c : 0));
+      if (c >= N) w[k] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+  };
+  f32x4_t acc[2][JT];
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+    for (int c = 0; c < JT; ++c) acc[sd][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
+  if (s0 < s1) load(s0);
+  for (int s = s0; s < s1; ++s) {
+    uint16_t(*buf)[ROWS * GD_K] = sW[(s - s0) & 1];
+    if (has) {
+#pragma unroll
+      for (int k = 0; k < JT; ++k) {
+        const int i = threadIdx.x + 256 * k, sd = i / (8 * ROWS), j = (i >> 3) % ROWS;
+        *reinterpret_cast<u32x4_t*>(buf[sd] + j * GD_K + 8 * ((i & 7) ^ (j & 7))) = w[k];
+      }
+    }
+    const Q now = q;
+    // (one barrier a step: the buffer written at step s + 1 was read at s - 1, and
+    // those reads are done before a wave reaches step s's barrier)
+    if (has) lds_barrier();
+    if (s + 1 < s1) load(s + 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float d[2][8];
+      gate_grads<ACT>(now.G[h], now.g[h], now.u[h], d[0], d[1]);
+      u32x4_t t[2];
+#pragma unroll
+      for (int sd = 0; sd < 2; ++sd) t[sd] = take8(d[sd]);
+      if (p.D && live) {
+        uint16_t* o = p.D + token * 2 * p.Np + GD_K * (int64_t)s + 32 * h + 8 * lg;
+        *reinterpret_cast<u32x4_t*>(o) = t[0];
+        *reinterpret_cast<u32x4_t*>(o + p.Np) = t[1];
+      }
+      if (!has) continue;
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int sd = 0; sd < 2; ++sd) {
+#pragma unroll
+          for (int c = 0; c < JT; ++c)
+            acc[sd][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                as_bf16x8(t[sd]), as_bf16x8(ld16(buf[sd] + (16 * c + li) * GD_K + slot[h])), acc[sd][c], 0, 0, 0);
+          if (k < 2) t[sd] = take8(d[sd]);
+        }
+    }
+  }
+  if (!has) return;
+  // lane: tokens 16 wave + 4 lg + e, row 16 c + li of the adapter
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd) {
+    float* part = p.part[sd] + (int64_t)blockIdx.y * M * p.v[sd].rs;
+#pragma unroll
+    for (int c = 0; c < JT; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int m = 16 * wave + 4 * lg + e, j = 16 * c + li;
+        if (m < it.count && j < r[sd]) part[(int64_t)(it.start + m) * p.v[sd].rs + j] = acc[sd][c][e];
+      }
+  }
+}
+
+// ===========================================================================
+// Column form of both sides: one workgroup per 128 columns and run of at most
+// `rows` sorted positions, 32 tokens a step; waves 0, 1 take dg with the gate's
+// t, waves 2, 3 du with up's, 64 columns each. The terms of dg and du lie in LDS
+// with tokens as rows and are read transposed, as the terms of s t. Of the nine
+// products of terms the six whose places add up to at most the third are formed:
+// the others are below 2^-24 of the value.
+// ===========================================================================
+constexpr int GC_COLS = 128, GC_PITCH = GC_COLS + 16;
+
+template <int JT, int ACT>
+__global__ __launch_bounds__(256) void k_gated_col(GatedGrad gr, ColReq r0, ColReq r1, int rows, Route rt) {
+  constexpr int PP = 16 * JT + 16;
+  constexpr int PQ = (2 * 3 * 32 * 2 * JT + 255) / 256;   // 16-byte pieces of both sides' t per thread
+  __shared__ __attribute__((aligned(16))) uint16_t sQ[2][3][32 * GC_PITCH];
+  __shared__ __attribute__((aligned(16))) uint16_t sP[2][3 * 32 * PP];
+  Item it;
+  if (!find_item(rt.off, r0.v.n, rows, (int)blockIdx.y, it)) return;
+  const lq_adapter ad0 = r0.v.tab[it.seg], ad1 = r1.v.tab[it.seg];
+  const int r80 = (min(ad0.r, 16 * JT) + 7) & ~7, r81 = (min(ad1.r, 16 * JT) + 7) & ~7;
+  const int64_t N = gr.N, c0 = (int64_t)blockIdx.x * GC_COLS;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int li = lane & 15, lg = lane >> 4;
+  const int side = uniform(wave >> 1), half = wave & 1;
+  const int qc = 8 * (threadIdx.x & 15), qr = threadIdx.x >> 4;   // columns of tokens qr, qr + 16
+  const bool qin = c0 + qc < N;                                   // N % 8 == 0
+  u32x4_t xG[2], xg[2], xu[2], xp[PQ];
+  int tok[2];
+  auto tokens = [&](int mb) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) tok[u] = rt.perm[it.start + min(mb + qr + 16 * u, it.count - 1)];
+  };
+  auto load = [&](int mb) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t o = (int64_t)tok[u] * N + (qin ? c0 + qc : 0);
+      xG[u] = ld16(gr.G + o);
+      xg[u] = ld16(gr.g + o);
+      xu[u] = ld16(gr.u + o);
+    }
+#pragma unroll
+    for (int k = 0; k < PQ; ++k) {
+      const int i = threadIdx.x + 256 * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, t = min(i / (64 * JT), 5);
+      const bool up = t >= 3;
+      const int term = up ? t - 3 : t, r8 = up ? r81 : r80;
+      xp[k] = ld16((up ? r1.terms : r0.terms) + (int64_t)(it.start + min(mb + row, it.count - 1)) * 3 * (up ? r1.v.rs : r0.v.rs) +
+                   (8 * c8 < r8 ? term * r8 + 8 * c8 : 0));
+    }
+  };
+  auto store = [&](int mb) {
+    const u32x4_t none = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool in = qin && mb + qr + 16 * u < it.count;   // others are zero: no neighbour's infinity enters
+      float d[2][8];
+      gate_grads<ACT>(xG[u], xg[u], xu[u], d[0], d[1]);
+#pragma unroll
+      for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const u32x4_t t = take8(d[sd]);
+          *reinterpret_cast<u32x4_t*>(sQ[sd][k] + (qr + 16 * u) * GC_PITCH + qc) = in ? t : none;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < PQ; ++k) {
+      const int i = threadIdx.x + 256 * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, t = i / (64 * JT);
+      if (t < 6)
+        *reinterpret_cast<u32x4_t*>(sP[t >= 3] + (32 * (t >= 3 ? t - 3 : t) + row) * PP + 8 * c8) =
+            mb + row < it.count && 8 * c8 < (t >= 3 ? r81 : r80) ? xp[k] : none;
+    }
+  };
+  f32x4_t acc[JT][4];
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) acc[jt][ct] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  tokens(0);
+  load(0);
+  tokens(32);
+  for (int m = 0; m < it.count; m += 32) {
+    store(m);
+    lds_barrier();
+    load(m + 32);
+    tokens(m + 64);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      u32x4_t fq[4];
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) fq[ct] = tr_frag(sQ[side][k] + 64 * half + 16 * ct, GC_PITCH, li, lg);
+#pragma unroll
+      for (int t = 0; t < 3 - k; ++t)
+#pragma unroll
+        for (int jt = 0; jt < JT; ++jt) {
+          const u32x4_t a = tr_frag(sP[side] + 32 * t * PP + 16 * jt, PP, li, lg);
+#pragma unroll
+          for (int ct = 0; ct < 4; ++ct)
+            acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(fq[ct]), acc[jt][ct], 0, 0, 0);
+        }
+    }
+    lds_barrier();   // read by everyone; the next step's loads stay in flight
+  }
+  // lane: column li of each tile, rows j = 4 lg + e
+  const ColReq& rq = side ? r1 : r0;
+  if (!rq.out) return;
+  const lq_adapter ad = side ? ad1 : ad0;
+  const int r = min(ad.r, 16 * JT);
+  const bool vec = it.slot < 0 && r % 4 == 0 && (reinterpret_cast<uintptr_t>(rq.out) & 15) == 0;
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+      const int64_t c = c0 + 64 * half + 16 * ct + li;
+      const int j0 = 16 * jt + 4 * lg;
+      if (c >= N || j0 >= r) continue;
+      if (vec) {   // N * row and c * r are multiples of 4
+        *reinterpret_cast<f32x4_t*>(rq.out + N * ad.row + c * r + j0) = acc[jt][ct];
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + e;
+        if (j >= r) break;
+        if (it.slot >= 0) rq.part[((int64_t)it.slot * rq.v.rs + j) * N + c] = acc[jt][ct][e];
+        else rq.out[N * ad.row + c * r + j] = acc[jt][ct][e];
+      }
+    }
+}
+
+// Runs of positions per workgroup: enough workgroups for the chip, runs of at
+// least 256 so that the partial sums stay few.
+int gated_col_rows(int64_t M, int64_t N) {
+  const int64_t tiles = (N + GC_COLS - 1) / GC_COLS;
+  return (int)std::max<int64_t>(256, std::min<int64_t>(M * tiles / 512 / 32 * 32, 4096));
+}
+
+}  // namespace
+
+// Shares of the columns: two workgroups per CU, at least 4 steps each.
+int gated_down_shares(int64_t M, int64_t N) {
+  const int64_t tiles = (M + GD_M - 1) / GD_M, steps = (N + GD_K - 1) / GD_K;
+  int s = 1;
+  while (s < 16 && tiles * s * 2 <= 512 && steps / (s * 2) >= 4) s *= 2;
+  return s;
+}
+size_t gated_down_ws_floats(int64_t M, int64_t N, int32_t rs) { return (size_t)gated_down_shares(M, N) * M * rs; }
+
+#define LQ_ACTS(CALL, JT)                      \
+  do {                                         \
+    if (act == LQ_SILU) CALL(JT, LQ_SILU);     \
+    else if (act == LQ_GELU) CALL(JT, LQ_GELU); \
+    else CALL(JT, LQ_GELU_TANH);               \
+  } while (0)
+
+hipError_t launch_gated_down(const GatedGrad& gr, int64_t M, const AdapterView (&v)[2], const uint16_t* const (&bt)[2],
+                             float* const (&part)[2], uint16_t* D, const Route& rt, hipStream_t s) {
+  LQ_DASSERT(gr.N % 8 == 0 && M > 0);
+  const GatedDown p{gr, {v[0], v[1]}, {bt[0], bt[1]}, {part[0], part[1]}, D, (gr.N + 63) / 64 * 64};
+  const dim3 grid((unsigned)((M + GD_M - 1) / GD_M + std::min<int64_t>(v[0].n + 1, M)), (unsigned)gated_down_shares(M, gr.N));
+  const int act = gr.act;
+  const int32_t r = std::max(v[0].r_max, v[1].r_max);
+#define LQ_GD(JT, ACT) hipLaunchKernelGGL((k_gated_down<JT, ACT>), grid, dim3(256), 0, s, p, M, rt)
+  if (r <= 16) LQ_ACTS(LQ_GD, 1);
+  else if (r <= 32) LQ_ACTS(LQ_GD, 2);
+  else if (r <= 64) LQ_ACTS(LQ_GD, 4);
+  else LQ_ACTS(LQ_GD, 8);
+#undef LQ_GD
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t M, const Route& rt, hipStream_t s) {
+  LQ_DASSERT(gr.N % 8 == 0 && M > 0 && req[0].v.n > 0);
+  const int rows = gated_col_rows(M, gr.N), act = gr.act;
+  const dim3 grid((unsigned)((gr.N + GC_COLS - 1) / GC_COLS), (unsigned)((M + rows - 1) / rows + std::min<int64_t>(req[0].v.n, M)));
+  const int32_t r = std::max(req[0].v.r_max, req[1].v.r_max);
+#define LQ_GC(JT, ACT) hipLaunchKernelGGL((k_gated_col<JT, ACT>), grid, dim3(256), 0, s, gr, req[0], req[1], rows, rt)
+  if (r <= 16) LQ_ACTS(LQ_GC, 1);
+  else if (r <= 32) LQ_ACTS(LQ_GC, 2);
+  else if (r <= 64) LQ_ACTS(LQ_GC, 4);
+  else LQ_ACTS(LQ_GC, 8);
+#undef LQ_GC
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  ColReq out[2];
+  int n = 0;
+  for (int i = 0; i < 2; ++i)
+    if (req[i].out) out[n++] = req[i];
+  return n ? launch_adapter_col_reduce(out, n, rows, rt, s) : hipSuccess;
+}
+#undef LQ_ACTS
+
+}  // namespace lq
