@@ -1,5 +1,6 @@
 // Many adapters at decode sizes (up to 64 tokens), NF4 weight:
 //   t[m] = A_a x[m],  h[m] = W' x[m] + s_a B_a t[m],  a = ids[m],
+// or of a gated pair act(g) u with g and u two such projections of one x,
 // without sorting the tokens: a wave holds one id per lane, so the tokens of
 // an adapter are one ballot. Bound by reading the packed weight once and, per
 // code, by the lookup, product and rounding that make its bfloat16 weight.
@@ -7,6 +8,7 @@
 // QLoRA (Heng's Blog), introduction: h = dequant(W0_NF4) x + (alpha/r) B A x.
 #include <algorithm>
 
+#include "lq_act.h"
 #include "lq_adapters.h"
 #include "lq_device.h"
 
@@ -68,11 +70,11 @@ struct DcRecord {
   uint64_t B, same;    // B_a, its tokens
   float scale;
   int32_t r;
-  uint32_t runs;       // byte q, run q of the step: rank / 8, term << 4, 64 where it is one of the adapter's
+  uint32_t runs;       // byte q, run q of the step: rank / 8, term << 4, 64 where it is one of the adapter's, 128 of side 1
   int32_t total;       // steps in all (every record)
 };
 constexpr int DC_PAD = 64;                        // no token's steps past the last: the projection asks for them too
-constexpr int DC_RECORDS = 64 * 12 + DC_PAD;
+constexpr int DC_RECORDS = 64 * 12 + DC_PAD;      // of a side
 
 // ===========================================================================
 // t = A_a x: one workgroup per adapter in use (workgroup b takes the b-th in
@@ -89,43 +91,81 @@ constexpr int DC_RECORDS = 64 * 12 + DC_PAD;
 // of X, zero past K.
 __device__ __forceinline__ int xp_units(int64_t K, int TT) { return (int)((K + 127) / 128) * TT * 256; }
 
-template <int JT, int W>
-__global__ __launch_bounds__(64 * W) void k_decode_down(const uint16_t* __restrict__ X, int M, int64_t K,
-                                                        AdapterView v, const int32_t* __restrict__ ids,
-                                                        float* __restrict__ t, u32x4_t* __restrict__ xp, int TT,
-                                                        int wgs, DcRecord* __restrict__ records, int terms) {
+//
+// PAIR: the adapters of two sets, side 1's workgroups after side 0's, and its
+// steps after side 0's. A pair may have no sets (n = 0): the steps past the last
+// then point into the codes of a weight, whose rows are 32 bytes or more.
+struct DecodeDown {
+  const uint16_t* X;
+  int M;
+  int64_t K;
+  AdapterView v[2];
+  const int32_t* ids;
+  float* t[2];         // [parts][M][rs]
+  u32x4_t* xp;
+  int TT, wgs;         // token tiles; workgroups of a side's adapters
+  DcRecord* records;
+  int terms;
+  const void* anywhere;
+};
+
+template <int JT, int W, bool PAIR>
+__global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown p) {
   __shared__ f32x4_t part[W][JT][64];
-  if ((int)blockIdx.x == wgs) {   // the steps, by the lanes that lead an adapter
+  const uint16_t* __restrict__ X = p.X;
+  const int32_t* __restrict__ ids = p.ids;
+  const int M = p.M, TT = p.TT, wgs = p.wgs, all_wgs = PAIR ? 2 * wgs : wgs;
+  const int64_t K = p.K;
+  if ((int)blockIdx.x == all_wgs) {   // the steps, by the lanes that lead an adapter
     if (blockIdx.y || threadIdx.x >= 64) return;
-    const int key = lane_key(ids, M, v.n);
-    const DcSteps st = dc_steps(v.tab[max(key, 0)], key, terms);
-    const int runs = (st.ad.r + 7) >> 3;
-    for (int k = 0, term = 0, run = 0; k < st.count; ++k) {
-      uint32_t packed = 0;
-      for (int q = 0; q < 4; ++q) {
-        if (term < terms) packed |= (uint32_t)(run | term << 4 | 64) << (8 * q);
-        if (++run == runs) run = 0, ++term;
+    const int n = p.v[0].n, key = PAIR && !n ? -1 : lane_key(ids, M, n);
+    int total = 0;
+    lq_adapter any{};
+    any.B = reinterpret_cast<const uint16_t*>(p.anywhere);
+    any.r = 8;
+    DcSteps st[PAIR ? 2 : 1];
+    if (!PAIR || n) {
+      any = p.v[0].tab[0];
+#pragma unroll
+      for (int sd = 0; sd < (PAIR ? 2 : 1); ++sd) {
+        st[sd] = dc_steps(p.v[sd].tab[max(key, 0)], key, p.terms);
+        st[sd].first += total;
+        total += st[sd].total;
       }
-      records[st.first + k] = DcRecord{(uint64_t)reinterpret_cast<uintptr_t>(st.ad.B), st.same, st.ad.scale, st.ad.r, packed,
-                                       st.total};
+#pragma unroll
+      for (int sd = 0; sd < (PAIR ? 2 : 1); ++sd) {
+        const DcSteps& at = st[sd];
+        const int runs = (at.ad.r + 7) >> 3;
+        for (int k = 0, term = 0, run = 0; k < at.count; ++k) {
+          uint32_t packed = sd ? 0x80808080u : 0u;
+          for (int q = 0; q < 4; ++q) {
+            if (term < p.terms) packed |= (uint32_t)(run | term << 4 | 64) << (8 * q);
+            if (++run == runs) run = 0, ++term;
+          }
+          p.records[at.first + k] = DcRecord{(uint64_t)reinterpret_cast<uintptr_t>(at.ad.B), at.same, at.ad.scale, at.ad.r, packed,
+                                             total};
+        }
+      }
     }
-    const lq_adapter any = v.tab[0];
     if (threadIdx.x < DC_PAD)
-      records[st.total + threadIdx.x] = DcRecord{(uint64_t)reinterpret_cast<uintptr_t>(any.B), 0, 0.0f, any.r, 0, st.total};
+      p.records[total + threadIdx.x] = DcRecord{(uint64_t)reinterpret_cast<uintptr_t>(any.B), 0, 0.0f, any.r, 0, total};
     return;
   }
-  if ((int)blockIdx.x > wgs) {
-    const int workers = ((int)gridDim.x - wgs - 1) * (int)gridDim.y * 64 * W;
-    int i = (((int)blockIdx.x - wgs - 1) * (int)gridDim.y + (int)blockIdx.y) * 64 * W + (int)threadIdx.x;
+  if ((int)blockIdx.x > all_wgs) {
+    const int workers = ((int)gridDim.x - all_wgs - 1) * (int)gridDim.y * 64 * W;
+    int i = (((int)blockIdx.x - all_wgs - 1) * (int)gridDim.y + (int)blockIdx.y) * 64 * W + (int)threadIdx.x;
     for (; i < xp_units(K, TT); i += workers) {
       const int ln = i & 63, u = (i >> 6) & 3, tt = (i >> 8) % TT, s = (i >> 8) / TT;
       const int64_t k = 128 * (int64_t)s + 32 * (ln >> 4) + 8 * u;
       u32x4_t x = {0u, 0u, 0u, 0u};
       if (k < K) x = ld16(X + (int64_t)min(16 * tt + (ln & 15), M - 1) * K + k);
-      xp[i] = x;
+      p.xp[i] = x;
     }
     return;
   }
+  const int side = PAIR && (int)blockIdx.x >= wgs ? 1 : 0, which = (int)blockIdx.x - side * wgs;
+  const AdapterView v = side ? p.v[1] : p.v[0];
+  float* t = side ? p.t[1] : p.t[0];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
   const int key = lane_key(ids, M, v.n);
@@ -134,7 +174,7 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(const uint16_t* __restri
   for (int b = 0; left; ++b) {
     const int k = __shfl(key, __ffsll((unsigned long long)left) - 1);
     const uint64_t same = __ballot(key == k);
-    if (b == (int)blockIdx.x) {
+    if (b == which) {
       a = uniform(k);
       mine = same;
       break;
@@ -227,18 +267,24 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(const uint16_t* __restri
 // 16 tokens, N = K = 4096: 7.9 us after 5.6; one token: 7.5 after 4.4 (forming
 // t in the projection instead took 14.0 in all).
 // ===========================================================================
+//
+// GATED: the first half of the row groups are the gate's, the second half the
+// same rows of up, so that the join has g and u of an output side by side; the
+// workgroup is RG / 2 groups of 16 outputs.
 struct DecodeParams {
   const u32x4_t* xp;   // X in fragment order
   const DcRecord* records;
   int M;
   const int32_t* ids;
-  AdapterView v;
-  const float* t;      // [parts][M, rs]
+  AdapterView v[2];
+  const float* t[2];   // [parts][M, rs]
   int parts;
-  float* t_out;        // [M, r_max], or null
+  float* t_out[2];     // [M, r_max], or null
   void* out;
-  QWeight w;
+  QWeight w[2];
   Nf4Levels lv;
+  int act;
+  uint16_t *g_out, *u_out;
 };
 
 constexpr int DC_PAIRS = 256 * 16;   // f32x2_t, 32 KB
@@ -260,7 +306,7 @@ __host__ __device__ constexpr int dc_floats(int nb) {
   const int c = (16 * RG * (nb + 1) + 3) / 4 * 4, red = W * RG * 272;
   return c > red ? c : red;
 }
-size_t dc_lds_bytes(int rg, int tt, int w, int nb, int rs, int terms) {
+size_t dc_lds_bytes(int rg, int tt, int w, int nb, int rs, int terms) {   // rs: of both sides of a pair
   const int c = (16 * rg * (nb + 1) + 3) / 4 * 4, red = w * rg * 272;
   return DC_PAIRS * sizeof(f32x2_t) +
          4 * (size_t)(c > red ? c : red) + 2 * (size_t)(16 * tt * rs * terms);
@@ -274,26 +320,27 @@ __device__ __forceinline__ DcRecord of_lane(const DcRecord& x, int l) {
 }
 
 // A step as every lane needs it, with the weight-side operand loaded.
-template <int RG>
+template <int NG>
 struct DcStep {
-  u32x4_t w[RG];
+  u32x4_t w[NG];
   uint64_t same;
   float scale;
   int term, j0;
-  bool live;
+  bool live, side;
 };
-template <int RG>
-__device__ __forceinline__ void dc_step(const DcRecord& rec, const int64_t (&row)[RG], DcStep<RG>& o) {
+template <int NG, int RG>
+__device__ __forceinline__ void dc_step(const DcRecord& rec, const int64_t (&row)[RG], DcStep<NG>& o) {
   const uint16_t* B = reinterpret_cast<const uint16_t*>(rec.B);
   const int r = rec.r;
   const uint32_t run = rec.runs >> (threadIdx.x >> 1 & 24);   // the lane's: byte lane / 16
   o.scale = rec.scale;
   o.same = rec.same;
   o.live = run & 64;
+  o.side = rec.runs & 128;
   o.term = (run >> 4) & 3;
   o.j0 = 8 * (run & 15);
 #pragma unroll
-  for (int g = 0; g < RG; ++g) {
+  for (int g = 0; g < NG; ++g) {   // (a pair's two halves are the same rows)
     const uint16_t* b = B + row[g] * r;
     if (r % 8 == 0) {
       o.w[g] = ld16(b + o.j0);
@@ -309,8 +356,8 @@ __device__ __forceinline__ void dc_step(const DcRecord& rec, const int64_t (&row
   }
 }
 // Adds step o: each product goes to its own tokens' columns alone.
-template <int RG, int TT, int TERMS>
-__device__ __forceinline__ void dc_apply(const DcStep<RG>& o, const uint16_t* sT, int rs, int M, f32x4_t (&acc)[RG][TT]) {
+template <int NG, int RG, int TT, int TERMS>
+__device__ __forceinline__ void dc_apply(const DcStep<NG>& o, const uint16_t* sT, int rs, int M, f32x4_t (&acc)[RG][TT]) {
   const int lane = threadIdx.x & 63, li = lane & 15;
   const u32x4_t none = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -321,19 +368,47 @@ __device__ __forceinline__ void dc_apply(const DcStep<RG>& o, const uint16_t* sT
     u32x4_t tv = *reinterpret_cast<const u32x4_t*>(sT + (min(m, M - 1) * TERMS + o.term) * rs + o.j0);
     if (!o.live) tv = none;
 #pragma unroll
-    for (int g = 0; g < RG; ++g) {
+    for (int g = 0; g < NG; ++g) {
       const f32x4_t d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(o.w[g]), as_bf16x8(tv), zero4(), 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {   // selected last: a scale that is not finite makes NaN of 0, too
-        const float with = __builtin_fmaf(o.scale, d[e], acc[g][tt][e]);
-        acc[g][tt][e] = mine ? with : acc[g][tt][e];
-      }
+      for (int h = 0; h < RG / NG; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {   // selected last: a scale that is not finite makes NaN of 0, too
+          f32x4_t& sum = acc[g + NG * h][tt];
+          const float with = __builtin_fmaf(o.scale, d[e], sum[e]);
+          sum[e] = mine && (RG == NG || o.side == (h == 1)) ? with : sum[e];
+        }
     }
   }
 }
 
-template <int RG, int TT, int W, bool DQ, bool OUT_F32>
+// Outputs n .. n + 3 of a token, at element o.
+template <bool OUT_F32>
+__device__ __forceinline__ void dc_store(void* out, int64_t o, int64_t n, int64_t N, const f32x4_t& h) {
+  if (N % 4 == 0) {
+    if (OUT_F32) {
+      float* f = reinterpret_cast<float*>(out) + o;   // 4-byte aligned
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = h[e];
+    } else {
+      uint2 v;
+      v.x = pack_bf16x2(h[0], h[1]);
+      v.y = pack_bf16x2(h[2], h[3]);
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + o) = v;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (n + e >= N) break;
+      if (OUT_F32) reinterpret_cast<float*>(out)[o + e] = h[e];
+      else reinterpret_cast<uint16_t*>(out)[o + e] = (uint16_t)(pack_bf16x2(h[e], 0.f) & 0xFFFFu);
+    }
+  }
+}
+
+template <int RG, int TT, int W, bool DQ, bool OUT_F32, bool GATED>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) void k_decode_nf4(DecodeParams p) {
+  constexpr int NG = GATED ? RG / 2 : RG;   // groups of 16 outputs
   extern __shared__ __attribute__((aligned(16))) unsigned char dc_lds[];
   constexpr int TERMS = OUT_F32 ? 3 : 2;
   constexpr bool XA = TT == 1;   // X is loaded a stage ahead, with the codes
@@ -341,14 +416,15 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
   float* sC = reinterpret_cast<float*>(dc_lds + DC_PAIRS * sizeof(f32x2_t));
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
-  const int64_t N = p.w.N, K = p.w.K;
-  const int64_t n0 = (int64_t)blockIdx.x * 16 * RG;
+  const int64_t N = p.w[0].N, K = p.w[0].K;
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * NG;
+  const int rs0 = p.v[0].rs, rs1 = GATED ? p.v[1].rs : 0;
   const int nb = (int)(K / 64), pitch = nb + 1, ns = (nb + 1) / 2;
-  uint16_t* sT = reinterpret_cast<uint16_t*>(sC + dc_floats<RG, W>(nb));   // t's bf16 terms [M][TERMS][rs]
+  uint16_t* sT = reinterpret_cast<uint16_t*>(sC + dc_floats<RG, W>(nb));   // t's bf16 terms [M][TERMS][rs], side 1's after side 0's
 
   const uint8_t* crow[RG];
 #pragma unroll
-  for (int g = 0; g < RG; ++g) crow[g] = p.w.codes + min(n0 + 16 * g + li, N - 1) * (K / 2) + 16 * (lg & 1);
+  for (int g = 0; g < RG; ++g) crow[g] = (g < NG ? p.w[0] : p.w[1]).codes + min(n0 + 16 * (g % NG) + li, N - 1) * (K / 2) + 16 * (lg & 1);
   // The stages in an order rotated by workgroup: rows lie a power of two apart in
   // the common sizes, so workgroups in step would all read from the same few
   // channels of the L2.
@@ -382,19 +458,20 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
   static_assert(W * 2 * DEEP <= DC_PAD, "the steps asked for end within the padding");
   int64_t row[RG];
 #pragma unroll
-  for (int g = 0; g < RG; ++g) row[g] = min(n0 + 16 * g + li, N - 1);
-  DcStep<RG> steps[DEEP];
+  for (int g = 0; g < RG; ++g) row[g] = min(n0 + 16 * (g % NG) + li, N - 1);
+  DcStep<NG> steps[DEEP];
   DcStage<RG> s0, s1;
   load(wave, s0);
   if constexpr (XA) load(wave + W, s1);
+  constexpr int kRecords = GATED ? 2 * DC_RECORDS : DC_RECORDS;
   // Lane l keeps the record of the wave's step 64 c + l.
   DcRecord rec;
   auto load_records = [&](int i) {
-    const u32x4_t* at = reinterpret_cast<const u32x4_t*>(p.records + min(wave + W * (i + lane), DC_RECORDS - 1));
+    const u32x4_t* at = reinterpret_cast<const u32x4_t*>(p.records + min(wave + W * (i + lane), kRecords - 1));
     const u32x4_t a = at[0], b = at[1];
     rec = DcRecord{a[0] | (uint64_t)a[1] << 32, a[2] | (uint64_t)a[3] << 32, __uint_as_float(b[0]), (int)b[1], b[2], (int)b[3]};
   };
-  auto ask = [&](int i, DcStep<RG>& o) { dc_step<RG>(of_lane(rec, i & 63), row, o); };
+  auto ask = [&](int i, DcStep<NG>& o) { dc_step<NG>(of_lane(rec, i & 63), row, o); };
   load_records(0);
 #pragma unroll
   for (int d = 0; d < DEEP; ++d) ask(d, steps[d]);
@@ -407,23 +484,25 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
     const int e = 4 * (wave + W * k);   // e .. e + 3: one first level
     sPair[16 * e + lane] = f32x2_t{__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(level), e >> 4)), second};
   }
-  const float mean = DQ ? *p.w.qc.dq_mean : 0.0f;
   // the rows' constants, four a thread: thread t row t % (16 RG)
   if (nb % 4 == 0) {
     const int rr = threadIdx.x % (16 * RG);
-    const int64_t b0 = min(n0 + rr, N - 1) * nb;
+    const bool up = rr >= 16 * NG;
+    const QConst qc = up ? p.w[1].qc : p.w[0].qc;
+    const float mean = DQ ? *qc.dq_mean : 0.0f;
+    const int64_t b0 = min(n0 + (up ? rr - 16 * NG : rr), N - 1) * nb;
 #pragma unroll 4
     for (int c = 4 * (threadIdx.x / (16 * RG)); c < nb; c += 4 * (64 * W / (16 * RG))) {
       const int64_t blk = b0 + c;   // a multiple of 4: one second-level scale
       f32x4_t v;
       if constexpr (DQ) {
-        const uint32_t q8 = *reinterpret_cast<const uint32_t*>(p.w.qc.absmax_q + blk);
-        const float s2 = p.w.qc.dq_scale[blk >> 8];
+        const uint32_t q8 = *reinterpret_cast<const uint32_t*>(qc.absmax_q + blk);
+        const float s2 = qc.dq_scale[blk >> 8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(e4m3_decode((q8 >> (8 * e)) & 0xFFu), s2, mean);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = p.w.qc.absmax[blk + e];
+        for (int e = 0; e < 4; ++e) v[e] = qc.absmax[blk + e];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) sC[rr * pitch + c + e] = v[e];
@@ -431,39 +510,45 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
   } else {
     for (int i = threadIdx.x; i < 16 * RG * nb; i += 64 * W) {
       const int rr = i / nb, bl = i - rr * nb;
-      const int64_t blk = min(n0 + rr, N - 1) * nb + bl;
-      sC[rr * pitch + bl] = DQ ? __builtin_fmaf(e4m3_decode(p.w.qc.absmax_q[blk]), p.w.qc.dq_scale[blk >> 8], mean)
-                               : p.w.qc.absmax[blk];
+      const bool up = rr >= 16 * NG;
+      const QConst qc = up ? p.w[1].qc : p.w[0].qc;
+      const int64_t blk = min(n0 + (up ? rr - 16 * NG : rr), N - 1) * nb + bl;
+      sC[rr * pitch + bl] =
+          DQ ? __builtin_fmaf(e4m3_decode(qc.absmax_q[blk]), qc.dq_scale[blk >> 8], *qc.dq_mean) : qc.absmax[blk];
     }
   }
-  {
-    // t: its parts added in order, and split into bf16 terms: two keep 16 bits
-    // of it, 8 more than a bf16 H, three all 24 (rows of tokens without an
-    // adapter hold anything: no step takes them). Token m's t is saved by workgroup m % grid.
-    const int quads = p.v.rs / 4, nq = p.M * quads, nt = p.M * p.v.rs;
+  // t: its parts added in order, and split into bf16 terms: two keep 16 bits
+  // of it, 8 more than a bf16 H, three all 24 (rows of tokens without an
+  // adapter hold anything: no step takes them). Token m's t is saved by workgroup m % grid.
+#pragma unroll
+  for (int sd = 0; sd < (GATED ? 2 : 1); ++sd) {
+    const AdapterView& v = p.v[sd];
+    const float* t = p.t[sd];
+    uint16_t* to = sT + sd * p.M * TERMS * rs0;
+    const int quads = v.rs / 4, nq = p.M * quads, nt = p.M * v.rs;
 #pragma unroll 2
     for (int i = threadIdx.x; i < nq; i += 64 * W) {
       f32x4_t part[DC_PARTS];
 #pragma unroll
       for (int k = 0; k < DC_PARTS; ++k)
-        part[k] = *reinterpret_cast<const f32x4_t*>(p.t + (int64_t)min(k, p.parts - 1) * nt + 4 * i);
+        part[k] = *reinterpret_cast<const f32x4_t*>(t + (int64_t)min(k, p.parts - 1) * nt + 4 * i);
       f32x4_t sum = part[0];
 #pragma unroll
       for (int k = 1; k < DC_PARTS; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] += k < p.parts ? part[k][e] : 0.0f;
       const int m = (uint32_t)i / (uint32_t)quads, j = 4 * (i - m * quads);
-      if (p.t_out && m % gridDim.x == blockIdx.x) {
-        const bool has = (uint32_t)p.ids[m] < (uint32_t)p.v.n;
+      if (p.t_out[sd] && m % gridDim.x == blockIdx.x) {
+        const bool has = (uint32_t)p.ids[m] < (uint32_t)v.n;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (j + e < p.v.r_max) p.t_out[m * p.v.r_max + j + e] = has ? sum[e] : 0.0f;
+          if (j + e < v.r_max) p.t_out[sd][m * v.r_max + j + e] = has ? sum[e] : 0.0f;
       }
-      float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+      float x[4] = {sum[0], sum[1], sum[2], sum[3]};
 #pragma unroll
       for (int q = 0; q < TERMS; ++q) {
-        const uint2 bits = {take_bf16_terms(v[0], v[1]), take_bf16_terms(v[2], v[3])};
-        *reinterpret_cast<uint2*>(sT + (m * TERMS + q) * p.v.rs + j) = bits;
+        const uint2 bits = {take_bf16_terms(x[0], x[1]), take_bf16_terms(x[2], x[3])};
+        *reinterpret_cast<uint2*>(to + (m * TERMS + q) * v.rs + j) = bits;
       }
     }
   }
@@ -478,7 +563,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
     if (((i + DEEP) & 63) == 0) load_records(i + DEEP);
 #pragma unroll
     for (int d = 0; d < DEEP; ++d) {
-      dc_apply<RG, TT, TERMS>(steps[d], sT, p.v.rs, p.M, acc);
+      const bool up = GATED && steps[d].side;
+      dc_apply<NG, RG, TT, TERMS>(steps[d], sT + (up ? p.M * TERMS * rs0 : 0), up ? rs1 : rs0, p.M, acc);
       ask(i + DEEP + d, steps[d]);
     }
   }
@@ -548,46 +634,42 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
 #pragma unroll
     for (int g = 0; g < RG; ++g) sR[(wave * RG + g) * 68 + lane + lg] = acc[g][tt];
     __syncthreads();
-    for (int i = threadIdx.x; i < RG * 64; i += 64 * W) {
-      const int quad = i & 3, g = (i >> 2) % RG, m = i / (4 * RG);
-      f32x4_t h = sR[g * 68 + m + 17 * quad];
+    for (int i = threadIdx.x; i < NG * 64; i += 64 * W) {
+      const int quad = i & 3, g = (i >> 2) % NG, m = i / (4 * NG);
+      auto total = [&](int group) {
+        f32x4_t h = sR[group * 68 + m + 17 * quad];
 #pragma unroll
-      for (int w = 1; w < W; ++w) h += sR[(w * RG + g) * 68 + m + 17 * quad];
+        for (int w = 1; w < W; ++w) h += sR[(w * RG + group) * 68 + m + 17 * quad];
+        return h;
+      };
+      f32x4_t h = total(g);
       const int64_t n = n0 + 16 * g + 4 * quad;
       if (16 * tt + m >= p.M || n >= N) continue;
       const int64_t o = (int64_t)(16 * tt + m) * N + n;
-      if (N % 4 == 0) {
-        if (OUT_F32) {
-          float* f = reinterpret_cast<float*>(p.out) + o;   // 4-byte aligned
+      if constexpr (GATED) {
+        const f32x4_t u = total(g + NG);
+        if (p.g_out) dc_store<false>(p.g_out, o, n, N, h);
+        if (p.u_out) dc_store<false>(p.u_out, o, n, N, u);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = h[e];
-        } else {
-          uint2 v;
-          v.x = pack_bf16x2(h[0], h[1]);
-          v.y = pack_bf16x2(h[2], h[3]);
-          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + o) = v;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (n + e >= N) break;
-          if (OUT_F32) reinterpret_cast<float*>(p.out)[o + e] = h[e];
-          else reinterpret_cast<uint16_t*>(p.out)[o + e] = (uint16_t)(pack_bf16x2(h[e], 0.f) & 0xFFFFu);
-        }
+        for (int e = 0; e < 4; ++e)
+          h[e] = u[e] * (p.act == LQ_SILU ? act_value<LQ_SILU>(h[e]) : p.act == LQ_GELU ? act_value<LQ_GELU>(h[e])
+                                                                                      : act_value<LQ_GELU_TANH>(h[e]));
       }
+      dc_store<OUT_F32>(p.out, o, n, N, h);
     }
   }
 }
 
-template <int RG, int TT, int W>
+template <int RG, int TT, int W, bool GATED>
 hipError_t launch_rg(const DecodeParams& p, bool f32, hipStream_t s) {
-  const dim3 grid((unsigned)((p.w.N + 16 * RG - 1) / (16 * RG))), block(64 * W);
-  const size_t lds = dc_lds_bytes(RG, TT, W, (int)(p.w.K / 64), p.v.rs, f32 ? 3 : 2);
-  const bool dq = p.w.qc.absmax == nullptr;
-  if (dq && f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, true>), grid, block, lds, s, p);
-  else if (dq) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, false>), grid, block, lds, s, p);
-  else if (f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, true>), grid, block, lds, s, p);
-  else hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, false>), grid, block, lds, s, p);
+  constexpr int NG = GATED ? RG / 2 : RG;
+  const dim3 grid((unsigned)((p.w[0].N + 16 * NG - 1) / (16 * NG))), block(64 * W);
+  const size_t lds = dc_lds_bytes(RG, TT, W, (int)(p.w[0].K / 64), p.v[0].rs + (GATED ? p.v[1].rs : 0), f32 ? 3 : 2);
+  const bool dq = p.w[0].qc.absmax == nullptr;
+  if (dq && f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, true, GATED>), grid, block, lds, s, p);
+  else if (dq) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, false, GATED>), grid, block, lds, s, p);
+  else if (f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, true, GATED>), grid, block, lds, s, p);
+  else hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, false, GATED>), grid, block, lds, s, p);
   return hipGetLastError();
 }
 
@@ -596,12 +678,13 @@ constexpr size_t kLdsBytes = 160 * 1024;
 
 // Row groups per workgroup: the shortest queue of the longest CU, a workgroup
 // costing its row groups and about two more for its start and its X. Four need
-// the LDS of two workgroups (K up to some 10000).
-int decode_rg(int64_t N, int64_t K, int tt, int rs, int terms) {
-  const int64_t groups = (N + 15) / 16;
-  int best = 1;
+// the LDS of two workgroups (K up to some 10000). Of a pair at least two; 0:
+// none fits.
+int decode_rg(int64_t N, int64_t K, int tt, int rs, int terms, bool pair) {
+  const int64_t groups = (N + 15) / 16 * (pair ? 2 : 1);
+  int best = pair ? 0 : 1;
   int64_t cost = INT64_MAX;
-  for (int rg = 1; rg <= 4; rg *= 2) {
+  for (int rg = pair ? 2 : 1; rg <= 4; rg *= 2) {
     const size_t lds = rg == 4 ? 2 * dc_lds_bytes(rg, tt, 4, (int)(K / 64), rs, terms)
                                : dc_lds_bytes(rg, tt, 8, (int)(K / 64), rs, terms);
     if (lds > kLdsBytes) break;
@@ -614,6 +697,31 @@ int decode_rg(int64_t N, int64_t K, int tt, int rs, int terms) {
   return best;
 }
 
+// Token tiles of the projection; column parts of t: with few adapters the
+// columns are shared by several workgroups, at least eight 64-column blocks each.
+int token_tiles(int64_t M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
+int decode_parts(int64_t K, int64_t M, int32_t n, int sides) {
+  const int64_t wgs = std::min<int64_t>(M, n) * sides;
+  int parts = 1;
+  while (parts < DC_PARTS && wgs * parts * 2 <= kCus && K / 64 / (parts * 2) >= 8) parts *= 2;
+  return parts;
+}
+size_t t_bytes(int parts, int64_t M, const AdapterView& v) { return ((size_t)parts * M * v.rs * sizeof(float) + 255) / 256 * 256; }
+size_t xp_bytes(int64_t K, int64_t M) { return (size_t)((K + 127) / 128) * token_tiles(M) * 256 * 16; }
+
+template <bool PAIR>
+hipError_t launch_decode_down(const DecodeDown& d, int parts, hipStream_t s) {
+  const dim3 grid((unsigned)(d.wgs * (PAIR ? 2 : 1) + 1 + std::max(1, 16 * d.TT / parts)), (unsigned)parts);
+  const int jt = (std::max(d.v[0].r_max, PAIR ? d.v[1].r_max : 0) + 15) / 16;
+#define LQ_DD(JT, W) hipLaunchKernelGGL((k_decode_down<JT, W, PAIR>), grid, dim3(64 * W), 0, s, d)
+  if (jt <= 1) LQ_DD(1, 16);
+  else if (jt <= 2) LQ_DD(2, 16);
+  else if (jt <= 4) LQ_DD(4, 8);
+  else LQ_DD(8, 8);
+#undef LQ_DD
+  return hipGetLastError();
+}
+
 }  // namespace
 
 // NF4, at most 64 tokens, and one row group's constants within the LDS that the
@@ -621,53 +729,67 @@ int decode_rg(int64_t N, int64_t K, int tt, int rs, int terms) {
 bool adapter_decode_supported(const QWeight& w, int64_t M) {
   return w.format == LQ_FMT_NF4 && M <= 64 && w.K <= 49152;
 }
-// Token tiles of the projection, and the workspace: t's parts, the steps, and
-// X in fragment order.
-static int token_tiles(int64_t M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
-static int adapter_decode_parts(const QWeight& w, int64_t M, const AdapterView& v);
-static size_t t_bytes(const QWeight& w, int64_t M, const AdapterView& v) {
-  return ((size_t)adapter_decode_parts(w, M, v) * M * v.rs * sizeof(float) + 255) / 256 * 256;
-}
 size_t adapter_decode_ws_bytes(const QWeight& w, int64_t M, const AdapterView& v) {
-  return t_bytes(w, M, v) + DC_RECORDS * sizeof(DcRecord) + (size_t)((w.K + 127) / 128) * token_tiles(M) * 256 * 16;
-}
-
-// Column parts of t: with few adapters the columns are shared by several
-// workgroups, at least eight 64-column blocks each.
-static int adapter_decode_parts(const QWeight& w, int64_t M, const AdapterView& v) {
-  const int64_t wgs = std::min<int64_t>(M, v.n);
-  int parts = 1;
-  while (parts < DC_PARTS && wgs * parts * 2 <= kCus && w.K / 64 / (parts * 2) >= 8) parts *= 2;
-  return parts;
+  return t_bytes(decode_parts(w.K, M, v.n, 1), M, v) + DC_RECORDS * sizeof(DcRecord) + xp_bytes(w.K, M);
 }
 
 hipError_t launch_adapter_decode(const QWeight& w, const uint16_t* X, int64_t M, const int32_t* ids,
                                  const AdapterView& v, void* ws, float* t_save, void* H, bool f32, hipStream_t s) {
   if (!adapter_decode_supported(w, M)) return hipErrorInvalidValue;
-  const int parts = adapter_decode_parts(w, M, v), tt = token_tiles(M);
+  const int parts = decode_parts(w.K, M, v.n, 1), tt = token_tiles(M), terms = f32 ? 3 : 2;
   float* t_ws = reinterpret_cast<float*>(ws);
-  DcRecord* records = reinterpret_cast<DcRecord*>(reinterpret_cast<char*>(ws) + t_bytes(w, M, v));
+  DcRecord* records = reinterpret_cast<DcRecord*>(reinterpret_cast<char*>(ws) + t_bytes(parts, M, v));
   u32x4_t* xp = reinterpret_cast<u32x4_t*>(records + DC_RECORDS);
-  const int wgs = (int)std::min<int64_t>(M, v.n);
-  const dim3 grid((unsigned)(wgs + 1 + std::max(1, 16 * tt / parts)), (unsigned)parts);
-  const int jt = (v.r_max + 15) / 16;
-#define LQ_DD(JT, W)                                                                                                 \
-  hipLaunchKernelGGL((k_decode_down<JT, W>), grid, dim3(64 * W), 0, s, X, (int)M, w.K, v, ids, t_ws, xp, tt, wgs, records, \
-                     f32 ? 3 : 2)
-  if (jt <= 1) LQ_DD(1, 16);
-  else if (jt <= 2) LQ_DD(2, 16);
-  else if (jt <= 4) LQ_DD(4, 8);
-  else LQ_DD(8, 8);
-#undef LQ_DD
-  const hipError_t e = hipGetLastError();
+  const DecodeDown d{X, (int)M, w.K, {v, {}}, ids, {t_ws, nullptr}, xp, tt, (int)std::min<int64_t>(M, v.n), records, terms, nullptr};
+  const hipError_t e = launch_decode_down<false>(d, parts, s);
   if (e != hipSuccess) return e;
-  const DecodeParams p{xp, records, (int)M, ids, v, t_ws, parts, t_save, H, w, tables().lv};
-  const int rg = decode_rg(w.N, w.K, tt, v.rs, f32 ? 3 : 2);
-#define LQ_RG(TT)                                    \
-  do {                                               \
-    if (rg == 4) return launch_rg<4, TT, 4>(p, f32, s); \
-    if (rg == 2) return launch_rg<2, TT, 8>(p, f32, s); \
-    return launch_rg<1, TT, 8>(p, f32, s);           \
+  const DecodeParams p{xp, records, (int)M, ids, {v, {}}, {t_ws, nullptr}, parts, {t_save, nullptr}, H, {w, {}}, tables().lv,
+                       0, nullptr, nullptr};
+  const int rg = decode_rg(w.N, w.K, tt, v.rs, terms, false);
+#define LQ_RG(TT)                                           \
+  do {                                                      \
+    if (rg == 4) return launch_rg<4, TT, 4, false>(p, f32, s); \
+    if (rg == 2) return launch_rg<2, TT, 8, false>(p, f32, s); \
+    return launch_rg<1, TT, 8, false>(p, f32, s);           \
+  } while (0)
+  if (tt == 1) LQ_RG(1);
+  if (tt == 2) LQ_RG(2);
+  LQ_RG(4);
+#undef LQ_RG
+}
+
+// Both weights NF4 with constants of one kind, and two row groups' constants
+// and both sides' t within the LDS (float32: three terms of t).
+bool gated_decode_supported(const QWeight (&w)[2], int64_t M, const AdapterView (&v)[2]) {
+  return w[0].format == LQ_FMT_NF4 && w[1].format == LQ_FMT_NF4 && (w[0].qc.absmax == nullptr) == (w[1].qc.absmax == nullptr) &&
+         M <= 64 && w[0].K <= 49152 && decode_rg(w[0].N, w[0].K, token_tiles(M), v[0].rs + v[1].rs, 3, true) > 0;
+}
+size_t gated_decode_ws_bytes(const QWeight& w, int64_t M, const AdapterView (&v)[2]) {
+  const int parts = decode_parts(w.K, M, v[0].n, 2);
+  return t_bytes(parts, M, v[0]) + t_bytes(parts, M, v[1]) + 2 * DC_RECORDS * sizeof(DcRecord) + xp_bytes(w.K, M);
+}
+
+hipError_t launch_gated_decode(const QWeight (&w)[2], const uint16_t* X, int64_t M, const int32_t* ids,
+                               const AdapterView (&v)[2], void* ws, int act, float* t_gate, float* t_up, uint16_t* g,
+                               uint16_t* u, void* H, bool f32, hipStream_t s) {
+  if (!gated_decode_supported(w, M, v)) return hipErrorInvalidValue;
+  const int parts = decode_parts(w[0].K, M, v[0].n, 2), tt = token_tiles(M), terms = f32 ? 3 : 2;
+  char* at = reinterpret_cast<char*>(ws);
+  float* t0 = reinterpret_cast<float*>(at);
+  float* t1 = reinterpret_cast<float*>(at += t_bytes(parts, M, v[0]));
+  DcRecord* records = reinterpret_cast<DcRecord*>(at += t_bytes(parts, M, v[1]));
+  u32x4_t* xp = reinterpret_cast<u32x4_t*>(records + 2 * DC_RECORDS);
+  const DecodeDown d{X, (int)M, w[0].K, {v[0], v[1]}, ids, {t0, t1}, xp, tt, (int)std::min<int64_t>(M, v[0].n), records, terms,
+                     w[0].codes};
+  const hipError_t e = launch_decode_down<true>(d, parts, s);
+  if (e != hipSuccess) return e;
+  const DecodeParams p{xp, records, (int)M, ids, {v[0], v[1]}, {t0, t1}, parts, {t_gate, t_up}, H, {w[0], w[1]}, tables().lv,
+                       act, g, u};
+  const int rg = decode_rg(w[0].N, w[0].K, tt, v[0].rs + v[1].rs, terms, true);
+#define LQ_RG(TT)                                          \
+  do {                                                     \
+    if (rg == 4) return launch_rg<4, TT, 4, true>(p, f32, s); \
+    return launch_rg<2, TT, 8, true>(p, f32, s);           \
   } while (0)
   if (tt == 1) LQ_RG(1);
   if (tt == 2) LQ_RG(2);

@@ -153,6 +153,13 @@ hipError_t launch_gated_down(const GatedGrad& gr, int64_t M, const AdapterView (
 // side 0's dg, side 1's du; a null out: not wanted.
 hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t M, const Route& rt, hipStream_t s);
 
+// Decode sizes of a pair: the whole forward, in two launches.
+bool gated_decode_supported(const QWeight (&w)[2], int64_t M, const AdapterView (&v)[2]);
+size_t gated_decode_ws_bytes(const QWeight& w, int64_t M, const AdapterView (&v)[2]);
+hipError_t launch_gated_decode(const QWeight (&w)[2], const uint16_t* X, int64_t M, const int32_t* ids,
+                               const AdapterView (&v)[2], void* ws, int act, float* t_gate, float* t_up, uint16_t* g,
+                               uint16_t* u, void* H, bool f32, hipStream_t s);
+
 // ---- gradient lists ----------------------------------------------------------
 struct GradPiece {
   void* data;

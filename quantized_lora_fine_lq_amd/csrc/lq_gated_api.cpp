@@ -90,12 +90,19 @@ struct Backward {
   }
 };
 
+// Whether the forward runs as at decode sizes.
+bool decodes(const Pair& p, int64_t M, bool drops) { return !drops && gated_decode_supported(p.q, M, p.v); }
+
 template <class W>
 size_t ws_bytes_of(const Pair& p, int64_t M) {
   Carver cv(nullptr, 0);
   W w(cv, p, M);
   (void)w;
   return cv.used;
+}
+
+size_t forward_ws(const Pair& p, int64_t M, bool drops) {
+  return decodes(p, M, drops) ? align_up(gated_decode_ws_bytes(p.q[0], M, p.v)) : ws_bytes_of<Forward>(p, M);
 }
 
 }  // namespace
@@ -110,7 +117,7 @@ int lq_check_gated(const lq_gated* p) {
 size_t lq_gated_forward_workspace(const lq_gated* p, int64_t M, int32_t drops) {
   Pair o;
   if (check_pair(p, &o) != LQ_OK || !valid_M(M) || (drops && !drop_fits(M, o.K))) return 0;
-  return ws_bytes_of<Forward>(o, M);
+  return forward_ws(o, M, drops);
 }
 
 int lq_gated_forward(const lq_gated* p, const uint16_t* X, int64_t M, const int32_t* ids, const int32_t* route,
@@ -128,10 +135,13 @@ int lq_gated_forward(const lq_gated* p, const uint16_t* X, int64_t M, const int3
   if (!valid_M(M)) return LQ_ERR_SHAPE;
   if ((st = check_drops(o, M, drop_gate, drop_up, drop, factor)) != LQ_OK) return st;
   if (h_dtype != LQ_BF16 && h_dtype != LQ_F32) return LQ_ERR_UNSUPPORTED;
-  if (!workspace || ws_bytes < ws_bytes_of<Forward>(o, M)) return LQ_ERR_WORKSPACE;
+  const bool drops = drop_gate || drop_up;
+  if (!workspace || ws_bytes < forward_ws(o, M, drops)) return LQ_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   for (int i = 0; i < 2; ++i)
     if ((st = debug_check_weight(o.q[i], s)) != LQ_OK) return st;
+  if (decodes(o, M, drops))
+    return launch_status(launch_gated_decode(o.q, X, M, ids, o.v, workspace, o.act, t_gate, t_up, g, u, H, h_dtype == LQ_F32, s));
   Carver cv(workspace, ws_bytes);
   const Forward w(cv, o, M);
   if (!cv.ok()) return LQ_ERR_WORKSPACE;

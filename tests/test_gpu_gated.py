@@ -190,6 +190,10 @@ CASES = [
     (512, 1024, 64, [8, 16, 32], "mixed", "nf4_dq", "silu", 0.0),
     (104, 192, 64, [1, 128], "mixed", "nf4_f32+nf4_dq", "silu", 0.0),
     (64, 128, 7, [], None, "nf4_dq", "silu", 0.0),
+    (72, 128, 20, [16, 4, 1], "mixed", "nf4_dq", "silu", 0.3),
+    (4168, 192, 64, [128] * 64, "mixed", "nf4_dq", "silu", 0.0),
+    (8208, 64, 30, [7, 16], "mixed", "nf4_f32", "gelu", 0.0),
+    (16, 16448, 5, [8, 40], "mixed", "nf4_dq", "gelu_tanh", 0.0),
     (72, 192, 65, [5, 24], "runs", "nf4_dq", "silu", 0.1),
     (72, 192, 65, [5, 24], "runs", "codebook", "gelu", 0.5),
     (512, 256, 300, [16, 8, 64, 1, 7], "runs", "nf4_dq", "silu", 0.0),
