@@ -301,13 +301,17 @@ struct DcStage {
 
 // floats of LDS after the pair table: constants, then the partial sums of one
 // token tile
+// The constants' row stride, odd or, from 16 on, even: column b of row r then lies
+// at b + r % 16 (mod nb), so that 16 rows' constants of one block hit distinct
+// banks without the odd word (64 rows of K = 8192 then leave two workgroups room).
+__host__ __device__ constexpr int dc_pitch(int nb) { return nb >= 16 ? nb : nb | 1; }
 template <int RG, int W>
 __host__ __device__ constexpr int dc_floats(int nb) {
-  const int c = (16 * RG * (nb + 1) + 3) / 4 * 4, red = W * RG * 272;
+  const int c = (16 * RG * dc_pitch(nb) + 3) / 4 * 4, red = W * RG * 272;
   return c > red ? c : red;
 }
 size_t dc_lds_bytes(int rg, int tt, int w, int nb, int rs, int terms) {   // rs: of both sides of a pair
-  const int c = (16 * rg * (nb + 1) + 3) / 4 * 4, red = w * rg * 272;
+  const int c = (16 * rg * dc_pitch(nb) + 3) / 4 * 4, red = w * rg * 272;
   return DC_PAIRS * sizeof(f32x2_t) +
          4 * (size_t)(c > red ? c : red) + 2 * (size_t)(16 * tt * rs * terms);
 }
@@ -419,7 +423,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
   const int64_t N = p.w[0].N, K = p.w[0].K;
   const int64_t n0 = (int64_t)blockIdx.x * 16 * NG;
   const int rs0 = p.v[0].rs, rs1 = GATED ? p.v[1].rs : 0;
-  const int nb = (int)(K / 64), pitch = nb + 1, ns = (nb + 1) / 2;
+  const int nb = (int)(K / 64), pitch = dc_pitch(nb), ns = (nb + 1) / 2;
+  auto turned = [&](int r, int b) {   // place of block b's constant in row r
+    const int at = nb >= 16 ? b + (r & 15) : b;
+    return at < nb ? at : at - nb;
+  };
   uint16_t* sT = reinterpret_cast<uint16_t*>(sC + dc_floats<RG, W>(nb));   // t's bf16 terms [M][TERMS][rs], side 1's after side 0's
 
   const uint8_t* crow[RG];
@@ -505,7 +513,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
         for (int e = 0; e < 4; ++e) v[e] = qc.absmax[blk + e];
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sC[rr * pitch + c + e] = v[e];
+      for (int e = 0; e < 4; ++e) sC[rr * pitch + turned(rr, c + e)] = v[e];
     }
   } else {
     for (int i = threadIdx.x; i < 16 * RG * nb; i += 64 * W) {
@@ -513,7 +521,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
       const bool up = rr >= 16 * NG;
       const QConst qc = up ? p.w[1].qc : p.w[0].qc;
       const int64_t blk = min(n0 + (up ? rr - 16 * NG : rr), N - 1) * nb + bl;
-      sC[rr * pitch + bl] =
+      sC[rr * pitch + turned(rr, bl)] =
           DQ ? __builtin_fmaf(e4m3_decode(qc.absmax_q[blk]), qc.dq_scale[blk >> 8], *qc.dq_mean) : qc.absmax[blk];
     }
   }
@@ -583,7 +591,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
     // XPack holds zeros)
     float cp[RG];
 #pragma unroll
-    for (int g = 0; g < RG; ++g) cp[g] = sC[(16 * g + li) * pitch + st.bl];
+    for (int g = 0; g < RG; ++g) cp[g] = sC[(16 * g + li) * pitch + turned(li, st.bl)];
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {

@@ -32,10 +32,36 @@ __device__ __forceinline__ void gate_grads(u32x4_t G, u32x4_t g, u32x4_t u, floa
     du[2 * w + 1] = G1 * a1.value;
   }
 }
-// The next bfloat16 term of 8 values.
-__device__ __forceinline__ u32x4_t take8(float (&v)[8]) {
-  return u32x4_t{take_bf16_terms(v[0], v[1]), take_bf16_terms(v[2], v[3]), take_bf16_terms(v[4], v[5]),
-                 take_bf16_terms(v[6], v[7])};
+// dg's and du's three bfloat16 terms. Below the largest bfloat16 the terms are
+// the plain ones, hi = bf16(v), mid = bf16(v - hi), lo = bf16(v - hi - mid); a
+// wave that holds a larger value (or an infinity) takes them as take_bf16_terms
+// does. A NaN gives NaN either way.
+__device__ __forceinline__ void split_grads(float (&d)[2][8], u32x4_t (&t)[2][3]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(d[0][e]), fabsf(d[1][e])));
+  if (__ballot(top >= 0x1.fep127f)) {   // 0x1.fep127: the largest bfloat16
+#pragma unroll
+    for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) t[sd][k][w] = take_bf16_terms(d[sd][2 * w], d[sd][2 * w + 1]);
+    return;
+  }
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float a = d[sd][2 * w], b = d[sd][2 * w + 1];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t x = pack_bf16x2(a, b);
+        a -= bf16lo_to_f32(x);
+        b -= bf16hi_to_f32(x);
+        t[sd][k][w] = x;
+      }
+    }
 }
 
 // ===========================================================================
@@ -131,24 +157,22 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
     for (int h = 0; h < 2; ++h) {
       float d[2][8];
       gate_grads<ACT>(now.G[h], now.g[h], now.u[h], d[0], d[1]);
-      u32x4_t t[2];
-#pragma unroll
-      for (int sd = 0; sd < 2; ++sd) t[sd] = take8(d[sd]);
+      u32x4_t t[2][3];
+      split_grads(d, t);
       if (p.D && live) {
         uint16_t* o = p.D + token * 2 * p.Np + GD_K * (int64_t)s + 32 * h + 8 * lg;
-        *reinterpret_cast<u32x4_t*>(o) = t[0];
-        *reinterpret_cast<u32x4_t*>(o + p.Np) = t[1];
+        *reinterpret_cast<u32x4_t*>(o) = t[0][0];
+        *reinterpret_cast<u32x4_t*>(o + p.Np) = t[1][0];
       }
       if (!has) continue;
 #pragma unroll
-      for (int k = 0; k < 3; ++k)
+      for (int sd = 0; sd < 2; ++sd)
 #pragma unroll
-        for (int sd = 0; sd < 2; ++sd) {
+        for (int c = 0; c < JT; ++c) {
+          const u32x4_t b = ld16(buf[sd] + (16 * c + li) * GD_K + slot[h]);
 #pragma unroll
-          for (int c = 0; c < JT; ++c)
-            acc[sd][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                as_bf16x8(t[sd]), as_bf16x8(ld16(buf[sd] + (16 * c + li) * GD_K + slot[h])), acc[sd][c], 0, 0, 0);
-          if (k < 2) t[sd] = take8(d[sd]);
+          for (int k = 0; k < 3; ++k)
+            acc[sd][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(t[sd][k]), as_bf16x8(b), acc[sd][c], 0, 0, 0);
         }
     }
   }
@@ -168,19 +192,19 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
 }
 
 // ===========================================================================
-// Column form of both sides: one workgroup per 128 columns and run of at most
-// `rows` sorted positions, 32 tokens a step; waves 0, 1 take dg with the gate's
-// t, waves 2, 3 du with up's, 64 columns each. The terms of dg and du lie in LDS
-// with tokens as rows and are read transposed, as the terms of s t. Of the nine
-// products of terms the six whose places add up to at most the third are formed:
-// the others are below 2^-24 of the value.
+// Column form of both sides: one workgroup of eight waves per 128 columns and
+// run of at most `rows` sorted positions, 32 tokens a step; waves 0 to 3 take dg
+// with the gate's t, 4 to 7 du with up's, 32 columns each. The terms of dg and
+// du lie in LDS with tokens as rows and are read transposed, as the terms of s t.
+// Of the nine products of terms the six whose places add up to at most the third
+// are formed: the others are below 2^-24 of the value.
 // ===========================================================================
-constexpr int GC_COLS = 128, GC_PITCH = GC_COLS + 16;
+constexpr int GC_COLS = 128, GC_PITCH = GC_COLS + 16, GC_THREADS = 512;
 
 template <int JT, int ACT>
-__global__ __launch_bounds__(256) void k_gated_col(GatedGrad gr, ColReq r0, ColReq r1, int rows, Route rt) {
+__global__ __launch_bounds__(GC_THREADS) void k_gated_col(GatedGrad gr, ColReq r0, ColReq r1, int rows, Route rt) {
   constexpr int PP = 16 * JT + 16;
-  constexpr int PQ = (2 * 3 * 32 * 2 * JT + 255) / 256;   // 16-byte pieces of both sides' t per thread
+  constexpr int PQ = (2 * 3 * 32 * 2 * JT + GC_THREADS - 1) / GC_THREADS;   // 16-byte pieces of both sides' t per thread
   __shared__ __attribute__((aligned(16))) uint16_t sQ[2][3][32 * GC_PITCH];
   __shared__ __attribute__((aligned(16))) uint16_t sP[2][3 * 32 * PP];
   Item it;
@@ -190,26 +214,20 @@ __global__ __launch_bounds__(256) void k_gated_col(GatedGrad gr, ColReq r0, ColR
   const int64_t N = gr.N, c0 = (int64_t)blockIdx.x * GC_COLS;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
-  const int side = uniform(wave >> 1), half = wave & 1;
-  const int qc = 8 * (threadIdx.x & 15), qr = threadIdx.x >> 4;   // columns of tokens qr, qr + 16
+  const int side = uniform(wave >> 2), quarter = wave & 3;
+  const int qc = 8 * (threadIdx.x & 15), qr = threadIdx.x >> 4;   // 8 columns of token qr
   const bool qin = c0 + qc < N;                                   // N % 8 == 0
-  u32x4_t xG[2], xg[2], xu[2], xp[PQ];
-  int tok[2];
-  auto tokens = [&](int mb) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) tok[u] = rt.perm[it.start + min(mb + qr + 16 * u, it.count - 1)];
-  };
+  u32x4_t xG, xg, xu, xp[PQ];
+  int tok;
+  auto tokens = [&](int mb) { tok = rt.perm[it.start + min(mb + qr, it.count - 1)]; };
   auto load = [&](int mb) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t o = (int64_t)tok[u] * N + (qin ? c0 + qc : 0);
-      xG[u] = ld16(gr.G + o);
-      xg[u] = ld16(gr.g + o);
-      xu[u] = ld16(gr.u + o);
-    }
+    const int64_t o = (int64_t)tok * N + (qin ? c0 + qc : 0);
+    xG = ld16(gr.G + o);
+    xg = ld16(gr.g + o);
+    xu = ld16(gr.u + o);
 #pragma unroll
     for (int k = 0; k < PQ; ++k) {
-      const int i = threadIdx.x + 256 * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, t = min(i / (64 * JT), 5);
+      const int i = threadIdx.x + GC_THREADS * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, t = min(i / (64 * JT), 5);
       const bool up = t >= 3;
       const int term = up ? t - 3 : t, r8 = up ? r81 : r80;
       xp[k] = ld16((up ? r1.terms : r0.terms) + (int64_t)(it.start + min(mb + row, it.count - 1)) * 3 * (up ? r1.v.rs : r0.v.rs) +
@@ -218,32 +236,28 @@ __global__ __launch_bounds__(256) void k_gated_col(GatedGrad gr, ColReq r0, ColR
   };
   auto store = [&](int mb) {
     const u32x4_t none = {0u, 0u, 0u, 0u};
+    const bool in = qin && mb + qr < it.count;   // others are zero: no neighbour's infinity enters
+    float d[2][8];
+    gate_grads<ACT>(xG, xg, xu, d[0], d[1]);
+    u32x4_t t3[2][3];
+    split_grads(d, t3);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const bool in = qin && mb + qr + 16 * u < it.count;   // others are zero: no neighbour's infinity enters
-      float d[2][8];
-      gate_grads<ACT>(xG[u], xg[u], xu[u], d[0], d[1]);
+    for (int sd = 0; sd < 2; ++sd)
 #pragma unroll
-      for (int sd = 0; sd < 2; ++sd)
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const u32x4_t t = take8(d[sd]);
-          *reinterpret_cast<u32x4_t*>(sQ[sd][k] + (qr + 16 * u) * GC_PITCH + qc) = in ? t : none;
-        }
-    }
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t*>(sQ[sd][k] + qr * GC_PITCH + qc) = in ? t3[sd][k] : none;
 #pragma unroll
     for (int k = 0; k < PQ; ++k) {
-      const int i = threadIdx.x + 256 * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, t = i / (64 * JT);
+      const int i = threadIdx.x + GC_THREADS * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, t = i / (64 * JT);
       if (t < 6)
         *reinterpret_cast<u32x4_t*>(sP[t >= 3] + (32 * (t >= 3 ? t - 3 : t) + row) * PP + 8 * c8) =
             mb + row < it.count && 8 * c8 < (t >= 3 ? r81 : r80) ? xp[k] : none;
     }
   };
-  f32x4_t acc[JT][4];
+  f32x4_t acc[JT][2];
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) acc[jt][ct] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int ct = 0; ct < 2; ++ct) acc[jt][ct] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   tokens(0);
   load(0);
   tokens(32);
@@ -252,21 +266,22 @@ __global__ __launch_bounds__(256) void k_gated_col(GatedGrad gr, ColReq r0, ColR
     lds_barrier();
     load(m + 32);
     tokens(m + 64);
+    u32x4_t fq[3][2];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      u32x4_t fq[4];
+    for (int k = 0; k < 3; ++k)
 #pragma unroll
-      for (int ct = 0; ct < 4; ++ct) fq[ct] = tr_frag(sQ[side][k] + 64 * half + 16 * ct, GC_PITCH, li, lg);
+      for (int ct = 0; ct < 2; ++ct) fq[k][ct] = tr_frag(sQ[side][k] + 32 * quarter + 16 * ct, GC_PITCH, li, lg);
 #pragma unroll
-      for (int t = 0; t < 3 - k; ++t)
+    for (int t = 0; t < 3; ++t)
 #pragma unroll
-        for (int jt = 0; jt < JT; ++jt) {
-          const u32x4_t a = tr_frag(sP[side] + 32 * t * PP + 16 * jt, PP, li, lg);
+      for (int jt = 0; jt < JT; ++jt) {
+        const u32x4_t a = tr_frag(sP[side] + 32 * t * PP + 16 * jt, PP, li, lg);
 #pragma unroll
-          for (int ct = 0; ct < 4; ++ct)
-            acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(fq[ct]), acc[jt][ct], 0, 0, 0);
-        }
-    }
+        for (int k = 0; k < 3 - t; ++k)
+#pragma unroll
+          for (int ct = 0; ct < 2; ++ct)
+            acc[jt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(fq[k][ct]), acc[jt][ct], 0, 0, 0);
+      }
     lds_barrier();   // read by everyone; the next step's loads stay in flight
   }
   // lane: column li of each tile, rows j = 4 lg + e
@@ -278,8 +293,8 @@ __global__ __launch_bounds__(256) void k_gated_col(GatedGrad gr, ColReq r0, ColR
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-      const int64_t c = c0 + 64 * half + 16 * ct + li;
+    for (int ct = 0; ct < 2; ++ct) {
+      const int64_t c = c0 + 32 * quarter + 16 * ct + li;
       const int j0 = 16 * jt + 4 * lg;
       if (c >= N || j0 >= r) continue;
       if (vec) {   // N * row and c * r are multiples of 4
@@ -305,12 +320,20 @@ int gated_col_rows(int64_t M, int64_t N) {
 
 }  // namespace
 
-// Shares of the columns: two workgroups per CU, at least 4 steps each.
+// Shares of the columns: what leaves the shortest queue of 64-column steps where
+// two workgroups run on each CU, a share costing about two steps more.
 int gated_down_shares(int64_t M, int64_t N) {
   const int64_t tiles = (M + GD_M - 1) / GD_M, steps = (N + GD_K - 1) / GD_K;
-  int s = 1;
-  while (s < 16 && tiles * s * 2 <= 512 && steps / (s * 2) >= 4) s *= 2;
-  return s;
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int s = 1; s <= 16 && s <= steps; ++s) {
+    const int64_t c = (tiles * s + 511) / 512 * ((steps + s - 1) / s + 2);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
 }
 size_t gated_down_ws_floats(int64_t M, int64_t N, int32_t rs) { return (size_t)gated_down_shares(M, N) * M * rs; }
 
@@ -342,7 +365,7 @@ hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t
   const int rows = gated_col_rows(M, gr.N), act = gr.act;
   const dim3 grid((unsigned)((gr.N + GC_COLS - 1) / GC_COLS), (unsigned)((M + rows - 1) / rows + std::min<int64_t>(req[0].v.n, M)));
   const int32_t r = std::max(req[0].v.r_max, req[1].v.r_max);
-#define LQ_GC(JT, ACT) hipLaunchKernelGGL((k_gated_col<JT, ACT>), grid, dim3(256), 0, s, gr, req[0], req[1], rows, rt)
+#define LQ_GC(JT, ACT) hipLaunchKernelGGL((k_gated_col<JT, ACT>), grid, dim3(GC_THREADS), 0, s, gr, req[0], req[1], rows, rt)
   if (r <= 16) LQ_ACTS(LQ_GC, 1);
   else if (r <= 32) LQ_ACTS(LQ_GC, 2);
   else if (r <= 64) LQ_ACTS(LQ_GC, 4);
