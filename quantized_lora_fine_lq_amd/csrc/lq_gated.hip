@@ -68,7 +68,8 @@ __device__ __forceinline__ void split_grads(float (&d)[2][8], u32x4_t (&t)[2][3]
 // Row form: 64 routed tokens of one adapter (or of none: D alone) per workgroup
 // and share of the columns, 16 a wave, in steps of 64 columns. A lane forms dg
 // and du of 8 columns of a token in registers, which is the matrix product's
-// operand; B^T's rows pass through LDS, double buffered, loaded a step ahead.
+// operand; G, g and u are loaded two steps ahead, B^T's rows one, through LDS,
+// double buffered.
 // ===========================================================================
 constexpr int GD_M = 64, GD_K = 64;
 
@@ -110,9 +111,10 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
   struct Q {
     u32x4_t G[2], g[2], u[2];
   };
-  Q q;
+  Q q0, q1;
   u32x4_t w[JT];
-  auto load = [&](int s) {
+  auto load = [&](int s, Q& q) __attribute__((always_inline)) {   // (past the share's end its last step again)
+    s = min(s, s1 - 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t c = GD_K * (int64_t)s + 32 * h + 8 * lg;
@@ -123,7 +125,10 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
       q.u[h] = ld16(pu + o);
       if (!ok) q.G[h] = q.g[h] = q.u[h] = u32x4_t{0u, 0u, 0u, 0u};
     }
+  };
+  auto load_w = [&](int s) __attribute__((always_inline)) {
     if (!has) return;
+    s = min(s, s1 - 1);
 #pragma unroll
     for (int k = 0; k < JT; ++k) {
       const int i = threadIdx.x + 256 * k, sd = i / (8 * ROWS), j = (i >> 3) % ROWS;
@@ -138,8 +143,7 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
 #pragma unroll
     for (int c = 0; c < JT; ++c) acc[sd][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
-  if (s0 < s1) load(s0);
-  for (int s = s0; s < s1; ++s) {
+  auto step = [&](int s, Q& q) __attribute__((always_inline)) {
     uint16_t(*buf)[ROWS * GD_K] = sW[(s - s0) & 1];
     if (has) {
 #pragma unroll
@@ -148,15 +152,14 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
         *reinterpret_cast<u32x4_t*>(buf[sd] + j * GD_K + 8 * ((i & 7) ^ (j & 7))) = w[k];
       }
     }
-    const Q now = q;
     // (one barrier a step: the buffer written at step s + 1 was read at s - 1, and
     // those reads are done before a wave reaches step s's barrier)
     if (has) lds_barrier();
-    if (s + 1 < s1) load(s + 1);
+    load_w(s + 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float d[2][8];
-      gate_grads<ACT>(now.G[h], now.g[h], now.u[h], d[0], d[1]);
+      gate_grads<ACT>(q.G[h], q.g[h], q.u[h], d[0], d[1]);
       u32x4_t t[2][3];
       split_grads(d, t);
       if (p.D && live) {
@@ -166,15 +169,29 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
       }
       if (!has) continue;
 #pragma unroll
-      for (int sd = 0; sd < 2; ++sd)
+      for (int sd = 0; sd < 2; ++sd) {
+        u32x4_t b[JT];
 #pragma unroll
-        for (int c = 0; c < JT; ++c) {
-          const u32x4_t b = ld16(buf[sd] + (16 * c + li) * GD_K + slot[h]);
+        for (int c = 0; c < JT; ++c) b[c] = ld16(buf[sd] + (16 * c + li) * GD_K + slot[h]);
 #pragma unroll
-          for (int k = 0; k < 3; ++k)
-            acc[sd][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(t[sd][k]), as_bf16x8(b), acc[sd][c], 0, 0, 0);
-        }
+        for (int k = 0; k < 3; ++k)   // (the chains of one sum are JT products apart)
+#pragma unroll
+          for (int c = 0; c < JT; ++c)
+            acc[sd][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(t[sd][k]), as_bf16x8(b[c]), acc[sd][c], 0, 0, 0);
+      }
     }
+    load(s + 2, q);
+  };
+  if (s0 < s1) {
+    load(s0, q0);
+    load_w(s0);
+    load(s0 + 1, q1);
+    int s = s0;
+    for (; s + 1 < s1; s += 2) {
+      step(s, q0);
+      step(s + 1, q1);
+    }
+    if (s < s1) step(s, q0);
   }
   if (!has) return;
   // lane: tokens 16 wave + 4 lg + e, row 16 c + li of the adapter
@@ -199,13 +216,27 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
 // Of the nine products of terms the six whose places add up to at most the third
 // are formed: the others are below 2^-24 of the value.
 // ===========================================================================
-constexpr int GC_COLS = 128, GC_PITCH = GC_COLS + 16, GC_THREADS = 512;
+constexpr int GC_COLS = 128, GC_THREADS = 512;
+
+// lane's 8 values k = 8 lg + [0, 8) of column c0 + li (c0 a multiple of 16) of
+// rows of 128 whose 16-byte chunks lie at chunk ^ 2 (row % 4): the four rows that
+// a transposing read takes at once hit distinct banks.
+__device__ __forceinline__ u32x4_t tr_frag_swizzled(const uint16_t* base, int c0, int li, int lg) {
+  typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) v4b* lds_p;
+  const int row = 8 * lg + (li >> 2), chunk = (c0 >> 3) + ((li & 3) >> 1);
+  const uint16_t* p = base + row * GC_COLS + 8 * (chunk ^ (2 * (li >> 2))) + 4 * (li & 1);   // row % 4 = li >> 2, also 4 rows on
+  const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)p));
+  const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_p)(p + 4 * GC_COLS)));
+  return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+}
 
 template <int JT, int ACT>
-__global__ __launch_bounds__(GC_THREADS) void k_gated_col(GatedGrad gr, ColReq r0, ColReq r1, int rows, Route rt) {
+__global__ __launch_bounds__(GC_THREADS, JT <= 4 ? 4 : 2) void k_gated_col(GatedGrad gr, ColReq r0, ColReq r1, int rows, Route rt) {
   constexpr int PP = 16 * JT + 16;
   constexpr int PQ = (2 * 3 * 32 * 2 * JT + GC_THREADS - 1) / GC_THREADS;   // 16-byte pieces of both sides' t per thread
-  __shared__ __attribute__((aligned(16))) uint16_t sQ[2][3][32 * GC_PITCH];
+  __shared__ __attribute__((aligned(16))) uint16_t sQ[2][3][32 * GC_COLS];
   __shared__ __attribute__((aligned(16))) uint16_t sP[2][3 * 32 * PP];
   Item it;
   if (!find_item(rt.off, r0.v.n, rows, (int)blockIdx.y, it)) return;
@@ -244,7 +275,7 @@ __global__ __launch_bounds__(GC_THREADS) void k_gated_col(GatedGrad gr, ColReq r
 #pragma unroll
     for (int sd = 0; sd < 2; ++sd)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t*>(sQ[sd][k] + qr * GC_PITCH + qc) = in ? t3[sd][k] : none;
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t*>(sQ[sd][k] + qr * GC_COLS + (qc ^ (16 * (qr & 3)))) = in ? t3[sd][k] : none;
 #pragma unroll
     for (int k = 0; k < PQ; ++k) {
       const int i = threadIdx.x + GC_THREADS * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, t = i / (64 * JT);
@@ -270,7 +301,7 @@ __global__ __launch_bounds__(GC_THREADS) void k_gated_col(GatedGrad gr, ColReq r
 #pragma unroll
     for (int k = 0; k < 3; ++k)
 #pragma unroll
-      for (int ct = 0; ct < 2; ++ct) fq[k][ct] = tr_frag(sQ[side][k] + 32 * quarter + 16 * ct, GC_PITCH, li, lg);
+      for (int ct = 0; ct < 2; ++ct) fq[k][ct] = tr_frag_swizzled(sQ[side][k], 32 * quarter + 16 * ct, li, lg);
 #pragma unroll
     for (int t = 0; t < 3; ++t)
 #pragma unroll
