@@ -411,7 +411,7 @@ __device__ __forceinline__ void dc_store(void* out, int64_t o, int64_t n, int64_
 }
 
 template <int RG, int TT, int W, bool DQ, bool OUT_F32, bool GATED>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) void k_decode_nf4(DecodeParams p) {
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED && RG == 2 && W == 4 ? 4 : 2))) void k_decode_nf4(DecodeParams p) {
   constexpr int NG = GATED ? RG / 2 : RG;   // groups of 16 outputs
   extern __shared__ __attribute__((aligned(16))) unsigned char dc_lds[];
   constexpr int TERMS = OUT_F32 ? 3 : 2;
@@ -794,6 +794,15 @@ hipError_t launch_gated_decode(const QWeight (&w)[2], const uint16_t* X, int64_t
   const DecodeParams p{xp, records, (int)M, ids, {v[0], v[1]}, {t0, t1}, parts, {t_gate, t_up}, H, {w[0], w[1]}, tables().lv,
                        act, g, u};
   const int rg = decode_rg(w[0].N, w[0].K, tt, v[0].rs + v[1].rs, terms, true);
+  // Up to 32 tokens and between one and four times as many groups of 16 outputs
+  // as CUs: workgroups of four waves over one group, three on a CU and all of
+  // them at once, beat two rounds of larger ones (N = 11008, K = 4096: one token
+  // 22 us for 28, 16 tokens 27 for 36, 32 tokens 29 for 36; N = 4096: 17 for 16;
+  // N = 28672, K = 8192: 91 for 88).
+  const int64_t groups = (w[0].N + 15) / 16;
+  const bool flat = tt <= 2 && groups > kCus && groups <= 4 * kCus;
+  if (flat && tt == 1) return launch_rg<2, 1, 4, true>(p, f32, s);
+  if (flat) return launch_rg<2, 2, 4, true>(p, f32, s);
 #define LQ_RG(TT)                                          \
   do {                                                     \
     if (rg == 4) return launch_rg<4, TT, 4, true>(p, f32, s); \

@@ -751,10 +751,14 @@ __global__ __launch_bounds__(S_THREADS * GROUPS, 2) void k_adapter_gemm_small(Ad
 }
 
 // 64 x 64 tiles through LDS; columns past N, up to a multiple of 64, are zero.
-__global__ __launch_bounds__(256) void k_transpose_weight(const uint16_t* __restrict__ w, int64_t N, int64_t K,
-                                                          int64_t ldb, uint16_t* __restrict__ out) {
+__global__ __launch_bounds__(256) void k_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out,
+                                                          const uint16_t* w2, uint16_t* out2) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];   // [n][k]
   const int64_t n0 = (int64_t)blockIdx.x * 64, k0 = (int64_t)blockIdx.y * 64;   // K % 64 == 0
+  if (blockIdx.z) {
+    w = w2;
+    out = out2;
+  }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = threadIdx.x + 256 * u, n = i >> 3, c = 8 * (i & 7);
@@ -828,11 +832,11 @@ hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s) {
   return c256 <= c128 ? launch_tile<256>(g, s) : launch_tile<128>(g, s);
 }
 
-hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out,
-                                   hipStream_t s) {
+hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out, const uint16_t* w2,
+                                   uint16_t* out2, hipStream_t s) {
   LQ_DASSERT(K % 64 == 0 && ldb % 64 == 0 && ldb >= N);
-  hipLaunchKernelGGL(k_transpose_weight, dim3((unsigned)((N + 63) / 64), (unsigned)(K / 64)), dim3(256), 0, s, w, N, K, ldb,
-                     out);
+  hipLaunchKernelGGL(k_transpose_weight, dim3((unsigned)((N + 63) / 64), (unsigned)(K / 64), w2 ? 2u : 1u), dim3(256), 0, s, w, N,
+                     K, ldb, out, w2, out2);
   return hipGetLastError();
 }
 

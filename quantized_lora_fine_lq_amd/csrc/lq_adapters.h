@@ -72,9 +72,16 @@ hipError_t launch_adapter_join(const DownJob* jobs, int njobs, int64_t M, const 
 // matrix kernels: at = A^T [K, r8] at K * row8_a, bt = B^T [r, N] at N *
 // row8_a, bp = B [N, r8] at N * row8_a of the adapters whose rank is not a
 // multiple of 8 (zero columns past r_a).
-hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, const QWeight& w, uint16_t* wd,
-                               int64_t ldb, const AdapterView& v, uint16_t* at, uint16_t* bt, uint16_t* bp,
-                               uint16_t* zeros, hipStream_t s);
+struct Prep {
+  int32_t* route;
+  QWeight w;
+  uint16_t* wd;
+  int64_t ldb;
+  AdapterView v;
+  uint16_t *at, *bt, *bp, *zeros;
+};
+// Of one weight, or of two of one size (the route of the first's).
+hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, const Prep* a, int n, hipStream_t s);
 
 // Column form over routed tokens: out_a[j][c] = sum over a's tokens of
 // (s_a P)[m][j] Q[m][c], written [r, C] at C * row_a, or transposed [C, r].
@@ -89,10 +96,15 @@ struct ColReq {
   AdapterView v;           // sets of one n
 };
 size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs);
-hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Route& rt, hipStream_t s);
-// Its second part: joins the runs of `rows` positions of adapters with more than
-// one, and writes the zeros of adapters without tokens.
-hipError_t launch_adapter_col_reduce(const ColReq* reqs, int nreq, int rows, const Route& rt, hipStream_t s);
+// Two launches: the products, and the join of the runs of `rows` positions of
+// adapters with more than one, which also writes the zeros of adapters without
+// tokens (of one or two such products).
+struct ColJoin {
+  ColReq q[2];
+  int n, rows;
+};
+hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Route& rt, ColJoin* join, hipStream_t s);
+hipError_t launch_adapter_col_reduce(const ColJoin* joins, int n, const Route& rt, hipStream_t s);
 
 // out[token][c] = sum_k A[token][k] Bt[c][k] + sum_j (s_a L)[token][j] Lb_a(c, j)
 // over the sorted positions; Lb_a(c, j): row c of lt + Ncols * row8_a
@@ -126,7 +138,9 @@ struct AdapterGemm {
 };
 hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s);
 // [N, K] -> [K, N rounded up to a multiple of 64] bf16 of row stride ldb (zero columns past N)
-hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out, hipStream_t s);
+// (two of a size where w2 is given)
+hipError_t launch_transpose_weight(const uint16_t* w, int64_t N, int64_t K, int64_t ldb, uint16_t* out, const uint16_t* w2,
+                                   uint16_t* out2, hipStream_t s);
 
 // Decode sizes (NF4, M <= 64): the whole forward without a route, in two
 // launches.
@@ -150,8 +164,8 @@ int gated_down_shares(int64_t M, int64_t N);
 hipError_t launch_gated_down(const GatedGrad& gr, int64_t M, const AdapterView (&v)[2], const uint16_t* const (&bt)[2],
                              float* const (&part)[2], uint16_t* D, const Route& rt, hipStream_t s);
 // dB of both sides: requests as launch_adapter_col's (transposed), Q in place of
-// side 0's dg, side 1's du; a null out: not wanted.
-hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t M, const Route& rt, hipStream_t s);
+// side 0's dg, side 1's du; a null out: not wanted (one is). The join is the caller's.
+hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t M, const Route& rt, ColJoin* join, hipStream_t s);
 
 // Decode sizes of a pair: the whole forward, in two launches.
 bool gated_decode_supported(const QWeight (&w)[2], int64_t M, const AdapterView (&v)[2]);

@@ -335,9 +335,19 @@ __device__ __forceinline__ void prep_adapter(const PrepJob& p, unsigned a, unsig
     }
 }
 
-__global__ __launch_bounds__(1024) void k_adapter_prep(PrepJob p) {
+// PAIR: two weights with their sets, the second's workgroups after the first's.
+template <bool PAIR>
+struct PrepJobs {
+  PrepJob j[PAIR ? 2 : 1];
+  unsigned first;   // workgroups of the first
+};
+
+template <bool PAIR>
+__global__ __launch_bounds__(1024) void k_adapter_prep(PrepJobs<PAIR> jobs) {
   extern __shared__ __attribute__((aligned(16))) unsigned char prep_lds[];
-  unsigned wg = blockIdx.x;
+  const unsigned second = PAIR && blockIdx.x >= jobs.first ? 1 : 0;
+  const PrepJob& p = jobs.j[second];
+  unsigned wg = blockIdx.x - second * jobs.first;
   if (wg == 0 && threadIdx.x < 8 && p.zeros) p.zeros[threadIdx.x] = 0;
   if (wg < p.route_wgs) {
     route_tokens(p.route, reinterpret_cast<int32_t*>(prep_lds));
@@ -765,7 +775,13 @@ __global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0,
 // Joins the runs of adapters with more than one, in order, and writes the zero
 // gradients of adapters without tokens. 7 us at 2048 tokens of rank 16, 16 at
 // 4096 of rank 64 (four partial sums a thread at a time).
-__global__ __launch_bounds__(256) void k_adapter_col_reduce(ColReq q0, ColReq q1, int nreq, int rows, Route rt) {
+struct ColJoins {
+  ColJoin j[2];
+};
+__global__ __launch_bounds__(256) void k_adapter_col_reduce(ColJoins joins, Route rt) {
+  const ColJoin& jn = joins.j[blockIdx.z];
+  const ColReq &q0 = jn.q[0], &q1 = jn.q[1];
+  const int nreq = jn.n, rows = jn.rows;
   const int a = blockIdx.y, lane = threadIdx.x & 63;
   int before = 0;   // slots of the adapters before a
   for (int b = lane; b < a; b += 64) {
@@ -821,45 +837,64 @@ int col_rows(int64_t M, int64_t cols) {
 
 }  // namespace
 
-hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, int32_t* route, const QWeight& w, uint16_t* wd,
-                               int64_t ldb, const AdapterView& v, uint16_t* at, uint16_t* bt, uint16_t* bp,
-                               uint16_t* zeros, hipStream_t s) {
-  LQ_DASSERT(!wd || w.format == LQ_FMT_NF4 || !ldb);
+namespace {
+
+// Fills a job; returns its workgroups and raises lds to what they need.
+int64_t prep_job(const Prep& a, int64_t M, const int32_t* ids, PrepJob* out, size_t* lds) {
   PrepJob p{};
-  size_t lds = 0;
-  if (route) {
-    const Route r = route_view(route, M, v.n);
-    p.route = RouteJob{ids, M, v.n, const_cast<int32_t*>(r.off), const_cast<int32_t*>(r.perm), const_cast<int32_t*>(r.sid)};
+  if (a.route) {
+    const Route r = route_view(a.route, M, a.v.n);
+    p.route = RouteJob{ids, M, a.v.n, const_cast<int32_t*>(r.off), const_cast<int32_t*>(r.perm), const_cast<int32_t*>(r.sid)};
     p.route_wgs = 1;
-    lds = route_lds_bytes(v.n);
+    *lds = std::max(*lds, route_lds_bytes(a.v.n));
   }
-  p.w = w;
+  p.w = a.w;
   p.lv = tables().lv;
-  p.wd = wd;
-  p.ldb = ldb;
-  p.wcols = (w.N + 63) / 64 * 64;
-  if (wd) {
+  p.wd = a.wd;
+  p.ldb = a.ldb;
+  p.wcols = (a.w.N + 63) / 64 * 64;
+  if (a.wd) {
     const int64_t flat = PW_FLAT * 1024 * 16;
-    if (w.format == LQ_FMT_CODEBOOK) {
-      p.weight_wgs = (unsigned)((w.N + PC_ROWS - 1) / PC_ROWS);
-      lds = std::max(lds, (size_t)PC_ROWS * 256 * sizeof(f32x2_t));
+    if (a.w.format == LQ_FMT_CODEBOOK) {
+      p.weight_wgs = (unsigned)((a.w.N + PC_ROWS - 1) / PC_ROWS);
+      *lds = std::max(*lds, (size_t)PC_ROWS * 256 * sizeof(f32x2_t));
     } else {
-      p.weight_wgs = (unsigned)(ldb ? ((w.N + PW_T - 1) / PW_T) * ((w.K + PW_T - 1) / PW_T) : (w.N * w.K + flat - 1) / flat);
-      lds = std::max(lds, 256 * sizeof(f32x2_t) + (ldb ? (size_t)PW_T * PW_PITCH * 2 : 0));
+      p.weight_wgs = (unsigned)(a.ldb ? ((a.w.N + PW_T - 1) / PW_T) * ((a.w.K + PW_T - 1) / PW_T) : (a.w.N * a.w.K + flat - 1) / flat);
+      *lds = std::max(*lds, 256 * sizeof(f32x2_t) + (a.ldb ? (size_t)PW_T * PW_PITCH * 2 : 0));
     }
   }
-  p.v = v;
-  p.at = at;
-  p.bt = bt;
-  p.bp = bp;
-  p.zeros = zeros;
-  p.at_wgs = at ? (unsigned)((w.K + RL_C - 1) / RL_C) : 0;
-  p.b_wgs = bt || bp ? (unsigned)((w.N + RL_C - 1) / RL_C) : 0;
+  p.v = a.v;
+  p.at = a.at;
+  p.bt = a.bt;
+  p.bp = a.bp;
+  p.zeros = a.zeros;
+  p.at_wgs = a.at ? (unsigned)((a.w.K + RL_C - 1) / RL_C) : 0;
+  p.b_wgs = a.bt || a.bp ? (unsigned)((a.w.N + RL_C - 1) / RL_C) : 0;
   p.per_adapter = p.at_wgs + p.b_wgs;
-  if (p.per_adapter) lds = std::max(lds, (size_t)RL_C * (v.rs + 2) * 2);
-  const int64_t grid = std::max<int64_t>(1, (int64_t)p.route_wgs + p.weight_wgs + (int64_t)v.n * p.per_adapter);
-  LQ_DASSERT(grid < (int64_t(1) << 31) && lds <= 65536);
-  hipLaunchKernelGGL(k_adapter_prep, dim3((unsigned)grid), dim3(1024), lds, s, p);
+  if (p.per_adapter) *lds = std::max(*lds, (size_t)RL_C * (a.v.rs + 2) * 2);
+  *out = p;
+  return (int64_t)p.route_wgs + p.weight_wgs + (int64_t)a.v.n * p.per_adapter;
+}
+
+}  // namespace
+
+hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, const Prep* a, int n, hipStream_t s) {
+  if (n < 1 || n > 2) return hipErrorInvalidValue;
+  for (int i = 0; i < n; ++i) LQ_DASSERT(!a[i].wd || a[i].w.format == LQ_FMT_NF4 || !a[i].ldb);
+  size_t lds = 0;
+  if (n == 1) {
+    PrepJobs<false> jobs{};
+    const int64_t grid = std::max<int64_t>(1, prep_job(a[0], M, ids, &jobs.j[0], &lds));
+    LQ_DASSERT(grid < (int64_t(1) << 31) && lds <= 65536);
+    hipLaunchKernelGGL(k_adapter_prep<false>, dim3((unsigned)grid), dim3(1024), lds, s, jobs);
+  } else {
+    PrepJobs<true> jobs{};
+    const int64_t first = std::max<int64_t>(1, prep_job(a[0], M, ids, &jobs.j[0], &lds));   // (one clears the zeros)
+    const int64_t grid = first + prep_job(a[1], M, ids, &jobs.j[1], &lds);
+    LQ_DASSERT(grid < (int64_t(1) << 31) && lds <= 65536);
+    jobs.first = (unsigned)first;
+    hipLaunchKernelGGL(k_adapter_prep<true>, dim3((unsigned)grid), dim3(1024), lds, s, jobs);
+  }
   return hipGetLastError();
 }
 
@@ -948,7 +983,7 @@ size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs) {
   return (size_t)(2 * ((M + rows - 1) / rows)) * rs * C;
 }
 
-hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Route& rt, hipStream_t s) {
+hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Route& rt, ColJoin* join, hipStream_t s) {
   if (nreq < 1 || nreq > 2) return hipErrorInvalidValue;
   const ColReq q0 = reqs[0], q1 = reqs[nreq - 1];
   const bool drops = q0.drop.T || q1.drop.T;
@@ -968,16 +1003,21 @@ hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Rou
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_adapter_col_reduce(reqs, nreq, rows, rt, s);
+  *join = ColJoin{{q0, q1}, nreq, rows};
+  return hipSuccess;
 }
 
-hipError_t launch_adapter_col_reduce(const ColReq* reqs, int nreq, int rows, const Route& rt, hipStream_t s) {
-  if (nreq < 1 || nreq > 2) return hipErrorInvalidValue;
-  const ColReq q0 = reqs[0], q1 = reqs[nreq - 1];
-  const int64_t most = q0.v.r_max * q0.C + (nreq > 1 ? q1.v.r_max * q1.C : 0);
-  const unsigned gx =
-      (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 255) / 256, std::max(32, 4096 / q0.v.n)));
-  hipLaunchKernelGGL(k_adapter_col_reduce, dim3(gx, (unsigned)q0.v.n), dim3(256), 0, s, q0, q1, nreq, rows, rt);
+hipError_t launch_adapter_col_reduce(const ColJoin* joins, int n, const Route& rt, hipStream_t s) {
+  if (n < 1 || n > 2) return hipErrorInvalidValue;
+  ColJoins all{};
+  int64_t most = 0;
+  for (int i = 0; i < n; ++i) {
+    const ColJoin& j = all.j[i] = joins[i];
+    most = std::max(most, j.q[0].v.r_max * j.q[0].C + (j.n > 1 ? j.q[1].v.r_max * j.q[1].C : 0));
+  }
+  const int32_t sets = joins[0].q[0].v.n;
+  const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 255) / 256, std::max(32, 4096 / sets)));
+  hipLaunchKernelGGL(k_adapter_col_reduce, dim3(gx, (unsigned)sets, (unsigned)n), dim3(256), 0, s, all, rt);
   return hipGetLastError();
 }
 

@@ -87,7 +87,8 @@ int run_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const lq_adap
   uint16_t* bp = any_odd_rank(set) ? cv.take<uint16_t>((size_t)sum_r8(set) * q.N) : nullptr;
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
 
-  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, wd, 0, v, nullptr, nullptr, bp, zeros, s);
+  const Prep prep{route ? nullptr : rws, q, wd, 0, v, nullptr, nullptr, bp, zeros};
+  hipError_t e = launch_adapter_prep(ids, M, &prep, 1, s);
   if (e != hipSuccess) return LQ_ERR_LAUNCH;
   const Route rt = route_view(route ? route : rws, M, v.n);
   const DownJob job{X, q.K, nullptr, nullptr, terms, t_save, part, drop, factor, v, 1};
@@ -136,8 +137,9 @@ int run_backward(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int6
   if (!grad_X && !dA && !dB) return LQ_OK;
 
   const bool need_u = grad_X || dA, nf4 = q.format == LQ_FMT_NF4;
-  hipError_t e = launch_adapter_prep(ids, M, route ? nullptr : rws, q, !grad_X ? nullptr : nf4 ? wt : wd, nf4 ? ldb : 0,
-                                     v, grad_X ? at : nullptr, need_u ? bt : nullptr, nullptr, zeros, s);
+  const Prep prep{route ? nullptr : rws,   q, !grad_X ? nullptr : nf4 ? wt : wd, nf4 ? ldb : 0, v, grad_X ? at : nullptr,
+                  need_u ? bt : nullptr, nullptr, zeros};
+  hipError_t e = launch_adapter_prep(ids, M, &prep, 1, s);
   if (e != hipSuccess) return LQ_ERR_LAUNCH;
   const Route rt = route_view(route ? route : rws, M, v.n);
   DownJob jobs[2];
@@ -150,9 +152,12 @@ int run_backward(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int6
   int nc = 0;
   if (dB) cols[nc++] = ColReq{t, G, q.N, dB, 1, part_b, DropView{}, v};
   if (dA) cols[nc++] = ColReq{u, X, q.K, dA, 0, part_a, drop, v};
-  if (nc && (e = launch_adapter_col(cols, nc, M, rt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  ColJoin join;
+  if (nc && ((e = launch_adapter_col(cols, nc, M, rt, &join, s)) != hipSuccess ||
+             (e = launch_adapter_col_reduce(&join, 1, rt, s)) != hipSuccess))
+    return LQ_ERR_LAUNCH;
   if (!grad_X) return LQ_OK;
-  if (!nf4 && (e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, s)) != hipSuccess) return LQ_ERR_LAUNCH;
+  if (!nf4 && (e = launch_transpose_weight(wd, q.N, q.K, ldb, wt, nullptr, nullptr, s)) != hipSuccess) return LQ_ERR_LAUNCH;
   const AdapterGemm g{G,  M, q.K, q.N, q.N, wt, ldb, {{u, v, at, drop}, {}}, 1, rt, grad_X,
                       0,  zeros, GEMM_ONE, nullptr, 0, nullptr, nullptr};
   return launch_status(launch_adapter_gemm(g, s));
@@ -176,10 +181,8 @@ int lq_adapter_route(const int32_t* ids, int64_t M, int32_t n, int32_t* route, s
   if (!ids || !route || !al(ids, 4) || !al(route, kVec)) return LQ_ERR_ARG;
   if (!valid_M(M) || n < 1 || n > LQ_ADAPTERS_MAX) return LQ_ERR_SHAPE;
   if (bytes < route_bytes(M, n)) return LQ_ERR_WORKSPACE;
-  QWeight none{};
-  const AdapterView v{nullptr, n, 0, 0};
-  return launch_status(launch_adapter_prep(ids, M, route, none, nullptr, 0, v, nullptr, nullptr, nullptr,
-                                           nullptr, (hipStream_t)stream));
+  const Prep prep{route, QWeight{}, nullptr, 0, AdapterView{nullptr, n, 0, 0}, nullptr, nullptr, nullptr, nullptr};
+  return launch_status(launch_adapter_prep(ids, M, &prep, 1, (hipStream_t)stream));
 }
 
 size_t lq_adapters_forward_workspace(const lq_qweight* w, int64_t M, const lq_adapter_set* set) {

@@ -391,7 +391,8 @@ hipError_t launch_gated_down(const GatedGrad& gr, int64_t M, const AdapterView (
   return hipGetLastError();
 }
 
-hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t M, const Route& rt, hipStream_t s) {
+hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t M, const Route& rt, ColJoin* join,
+                            hipStream_t s) {
   LQ_DASSERT(gr.N % 8 == 0 && M > 0 && req[0].v.n > 0);
   const int rows = gated_col_rows(M, gr.N), act = gr.act;
   const dim3 grid((unsigned)((gr.N + GC_COLS - 1) / GC_COLS), (unsigned)((M + rows - 1) / rows + std::min<int64_t>(req[0].v.n, M)));
@@ -402,13 +403,10 @@ hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t
   else if (r <= 64) LQ_ACTS(LQ_GC, 4);
   else LQ_ACTS(LQ_GC, 8);
 #undef LQ_GC
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  ColReq out[2];
-  int n = 0;
+  *join = ColJoin{{req[0], req[1]}, 0, rows};
   for (int i = 0; i < 2; ++i)
-    if (req[i].out) out[n++] = req[i];
-  return n ? launch_adapter_col_reduce(out, n, rows, rt, s) : hipSuccess;
+    if (req[i].out) join->q[join->n++] = req[i];
+  return hipGetLastError();
 }
 #undef LQ_ACTS
 

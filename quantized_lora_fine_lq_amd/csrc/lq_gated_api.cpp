@@ -146,11 +146,11 @@ int lq_gated_forward(const lq_gated* p, const uint16_t* X, int64_t M, const int3
   const Forward w(cv, o, M);
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
 
-  hipError_t e = hipSuccess;
-  for (int i = 0; i < 2 && e == hipSuccess; ++i)
-    e = launch_adapter_prep(ids, M, i == 0 && !route ? w.route : nullptr, o.q[i], w.wd[i], 0, o.v[i], nullptr, nullptr,
-                            w.bp[i], i == 0 ? w.zeros : nullptr, s);
-  if (e != hipSuccess) return LQ_ERR_LAUNCH;
+  Prep prep[2];
+  for (int i = 0; i < 2; ++i)
+    prep[i] = Prep{i == 0 && !route ? w.route : nullptr, o.q[i], w.wd[i], 0, o.v[i], nullptr, nullptr, w.bp[i],
+                   i == 0 ? w.zeros : nullptr};
+  if (launch_adapter_prep(ids, M, prep, 2, s) != hipSuccess) return LQ_ERR_LAUNCH;
   const Route rt = route_view(route ? route : w.route, M, o.v[0].n);
   if (o.sets) {
     float* const save[2] = {t_gate, t_up};
@@ -216,51 +216,57 @@ int lq_gated_backward(const lq_gated* p, const uint16_t* X, const uint16_t* G, i
 
   const int64_t Np = ldb_of(o.N), ldb = 2 * Np;
   const bool need_u = o.sets && (grad_X || any_dA);
-  for (int i = 0; i < 2; ++i) {
-    const bool nf4 = o.q[i].format == LQ_FMT_NF4;
-    uint16_t* wt = w.wt + i * Np;
-    hipError_t e = launch_adapter_prep(ids, M, i == 0 && !route ? w.route : nullptr, o.q[i],
-                                       !grad_X ? nullptr : nf4 ? wt : w.wd[i], nf4 ? ldb : 0, o.v[i],
-                                       o.sets && grad_X ? w.at[i] : nullptr, need_u ? w.bt[i] : nullptr, nullptr,
-                                       i == 0 ? w.zeros : nullptr, s);
-    if (e == hipSuccess && grad_X && !nf4) e = launch_transpose_weight(w.wd[i], o.N, o.K, ldb, wt, s);
-    if (e != hipSuccess) return LQ_ERR_LAUNCH;
+  Prep prep[2];
+  uint16_t* const wt[2] = {w.wt, w.wt + Np};
+  const bool nf4[2] = {o.q[0].format == LQ_FMT_NF4, o.q[1].format == LQ_FMT_NF4};
+  for (int i = 0; i < 2; ++i)
+    prep[i] = Prep{i == 0 && !route ? w.route : nullptr, o.q[i], !grad_X ? nullptr : nf4[i] ? wt[i] : w.wd[i], nf4[i] ? ldb : 0,
+                   o.v[i], o.sets && grad_X ? w.at[i] : nullptr, need_u ? w.bt[i] : nullptr, nullptr,
+                   i == 0 ? w.zeros : nullptr};
+  if (launch_adapter_prep(ids, M, prep, 2, s) != hipSuccess) return LQ_ERR_LAUNCH;
+  if (grad_X && (!nf4[0] || !nf4[1])) {   // codebook weights: transposed from the decoded ones
+    const int i = nf4[0] ? 1 : 0;
+    const bool both = !nf4[0] && !nf4[1];
+    if (launch_transpose_weight(w.wd[i], o.N, o.K, ldb, wt[i], both ? w.wd[1] : nullptr, wt[1], s) != hipSuccess)
+      return LQ_ERR_LAUNCH;
   }
   const Route rt = route_view(route ? route : w.route, M, o.v[0].n);
   const GatedGrad gr{G, g, u, o.N, o.act};
-  if (any_dB) {
-    DownJob jobs[2];
-    int n = 0;
-    for (int i = 0; i < 2; ++i)
-      if (dB[i])
-        jobs[n++] = DownJob{t_saved[i] ? nullptr : X, o.K, nullptr, t_saved[i], w.t[i], nullptr, w.down_t[i],
-                            t_saved[i] ? DropView{} : drop[i], t_saved[i] ? 1.0f : factor[i], o.v[i], 1};
-    if (launch_adapter_down(jobs, n, M, rt, w.zeros, s) != hipSuccess) return LQ_ERR_LAUNCH;
-  }
+  // t formed from X in launches of its own; given t and the partial sums of u become terms in one
+  DownJob down[2], join[kDownJobs];
+  int ndown = 0, njoin = 0;
+  for (int i = 0; i < 2; ++i)
+    if (dB[i]) {
+      DownJob& job = t_saved[i] ? join[njoin++] : down[ndown++];
+      job = DownJob{t_saved[i] ? nullptr : X, o.K, nullptr, t_saved[i], w.t[i], nullptr, w.down_t[i],
+                    t_saved[i] ? DropView{} : drop[i], t_saved[i] ? 1.0f : factor[i], o.v[i], 1};
+    }
+  if (ndown && launch_adapter_down(down, ndown, M, rt, w.zeros, s) != hipSuccess) return LQ_ERR_LAUNCH;
   if (grad_X || need_u) {
     if (launch_gated_down(gr, M, o.v, {w.bt[0], w.bt[1]}, {w.down_u[0], w.down_u[1]}, grad_X ? w.D : nullptr, rt, s) !=
         hipSuccess)
       return LQ_ERR_LAUNCH;
   }
-  if (need_u) {
-    DownJob jobs[2];
+  if (need_u)
     for (int i = 0; i < 2; ++i)
-      jobs[i] = DownJob{G, o.N, nullptr, nullptr, w.u[i], nullptr, w.down_u[i], DropView{}, factor[i], o.v[i],
-                        gated_down_shares(M, o.N)};
-    if (launch_adapter_join(jobs, 2, M, rt, s) != hipSuccess) return LQ_ERR_LAUNCH;
-  }
+      join[njoin++] = DownJob{G, o.N, nullptr, nullptr, w.u[i], nullptr, w.down_u[i], DropView{}, factor[i], o.v[i],
+                              gated_down_shares(M, o.N)};
+  if (njoin && launch_adapter_join(join, njoin, M, rt, s) != hipSuccess) return LQ_ERR_LAUNCH;
+  ColJoin sums[2];
+  int nsums = 0;
   if (any_dB) {
     const ColReq req[2] = {ColReq{w.t[0], nullptr, o.N, dB_gate, 1, w.part_b[0], DropView{}, o.v[0]},
                            ColReq{w.t[1], nullptr, o.N, dB_up, 1, w.part_b[1], DropView{}, o.v[1]}};
-    if (launch_gated_col(gr, req, M, rt, s) != hipSuccess) return LQ_ERR_LAUNCH;
+    if (launch_gated_col(gr, req, M, rt, &sums[nsums++], s) != hipSuccess) return LQ_ERR_LAUNCH;
   }
   if (any_dA) {
     ColReq req[2];
     int n = 0;
     for (int i = 0; i < 2; ++i)
       if (dA[i]) req[n++] = ColReq{w.u[i], X, o.K, dA[i], 0, w.part_a[i], drop[i], o.v[i]};
-    if (launch_adapter_col(req, n, M, rt, s) != hipSuccess) return LQ_ERR_LAUNCH;
+    if (launch_adapter_col(req, n, M, rt, &sums[nsums++], s) != hipSuccess) return LQ_ERR_LAUNCH;
   }
+  if (nsums && launch_adapter_col_reduce(sums, nsums, rt, s) != hipSuccess) return LQ_ERR_LAUNCH;
   if (!grad_X) return LQ_OK;
   AdapterGemm gm{};
   gm.A = w.D;
