@@ -507,6 +507,10 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJobs jobs, int64_t 
 // 34 MB of X (7 us at the rate of a large copy); 1999 tokens of rank 8 to 64:
 // 8.6 + 5.
 // ===========================================================================
+//
+// DROP: the generator's rounds (two blocks a lane and step) cost more issue than
+// a step's products, so three buffers, whose three workgroups per CU fill each
+// other's gaps, and shares of each job's own columns.
 constexpr int DT_M = 64, DT_K = 64, DT_RING = 4;
 
 __device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
@@ -516,15 +520,16 @@ __device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
 
 template <int BN, bool DROP>
 __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJobs jobs, int64_t M, Route rt, const uint16_t* zeros) {
-  constexpr int CT = BN / 16, QW = BN >= 32 ? BN / 32 : 1;
+  constexpr int CT = BN / 16, QW = BN >= 32 ? BN / 32 : 1, RING = DROP ? 3 : DT_RING;
   struct __attribute__((aligned(16))) Lds {
-    uint16_t x[DT_RING][DT_M * DT_K];
-    uint16_t w[DT_RING][(BN < 32 ? 32 : BN) * DT_K];
+    uint16_t x[RING][DT_M * DT_K];
+    uint16_t w[RING][(BN < 32 ? 32 : BN) * DT_K];
   };
   __shared__ Lds lds;
   const DownJob jb = jobs.j[blockIdx.z];
   const AdapterView& v = jb.v;
-  if (!jb.Q) return;
+  const int shares = DROP ? jb.shares : (int)gridDim.y;
+  if (!jb.Q || (DROP && (int)blockIdx.y >= shares)) return;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
   Item it;
@@ -533,7 +538,7 @@ __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJobs jobs, int64
   const int r = min(ad.r, BN);
   const int64_t C = jb.C;
   const uint16_t* R = jb.rbase ? jb.rbase + C * ad.row8 : ad.A;
-  const int all = (int)((C + DT_K - 1) / DT_K), per = (all + gridDim.y - 1) / gridDim.y;
+  const int all = (int)((C + DT_K - 1) / DT_K), per = (all + shares - 1) / shares;
   const int s0 = min(all, (int)blockIdx.y * per), s1 = min(all, s0 + per);
   // a load instruction of a wave fills 8 rows of 128 bytes: lane l row l / 8,
   // slot l % 8 with chunk slot ^ (row % 8)
@@ -545,7 +550,7 @@ __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJobs jobs, int64
 #pragma unroll
   for (int q = 0; q < QW; ++q) pw[q] = R + (int64_t)min((wave * QW + q) * 8 + sub, r - 1) * C + 8 * ch;
   auto load = [&](int s) {   // step s into its buffer; past the end zeros (the count of outstanding loads stays)
-    const int buf = (s - s0) % DT_RING;
+    const int buf = (s - s0) % RING;
     const int64_t k0 = (int64_t)s * DT_K;
     const bool ok = s < s1 && k0 + 8 * ch + 8 <= C;
 #pragma unroll
@@ -557,7 +562,7 @@ __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJobs jobs, int64
 #pragma unroll
   for (int c = 0; c < CT; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < DT_RING - 1; ++k) load(s0 + k);
+  for (int k = 0; k < RING - 1; ++k) load(s0 + k);
   const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
   const bool drops = DROP && jb.drop.T;
   DropGen gen{};
@@ -572,9 +577,9 @@ __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJobs jobs, int64
 #pragma unroll
       for (int u = 0; u < 2; ++u) bits[u] = drop_bits(gen, (uint64_t)(block + 8 * (int64_t)s + 4 * u));
     // this wave's share of step s is there and its reads of s - 1 are done; then everyone's
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((DT_RING - 2) * (2 + QW)) : "memory");
-    load(s + DT_RING - 1);
-    const int buf = (s - s0) % DT_RING;
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((RING - 2) * (2 + QW)) : "memory");
+    load(s + RING - 1);
+    const int buf = (s - s0) % RING;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       u32x4_t a = ld16(lds.x[buf] + (16 * wave + li) * DT_K + slot[u]);
@@ -626,6 +631,24 @@ __global__ __launch_bounds__(256) void k_adapter_down_join(DownJobs jobs, int64_
 // The tiled form pays once the tokens fill it: at 2048 tokens of rank 16 the
 // two took 10.5 us alike, at 4096 tokens of rank 64 45 against 23 us.
 bool down_tiled(int64_t M, int32_t rs) { return M * rs >= 65536; }
+
+// DROP: shares of each job's columns, of about `len` steps each, len chosen for the
+// shortest queue where three workgroups run on a CU, a share costing about three
+// steps more.
+constexpr int kDropShares = 16;
+void drop_shares(int64_t M, const int64_t* steps, int n, int* shares) {
+  const int64_t tiles = (M + DT_M - 1) / DT_M;
+  int64_t most = 1, best = INT64_MAX;
+  for (int i = 0; i < n; ++i) most = std::max(most, steps[i]);
+  for (int64_t len = (most + kDropShares - 1) / kDropShares; len <= most; ++len) {
+    int64_t all = 0;
+    for (int i = 0; i < n; ++i) all += (steps[i] + len - 1) / len;
+    const int64_t cost = (tiles * all + 767) / 768 * (len + 3);
+    if (cost >= best) continue;
+    best = cost;
+    for (int i = 0; i < n; ++i) shares[i] = (int)std::max<int64_t>(1, (steps[i] + len - 1) / len);
+  }
+}
 
 // Shares of the columns: two workgroups per CU, at least 8 steps each.
 int down_shares(int64_t M, int64_t C) {
@@ -775,13 +798,17 @@ __global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0,
 // Joins the runs of adapters with more than one, in order, and writes the zero
 // gradients of adapters without tokens. 7 us at 2048 tokens of rank 16, 16 at
 // 4096 of rank 64 (four partial sums a thread at a time).
+//
+// A transposed output's rows (a column's r sums) are put together in LDS, 64
+// columns a workgroup: written from registers, 16 bytes here and there, they
+// took twice as long.
 struct ColJoins {
   ColJoin j[2];
 };
 __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColJoins joins, Route rt) {
+  extern __shared__ float reduce_tile[];   // [64][r_max rounded up to 4, and 1]
   const ColJoin& jn = joins.j[blockIdx.z];
-  const ColReq &q0 = jn.q[0], &q1 = jn.q[1];
-  const int nreq = jn.n, rows = jn.rows;
+  const int rows = jn.rows;
   const int a = blockIdx.y, lane = threadIdx.x & 63;
   int before = 0;   // slots of the adapters before a
   for (int b = lane; b < a; b += 64) {
@@ -792,35 +819,43 @@ __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColJoins joins, Rout
   for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
   const int runs = (rt.off[a + 1] - rt.off[a] + rows - 1) / rows;
   if (runs == 1) return;
-  // four values a thread: of one row (C % 8 == 0), or of four rows where the
-  // output is transposed (then consecutive threads still read consecutive columns)
-  auto count = [&](const ColReq& q) {
-    const int r = q.v.tab[a].r;
-    return q.transposed ? (r + 3) / 4 * q.C : r * q.C / 4;
+  // workgroups' shares: 64 columns of a transposed output, 1024 values of another (C % 8 == 0)
+  auto units = [&](const ColReq& q) {
+    return q.transposed ? (q.C + 63) / 64 : (q.v.tab[a].r * q.C / 4 + 255) / 256;
   };
-  const int64_t n0 = count(q0), n1 = nreq > 1 ? count(q1) : 0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n0 + n1; i += (int64_t)gridDim.x * 256) {
-    const ColReq& q = i < n0 ? q0 : q1;
+  const int64_t n0 = units(jn.q[0]), n1 = jn.n > 1 ? units(jn.q[1]) : 0;
+  for (int64_t unit = blockIdx.x; unit < n0 + n1; unit += gridDim.x) {
+    const ColReq& q = jn.q[unit < n0 ? 0 : 1];
+    const int64_t t = unit < n0 ? unit : unit - n0;
     const lq_adapter ad = q.v.tab[a];
-    const int64_t e = i < n0 ? i : i - n0;
+    const int64_t C = q.C;
     if (q.transposed) {
-      const int64_t c = e % q.C;
-      const int j = 4 * (int)(e / q.C);
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int k = 0; k < runs; ++k) {
-        const float* p = q.part + ((int64_t)(before + k) * q.v.rs + j) * q.C + c;   // rs rows: a multiple of 8
+      const int r = ad.r, pitch = ((r + 3) & ~3) + 1, c = threadIdx.x & 63;
+      const int64_t c0 = 64 * t;
+      const int cols = (int)min((int64_t)64, C - c0);
+      for (int j = 4 * (threadIdx.x >> 6); j < r; j += 16) {   // four rows a thread (rs, a multiple of 8, are there)
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (c < cols)
+          for (int k = 0; k < runs; ++k) {
+            const float* p = q.part + ((int64_t)(before + k) * q.v.rs + j) * C + c0 + c;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) sum[u] += p[u * q.C];
+            for (int u = 0; u < 4; ++u) sum[u] += p[u * C];
+          }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) reduce_tile[c * pitch + j + u] = sum[u];
       }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (j + u < ad.r) q.out[q.C * ad.row + c * ad.r + j + u] = sum[u];
+      __syncthreads();
+      float* o = q.out + C * ad.row + c0 * r;
+      for (int i = threadIdx.x; i < cols * r; i += 256) o[i] = reduce_tile[i / r * pitch + i % r];
+      __syncthreads();
     } else {
-      const int64_t j = 4 * e / q.C, c = 4 * e % q.C;
+      const int64_t i = t * 256 + threadIdx.x;
+      if (i >= ad.r * C / 4) continue;
+      const int64_t j = 4 * i / C, c = 4 * i % C;
       f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int k = 0; k < runs; ++k)
-        sum += *reinterpret_cast<const f32x4_t*>(q.part + ((int64_t)(before + k) * q.v.rs + j) * q.C + c);
-      float* o = q.out + (q.C * (ad.row + j) + c);   // 4-byte aligned
+        sum += *reinterpret_cast<const f32x4_t*>(q.part + ((int64_t)(before + k) * q.v.rs + j) * C + c);
+      float* o = q.out + (C * (ad.row + j) + c);   // 4-byte aligned
 #pragma unroll
       for (int u = 0; u < 4; ++u) o[u] = sum[u];
     }
@@ -899,7 +934,8 @@ hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, const Prep* a, int
 }
 
 size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs) {
-  return down_tiled(M, rs) ? (size_t)down_shares(M, C) * M * rs : 0;
+  const int64_t steps = (C + DT_K - 1) / DT_K;   // (with dropout up to kDropShares)
+  return down_tiled(M, rs) ? (size_t)std::max<int64_t>(down_shares(M, C), std::min<int64_t>(kDropShares, steps)) * M * rs : 0;
 }
 
 hipError_t launch_adapter_join(const DownJob* jobs, int njobs, int64_t M, const Route& rt, hipStream_t s) {
@@ -943,8 +979,16 @@ hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const 
     int64_t C = 0;
     for (int i = 0; i < njobs; ++i)
       if (jobs[i].Q) C = C ? std::min(C, jobs[i].C) : jobs[i].C;   // all jobs' workspaces hold these shares
-    const int shares = C ? down_shares(M, C) : 1;
+    int shares = C ? down_shares(M, C) : 1;
     for (int i = 0; i < njobs; ++i) all.j[i].shares = shares;
+    if (C && drops) {
+      int64_t steps[kDownJobs];
+      int own[kDownJobs];
+      for (int i = 0; i < njobs; ++i) steps[i] = jobs[i].Q ? (jobs[i].C + DT_K - 1) / DT_K : 0;
+      drop_shares(M, steps, njobs, own);
+      shares = 1;
+      for (int i = 0; i < njobs; ++i) shares = std::max(shares, all.j[i].shares = own[i]);
+    }
     if (C) {
       const dim3 grid((unsigned)((M + DT_M - 1) / DT_M + std::min<int64_t>(n, M)), (unsigned)shares, (unsigned)njobs);
 #define LQ_AT(BN)                                                                                      \
@@ -1011,13 +1055,20 @@ hipError_t launch_adapter_col_reduce(const ColJoin* joins, int n, const Route& r
   if (n < 1 || n > 2) return hipErrorInvalidValue;
   ColJoins all{};
   int64_t most = 0;
+  int32_t r = 0;
   for (int i = 0; i < n; ++i) {
     const ColJoin& j = all.j[i] = joins[i];
-    most = std::max(most, j.q[0].v.r_max * j.q[0].C + (j.n > 1 ? j.q[1].v.r_max * j.q[1].C : 0));
+    int64_t units = 0;
+    for (int k = 0; k < j.n; ++k) {
+      units += j.q[k].transposed ? (j.q[k].C + 63) / 64 : (j.q[k].v.r_max * j.q[k].C / 4 + 255) / 256;
+      r = std::max(r, j.q[k].v.r_max);
+    }
+    most = std::max(most, units);
   }
   const int32_t sets = joins[0].q[0].v.n;
-  const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 255) / 256, std::max(32, 4096 / sets)));
-  hipLaunchKernelGGL(k_adapter_col_reduce, dim3(gx, (unsigned)sets, (unsigned)n), dim3(256), 0, s, all, rt);
+  const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, std::max(32, 4096 / sets)));
+  const size_t lds = (size_t)64 * (((r + 3) & ~3) + 1) * sizeof(float);
+  hipLaunchKernelGGL(k_adapter_col_reduce, dim3(gx, (unsigned)sets, (unsigned)n), dim3(256), lds, s, all, rt);
   return hipGetLastError();
 }
 

@@ -83,7 +83,7 @@ struct GatedDown {
 };
 
 template <int JT, int ACT>
-__global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Route rt) {
+__global__ __launch_bounds__(256, JT <= 4 ? 2 : 1) void k_gated_down(GatedDown p, int64_t M, Route rt) {
   constexpr int ROWS = 16 * JT;
   __shared__ __attribute__((aligned(16))) uint16_t sW[2][2][ROWS * GD_K];   // [buffer][side]
   Item it;
@@ -123,7 +123,6 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
       q.G[h] = ld16(pG + o);
       q.g[h] = ld16(pg + o);
       q.u[h] = ld16(pu + o);
-      if (!ok) q.G[h] = q.g[h] = q.u[h] = u32x4_t{0u, 0u, 0u, 0u};
     }
   };
   auto load_w = [&](int s) __attribute__((always_inline)) {
@@ -134,7 +133,6 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
       const int i = threadIdx.x + 256 * k, sd = i / (8 * ROWS), j = (i >> 3) % ROWS;
       const int64_t c = GD_K * (int64_t)s + 8 * (i & 7);
       w[k] = ld16((sd ? bt[1] : bt[0]) + min(j, (sd ? r[1] : r[0]) - 1) * N + (c < N ? c : 0));
-      if (c >= N) w[k] = u32x4_t{0u, 0u, 0u, 0u};
     }
   };
   f32x4_t acc[2][JT];
@@ -145,10 +143,15 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
   const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
   auto step = [&](int s, Q& q) __attribute__((always_inline)) {
     uint16_t(*buf)[ROWS * GD_K] = sW[(s - s0) & 1];
+    // Past the last column both operands are zero: set here, not where they are
+    // loaded, which would wait for the loads.
+    const bool tail = GD_K * (int64_t)(s + 1) > N;
+    const u32x4_t none = {0u, 0u, 0u, 0u};
     if (has) {
 #pragma unroll
       for (int k = 0; k < JT; ++k) {
         const int i = threadIdx.x + 256 * k, sd = i / (8 * ROWS), j = (i >> 3) % ROWS;
+        if (tail && GD_K * (int64_t)s + 8 * (i & 7) >= N) w[k] = none;
         *reinterpret_cast<u32x4_t*>(buf[sd] + j * GD_K + 8 * ((i & 7) ^ (j & 7))) = w[k];
       }
     }
@@ -158,6 +161,7 @@ __global__ __launch_bounds__(256) void k_gated_down(GatedDown p, int64_t M, Rout
     load_w(s + 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      if (tail && GD_K * (int64_t)s + 32 * h + 8 * lg >= N) q.G[h] = q.g[h] = q.u[h] = none;
       float d[2][8];
       gate_grads<ACT>(q.G[h], q.g[h], q.u[h], d[0], d[1]);
       u32x4_t t[2][3];
