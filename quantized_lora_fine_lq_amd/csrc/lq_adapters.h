@@ -159,8 +159,8 @@ struct GatedGrad {
 // u_g = B_g^T dg and u_u = B_u^T du as partial sums [shares][M][rs] of each side
 // (bt: B^T [r, N] at N * row8_a; v.n == 0: of neither), and dg, du in bfloat16 as
 // D [M, 2 Np], Np = N rounded up to a multiple of 64, zero between (null: not wanted).
-size_t gated_down_ws_floats(int64_t M, int64_t N, int32_t rs);
-int gated_down_shares(int64_t M, int64_t N);
+size_t gated_down_ws_floats(int64_t M, int64_t N, const AdapterView& v);
+int gated_down_shares(int64_t M, int64_t N, int32_t n);
 hipError_t launch_gated_down(const GatedGrad& gr, int64_t M, const AdapterView (&v)[2], const uint16_t* const (&bt)[2],
                              float* const (&part)[2], uint16_t* D, const Route& rt, hipStream_t s);
 // dB of both sides: requests as launch_adapter_col's (transposed), Q in place of

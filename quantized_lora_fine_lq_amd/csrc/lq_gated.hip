@@ -68,8 +68,9 @@ __device__ __forceinline__ void split_grads(float (&d)[2][8], u32x4_t (&t)[2][3]
 // Row form: 64 routed tokens of one adapter (or of none: D alone) per workgroup
 // and share of the columns, 16 a wave, in steps of 64 columns. A lane forms dg
 // and du of 8 columns of a token in registers, which is the matrix product's
-// operand; G, g and u are loaded two steps ahead, B^T's rows one, through LDS,
-// double buffered.
+// operand; as soon as a half step's G, g and u are used, the next step's are
+// asked for into the same registers. B^T's rows pass through LDS, double
+// buffered, loaded a step ahead.
 // ===========================================================================
 constexpr int GD_M = 64, GD_K = 64;
 
@@ -83,9 +84,9 @@ struct GatedDown {
 };
 
 template <int JT, int ACT>
-__global__ __launch_bounds__(256, JT <= 4 ? 2 : 1) void k_gated_down(GatedDown p, int64_t M, Route rt) {
-  constexpr int ROWS = 16 * JT;
-  __shared__ __attribute__((aligned(16))) uint16_t sW[2][2][ROWS * GD_K];   // [buffer][side]
+__global__ __launch_bounds__(256, JT <= 4 ? 3 : 2) void k_gated_down(GatedDown p, int64_t M, Route rt) {
+  constexpr int ROWS = 16 * JT, PW = JT;                                  // 16-byte pieces of both sides' B^T per thread
+  __shared__ __attribute__((aligned(16))) uint16_t sW[2][2][ROWS * GD_K];       // [buffer][side]
   Item it;
   if (!find_item(rt.off, p.v[0].n + 1, GD_M, (int)blockIdx.x, it)) return;
   const bool has = it.seg < p.v[0].n;
@@ -108,28 +109,18 @@ __global__ __launch_bounds__(256, JT <= 4 ? 2 : 1) void k_gated_down(GatedDown p
   const bool live = row < it.count;
   const int64_t token = rt.perm[it.start + min(row, it.count - 1)];
   const uint16_t *pG = p.gr.G + token * N, *pg = p.gr.g + token * N, *pu = p.gr.u + token * N;
-  struct Q {
-    u32x4_t G[2], g[2], u[2];
+  u32x4_t qG[2], qg[2], qu[2], w[PW];
+  auto load = [&](int s, int h) __attribute__((always_inline)) {
+    const int64_t c = GD_K * (int64_t)s + 32 * h + 8 * lg, o = c < N ? c : 0;   // N % 8 == 0
+    qG[h] = ld16(pG + o);
+    qg[h] = ld16(pg + o);
+    qu[h] = ld16(pu + o);
   };
-  Q q0, q1;
-  u32x4_t w[JT];
-  auto load = [&](int s, Q& q) __attribute__((always_inline)) {   // (past the share's end its last step again)
-    s = min(s, s1 - 1);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t c = GD_K * (int64_t)s + 32 * h + 8 * lg;
-      const bool ok = c < N;   // N % 8 == 0
-      const int64_t o = ok ? c : 0;
-      q.G[h] = ld16(pG + o);
-      q.g[h] = ld16(pg + o);
-      q.u[h] = ld16(pu + o);
-    }
-  };
+  // piece i: side, row and chunk of 8 columns
   auto load_w = [&](int s) __attribute__((always_inline)) {
     if (!has) return;
-    s = min(s, s1 - 1);
 #pragma unroll
-    for (int k = 0; k < JT; ++k) {
+    for (int k = 0; k < PW; ++k) {
       const int i = threadIdx.x + 256 * k, sd = i / (8 * ROWS), j = (i >> 3) % ROWS;
       const int64_t c = GD_K * (int64_t)s + 8 * (i & 7);
       w[k] = ld16((sd ? bt[1] : bt[0]) + min(j, (sd ? r[1] : r[0]) - 1) * N + (c < N ? c : 0));
@@ -141,29 +132,36 @@ __global__ __launch_bounds__(256, JT <= 4 ? 2 : 1) void k_gated_down(GatedDown p
 #pragma unroll
     for (int c = 0; c < JT; ++c) acc[sd][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int slot[2] = {8 * (lg ^ (li & 7)), 8 * ((4 + lg) ^ (li & 7))};
-  auto step = [&](int s, Q& q) __attribute__((always_inline)) {
+  if (s0 < s1) {
+    load(s0, 0);
+    load(s0, 1);
+    load_w(s0);
+  }
+  for (int s = s0; s < s1; ++s) {
     uint16_t(*buf)[ROWS * GD_K] = sW[(s - s0) & 1];
+    const int next = min(s + 1, s1 - 1);
     // Past the last column both operands are zero: set here, not where they are
     // loaded, which would wait for the loads.
     const bool tail = GD_K * (int64_t)(s + 1) > N;
     const u32x4_t none = {0u, 0u, 0u, 0u};
     if (has) {
 #pragma unroll
-      for (int k = 0; k < JT; ++k) {
+      for (int k = 0; k < PW; ++k) {
         const int i = threadIdx.x + 256 * k, sd = i / (8 * ROWS), j = (i >> 3) % ROWS;
         if (tail && GD_K * (int64_t)s + 8 * (i & 7) >= N) w[k] = none;
         *reinterpret_cast<u32x4_t*>(buf[sd] + j * GD_K + 8 * ((i & 7) ^ (j & 7))) = w[k];
       }
+      // (one barrier a step: the buffer written at step s + 1 was read at s - 1, and
+      // those reads are done before a wave reaches step s's barrier)
+      lds_barrier();
     }
-    // (one barrier a step: the buffer written at step s + 1 was read at s - 1, and
-    // those reads are done before a wave reaches step s's barrier)
-    if (has) lds_barrier();
-    load_w(s + 1);
+    load_w(next);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (tail && GD_K * (int64_t)s + 32 * h + 8 * lg >= N) q.G[h] = q.g[h] = q.u[h] = none;
+      if (tail && GD_K * (int64_t)s + 32 * h + 8 * lg >= N) qG[h] = qg[h] = qu[h] = none;
       float d[2][8];
-      gate_grads<ACT>(q.G[h], q.g[h], q.u[h], d[0], d[1]);
+      gate_grads<ACT>(qG[h], qg[h], qu[h], d[0], d[1]);
+      load(next, h);
       u32x4_t t[2][3];
       split_grads(d, t);
       if (p.D && live) {
@@ -184,18 +182,6 @@ __global__ __launch_bounds__(256, JT <= 4 ? 2 : 1) void k_gated_down(GatedDown p
             acc[sd][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(t[sd][k]), as_bf16x8(b[c]), acc[sd][c], 0, 0, 0);
       }
     }
-    load(s + 2, q);
-  };
-  if (s0 < s1) {
-    load(s0, q0);
-    load_w(s0);
-    load(s0 + 1, q1);
-    int s = s0;
-    for (; s + 1 < s1; s += 2) {
-      step(s, q0);
-      step(s + 1, q1);
-    }
-    if (s < s1) step(s, q0);
   }
   if (!has) return;
   // lane: tokens 16 wave + 4 lg + e, row 16 c + li of the adapter
@@ -255,37 +241,53 @@ __global__ __launch_bounds__(GC_THREADS, JT <= 4 ? 4 : 2) void k_gated_col(Gated
   u32x4_t xG, xg, xu, xp[PQ];
   int tok;
   auto tokens = [&](int mb) { tok = rt.perm[it.start + min(mb + qr, it.count - 1)]; };
+  // piece k of t: (side and term) of a token row and 8 of its columns, at `from` in
+  // the run's first 32 rows, to `to` in LDS (both sides' tiles in one array)
+  const uint16_t* from[PQ];
+  int prow[PQ], to[PQ];
+  bool pin[PQ];
+#pragma unroll
+  for (int k = 0; k < PQ; ++k) {
+    const int i = threadIdx.x + GC_THREADS * k, c8 = i % (2 * JT), t = min(i / (64 * JT), 5);
+    const bool up = t >= 3;
+    const int term = up ? t - 3 : t, r8 = up ? r81 : r80;
+    prow[k] = (i / (2 * JT)) % 32;
+    pin[k] = 8 * c8 < r8;
+    from[k] = (up ? r1.terms : r0.terms) + (int64_t)(it.start + min(prow[k], it.count - 1)) * 3 * (up ? r1.v.rs : r0.v.rs) +
+              (pin[k] ? term * r8 + 8 * c8 : 0);
+    to[k] = i < 384 * JT ? (32 * t + prow[k]) * PP + 8 * c8 : -1;
+  }
   auto load = [&](int mb) {
     const int64_t o = (int64_t)tok * N + (qin ? c0 + qc : 0);
     xG = ld16(gr.G + o);
     xg = ld16(gr.g + o);
     xu = ld16(gr.u + o);
 #pragma unroll
-    for (int k = 0; k < PQ; ++k) {
-      const int i = threadIdx.x + GC_THREADS * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, t = min(i / (64 * JT), 5);
-      const bool up = t >= 3;
-      const int term = up ? t - 3 : t, r8 = up ? r81 : r80;
-      xp[k] = ld16((up ? r1.terms : r0.terms) + (int64_t)(it.start + min(mb + row, it.count - 1)) * 3 * (up ? r1.v.rs : r0.v.rs) +
-                   (8 * c8 < r8 ? term * r8 + 8 * c8 : 0));
+    for (int k = 0; k < PQ; ++k) {   // (past the run its first rows again)
+      const int64_t step = (int64_t)mb * 3 * ((threadIdx.x + GC_THREADS * k) / (192 * JT) ? r1.v.rs : r0.v.rs);
+      xp[k] = ld16(from[k] + (mb + prow[k] < it.count ? step : 0));
     }
   };
   auto store = [&](int mb) {
     const u32x4_t none = {0u, 0u, 0u, 0u};
-    const bool in = qin && mb + qr < it.count;   // others are zero: no neighbour's infinity enters
+    const bool whole = mb + 32 <= it.count && c0 + GC_COLS <= N;   // others are zero past the run and the last column
     float d[2][8];
     gate_grads<ACT>(xG, xg, xu, d[0], d[1]);
     u32x4_t t3[2][3];
     split_grads(d, t3);
+    if (!whole && !(qin && mb + qr < it.count))   // no neighbour's infinity enters
+#pragma unroll
+      for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) t3[sd][k] = none;
 #pragma unroll
     for (int sd = 0; sd < 2; ++sd)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t*>(sQ[sd][k] + qr * GC_COLS + (qc ^ (16 * (qr & 3)))) = in ? t3[sd][k] : none;
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4_t*>(sQ[sd][k] + qr * GC_COLS + (qc ^ (16 * (qr & 3)))) = t3[sd][k];
 #pragma unroll
     for (int k = 0; k < PQ; ++k) {
-      const int i = threadIdx.x + GC_THREADS * k, c8 = i % (2 * JT), row = (i / (2 * JT)) % 32, t = i / (64 * JT);
-      if (t < 6)
-        *reinterpret_cast<u32x4_t*>(sP[t >= 3] + (32 * (t >= 3 ? t - 3 : t) + row) * PP + 8 * c8) =
-            mb + row < it.count && 8 * c8 < (t >= 3 ? r81 : r80) ? xp[k] : none;
+      if (!pin[k] || mb + prow[k] >= it.count) xp[k] = none;
+      if (to[k] >= 0) *reinterpret_cast<u32x4_t*>(&sP[0][0] + to[k]) = xp[k];
     }
   };
   f32x4_t acc[JT][2];
@@ -356,13 +358,14 @@ int gated_col_rows(int64_t M, int64_t N) {
 }  // namespace
 
 // Shares of the columns: what leaves the shortest queue of 64-column steps where
-// two workgroups run on each CU, a share costing about two steps more.
-int gated_down_shares(int64_t M, int64_t N) {
-  const int64_t tiles = (M + GD_M - 1) / GD_M, steps = (N + GD_K - 1) / GD_K;
+// three workgroups run on each CU, a share costing about two steps more. n: one
+// more tile for each adapter's remainder.
+int gated_down_shares(int64_t M, int64_t N, int32_t n) {
+  const int64_t tiles = (M + GD_M - 1) / GD_M, steps = (N + GD_K - 1) / GD_K, items = tiles + std::min<int64_t>(n, tiles);
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int s = 1; s <= 16 && s <= steps; ++s) {
-    const int64_t c = (tiles * s + 511) / 512 * ((steps + s - 1) / s + 2);
+    const int64_t c = (items * s + 767) / 768 * ((steps + s - 1) / s + 2);
     if (c < cost) {
       cost = c;
       best = s;
@@ -370,7 +373,7 @@ int gated_down_shares(int64_t M, int64_t N) {
   }
   return best;
 }
-size_t gated_down_ws_floats(int64_t M, int64_t N, int32_t rs) { return (size_t)gated_down_shares(M, N) * M * rs; }
+size_t gated_down_ws_floats(int64_t M, int64_t N, const AdapterView& v) { return (size_t)gated_down_shares(M, N, v.n) * M * v.rs; }
 
 #define LQ_ACTS(CALL, JT)                      \
   do {                                         \
@@ -383,8 +386,9 @@ hipError_t launch_gated_down(const GatedGrad& gr, int64_t M, const AdapterView (
                              float* const (&part)[2], uint16_t* D, const Route& rt, hipStream_t s) {
   LQ_DASSERT(gr.N % 8 == 0 && M > 0);
   const GatedDown p{gr, {v[0], v[1]}, {bt[0], bt[1]}, {part[0], part[1]}, D, (gr.N + 63) / 64 * 64};
-  const dim3 grid((unsigned)((M + GD_M - 1) / GD_M + std::min<int64_t>(v[0].n + 1, M)), (unsigned)gated_down_shares(M, gr.N));
   const int act = gr.act;
+  const dim3 grid((unsigned)((M + GD_M - 1) / GD_M + std::min<int64_t>(v[0].n + 1, M)),
+                  (unsigned)gated_down_shares(M, gr.N, v[0].n));
   const int32_t r = std::max(v[0].r_max, v[1].r_max);
 #define LQ_GD(JT, ACT) hipLaunchKernelGGL((k_gated_down<JT, ACT>), grid, dim3(256), 0, s, p, M, rt)
   if (r <= 16) LQ_ACTS(LQ_GD, 1);

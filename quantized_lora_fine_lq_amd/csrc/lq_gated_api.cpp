@@ -80,7 +80,7 @@ struct Backward {
       bt[i] = cv.take<uint16_t>(r8 * p.N);
       wd[i] = p.q[i].format == LQ_FMT_NF4 ? nullptr : cv.take<uint16_t>((size_t)p.N * p.K);
       down_t[i] = cv.take<float>(p.sets ? adapter_down_ws_floats(M, p.K, v.rs) : 0);
-      down_u[i] = cv.take<float>(gated_down_ws_floats(M, p.N, v.rs));
+      down_u[i] = cv.take<float>(gated_down_ws_floats(M, p.N, v));
       part_a[i] = cv.take<float>(adapter_col_ws_floats(M, p.K, v.rs));
       part_b[i] = cv.take<float>(adapter_col_ws_floats(M, p.N, v.rs));
     }
@@ -250,7 +250,7 @@ int lq_gated_backward(const lq_gated* p, const uint16_t* X, const uint16_t* G, i
   if (need_u)
     for (int i = 0; i < 2; ++i)
       join[njoin++] = DownJob{G, o.N, nullptr, nullptr, w.u[i], nullptr, w.down_u[i], DropView{}, factor[i], o.v[i],
-                              gated_down_shares(M, o.N)};
+                              gated_down_shares(M, o.N, o.v[i].n)};
   if (njoin && launch_adapter_join(join, njoin, M, rt, s) != hipSuccess) return LQ_ERR_LAUNCH;
   ColJoin sums[2];
   int nsums = 0;
