@@ -192,7 +192,7 @@ __device__ __forceinline__ void with_act(int act, const F& f) {
 // BN / 2 outputs wide. TWO and GATED also form the adapters' part apart.
 template <int BN, bool OUT_F32, bool BWD, bool DROP, int MODE>
 __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
-  constexpr bool BIG = BN == 256, GATED = MODE == GEMM_GATED, APART = DROP || MODE != GEMM_ONE;
+  constexpr bool BIG = BN == 256, GATED = MODE == GEMM_GATED, APART = DROP, PAIR = MODE != GEMM_ONE;
   constexpr int NT = GATED ? BN / 2 : BN;              // outputs per tile
   constexpr int WN = BIG ? 4 : 2, WM = 8 / WN;         // waves over weight rows, tokens
   constexpr int CT = BN / WN / 16, RT = GM / WM / 16;  // 16 x 16 tiles per wave
@@ -274,30 +274,64 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   // more: the count of outstanding loads, on which the waits rely, stays the
   // same.
   Adapter whole{0, 0, nullptr, 8, 1, 0, 0, 0, nullptr, 0};   // the tile's one adapter, if it has one
+  Adapter whole1 = whole;                                    // PAIR: side 1's
   typedef std::integral_constant<bool, true> Plain;
   typedef std::integral_constant<bool, false> Any;
+  // (The adapter's rows take the place of the base's pointers at its first step,
+  // for each part when it gets there: a step then adds to them, and multiplies no
+  // row by a pitch.)
   auto load_x = [&](auto plain, int it, int i, int buf) __attribute__((always_inline)) {
-    const bool base = plain.value || it < nk;
-    const int64_t k0 = base ? column(it) : 0;
-    const bool ok = plain.value || !BWD || k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (0 * NaN is not 0)
+    const uint16_t* src[QX];
+    if (plain.value || it < nk) {
+      const int64_t k0 = column(it);
+      const bool ok = plain.value || !BWD || k0 + 8 * ch + 8 <= p.Kc;   // past the contraction: zeros (0 * NaN is not 0)
 #pragma unroll
-    for (int q = 0; q < QX; ++q) {
-      const uint16_t* src = p.zeros;
-      if (base) src = ok ? px[i][q] + k0 : p.zeros;
-      else if (!APART) src = lora_x(whole, it - nk, i, q);
-      load_lds16(src, lds.x[buf] + xrow(i, q) * GK);
+      for (int q = 0; q < QX; ++q) src[q] = ok ? px[i][q] + k0 : p.zeros;
+    } else if constexpr (APART) {
+#pragma unroll
+      for (int q = 0; q < QX; ++q) src[q] = p.zeros;
+    } else {
+      const int from = PAIR && it >= nk + whole.steps ? nk + whole.steps : nk;
+      const bool second = from != nk;
+      if (it == from) {
+        const uint16_t* const terms = PAIR && second ? whole1.terms : whole.terms;
+        const int64_t pitch = PAIR && second ? whole1.pitch : whole.pitch;
+#pragma unroll
+        for (int q = 0; q < QX; ++q) px[i][q] = terms + min(m0 + xrow(i, q) + sub, p.M - 1) * pitch;
+      }
+      const int c = 8 * (it - from) + ch, live = PAIR && second ? whole1.live : whole.live;
+#pragma unroll
+      for (int q = 0; q < QX; ++q) src[q] = c < live ? px[i][q] + 8 * c : p.zeros;
     }
+#pragma unroll
+    for (int q = 0; q < QX; ++q) load_lds16(src[q], lds.x[buf] + xrow(i, q) * GK);
   };
   auto load_y = [&](auto plain, int it, int i, int buf) __attribute__((always_inline)) {
-    const bool base = plain.value || it < nk;
-    const int64_t k0 = base ? column(it) : 0;
+    const uint16_t* src[QY];
+    if (plain.value || it < nk) {
+      const int64_t k0 = column(it);
 #pragma unroll
-    for (int q = 0; q < QY; ++q) {
-      const uint16_t* src = p.zeros;
-      if (base) src = py[i][q] + k0;
-      else if (!APART) src = lora_y(whole, it - nk, i, q);
-      load_lds16(src, lds.y[buf] + yrow(i, q) * GK);
+      for (int q = 0; q < QY; ++q) src[q] = py[i][q] + k0;
+    } else if constexpr (APART) {
+#pragma unroll
+      for (int q = 0; q < QY; ++q) src[q] = p.zeros;
+    } else {
+      const int from = PAIR && it >= nk + whole.steps ? nk + whole.steps : nk;
+      const bool second = from != nk;
+      if (it == from) {
+        const uint16_t* const base = PAIR && second ? whole1.base : whole.base;
+        const int64_t stride = PAIR && second ? whole1.stride : whole.stride;
+#pragma unroll
+        for (int q = 0; q < QY; ++q) py[i][q] = base + wrow(i, q) * stride;
+      }
+      const int c = 8 * (it - from) + ch, live = PAIR && second ? whole1.live : whole.live;
+      const int run = c % (PAIR && second ? whole1.runs : whole.runs);
+      const bool in = c < live && (!GATED || second == (i == 1));   // GATED: the side's own weight rows
+#pragma unroll
+      for (int q = 0; q < QY; ++q) src[q] = in ? py[i][q] + 8 * run : p.zeros;
     }
+#pragma unroll
+    for (int q = 0; q < QY; ++q) load_lds16(src[q], lds.y[buf] + yrow(i, q) * GK);
   };
 
   f32x4_t acc[CT][RT];
@@ -329,8 +363,9 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
     barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto multiply = [&](int xi, int yi) __attribute__((always_inline)) {
+  auto multiply = [&](int xi, int yi, bool on) __attribute__((always_inline)) {
     __builtin_amdgcn_s_setprio(1);
+    if (on)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -352,30 +387,37 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
     whole = next;
     whole.steps = one ? next.steps : 0;
     whole.live = one ? next.live : 0;
+    if constexpr (PAIR) {
+      whole1 = adapter_at<TERMS>(p, 1, m0, mend);
+      whole1.steps = one ? whole1.steps : 0;
+      whole1.live = one ? whole1.live : 0;
+    }
   }
-  const int nsteps = nk + whole.steps;
+  const int nsteps = nk + whole.steps + (PAIR ? whole1.steps : 0);
   int it = 0, buf = 0;
   auto step = [&](auto plain) __attribute__((always_inline)) {
+    // GATED, a side's adapter: its own weight rows alone (a zero against an infinite t is NaN)
+    const bool gate = plain.value || !GATED || it < nk + whole.steps, up = plain.value || !GATED || it < nk || !gate;
     if constexpr (BIG) {
       read_x(0, buf);
       read_y(0, buf);
       load_x(plain, it + 1, 1, buf ^ 1);
       wait_vm<10>();          // Y1 of this step
       end_memory();
-      multiply(0, 0);
+      multiply(0, 0, gate);
       read_y(1, buf);
       load_x(plain, it + 2, 0, buf);
       wait_vm<10>();          // X1 of this step
       end_memory();
-      multiply(0, 1);
+      multiply(0, 1, up);
       read_x(1, buf);
       load_y(plain, it + 2, 0, buf);
       end_memory();
-      multiply(1, 1);
+      multiply(1, 1, up);
       load_y(plain, it + 2, 1, buf);
       wait_vm<10>();          // X0 and Y0 of the next step
       end_memory();
-      multiply(1, 0);
+      multiply(1, 0, gate);
       buf ^= 1;
     } else {
       const int b2 = buf == 0 ? 2 : buf - 1;   // buffer of step it + 2
@@ -383,13 +425,13 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
       read_y(0, buf);
       load_x(plain, it + 2, 0, b2);
       end_memory();
-      multiply(0, 0);
+      multiply(0, 0, gate);
       read_y(1, buf);
       load_y(plain, it + 2, 0, b2);
       load_y(plain, it + 2, 1, b2);
       wait_vm<QX + 2 * QY>();   // the next step
       end_memory();
-      multiply(0, 1);
+      multiply(0, 1, up);
       buf = buf == 2 ? 0 : buf + 1;
     }
     ++it;
