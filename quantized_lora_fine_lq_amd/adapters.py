@@ -122,6 +122,22 @@ def _stream(dev):
     return _torch()._C._cuda_getCurrentRawStream(dev.index)
 
 
+class _Here:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def on_device(torch, dev):
+    """A launch goes to the current device: makes dev that, where it is not."""
+    return _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
+
+
 def _tokens(torch, x, name, cols, device):
     if not (x.is_cuda and x.dtype is torch.bfloat16 and x.dim() == 2 and x.size(1) == cols and x.is_contiguous()
             and x.device == device):
@@ -186,9 +202,10 @@ def adapters_forward(qw: QWeight, X, adapters: AdapterSet, ids, out_dtype=None, 
         _drop_args(dropout, dev)
         ws_bytes = lib.lq_adapters_forward_dropout_workspace(w, M, s)
         ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
-        _check(lib.lq_adapters_forward_dropout(w, X.data_ptr(), M, s, ids.data_ptr(), _at(route), dropout.ref(),
-                                               H.data_ptr(), LQ_F32 if f32 else LQ_BF16, _at(t), ws.data_ptr(),
-                                               ws_bytes, _stream(dev)), "lq_adapters_forward_dropout")
+        with on_device(torch, dev):
+            _check(lib.lq_adapters_forward_dropout(w, X.data_ptr(), M, s, ids.data_ptr(), _at(route), dropout.ref(),
+                                                   H.data_ptr(), LQ_F32 if f32 else LQ_BF16, _at(t), ws.data_ptr(),
+                                                   ws_bytes, _stream(dev)), "lq_adapters_forward_dropout")
         return H, t
     ws_bytes = lib.lq_adapters_forward_workspace(w, M, s)
     ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
@@ -224,9 +241,10 @@ def adapters_backward(qw: QWeight, X, G, adapters: AdapterSet, ids, t=None, need
         _drop_args(dropout, dev)
         ws_bytes = lib.lq_adapters_backward_dropout_workspace(w, M, s)
         ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
-        _check(lib.lq_adapters_backward_dropout(w, _at(X), G.data_ptr(), M, s, ids.data_ptr(), _at(route),
-                                                dropout.ref(), _at(t), _at(gx), _at(dA), _at(dB), ws.data_ptr(),
-                                                ws_bytes, _stream(dev)), "lq_adapters_backward_dropout")
+        with on_device(torch, dev):
+            _check(lib.lq_adapters_backward_dropout(w, _at(X), G.data_ptr(), M, s, ids.data_ptr(), _at(route),
+                                                    dropout.ref(), _at(t), _at(gx), _at(dA), _at(dB), ws.data_ptr(),
+                                                    ws_bytes, _stream(dev)), "lq_adapters_backward_dropout")
         return gx, dA, dB
     ws_bytes = lib.lq_adapters_backward_workspace(w, M, s)
     ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)

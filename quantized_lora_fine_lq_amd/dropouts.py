@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _check, _dtype_code, _torch, c_i32, c_i64, c_sz, c_vp, lib, QW_P
-from .adapters import SET_P
+from .adapters import SET_P, on_device
 
 LQ_DROPOUT_SITES = 1 << 20
 
@@ -104,19 +104,3 @@ def dropout(x, drop: Dropout, out=None):
         _check(lib.lq_dropout_apply(drop.ref(), x.data_ptr(), x.numel(), _dtype_code(x), out.data_ptr(),
                                     torch._C._cuda_getCurrentRawStream(dev.index)), "lq_dropout_apply")
     return out
-
-
-class _Here:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
-
-
-def on_device(torch, dev):
-    """A launch goes to the current device: makes dev that, where it is not."""
-    return _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)

@@ -12,8 +12,8 @@ import ctypes
 from typing import NamedTuple, Optional
 
 from . import LQ_BF16, LQ_F32, QWeight, QW_P, _check, _torch, c_i32, c_i64, c_sz, c_vp, lib
-from .adapters import SET_P, AdapterSet, _at, _drop_args, _stream, _tokens, _tokens_args
-from .dropouts import DROP_P, on_device
+from .adapters import SET_P, AdapterSet, _at, _drop_args, _stream, _tokens, _tokens_args, on_device
+from .dropouts import DROP_P
 
 LQ_SILU, LQ_GELU, LQ_GELU_TANH = 0, 1, 2
 ACTS = {"silu": LQ_SILU, "gelu": LQ_GELU, "gelu_tanh": LQ_GELU_TANH}

@@ -308,3 +308,53 @@ def test_gradients_against_differences(lq, torch):
         for got, v, d in ((f64(da), VA, (loss(h, 0) - loss(-h, 0)) / (2 * h)), (f64(db), VB, (loss(0, h) - loss(0, -h)) / (2 * h))):
             terms = np.abs(got * v).sum()
             assert abs((got * v).sum() - d) <= (3 * len(m) + 128 + 64 + 32) * U * 40 * terms + 1e-7 * abs(d)
+
+
+def test_elements_past_32_bits(lq, torch):
+    """A tensor of more than 2^35 elements: the block counter's upper word, and more than one share a workgroup."""
+    numel = (1 << 35) + 1003
+    if torch.cuda.mem_get_info()[0] < 3 * numel:
+        pytest.skip("needs 96 GiB of device memory")
+    x = torch.ones(numel, dtype=torch.bfloat16, device="cuda")
+    drop = lq.Dropout(0.5, lq.dropout_key(SEED, STEP), site=(1 << 20) - 1)
+    lq.dropout(x, drop, out=x)
+    for first in (0, (1 << 31) - 500, (1 << 32) - 500, (1 << 34) + 77, (1 << 35) - 500, numel - 1000):
+        kept = odr.fields(SEED, STEP, (1 << 20) - 1, first, 1000) >= 32768
+        assert np.array_equal(x[first:first + 1000].float().cpu().numpy(), 2.0 * kept), first
+
+
+def test_adapters_past_32_bits(lq, torch):
+    """M K past 2^31 elements: the rows at the end against the formulas (t, grad_X), and every row's dropout in dA."""
+    N, K, r, p, site = 64, 65536, 4, 0.25, 3
+    M = (1 << 31) // K + 300
+    L = Layer(lq, torch, N, K, 40, [r], ids=np.zeros(40, dtype=np.int64))
+    X = torch.randn(M, K, dtype=torch.bfloat16, device="cuda")
+    G = torch.randn(M, N, dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    drop = lq.Dropout(p, lq.dropout_key(SEED, STEP), site)
+    H, t = lq.adapters_forward(L.qw, X, L.set, ids, dropout=drop)
+    gx, dA, dB = lq.adapters_backward(L.qw, X, G, L.set, ids, t=t, dropout=drop)
+    (A, B, _), s = L.adapters[0], L.host[0][2]
+    A, B, W = A.double(), B.double(), torch.from_numpy(L.Wd).cuda()
+    cols = torch.arange(K - 64, K, device="cuda")          # of dA: 64 columns over all rows
+    keepc = torch.empty(M, 64, dtype=torch.bool)
+    rows = np.arange(M - 20, M)
+    factor = 65536.0 / (65536.0 - odr.threshold(p))
+    for m in range(M):
+        keepc[m] = torch.from_numpy(odr.fields(SEED, STEP, site, m * K + K - 64, 64) >= odr.threshold(p))
+    u = G.double() @ B
+    D = X[:, cols].double() * keepc.cuda() * factor
+    ref, mag = s * u.T @ D, s * (G.double().abs() @ B.abs()).T @ D.abs()
+    got = L.set.split(dA, dB)[0][0]
+    inside(got[:, cols], ref, (3 * M + N + 18) * U * mag, "dA")
+    keep = torch.from_numpy(odr.fields(SEED, STEP, site, int(rows[0]) * K, 20 * K).reshape(20, K) >= odr.threshold(p)).cuda()
+    D = X[M - 20:].double() * keep * factor
+    ta, tm = D @ A.T, D.abs() @ A.abs().T
+    inside(t[M - 20:], ta, (K + 10) * U * tm, "t")
+    x, g = X[M - 20:].double(), G[M - 20:].double()
+    h, mh, lh = x @ W.T + s * ta @ B.T, x.abs() @ W.abs().T, s * tm @ B.abs().T
+    inside(H[M - 20:], h, (K + 3 * r + 8) * U * (mh + lh) + (K + 2) * U * lh + 2.0 ** -16 * lh + 2.0 ** -8 * h.abs(), "H")
+    lx = s * (g.abs() @ B.abs()) @ A.abs() * keep * factor
+    rx, mx = g @ W + s * (g @ B) @ A * keep * factor, g.abs() @ W.abs()
+    inside(gx[M - 20:], rx, (N + 3 * r + 8) * U * (mx + lx) + (N + 2) * U * lx + 2.0 ** -16 * lx + 2.0 ** -8 * rx.abs() + 2.0 ** -130,
+           "grad_X")

@@ -441,6 +441,79 @@ def test_gradients_against_differences(lq, torch):
         close([b for _, b in parts], VB[i], loss(eb=e(h)), loss(eb=e(-h)), f"B {i}")
 
 
+def test_both_sides_alike(lq, torch):
+    """One weight, one set and one dropout on both sides: what copies of them give."""
+    for M in (20, 300):
+        L = Layer(lq, torch, 136, 192, M, [16, 8], p=0.2 if M > 64 else 0.0)
+        q, st = L.qw[0], L.set[0]
+        drops = L.drops and (L.drops[0], L.drops[0])
+        copies = [lq.AdapterSet([(A.clone(), B.clone(), a) for A, B, a in L.adapters[0]]) for _ in range(2)]
+        runs = []
+        for sets in ((st, st), copies):
+            pair = lq.GatedPair(q, q, *sets)
+            H, s = lq.gated_forward(pair, L.X, L.ids, dropout=drops)
+            runs.append((H, *s, *lq.gated_backward(pair, L.X, L.G, L.ids, s, dropout=drops)))
+        assert all(torch.equal(a, b) for a, b in zip(*runs))
+        assert torch.equal(runs[0][1], runs[0][2]) and torch.equal(runs[0][3], runs[0][4])
+
+
+def test_outputs_past_32_bits(lq, torch):
+    """M N past 2^31 elements: rows at the end against the formulas, and the adapters' gradients over all rows."""
+    N, K, r = 65600, 64, 4
+    M = (1 << 31) // N + 300
+    L = Layer(lq, torch, N, K, 24, [r], ids=np.zeros(24, dtype=np.int64))
+    small = L.M
+    X = torch.randn(M, K, dtype=torch.bfloat16, device="cuda")
+    G = torch.randn(M, N, dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    X[M - small:], G[M - small:] = L.X, L.G
+    H, saved = lq.gated_forward(L.pair, X, ids)
+    got = lq.gated_backward(L.pair, X, G, ids, saved)
+    value, err = [], []
+    for i in range(2):
+        v, mag, lora, T, mT = project(L, i)
+        e = (K + 3 * r + 8) * U * (mag + lora) + (K + 2) * U * lora + 2.0 ** -16 * lora
+        inside(saved[i][M - small:], v, e + 2.0 ** -8 * v.abs() + 2.0 ** -130, "gu"[i])
+        inside(saved[2 + i][M - small:], T, (K + 10) * U * mT, f"t {i}")
+        value.append(v)
+        err.append(e)
+    a, _, ea, _ = acts(torch, value[0], L.act)
+    ref = a * value[1]
+    bound = (1.13 * err[0] + 2 * ea) * (value[1].abs() + err[1]) + a.abs() * err[1] + 2 * U * ref.abs()
+    inside(H[M - small:], ref, bound + 2.0 ** -8 * ref.abs() + 2.0 ** -8 * bound + 2.0 ** -130, "H")
+    dA = [torch.zeros(r, K, dtype=torch.float64, device="cuda") for _ in range(2)]
+    mA, dB, mB = [d.clone() for d in dA], [], []
+    for i in range(2):
+        dB.append(torch.zeros(N, r, dtype=torch.float64, device="cuda"))
+        mB.append(dB[i].clone())
+    for m in range(0, M, 1024):
+        sl = slice(m, min(m + 1024, M))
+        g, u, Gd = saved.g[sl].double(), saved.u[sl].double(), G[sl].double()
+        sig = torch.sigmoid(g)      # silu and the errors of acts(), on the device
+        act, slope, k = g * sig, sig + g * sig * torch.sigmoid(-g), g.abs() + 8
+        ea, es = act.abs() * k * 2.0 ** -23 + 2.0 ** -120, k * (1 + g.abs()) * 2.0 ** -22
+        d = (Gd * u * slope, Gd * act)
+        e = ((Gd * u).abs() * es + 3 * U * d[0].abs() + 2.0 ** -130, Gd.abs() * ea + 2 * U * d[1].abs() + 2.0 ** -130)
+        rX = bX = 0.0
+        for i in range(2):
+            A, B, s, _ = next(L.groups(i))
+            um, ue = d[i].abs() @ B.abs(), e[i] @ B.abs()
+            dA[i] += s * (d[i] @ B).T @ X[sl].double()
+            mA[i] += ((3 * M + N + 18) * U * s * um.T + 1.01 * s * ue.T) @ X[sl].double().abs()
+            t = saved[2 + i][sl].double()
+            dB[i] += s * d[i].T @ t
+            mB[i] += ((6 * M + 32) * U * s * d[i].abs().T + 1.01 * s * e[i].T) @ t.abs()
+            mag, lora = d[i].abs() @ L.W[i].abs(), s * um @ A.abs()
+            rX = rX + d[i] @ L.W[i] + s * (d[i] @ B) @ A
+            bX = bX + ((2 * N + 8) * U * mag + 2.0 ** -8 * mag + 1.01 * e[i] @ L.W[i].abs() +
+                       (3 * N + 3 * r + 8) * U * lora + 2.0 ** -16 * lora + 1.01 * s * ue @ A.abs())
+        inside(got.grad_X[sl], rX, bX + 2.0 ** -8 * (rX.abs() + bX) + 2.0 ** -130, f"grad_X {m}")
+    for i in range(2):
+        (a, b), = L.set[i].split(got[1 + 2 * i], got[2 + 2 * i])
+        inside(a, dA[i], mA[i], f"dA {i}")
+        inside(b, dB[i], mB[i], f"dB {i}")
+
+
 def test_refusals(lq, torch):
     L = Layer(lq, torch, 64, 128, 20, [8, 4])
     other = Layer(lq, torch, 72, 128, 20, [8, 4])
