@@ -441,6 +441,30 @@ def test_gradients_against_differences(lq, torch):
         close([b for _, b in parts], VB[i], loss(eb=e(h)), loss(eb=e(-h)), f"B {i}")
 
 
+@pytest.mark.parametrize("M", [16, 100, 300, 2048])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -3e38])
+def test_padding_of_any_value(lq, torch, M, what):
+    """Rows without an adapter (a padded batch's) may hold anything: every other row and all gradients of the
+    adapters are bit for bit those of zero rows. So may one adapter's tokens: the other adapters' are."""
+    N = 1024 if M == 2048 else 136
+    L = Layer(lq, torch, N, 192, M, [16, 8, 40], ids="mixed", base=0.3, p=0.2 if M > 64 else 0.0)
+    for who in (-1, 1):
+        bad = L.ids == who
+        assert bad.any() and not bad.all()
+        runs = []
+        for v in (0.0, what):
+            X, G, g, u = (torch.where(bad[:, None], v, x.float()).to(torch.bfloat16) for x in (L.X, L.G, L.g, L.u))
+            H, s = lq.gated_forward(L.pair, X, L.ids, dropout=L.drops)
+            b = lq.gated_backward(L.pair, X, G, L.ids, lq.GatedSaved(g, u), dropout=L.drops)
+            runs.append((H, s, b))
+        (H0, s0, b0), (H1, s1, b1) = runs
+        for a, c in ((H0, H1), *zip(s0, s1), (b0.grad_X, b1.grad_X)):
+            assert torch.equal(a[~bad], c[~bad])
+        for i in range(2):
+            for k, (x, y) in enumerate(zip(L.set[i].split(b0[1 + 2 * i], b0[2 + 2 * i]), L.set[i].split(b1[1 + 2 * i], b1[2 + 2 * i]))):
+                assert k == who or (torch.equal(x[0], y[0]) and torch.equal(x[1], y[1]))
+
+
 def test_both_sides_alike(lq, torch):
     """One weight, one set and one dropout on both sides: what copies of them give."""
     for M in (20, 300):
