@@ -170,15 +170,18 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown p) {
   const int li = lane & 15, lg = lane >> 4;
   const int key = lane_key(ids, M, v.n);
   uint64_t left = __ballot(key >= 0), mine = 0;
-  int a = -1;
-  for (int b = 0; left; ++b) {
-    const int k = __shfl(key, __ffsll((unsigned long long)left) - 1);
+  int a = -1, t0 = 0;
+  for (int b = 0; left;) {
+    const int k = __builtin_amdgcn_readlane(key, __ffsll((unsigned long long)left) - 1);
     const uint64_t same = __ballot(key == k);
-    if (b == which) {
-      a = uniform(k);
+    const int tiles = (__popcll(same) + 15) >> 4;
+    if (which < b + tiles) {
+      a = k;
       mine = same;
+      t0 = 16 * (which - b);
       break;
     }
+    b += tiles;
     left &= ~same;
   }
   if (a < 0) return;
@@ -190,57 +193,54 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown p) {
   const int all = (int)(K / 64), per = (all + gridDim.y - 1) / gridDim.y;
   const int first = min(all, (int)blockIdx.y * per), blocks = min(all, first + per);   // this part's 64-column blocks
   t += (int64_t)blockIdx.y * M * v.rs;
-  for (int t0 = 0; t0 < count; t0 += 16) {
-    // token of row i of this 16: the (t0 + i)-th set bit of `mine`
-    int tok = 0;
-    {
-      uint64_t m = mine;
-      const int want = min(t0 + li, count - 1);
-      for (int i = 0; i < want; ++i) m &= m - 1;
-      tok = __ffsll((unsigned long long)m) - 1;
-    }
-    const uint16_t* q = X + (int64_t)tok * K;
-    f32x4_t acc[JT];
+  // token of row i of this 16: the (t0 + i)-th set bit of `mine`
+  int tok = 0;
+  {
+    uint64_t m = mine;
+    const int want = min(t0 + li, count - 1);
+    for (int i = 0; i < want; ++i) m &= m - 1;
+    tok = __ffsll((unsigned long long)m) - 1;
+  }
+  const uint16_t* q = X + (int64_t)tok * K;
+  f32x4_t acc[JT];
 #pragma unroll
-    for (int jt = 0; jt < JT; ++jt) acc[jt] = zero4();
-    constexpr int UB = JT <= 2 ? 4 : 1;   // blocks of 64 columns in flight
-    for (int b = first + wave; b < blocks; b += W * UB) {
-      u32x4_t x[UB][2], w[UB][2][JT];
+  for (int jt = 0; jt < JT; ++jt) acc[jt] = zero4();
+  constexpr int UB = JT <= 2 ? 4 : 1;   // blocks of 64 columns in flight
+  for (int b = first + wave; b < blocks; b += W * UB) {
+    u32x4_t x[UB][2], w[UB][2][JT];
 #pragma unroll
-      for (int u = 0; u < UB; ++u) {
-        const int64_t c = 64 * (int64_t)min(b + W * u, blocks - 1) + 8 * lg;   // 64 bytes of each row a load
+    for (int u = 0; u < UB; ++u) {
+      const int64_t c = 64 * (int64_t)min(b + W * u, blocks - 1) + 8 * lg;   // 64 bytes of each row a load
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          x[u][h] = ld16(q + c + 32 * h);
+      for (int h = 0; h < 2; ++h) {
+        x[u][h] = ld16(q + c + 32 * h);
 #pragma unroll
-          for (int jt = 0; jt < JT; ++jt) w[u][h][jt] = ld16(rr[jt] + c + 32 * h);
-        }
+        for (int jt = 0; jt < JT; ++jt) w[u][h][jt] = ld16(rr[jt] + c + 32 * h);
       }
-#pragma unroll
-      for (int u = 0; u < UB; ++u)
-        if (b + W * u < blocks)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int jt = 0; jt < JT; ++jt)
-              acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[u][h]), as_bf16x8(w[u][h][jt]), acc[jt], 0, 0, 0);
     }
 #pragma unroll
-    for (int jt = 0; jt < JT; ++jt) part[wave][jt][lane] = acc[jt];
-    __syncthreads();
-    for (int i = threadIdx.x; i < JT * 64 * 4; i += 64 * W) {
-      const int e = i & 3, ln = (i >> 2) & 63, jt = i >> 8, j = 16 * jt + (ln & 15);
-      float sum = 0.0f;
+    for (int u = 0; u < UB; ++u)
+      if (b + W * u < blocks)
 #pragma unroll
-      for (int w = 0; w < W; ++w) sum += part[w][jt][ln][e];
-      const int row = 4 * (ln >> 4) + e;
-      if (t0 + row >= count) continue;
-      uint64_t m = mine;
-      for (int k = 0; k < t0 + row; ++k) m &= m - 1;
-      const int token = __ffsll((unsigned long long)m) - 1;
-      if (j < v.rs) t[token * v.rs + j] = j < r ? sum : 0.0f;
-    }
-    __syncthreads();
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int jt = 0; jt < JT; ++jt)
+            acc[jt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[u][h]), as_bf16x8(w[u][h][jt]), acc[jt], 0, 0, 0);
+  }
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt) part[wave][jt][lane] = acc[jt];
+  __syncthreads();
+  for (int i = threadIdx.x; i < JT * 64 * 4; i += 64 * W) {
+    const int e = i & 3, ln = (i >> 2) & 63, jt = i >> 8, j = 16 * jt + (ln & 15);
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += part[w][jt][ln][e];
+    const int row = 4 * (ln >> 4) + e;
+    if (t0 + row >= count) continue;
+    uint64_t m = mine;
+    for (int k = 0; k < t0 + row; ++k) m &= m - 1;
+    const int token = __ffsll((unsigned long long)m) - 1;
+    if (j < v.rs) t[token * v.rs + j] = j < r ? sum : 0.0f;
   }
 }
 
@@ -717,13 +717,20 @@ int decode_parts(int64_t K, int64_t M, int32_t n, int sides) {
 size_t t_bytes(int parts, int64_t M, const AdapterView& v) { return ((size_t)parts * M * v.rs * sizeof(float) + 255) / 256 * 256; }
 size_t xp_bytes(int64_t K, int64_t M) { return (size_t)((K + 127) / 128) * token_tiles(M) * 256 * 16; }
 
+// Workgroups that suffice for the adapters in use and their tokens, 16 each
+// (none without adapters, where there are no ids either).
+int down_items(int64_t M, int32_t n) {
+  const int64_t used = std::min<int64_t>(M, n);
+  return used ? (int)(used + (M - used) / 16) : 0;
+}
+
 template <bool PAIR>
 hipError_t launch_decode_down(const DecodeDown& d, int parts, hipStream_t s) {
   const dim3 grid((unsigned)(d.wgs * (PAIR ? 2 : 1) + 1 + std::max(1, 16 * d.TT / parts)), (unsigned)parts);
   const int jt = (std::max(d.v[0].r_max, PAIR ? d.v[1].r_max : 0) + 15) / 16;
 #define LQ_DD(JT, W) hipLaunchKernelGGL((k_decode_down<JT, W, PAIR>), grid, dim3(64 * W), 0, s, d)
-  if (jt <= 1) LQ_DD(1, 16);
-  else if (jt <= 2) LQ_DD(2, 16);
+  if (jt <= 1) LQ_DD(1, (PAIR ? 8 : 16));
+  else if (jt <= 2) LQ_DD(2, (PAIR ? 8 : 16));
   else if (jt <= 4) LQ_DD(4, 8);
   else LQ_DD(8, 8);
 #undef LQ_DD
@@ -748,7 +755,7 @@ hipError_t launch_adapter_decode(const QWeight& w, const uint16_t* X, int64_t M,
   float* t_ws = reinterpret_cast<float*>(ws);
   DcRecord* records = reinterpret_cast<DcRecord*>(reinterpret_cast<char*>(ws) + t_bytes(parts, M, v));
   u32x4_t* xp = reinterpret_cast<u32x4_t*>(records + DC_RECORDS);
-  const DecodeDown d{X, (int)M, w.K, {v, {}}, ids, {t_ws, nullptr}, xp, tt, (int)std::min<int64_t>(M, v.n), records, terms, nullptr};
+  const DecodeDown d{X, (int)M, w.K, {v, {}}, ids, {t_ws, nullptr}, xp, tt, down_items(M, v.n), records, terms, nullptr};
   const hipError_t e = launch_decode_down<false>(d, parts, s);
   if (e != hipSuccess) return e;
   const DecodeParams p{xp, records, (int)M, ids, {v, {}}, {t_ws, nullptr}, parts, {t_save, nullptr}, H, {w, {}}, tables().lv,
@@ -787,7 +794,7 @@ hipError_t launch_gated_decode(const QWeight (&w)[2], const uint16_t* X, int64_t
   float* t1 = reinterpret_cast<float*>(at += t_bytes(parts, M, v[0]));
   DcRecord* records = reinterpret_cast<DcRecord*>(at += t_bytes(parts, M, v[1]));
   u32x4_t* xp = reinterpret_cast<u32x4_t*>(records + 2 * DC_RECORDS);
-  const DecodeDown d{X, (int)M, w[0].K, {v[0], v[1]}, ids, {t0, t1}, xp, tt, (int)std::min<int64_t>(M, v[0].n), records, terms,
+  const DecodeDown d{X, (int)M, w[0].K, {v[0], v[1]}, ids, {t0, t1}, xp, tt, down_items(M, v[0].n), records, terms,
                      w[0].codes};
   const hipError_t e = launch_decode_down<true>(d, parts, s);
   if (e != hipSuccess) return e;
