@@ -359,8 +359,8 @@ __device__ __forceinline__ void dc_step(const DcRecord& rec, const int64_t (&row
     if (!o.live) o.w[g] = u32x4_t{0u, 0u, 0u, 0u};
   }
 }
-// Adds step o: each product goes to its own tokens' columns alone.
-template <int NG, int RG, int TT, int TERMS>
+// Adds step o, of that side: each product goes to its own tokens' columns alone.
+template <int SIDE, int NG, int RG, int TT, int TERMS>
 __device__ __forceinline__ void dc_apply(const DcStep<NG>& o, const uint16_t* sT, int rs, int M, f32x4_t (&acc)[RG][TT]) {
   const int lane = threadIdx.x & 63, li = lane & 15;
   const u32x4_t none = {0u, 0u, 0u, 0u};
@@ -375,13 +375,11 @@ __device__ __forceinline__ void dc_apply(const DcStep<NG>& o, const uint16_t* sT
     for (int g = 0; g < NG; ++g) {
       const f32x4_t d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(o.w[g]), as_bf16x8(tv), zero4(), 0, 0, 0);
 #pragma unroll
-      for (int h = 0; h < RG / NG; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {   // selected last: a scale that is not finite makes NaN of 0, too
-          f32x4_t& sum = acc[g + NG * h][tt];
-          const float with = __builtin_fmaf(o.scale, d[e], sum[e]);
-          sum[e] = mine && (RG == NG || o.side == (h == 1)) ? with : sum[e];
-        }
+      for (int e = 0; e < 4; ++e) {   // selected last: a scale that is not finite makes NaN of 0, too
+        f32x4_t& sum = acc[g + SIDE * NG][tt];
+        const float with = __builtin_fmaf(o.scale, d[e], sum[e]);
+        sum[e] = mine ? with : sum[e];
+      }
     }
   }
 }
@@ -571,8 +569,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED &&
     if (((i + DEEP) & 63) == 0) load_records(i + DEEP);
 #pragma unroll
     for (int d = 0; d < DEEP; ++d) {
-      const bool up = GATED && steps[d].side;
-      dc_apply<NG, RG, TT, TERMS>(steps[d], sT + (up ? p.M * TERMS * rs0 : 0), up ? rs1 : rs0, p.M, acc);
+      if (GATED && steps[d].side) dc_apply<(GATED ? 1 : 0), NG, RG, TT, TERMS>(steps[d], sT + p.M * TERMS * rs0, rs1, p.M, acc);
+      else dc_apply<0, NG, RG, TT, TERMS>(steps[d], sT, rs0, p.M, acc);
       ask(i + DEEP + d, steps[d]);
     }
   }
