@@ -460,7 +460,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED &&
   // Everything that the start waits for is asked for before any of it is used:
   // the first codes, and B of the wave's first DEEP steps (a step is a round
   // trip to memory).
-  constexpr int DEEP = RG == 4 ? 4 : 1;   // (few row groups: 16 tokens' steps are one or two a wave)
+  constexpr int DEEP = RG == 4 || TT == 4 ? 4 : 1;   // (16 tokens' steps are one or two a wave)
   static_assert(W * 2 * DEEP <= DC_PAD, "the steps asked for end within the padding");
   int64_t row[RG];
 #pragma unroll
