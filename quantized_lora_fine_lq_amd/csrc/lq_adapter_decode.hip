@@ -77,24 +77,27 @@ constexpr int DC_PAD = 64;                        // no token's steps past the l
 constexpr int DC_RECORDS = 64 * 12 + DC_PAD;      // of a side
 
 // ===========================================================================
-// t = A_a x: one workgroup per adapter in use (workgroup b takes the b-th in
-// token order) and column part, 16 of its tokens at a time; the waves split
-// the part's columns. The parts' sums go to t [parts][M][rs]; the projection
+// t = A_a x: one workgroup per 16 tokens of an adapter (workgroup b takes the
+// b-th such tile, adapters in token order) and column part; the waves split
+// the part's columns. (One workgroup for all of an adapter's tokens: 64 tokens of
+// one adapter, K = 8192, 20 us more.) The parts' sums go to t [parts][M][rs]; the projection
 // adds them. The workgroups past the adapters' lay X out for the projection's
 // fragments (xp, see XPack): a load of 16 rows is then 1 KB in one piece, where
 // the rows themselves are 64 pieces of 16 bytes in 32 cache lines. Bound by
 // latency: one token 4.4 us, 16 tokens of 16 adapters 5.6 (K = 4096), 64 tokens
 // of 32 adapters, K = 8192, 13.
+//
+// PAIR: the adapters of two sets, side 1's workgroups after side 0's, and its
+// steps after side 0's. A pair may have no sets (n = 0): the steps past the last
+// then point into the codes of a weight, whose rows are 32 bytes or more. Its
+// workgroups are of eight waves: of sixteen, whose registers leave room for one
+// on a CU, two sides' would not all run at once.
 // ===========================================================================
 // XPack: 16 bytes for (stage s, token tile tt, sub-step u, lane) at
 // ((s TT + tt) 4 + u) 64 + lane: token 16 tt + lane % 16, columns 128 s + 32 (lane / 16) + 8 u
 // of X, zero past K.
 __device__ __forceinline__ int xp_units(int64_t K, int TT) { return (int)((K + 127) / 128) * TT * 256; }
 
-//
-// PAIR: the adapters of two sets, side 1's workgroups after side 0's, and its
-// steps after side 0's. A pair may have no sets (n = 0): the steps past the last
-// then point into the codes of a weight, whose rows are 32 bytes or more.
 struct DecodeDown {
   const uint16_t* X;
   int M;
@@ -266,11 +269,15 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown p) {
 // for one another at two waves a SIMD: 64 tokens' sums and X take 128 registers.
 // 16 tokens, N = K = 4096: 7.9 us after 5.6; one token: 7.5 after 4.4 (forming
 // t in the projection instead took 14.0 in all).
-// ===========================================================================
 //
 // GATED: the first half of the row groups are the gate's, the second half the
 // same rows of up, so that the join has g and u of an output side by side; the
-// workgroup is RG / 2 groups of 16 outputs.
+// workgroup is RG / 2 groups of 16 outputs. Measured, N = 28672, K = 8192, 64
+// tokens of 32 adapters of rank 8 to 32: 145 to 157 us, 121 without adapters; N =
+// 11008, K = 4096: one token 18 to 20 us. Past the memory's 47 and 9 us it is bound as
+// above; ranks whose t leaves one workgroup a CU room (64 tokens: both sides' ranks
+// past 96 together) cost half as much again.
+// ===========================================================================
 struct DecodeParams {
   const u32x4_t* xp;   // X in fragment order
   const DcRecord* records;
@@ -299,12 +306,12 @@ struct DcStage {
   int bl;         // the lane's 64-block (the last one where that lies past the row)
 };
 
-// floats of LDS after the pair table: constants, then the partial sums of one
-// token tile
 // The constants' row stride, odd or, from 16 on, even: column b of row r then lies
 // at b + r % 16 (mod nb), so that 16 rows' constants of one block hit distinct
 // banks without the odd word (64 rows of K = 8192 then leave two workgroups room).
 __host__ __device__ constexpr int dc_pitch(int nb) { return nb >= 16 ? nb : nb | 1; }
+// floats of LDS after the pair table: constants, then the partial sums of one
+// token tile
 template <int RG, int W>
 __host__ __device__ constexpr int dc_floats(int nb) {
   const int c = (16 * RG * dc_pitch(nb) + 3) / 4 * 4, red = W * RG * 272;
