@@ -275,8 +275,7 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown p) {
 // workgroup is RG / 2 groups of 16 outputs. Measured, N = 28672, K = 8192, 64
 // tokens of 32 adapters of rank 8 to 32: 145 to 157 us, 121 without adapters; N =
 // 11008, K = 4096: one token 18 to 20 us. Past the memory's 47 and 9 us it is bound as
-// above; ranks whose t leaves one workgroup a CU room (64 tokens: both sides' ranks
-// past 96 together) cost half as much again.
+// above.
 // ===========================================================================
 struct DecodeParams {
   const u32x4_t* xp;   // X in fragment order
@@ -691,15 +690,19 @@ constexpr size_t kLdsBytes = 160 * 1024;
 
 // Row groups per workgroup: the shortest queue of the longest CU, a workgroup
 // costing its row groups and about two more for its start and its X. Four need
-// the LDS of two workgroups (K up to some 10000). Of a pair at least two; 0:
-// none fits.
+// the LDS of two workgroups (K up to some 10000), but of a pair with more than 32
+// tokens, where t takes much of it, of one with eight waves: two row groups a
+// workgroup would ask the L2 for X twice as often (32 adapters of rank 64, N =
+// 28672, K = 8192: 258 us for 309; N = 14336, K = 4096: 105 for 142; N = 11008:
+// 103 for 102). Of a pair at least two; 0: none fits.
 int decode_rg(int64_t N, int64_t K, int tt, int rs, int terms, bool pair) {
   const int64_t groups = (N + 15) / 16 * (pair ? 2 : 1);
   int best = pair ? 0 : 1;
   int64_t cost = INT64_MAX;
   for (int rg = pair ? 2 : 1; rg <= 4; rg *= 2) {
-    const size_t lds = rg == 4 ? 2 * dc_lds_bytes(rg, tt, 4, (int)(K / 64), rs, terms)
-                               : dc_lds_bytes(rg, tt, 8, (int)(K / 64), rs, terms);
+    const bool two = rg == 4 && !(pair && tt == 4);
+    const size_t lds = two ? 2 * dc_lds_bytes(rg, tt, 4, (int)(K / 64), rs, terms)
+                           : dc_lds_bytes(rg, tt, 8, (int)(K / 64), rs, terms);
     if (lds > kLdsBytes) break;
     const int64_t sets = (groups + rg - 1) / rg, c = (sets + kCus - 1) / kCus * (rg + 2);
     if (c <= cost) {
@@ -822,6 +825,8 @@ hipError_t launch_gated_decode(const QWeight (&w)[2], const uint16_t* X, int64_t
   } while (0)
   if (tt == 1) LQ_RG(1);
   if (tt == 2) LQ_RG(2);
+  if (rg == 4 && 2 * dc_lds_bytes(4, 4, 4, (int)(w[0].K / 64), v[0].rs + v[1].rs, terms) > kLdsBytes)
+    return launch_rg<4, 4, 8, true>(p, f32, s);
   LQ_RG(4);
 #undef LQ_RG
 }
