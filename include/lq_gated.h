@@ -79,8 +79,9 @@ size_t lq_gated_backward_workspace(const lq_gated* p, int64_t M);
  *   again from X (and the dropout). X may be NULL where nothing needs it.
  *   grad_X [M, K] bf16; dA_gate, dA_up, dB_gate, dB_up float32, laid out as
  *   lq_adapters_backward's; each may be NULL to skip it (without sets they are).
- * dg and du are formed in float32; the adapters' products take all their bits
- * (as three bfloat16 terms), grad_X's large product their bfloat16 rounding.
+ * dg and du are formed in float32, G u first (an infinity where it passes
+ * float32's range); the adapters' products take all their bits (as three
+ * bfloat16 terms), grad_X's large product their bfloat16 rounding.
  * Needs N % 8 == 0 (LQ_ERR_SHAPE). Sums are formed in a fixed order. Errors: as
  * lq_check_gated and lq_adapters_backward_dropout.
  */

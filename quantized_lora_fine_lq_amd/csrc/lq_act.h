@@ -17,7 +17,9 @@ struct ActPair {
 };
 // silu: x s with s = sigmoid(x); slope s (1 + x (1 - s)).
 // gelu: x Phi(x), Phi by erfc so that its lower tail keeps its digits; slope Phi + x phi(x).
-// gelu_tanh: x s with s = sigmoid(2 y), y = c (x + b x^3), the same as x (1 + tanh y) / 2.
+// gelu_tanh: x s with s = sigmoid(2 y), y = c (x + b x^3), the same as x (1 + tanh y) / 2;
+// slope s + x s (1 - s) 2 y'. From |x| = 16 on s (1 - s) is 0: x is multiplied by it first,
+// and x^2 in y' ends at 1024, so that no infinity of large finite x meets it (an infinite x gives NaN).
 template <int ACT>
 __device__ __forceinline__ ActPair act_pair(float x) {
   if (ACT == LQ_SILU) {
@@ -31,8 +33,8 @@ __device__ __forceinline__ ActPair act_pair(float x) {
   }
   const float c = 0.7978845608028654f, b = 0.044715f, x2 = x * x;
   const float s = sigmoid(2.0f * c * x * __builtin_fmaf(b, x2, 1.0f));
-  const float slope = c * __builtin_fmaf(3.0f * b, x2, 1.0f);
-  return {x * s, __builtin_fmaf(2.0f * x * slope, s * (1.0f - s), s)};
+  const float slope = 2.0f * c * __builtin_fmaf(3.0f * b, fminf(x2, 1024.0f), 1.0f);
+  return {x * s, __builtin_fmaf(x * (s * (1.0f - s)), slope, s)};
 }
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {

@@ -316,6 +316,35 @@ def test_extreme_activations(lq, torch):
         assert bad[7:10].all() and not bad[:7].any() and not bad[10:].any()
 
 
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh"])
+def test_slopes_of_large_finite_values(lq, torch, kind):
+    """Past |g| = 100 act' is 1 or 0 to the last bit of float32, up to the largest finite g: up's weight and its adapter
+    are zero, so that grad_X and the gate's gradients are those of dg = G u act'(g) alone."""
+    sizes = [100.0, 1e4, 1e12, 1e13, 2e13, 1e15, 1e18, 1.8e19, 1e25, 3e38]
+    values = [v * sign for v in sizes for sign in (1.0, -1.0)]
+    N, K, r = 72, 64, 8
+    L = Layer(lq, torch, N, K, len(values), [r], ids=np.zeros(len(values)), act=kind, seed=7)
+    up = lq.QWeight.from_weight(torch.zeros(N, K, device="cuda"), double_quantize=False)
+    assert not lq.dequant(up).any()
+    L.adapters[1][0][1].zero_()
+    pair = lq.GatedPair(L.qw[0], up, *L.set, act=kind)
+    g = torch.tensor(values, device="cuda")[:, None].expand(-1, N).to(torch.bfloat16).contiguous()
+    L.G.div_(8)      # exact; du = G act(3e38) stays below float32's largest (an infinity times up's zeros is NaN)
+    assert float(L.G.abs().max()) < 1
+    got = lq.gated_backward(pair, L.X, L.G, L.ids, lq.GatedSaved(g, L.u))
+    A, B, s, m = next(L.groups(0))
+    d = L.G.double() * L.u.double() * (g > 0)      # a product of two bfloat16 values is a float32
+    t, X = L.X.double() @ A.T, L.X.double()
+    rX = d @ L.W[0] + s * (d @ B) @ A
+    mag, lora = d.abs() @ L.W[0].abs(), s * (d.abs() @ B.abs()) @ A.abs()
+    bound = (2 * N + 8) * U * mag + 2.0 ** -8 * mag + (3 * N + 3 * r + 8) * U * lora + 2.0 ** -16 * lora
+    inside(got.grad_X, rX, bound + 2.0 ** -8 * (rX.abs() + bound) + 2.0 ** -130, "grad_X")
+    (dA, dB), = L.set[0].split(got.dA_gate, got.dB_gate)
+    M = len(values)
+    inside(dA, s * (d @ B).T @ X, (3 * M + N + 18) * U * s * (d.abs() @ B.abs()).T @ X.abs() + 2.0 ** -130, "dA")
+    inside(dB, s * d.T @ t, (6 * M + K + 34) * U * s * d.abs().T @ (X.abs() @ A.abs().T) + 2.0 ** -130, "dB")
+
+
 def test_partial_outputs(lq, torch):
     L = Layer(lq, torch, 136, 192, 150, [16, 8], p=0.1)
     kept = lq.GatedSaved(L.g, L.u)
