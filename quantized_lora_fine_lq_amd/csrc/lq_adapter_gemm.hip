@@ -267,14 +267,27 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
   // the end of the contraction, steps nk .. nk + nl - 1 of the main loop.
   constexpr int TERMS = OUT_F32 ? 3 : 2;
   const int64_t mend = min(m0 + GM, p.M);
-  auto lora_x = [&](const Adapter& s, int kt, int i, int q) __attribute__((always_inline)) {   // the lane's 16 bytes of load q
+  // (One set: the address stands inside the load's own call. Returned from here by
+  // a function, as of a pair, it costs 7 registers too many.)
+  auto lora_x = [&](const Adapter& s, int kt, int i, int buf) __attribute__((always_inline)) {
     const int c = 8 * kt + ch;   // this lane's run of 8 columns
-    const int64_t pos = min(m0 + xrow(i, q) + sub, p.M - 1);
-    return chosen(c < s.live, s.terms + pos * s.pitch + 8 * c, p.zeros);
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int64_t pos = min(m0 + xrow(i, q) + sub, p.M - 1);
+      uint16_t* const dst = lds.x[buf] + xrow(i, q) * GK;
+      if constexpr (PAIR) load_lds16(chosen(c < s.live, s.terms + pos * s.pitch + 8 * c, p.zeros), dst);
+      else load_lds16(c < s.live ? p.s[0].terms + pos * 3 * p.s[0].v.rs + 8 * c : p.zeros, dst);
+    }
   };
-  auto lora_y = [&](const Adapter& s, int kt, int i, int q) __attribute__((always_inline)) {
+  auto lora_y = [&](const Adapter& s, int kt, int i, int buf) __attribute__((always_inline)) {
     const int c = 8 * kt + ch;
-    return chosen(c < s.live, s.base + wrow(i, q) * s.stride + 8 * (c % s.runs), p.zeros);
+#pragma unroll
+    for (int q = 0; q < QY; ++q) {
+      const int64_t n = wrow(i, q);
+      uint16_t* const dst = lds.y[buf] + yrow(i, q) * GK;
+      if constexpr (PAIR) load_lds16(chosen(c < s.live, s.base + n * s.stride + 8 * (c % s.runs), p.zeros), dst);
+      else load_lds16(c < s.live ? s.base + n * s.stride + 8 * (c % s.runs) : p.zeros, dst);
+    }
   };
 
   // Part i of step it into its buffer; Plain: a whole step of the base
@@ -299,8 +312,8 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
 #pragma unroll
       for (int q = 0; q < QX; ++q) src[q] = p.zeros;
     } else if constexpr (!PAIR) {
-#pragma unroll
-      for (int q = 0; q < QX; ++q) src[q] = lora_x(whole, it - nk, i, q);
+      lora_x(whole, it - nk, i, buf);
+      return;
     } else {
       const int from = PAIR && it >= nk + whole.steps ? nk + whole.steps : nk;
       const bool second = from != nk;
@@ -327,8 +340,8 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
 #pragma unroll
       for (int q = 0; q < QY; ++q) src[q] = p.zeros;
     } else if constexpr (!PAIR) {
-#pragma unroll
-      for (int q = 0; q < QY; ++q) src[q] = lora_y(whole, it - nk, i, q);
+      lora_y(whole, it - nk, i, buf);
+      return;
     } else {
       const int from = PAIR && it >= nk + whole.steps ? nk + whole.steps : nk;
       const bool second = from != nk;
@@ -490,13 +503,9 @@ __global__ __launch_bounds__(G_THREADS) void k_adapter_gemm(AdapterGemm p) {
     int kt = 0;
     auto load = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < XP; ++i)
+      for (int i = 0; i < XP; ++i) lora_x(cur, kt, i, b);
 #pragma unroll
-        for (int q = 0; q < QX; ++q) load_lds16(lora_x(cur, kt, i, q), lds.x[b] + xrow(i, q) * GK);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int q = 0; q < QY; ++q) load_lds16(lora_y(cur, kt, i, q), lds.y[b] + yrow(i, q) * GK);
+      for (int i = 0; i < 2; ++i) lora_y(cur, kt, i, b);
     };
     ring_barrier<0>();   // everyone has read the last step
     load(0);   // (APART: of a tile without adapters a step of zeros, no token's)

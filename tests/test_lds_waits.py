@@ -73,3 +73,12 @@ def test_no_lds_read_is_outstanding_at_a_barrier(functions):
             elif text.startswith("s_waitcnt") and "lgkmcnt(0)" in text:
                 pending = None
             assert not (text == "s_barrier" and pending), (name, pending)
+
+
+def test_kernels_without_a_mask_spill_nothing(functions):
+    """A lane's sums take most of its registers: no value of the kernels without dropout lies in scratch memory."""
+    plain = {n: b for n, b in functions.items()
+             if re.search(r"k_adapter_(down_tilesILi\d+E|gemmILi\d+ELb[01]ELb[01]E|gemm_smallILi\d+ELb[01]ELb[01]E)Lb0E", n)}
+    assert plain
+    for name, body in plain.items():
+        assert not [text for text, _ in body if text.startswith(("scratch_", "buffer_store_dword off"))], name
