@@ -102,6 +102,7 @@ size_t adapter_col_ws_floats(int64_t M, int64_t C, int32_t rs);
 struct ColJoin {
   ColReq q[2];
   int n, rows;
+  bool zeros;              // no adapter can have more than one run
 };
 hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Route& rt, ColJoin* join, hipStream_t s);
 hipError_t launch_adapter_col_reduce(const ColJoin* joins, int n, const Route& rt, hipStream_t s);

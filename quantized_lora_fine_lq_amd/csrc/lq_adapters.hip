@@ -40,16 +40,25 @@ __device__ __forceinline__ void route_tokens(const RouteJob& jb, int32_t* cnt) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t per = ((M + RT_WAVES - 1) / RT_WAVES + 63) / 64 * 64;
   const int64_t m0 = min(M, wave * per), m1 = min(M, m0 + per);
+  // (one branch for all of them: a branch at each load would wait for the one before)
   int keep[RT_KEEP];
+  if (jb.ids) {
 #pragma unroll
-  for (int g = 0; g < RT_KEEP; ++g) keep[g] = jb.ids ? jb.ids[min(m0 + 64 * g + lane, M - 1)] : -1;
+    for (int g = 0; g < RT_KEEP; ++g) keep[g] = jb.ids[min(m0 + 64 * g + lane, M - 1)];
+  } else {
+#pragma unroll
+    for (int g = 0; g < RT_KEEP; ++g) keep[g] = -1;
+  }
   for (int i = threadIdx.x; i < RT_WAVES * keys; i += 64 * RT_WAVES) cnt[i] = 0;
   __syncthreads();
   auto key_of = [&](int id) { return (uint32_t)id < (uint32_t)n ? id : n; };
 #pragma unroll
   for (int g = 0; g < RT_KEEP; ++g)
     if (m0 + 64 * g + lane < m1) atomicAdd(&cnt[wave * keys + key_of(keep[g])], 1);
-  for (int64_t m = m0 + 64 * RT_KEEP + lane; m < m1; m += 64) atomicAdd(&cnt[wave * keys + key_of(jb.ids ? jb.ids[m] : -1)], 1);
+  if (jb.ids)
+    for (int64_t m = m0 + 64 * RT_KEEP + lane; m < m1; m += 64) atomicAdd(&cnt[wave * keys + key_of(jb.ids[m])], 1);
+  else
+    for (int64_t m = m0 + 64 * RT_KEEP + lane; m < m1; m += 64) atomicAdd(&cnt[wave * keys + n], 1);
   __syncthreads();
   // totals per key (thread k; keys <= 1024), waves' counts to exclusive sums
   const int k = threadIdx.x;
@@ -800,20 +809,25 @@ __global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0,
 }
 
 // Joins the runs of adapters with more than one, in order, and writes the zero
-// gradients of adapters without tokens. 7 us at 2048 tokens of rank 16, 16 at
+// gradients of adapters without tokens. 7 us at 2048 tokens of rank 16, RED_US at
 // 4096 of rank 64 (four partial sums a thread at a time).
 //
 // A transposed output's rows (a column's r sums) are put together in LDS, 64
-// columns a workgroup: written from registers, 16 bytes here and there, they
-// took twice as long.
+// columns and 32 of the r a workgroup: written from registers, 16 bytes here and
+// there, they took twice as long. Zeros need no order and are written as they lie
+// (61 adapters of rank 1, five tokens: 9.6 us through LDS, RED_ZERO so). What both requests'
+// units need is loaded before the first of them, beside the route's offsets.
+constexpr int CR_COLS = 64, CR_ROWS = 32;
 struct ColJoins {
   ColJoin j[2];
 };
 __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColJoins joins, Route rt) {
-  extern __shared__ float reduce_tile[];   // [64][r_max rounded up to 4, and 1]
+  __shared__ float tile[CR_COLS * (CR_ROWS + 1)];
   const ColJoin& jn = joins.j[blockIdx.z];
+  const ColReq q0 = jn.q[0], q1 = jn.q[jn.n > 1 ? 1 : 0];
   const int rows = jn.rows;
   const int a = blockIdx.y, lane = threadIdx.x & 63;
+  const lq_adapter ad0 = q0.v.tab[a], ad1 = q1.v.tab[a];
   int before = 0;   // slots of the adapters before a
   for (int b = lane; b < a; b += 64) {
     const int c = (rt.off[b + 1] - rt.off[b] + rows - 1) / rows;
@@ -823,45 +837,42 @@ __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColJoins joins, Rout
   for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
   const int runs = (rt.off[a + 1] - rt.off[a] + rows - 1) / rows;
   if (runs == 1) return;
-  // workgroups' shares: 64 columns of a transposed output, 1024 values of another (C % 8 == 0)
-  auto units = [&](const ColReq& q) {
-    return q.transposed ? (q.C + 63) / 64 : (q.v.tab[a].r * q.C / 4 + 255) / 256;
+  // workgroups' shares: of a transposed output as above, 1024 values of another and of zeros (C % 8 == 0)
+  auto units = [&](const ColReq& q, int r) {
+    return q.transposed && runs ? (q.C + CR_COLS - 1) / CR_COLS * ((r + CR_ROWS - 1) / CR_ROWS) : (r * q.C / 4 + 255) / 256;
   };
-  const int64_t n0 = units(jn.q[0]), n1 = jn.n > 1 ? units(jn.q[1]) : 0;
+  const int64_t n0 = units(q0, ad0.r), n1 = jn.n > 1 ? units(q1, ad1.r) : 0;
   for (int64_t unit = blockIdx.x; unit < n0 + n1; unit += gridDim.x) {
-    const ColReq& q = jn.q[unit < n0 ? 0 : 1];
-    const int64_t t = unit < n0 ? unit : unit - n0;
-    const lq_adapter ad = q.v.tab[a];
-    const int64_t C = q.C;
-    if (q.transposed) {
-      const int r = ad.r, pitch = ((r + 3) & ~3) + 1, c = threadIdx.x & 63;
-      const int64_t c0 = 64 * t;
-      const int cols = (int)min((int64_t)64, C - c0);
-      for (int j = 4 * (threadIdx.x >> 6); j < r; j += 16) {   // four rows a thread (rs, a multiple of 8, are there)
+    const bool second = unit >= n0;
+    const int64_t t = second ? unit - n0 : unit, C = second ? q1.C : q0.C;
+    const int r = second ? ad1.r : ad0.r, rs = second ? q1.v.rs : q0.v.rs;
+    float* out = (second ? q1.out : q0.out) + C * (second ? ad1.row : ad0.row);   // 4-byte aligned
+    const float* part = (second ? q1.part : q0.part) + (int64_t)before * rs * C;
+    if (runs && (second ? q1.transposed : q0.transposed)) {
+      const int64_t tiles = (C + CR_COLS - 1) / CR_COLS, c0 = t % tiles * CR_COLS;
+      const int j0 = (int)(t / tiles) * CR_ROWS, n = min(CR_ROWS, r - j0), cols = (int)min((int64_t)CR_COLS, C - c0);
+      for (int j = 4 * (threadIdx.x >> 6); j < n; j += 16) {   // four rows a thread (rs, a multiple of 8, are there)
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (c < cols)
+        if (lane < cols)
           for (int k = 0; k < runs; ++k) {
-            const float* p = q.part + ((int64_t)(before + k) * q.v.rs + j) * C + c0 + c;
+            const float* p = part + ((int64_t)k * rs + j0 + j) * C + c0 + lane;
 #pragma unroll
             for (int u = 0; u < 4; ++u) sum[u] += p[u * C];
           }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) reduce_tile[c * pitch + j + u] = sum[u];
+        for (int u = 0; u < 4; ++u) tile[lane * (CR_ROWS + 1) + j + u] = sum[u];
       }
       __syncthreads();
-      float* o = q.out + C * ad.row + c0 * r;
-      for (int i = threadIdx.x; i < cols * r; i += 256) o[i] = reduce_tile[i / r * pitch + i % r];
+      for (int i = threadIdx.x; i < cols * n; i += 256) out[(c0 + i / n) * r + j0 + i % n] = tile[i / n * (CR_ROWS + 1) + i % n];
       __syncthreads();
     } else {
       const int64_t i = t * 256 + threadIdx.x;
-      if (i >= ad.r * C / 4) continue;
+      if (i >= r * C / 4) continue;
       const int64_t j = 4 * i / C, c = 4 * i % C;
       f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int k = 0; k < runs; ++k)
-        sum += *reinterpret_cast<const f32x4_t*>(q.part + ((int64_t)(before + k) * q.v.rs + j) * C + c);
-      float* o = q.out + (C * (ad.row + j) + c);   // 4-byte aligned
+      for (int k = 0; k < runs; ++k) sum += *reinterpret_cast<const f32x4_t*>(part + ((int64_t)k * rs + j) * C + c);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) o[u] = sum[u];
+      for (int u = 0; u < 4; ++u) out[4 * i + u] = sum[u];
     }
   }
 }
@@ -1051,7 +1062,7 @@ hipError_t launch_adapter_col(const ColReq* reqs, int nreq, int64_t M, const Rou
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  *join = ColJoin{{q0, q1}, nreq, rows};
+  *join = ColJoin{{q0, q1}, nreq, rows, M <= rows};
   return hipSuccess;
 }
 
@@ -1059,20 +1070,19 @@ hipError_t launch_adapter_col_reduce(const ColJoin* joins, int n, const Route& r
   if (n < 1 || n > 2) return hipErrorInvalidValue;
   ColJoins all{};
   int64_t most = 0;
-  int32_t r = 0;
   for (int i = 0; i < n; ++i) {
     const ColJoin& j = all.j[i] = joins[i];
     int64_t units = 0;
     for (int k = 0; k < j.n; ++k) {
-      units += j.q[k].transposed ? (j.q[k].C + 63) / 64 : (j.q[k].v.r_max * j.q[k].C / 4 + 255) / 256;
-      r = std::max(r, j.q[k].v.r_max);
+      const ColReq& q = j.q[k];
+      units += q.transposed && !j.zeros ? (q.C + CR_COLS - 1) / CR_COLS * ((q.v.r_max + CR_ROWS - 1) / CR_ROWS)
+                            : (q.v.r_max * q.C / 4 + 255) / 256;
     }
     most = std::max(most, units);
   }
   const int32_t sets = joins[0].q[0].v.n;
   const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, std::max(32, 4096 / sets)));
-  const size_t lds = (size_t)64 * (((r + 3) & ~3) + 1) * sizeof(float);
-  hipLaunchKernelGGL(k_adapter_col_reduce, dim3(gx, (unsigned)sets, (unsigned)n), dim3(256), lds, s, all, rt);
+  hipLaunchKernelGGL(k_adapter_col_reduce, dim3(gx, (unsigned)sets, (unsigned)n), dim3(256), 0, s, all, rt);
   return hipGetLastError();
 }
 

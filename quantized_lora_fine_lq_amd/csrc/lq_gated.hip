@@ -421,7 +421,7 @@ hipError_t launch_gated_col(const GatedGrad& gr, const ColReq (&req)[2], int64_t
   else if (r <= 64) LQ_ACTS(LQ_GC, 4);
   else LQ_ACTS(LQ_GC, 8);
 #undef LQ_GC
-  *join = ColJoin{{req[0], req[1]}, 0, rows};
+  *join = ColJoin{{req[0], req[1]}, 0, rows, M <= rows};
   for (int i = 0; i < 2; ++i)
     if (req[i].out) join->q[join->n++] = req[i];
   return hipGetLastError();
