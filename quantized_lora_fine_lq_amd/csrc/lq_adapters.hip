@@ -809,14 +809,13 @@ __global__ __launch_bounds__(256, JT <= 4 ? 3 : 1) void k_adapter_col(ColReq q0,
 }
 
 // Joins the runs of adapters with more than one, in order, and writes the zero
-// gradients of adapters without tokens. 7 us at 2048 tokens of rank 16, RED_US at
+// gradients of adapters without tokens. 6 us at 2048 tokens of rank 16, 13 at
 // 4096 of rank 64 (four partial sums a thread at a time).
 //
 // A transposed output's rows (a column's r sums) are put together in LDS, 64
 // columns and 32 of the r a workgroup: written from registers, 16 bytes here and
 // there, they took twice as long. Zeros need no order and are written as they lie
-// (61 adapters of rank 1, five tokens: 9.6 us through LDS, RED_ZERO so). What both requests'
-// units need is loaded before the first of them, beside the route's offsets.
+// (61 adapters of rank 1, five tokens: 9.6 us through LDS, 3.2 so).
 constexpr int CR_COLS = 64, CR_ROWS = 32;
 struct ColJoins {
   ColJoin j[2];
@@ -824,19 +823,21 @@ struct ColJoins {
 __global__ __launch_bounds__(256) void k_adapter_col_reduce(ColJoins joins, Route rt) {
   __shared__ float tile[CR_COLS * (CR_ROWS + 1)];
   const ColJoin& jn = joins.j[blockIdx.z];
-  const ColReq q0 = jn.q[0], q1 = jn.q[jn.n > 1 ? 1 : 0];
   const int rows = jn.rows;
   const int a = blockIdx.y, lane = threadIdx.x & 63;
-  const lq_adapter ad0 = q0.v.tab[a], ad1 = q1.v.tab[a];
-  int before = 0;   // slots of the adapters before a
-  for (int b = lane; b < a; b += 64) {
-    const int c = (rt.off[b + 1] - rt.off[b] + rows - 1) / rows;
-    before += c > 1 ? c : 0;
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
   const int runs = (rt.off[a + 1] - rt.off[a] + rows - 1) / rows;
   if (runs == 1) return;
+  const ColReq q0 = jn.q[0], q1 = jn.q[jn.n > 1 ? 1 : 0];
+  const lq_adapter ad0 = q0.v.tab[a], ad1 = q1.v.tab[a];
+  int before = 0;   // slots of the adapters before a, where there are runs to join
+  if (runs) {
+    for (int b = lane; b < a; b += 64) {
+      const int c = (rt.off[b + 1] - rt.off[b] + rows - 1) / rows;
+      before += c > 1 ? c : 0;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
+  }
   // workgroups' shares: of a transposed output as above, 1024 values of another and of zeros (C % 8 == 0)
   auto units = [&](const ColReq& q, int r) {
     return q.transposed && runs ? (q.C + CR_COLS - 1) / CR_COLS * ((r + CR_ROWS - 1) / CR_ROWS) : (r * q.C / 4 + 255) / 256;
