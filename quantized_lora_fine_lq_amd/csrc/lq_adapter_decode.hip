@@ -30,11 +30,10 @@ __device__ __forceinline__ int lane_key(const int32_t* ids, int M, int n) {
   return (uint32_t)id < (uint32_t)n ? id : -1;
 }
 
-// The tokens of the lane's adapter (of any key below 1024), from one ballot per bit.
-__device__ __forceinline__ uint64_t same_key(int key) {
+// The tokens of the lane's adapter, one of n, from one ballot per bit.
+__device__ __forceinline__ uint64_t same_key(int key, int n) {
   uint64_t peers = __ballot(key >= 0);
-#pragma unroll
-  for (int b = 0; b < 10; ++b) {
+  for (int b = 0; (n - 1) >> b; ++b) {
     const uint64_t one = __ballot((key >> b) & 1);
     peers &= ((key >> b) & 1) ? one : ~one;
   }
@@ -53,10 +52,10 @@ struct DcSteps {
   int first, count;  // its steps (0 unless the lane leads)
   int total;
 };
-__device__ __forceinline__ DcSteps dc_steps(const lq_adapter& ad, int key, int terms) {
+__device__ __forceinline__ DcSteps dc_steps(const lq_adapter& ad, int key, int n, int terms) {
   DcSteps st;
   st.ad = ad;
-  const uint64_t peers = same_key(key);
+  const uint64_t peers = same_key(key, n);
   st.same = peers;
   const bool leads = key >= 0 && bits_below(peers) == 0;
   st.count = leads ? (terms * ((st.ad.r + 7) >> 3) + 3) >> 2 : 0;   // at most 12
@@ -103,13 +102,16 @@ constexpr int DC_RECORDS = 64 * 12 + DC_PAD;      // of a side
 // of X, zero past K.
 __device__ __forceinline__ int xp_units(int64_t K, int TT) { return (int)((K + 127) / 128) * TT * 256; }
 
+// (The arguments of one set are as few as its kernels read: the size of both cost
+// the one-token launches half a microsecond.)
+template <bool PAIR>
 struct DecodeDown {
   const uint16_t* X;
   int M;
   int64_t K;
-  AdapterView v[2];
+  AdapterView v[PAIR ? 2 : 1];
   const int32_t* ids;
-  float* t[2];         // [parts][M][rs]
+  float* t[PAIR ? 2 : 1];   // [parts][M][rs]
   u32x4_t* xp;
   int TT, wgs;         // token tiles; workgroups of a side's adapters
   DcRecord* records;
@@ -118,7 +120,7 @@ struct DecodeDown {
 };
 
 template <int JT, int W, bool PAIR>
-__global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown p) {
+__global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown<PAIR> p) {
   __shared__ f32x4_t part[W][JT][64];
   const uint16_t* __restrict__ X = p.X;
   const int32_t* __restrict__ ids = p.ids;
@@ -136,7 +138,7 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown p) {
       any = p.v[0].tab[0];
 #pragma unroll
       for (int sd = 0; sd < (PAIR ? 2 : 1); ++sd) {
-        st[sd] = dc_steps(p.v[sd].tab[max(key, 0)], key, p.terms);
+        st[sd] = dc_steps(p.v[sd].tab[max(key, 0)], key, n, p.terms);
         st[sd].first += total;
         total += st[sd].total;
       }
@@ -172,23 +174,39 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown p) {
     return;
   }
   const int side = PAIR && (int)blockIdx.x >= wgs ? 1 : 0, which = (int)blockIdx.x - side * wgs;
-  const AdapterView v = side ? p.v[1] : p.v[0];
-  float* t = side ? p.t[1] : p.t[0];
+  const AdapterView v = side ? p.v[PAIR] : p.v[0];
+  float* t = side ? p.t[PAIR] : p.t[0];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
-  // The lanes that lead an adapter count its tiles and number them by a sum over the
-  // lanes below. (One adapter after the other instead: 2 us more at 32 adapters.)
+  // Few tokens: one adapter after the other, 0.07 us each. More: the lanes that lead
+  // an adapter count its tiles and number them by a sum over the lanes below, 0.3 us
+  // in all (64 tokens of 32 adapters: 10.6 us for 14.0 of this kernel).
   const int key = lane_key(ids, M, v.n);
-  const uint64_t peers = same_key(key);
-  const int tiles = key >= 0 && bits_below(peers) == 0 ? (__popcll(peers) + 15) >> 4 : 0;   // at most 4
-  int before = 0;
+  int a = -1, t0 = 0;
+  uint64_t mine = 0;
+  if (M <= 4) {
+    uint64_t left = __ballot(key >= 0);
+    for (int b = which; left; --b) {   // (at most 16 tokens: one tile each)
+      a = __builtin_amdgcn_readlane(key, __ffsll((unsigned long long)left) - 1);
+      mine = __ballot(key == a);
+      if (b == 0) break;
+      left &= ~mine;
+      a = -1;
+    }
+    if (a < 0) return;
+  } else {
+    const uint64_t peers = same_key(key, v.n);
+    const int tiles = key >= 0 && bits_below(peers) == 0 ? (__popcll(peers) + 15) >> 4 : 0;   // at most 4
+    int before = 0;
 #pragma unroll
-  for (int b = 0; b < 3; ++b) before += bits_below(__ballot((tiles >> b) & 1)) << b;
-  const uint64_t hit = __ballot(which >= before && which < before + tiles);
-  if (!hit) return;
-  const int leader = __ffsll((unsigned long long)hit) - 1;
-  const int a = __builtin_amdgcn_readlane(key, leader), t0 = 16 * (which - __builtin_amdgcn_readlane(before, leader));
-  const uint64_t mine = __ballot(key == a);
+    for (int b = 0; b < 3; ++b) before += bits_below(__ballot((tiles >> b) & 1)) << b;
+    const uint64_t hit = __ballot(which >= before && which < before + tiles);
+    if (!hit) return;
+    const int leader = __ffsll((unsigned long long)hit) - 1;
+    a = __builtin_amdgcn_readlane(key, leader);
+    t0 = 16 * (which - __builtin_amdgcn_readlane(before, leader));
+    mine = __ballot(key == a);
+  }
   const lq_adapter ad = v.tab[a];
   const int r = min(ad.r, 16 * JT), count = __popcll(mine);
   const uint16_t* rr[JT];
@@ -278,17 +296,20 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown p) {
 // 11008, K = 4096: one token 18 to 20 us. Past the memory's 47 and 9 us it is bound as
 // above.
 // ===========================================================================
+struct DecodeSide {
+  QWeight w;
+  AdapterView v;
+  const float* t;      // [parts][M, rs]
+  float* t_out;        // [M, r_max], or null
+};
+template <bool GATED>
 struct DecodeParams {
   const u32x4_t* xp;   // X in fragment order
   const DcRecord* records;
-  int M;
+  int M, parts;
   const int32_t* ids;
-  AdapterView v[2];
-  const float* t[2];   // [parts][M, rs]
-  int parts;
-  float* t_out[2];     // [M, r_max], or null
   void* out;
-  QWeight w[2];
+  DecodeSide s[GATED ? 2 : 1];
   Nf4Levels lv;
   int act;
   uint16_t *g_out, *u_out;
@@ -306,19 +327,22 @@ struct DcStage {
   int bl;         // the lane's 64-block (the last one where that lies past the row)
 };
 
-// The constants' row stride, odd or, from 16 on, even: column b of row r then lies
-// at b + r % 16 (mod nb), so that 16 rows' constants of one block hit distinct
-// banks without the odd word (64 rows of K = 8192 then leave two workgroups room).
-__host__ __device__ constexpr int dc_pitch(int nb) { return nb >= 16 ? nb : nb | 1; }
+// The constants' row stride. 16 rows' constants of one block have to hit distinct
+// banks, and four blocks' to lie in one piece where rows hold whole fours of them: any
+// odd stride, or an odd count of fours. Of four row groups a row of a multiple of 64
+// (K of 4096) keeps its length and is turned by 4 (row % 16) places instead: 64 rows of
+// K = 8192 and 64 tokens' t of rank 64 then leave two workgroups room.
+__host__ __device__ constexpr bool dc_turns(int rg, int nb) { return rg == 4 && nb % 64 == 0; }
+__host__ __device__ constexpr int dc_pitch(int rg, int nb) { return dc_turns(rg, nb) ? nb : nb % 4 == 0 ? nb | 4 : nb | 1; }
 // floats of LDS after the pair table: constants, then the partial sums of one
 // token tile
 template <int RG, int W>
 __host__ __device__ constexpr int dc_floats(int nb) {
-  const int c = (16 * RG * dc_pitch(nb) + 3) / 4 * 4, red = W * RG * 272;
+  const int c = (16 * RG * dc_pitch(RG, nb) + 3) / 4 * 4, red = W * RG * 272;
   return c > red ? c : red;
 }
 size_t dc_lds_bytes(int rg, int tt, int w, int nb, int rs, int terms) {   // rs: of both sides of a pair
-  const int c = (16 * rg * dc_pitch(nb) + 3) / 4 * 4, red = w * rg * 272;
+  const int c = (16 * rg * dc_pitch(rg, nb) + 3) / 4 * 4, red = w * rg * 272;
   return DC_PAIRS * sizeof(f32x2_t) +
          4 * (size_t)(c > red ? c : red) + 2 * (size_t)(16 * tt * rs * terms);
 }
@@ -353,7 +377,7 @@ __device__ __forceinline__ void dc_step(const DcRecord& rec, const int64_t (&row
 #pragma unroll
   for (int g = 0; g < NG; ++g) {   // (a pair's two halves are the same rows)
     const uint16_t* b = B + row[g] * r;
-    if (r % 8 == 0) {
+    if (NG == RG ? __builtin_expect(r % 8 == 0, 1) : r % 8 == 0) {   // (in line for one set; a pair's one group would spill)
       o.w[g] = ld16(b + o.j0);
     } else {
 #pragma unroll
@@ -415,8 +439,10 @@ __device__ __forceinline__ void dc_store(void* out, int64_t o, int64_t n, int64_
   }
 }
 
+// (A pair's four waves over one group of outputs: three such workgroups share a CU, and
+// registers for a fourth would spill.)
 template <int RG, int TT, int W, bool DQ, bool OUT_F32, bool GATED>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED && RG == 2 && W == 4 ? 4 : 2))) void k_decode_nf4(DecodeParams p) {
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED && RG == 2 && W == 4 ? 3 : 2))) void k_decode_nf4(DecodeParams<GATED> p) {
   constexpr int NG = GATED ? RG / 2 : RG;   // groups of 16 outputs
   extern __shared__ __attribute__((aligned(16))) unsigned char dc_lds[];
   constexpr int TERMS = OUT_F32 ? 3 : 2;
@@ -425,19 +451,21 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED &&
   float* sC = reinterpret_cast<float*>(dc_lds + DC_PAIRS * sizeof(f32x2_t));
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int li = lane & 15, lg = lane >> 4;
-  const int64_t N = p.w[0].N, K = p.w[0].K;
+  const int64_t N = p.s[0].w.N, K = p.s[0].w.K;
   const int64_t n0 = (int64_t)blockIdx.x * 16 * NG;
-  const int rs0 = p.v[0].rs, rs1 = GATED ? p.v[1].rs : 0;
-  const int nb = (int)(K / 64), pitch = dc_pitch(nb), ns = (nb + 1) / 2;
+  const int rs0 = p.s[0].v.rs, rs1 = GATED ? p.s[GATED].v.rs : 0;
+  const int nb = (int)(K / 64), pitch = dc_pitch(RG, nb), ns = (nb + 1) / 2;
+  const int turn = dc_turns(RG, nb) ? 15 : 0;
   auto turned = [&](int r, int b) {   // place of block b's constant in row r
-    const int at = nb >= 16 ? b + (r & 15) : b;
+    if (RG < 4) return b;
+    const int at = b + 4 * (r & turn);
     return at < nb ? at : at - nb;
   };
   uint16_t* sT = reinterpret_cast<uint16_t*>(sC + dc_floats<RG, W>(nb));   // t's bf16 terms [M][TERMS][rs], side 1's after side 0's
 
   const uint8_t* crow[RG];
 #pragma unroll
-  for (int g = 0; g < RG; ++g) crow[g] = (g < NG ? p.w[0] : p.w[1]).codes + min(n0 + 16 * (g % NG) + li, N - 1) * (K / 2) + 16 * (lg & 1);
+  for (int g = 0; g < RG; ++g) crow[g] = (g < NG ? p.s[0].w : p.s[GATED].w).codes + min(n0 + 16 * (g % NG) + li, N - 1) * (K / 2) + 16 * (lg & 1);
   // The stages in an order rotated by workgroup: rows lie a power of two apart in
   // the common sizes, so workgroups in step would all read from the same few
   // channels of the L2.
@@ -498,11 +526,16 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED &&
     sPair[16 * e + lane] = f32x2_t{__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(level), e >> 4)), second};
   }
   // the rows' constants, four a thread: thread t row t % (16 RG)
+  float means[2] = {0.0f, 0.0f};
+  if constexpr (DQ) {
+    means[0] = *p.s[0].w.qc.dq_mean;
+    if constexpr (GATED) means[1] = *p.s[GATED].w.qc.dq_mean;
+  }
   if (nb % 4 == 0) {
     const int rr = threadIdx.x % (16 * RG);
-    const bool up = rr >= 16 * NG;
-    const QConst qc = up ? p.w[1].qc : p.w[0].qc;
-    const float mean = DQ ? *qc.dq_mean : 0.0f;
+    const bool up = GATED && rr >= 16 * NG;
+    const QConst qc = up ? p.s[GATED].w.qc : p.s[0].w.qc;
+    const float mean = up ? means[1] : means[0];
     const int64_t b0 = min(n0 + (up ? rr - 16 * NG : rr), N - 1) * nb;
 #pragma unroll 4
     for (int c = 4 * (threadIdx.x / (16 * RG)); c < nb; c += 4 * (64 * W / (16 * RG))) {
@@ -517,17 +550,16 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED &&
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = qc.absmax[blk + e];
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sC[rr * pitch + turned(rr, c + e)] = v[e];
+      *reinterpret_cast<f32x4_t*>(sC + rr * pitch + turned(rr, c)) = v;   // in one piece: stride and turn are whole fours
     }
   } else {
     for (int i = threadIdx.x; i < 16 * RG * nb; i += 64 * W) {
       const int rr = i / nb, bl = i - rr * nb;
-      const bool up = rr >= 16 * NG;
-      const QConst qc = up ? p.w[1].qc : p.w[0].qc;
+      const bool up = GATED && rr >= 16 * NG;
+      const QConst qc = up ? p.s[GATED].w.qc : p.s[0].w.qc;
       const int64_t blk = min(n0 + (up ? rr - 16 * NG : rr), N - 1) * nb + bl;
-      sC[rr * pitch + turned(rr, bl)] =
-          DQ ? __builtin_fmaf(e4m3_decode(qc.absmax_q[blk]), qc.dq_scale[blk >> 8], *qc.dq_mean) : qc.absmax[blk];
+      sC[rr * pitch + bl] = DQ ? __builtin_fmaf(e4m3_decode(qc.absmax_q[blk]), qc.dq_scale[blk >> 8], up ? means[1] : means[0])
+                               : qc.absmax[blk];
     }
   }
   // t: its parts added in order, and split into bf16 terms: two keep 16 bits
@@ -535,8 +567,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED &&
   // adapter hold anything: no step takes them). Token m's t is saved by workgroup m % grid.
 #pragma unroll
   for (int sd = 0; sd < (GATED ? 2 : 1); ++sd) {
-    const AdapterView& v = p.v[sd];
-    const float* t = p.t[sd];
+    const AdapterView& v = p.s[sd].v;
+    const float* t = p.s[sd].t;
     uint16_t* to = sT + sd * p.M * TERMS * rs0;
     const int quads = v.rs / 4, nq = p.M * quads, nt = p.M * v.rs;
 #pragma unroll 2
@@ -551,11 +583,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED &&
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] += k < p.parts ? part[k][e] : 0.0f;
       const int m = (uint32_t)i / (uint32_t)quads, j = 4 * (i - m * quads);
-      if (p.t_out[sd] && m % gridDim.x == blockIdx.x) {
+      if (p.s[sd].t_out && m % gridDim.x == blockIdx.x) {
         const bool has = (uint32_t)p.ids[m] < (uint32_t)v.n;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (j + e < v.r_max) p.t_out[sd][m * v.r_max + j + e] = has ? sum[e] : 0.0f;
+          if (j + e < v.r_max) p.s[sd].t_out[m * v.r_max + j + e] = has ? sum[e] : 0.0f;
       }
       float x[4] = {sum[0], sum[1], sum[2], sum[3]};
 #pragma unroll
@@ -674,11 +706,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(GATED &&
 }
 
 template <int RG, int TT, int W, bool GATED>
-hipError_t launch_rg(const DecodeParams& p, bool f32, hipStream_t s) {
+hipError_t launch_rg(const DecodeParams<GATED>& p, bool f32, hipStream_t s) {
   constexpr int NG = GATED ? RG / 2 : RG;
-  const dim3 grid((unsigned)((p.w[0].N + 16 * NG - 1) / (16 * NG))), block(64 * W);
-  const size_t lds = dc_lds_bytes(RG, TT, W, (int)(p.w[0].K / 64), p.v[0].rs + (GATED ? p.v[1].rs : 0), f32 ? 3 : 2);
-  const bool dq = p.w[0].qc.absmax == nullptr;
+  const dim3 grid((unsigned)((p.s[0].w.N + 16 * NG - 1) / (16 * NG))), block(64 * W);
+  const size_t lds = dc_lds_bytes(RG, TT, W, (int)(p.s[0].w.K / 64), p.s[0].v.rs + (GATED ? p.s[GATED].v.rs : 0), f32 ? 3 : 2);
+  const bool dq = p.s[0].w.qc.absmax == nullptr;
   if (dq && f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, true, GATED>), grid, block, lds, s, p);
   else if (dq) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, true, false, GATED>), grid, block, lds, s, p);
   else if (f32) hipLaunchKernelGGL((k_decode_nf4<RG, TT, W, false, true, GATED>), grid, block, lds, s, p);
@@ -734,9 +766,9 @@ int down_items(int64_t M, int32_t n) {
 }
 
 template <bool PAIR>
-hipError_t launch_decode_down(const DecodeDown& d, int parts, hipStream_t s) {
+hipError_t launch_decode_down(const DecodeDown<PAIR>& d, int parts, hipStream_t s) {
   const dim3 grid((unsigned)(d.wgs * (PAIR ? 2 : 1) + 1 + std::max(1, 16 * d.TT / parts)), (unsigned)parts);
-  const int jt = (std::max(d.v[0].r_max, PAIR ? d.v[1].r_max : 0) + 15) / 16;
+  const int jt = (std::max(d.v[0].r_max, d.v[PAIR].r_max) + 15) / 16;
 #define LQ_DD(JT, W) hipLaunchKernelGGL((k_decode_down<JT, W, PAIR>), grid, dim3(64 * W), 0, s, d)
   if (jt <= 1) LQ_DD(1, (PAIR ? 8 : 16));
   else if (jt <= 2) LQ_DD(2, (PAIR ? 8 : 16));
@@ -764,11 +796,10 @@ hipError_t launch_adapter_decode(const QWeight& w, const uint16_t* X, int64_t M,
   float* t_ws = reinterpret_cast<float*>(ws);
   DcRecord* records = reinterpret_cast<DcRecord*>(reinterpret_cast<char*>(ws) + t_bytes(parts, M, v));
   u32x4_t* xp = reinterpret_cast<u32x4_t*>(records + DC_RECORDS);
-  const DecodeDown d{X, (int)M, w.K, {v, {}}, ids, {t_ws, nullptr}, xp, tt, down_items(M, v.n), records, terms, nullptr};
+  const DecodeDown<false> d{X, (int)M, w.K, {v}, ids, {t_ws}, xp, tt, down_items(M, v.n), records, terms, nullptr};
   const hipError_t e = launch_decode_down<false>(d, parts, s);
   if (e != hipSuccess) return e;
-  const DecodeParams p{xp, records, (int)M, ids, {v, {}}, {t_ws, nullptr}, parts, {t_save, nullptr}, H, {w, {}}, tables().lv,
-                       0, nullptr, nullptr};
+  const DecodeParams<false> p{xp, records, (int)M, parts, ids, H, {{w, v, t_ws, t_save}}, tables().lv, 0, nullptr, nullptr};
   const int rg = decode_rg(w.N, w.K, tt, v.rs, terms, false);
 #define LQ_RG(TT)                                           \
   do {                                                      \
@@ -803,12 +834,12 @@ hipError_t launch_gated_decode(const QWeight (&w)[2], const uint16_t* X, int64_t
   float* t1 = reinterpret_cast<float*>(at += t_bytes(parts, M, v[0]));
   DcRecord* records = reinterpret_cast<DcRecord*>(at += t_bytes(parts, M, v[1]));
   u32x4_t* xp = reinterpret_cast<u32x4_t*>(records + 2 * DC_RECORDS);
-  const DecodeDown d{X, (int)M, w[0].K, {v[0], v[1]}, ids, {t0, t1}, xp, tt, down_items(M, v[0].n), records, terms,
+  const DecodeDown<true> d{X, (int)M, w[0].K, {v[0], v[1]}, ids, {t0, t1}, xp, tt, down_items(M, v[0].n), records, terms,
                      w[0].codes};
   const hipError_t e = launch_decode_down<true>(d, parts, s);
   if (e != hipSuccess) return e;
-  const DecodeParams p{xp, records, (int)M, ids, {v[0], v[1]}, {t0, t1}, parts, {t_gate, t_up}, H, {w[0], w[1]}, tables().lv,
-                       act, g, u};
+  const DecodeParams<true> p{xp, records, (int)M, parts, ids, H, {{w[0], v[0], t0, t_gate}, {w[1], v[1], t1, t_up}},
+                             tables().lv, act, g, u};
   const int rg = decode_rg(w[0].N, w[0].K, tt, v[0].rs + v[1].rs, terms, true);
   // Up to 32 tokens and between one and four times as many groups of 16 outputs
   // as CUs: workgroups of four waves over one group, three on a CU and all of
