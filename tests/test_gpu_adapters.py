@@ -482,6 +482,16 @@ def test_decode_sizes(lq, torch, case, weight):
     assert torch.equal(again[0], H) and torch.equal(again[1], t)
 
 
+@pytest.mark.parametrize("case", [
+    # rows of a multiple of 64 blocks: one, two and four row groups; one, two and four token tiles
+    (4096, 4096, 2, [16, 7], "bf16"), (8200, 4096, 20, [8, 24], "f32"), (16390, 4096, 5, [16, 33], "bf16"),
+    (16390, 4096, 40, [8, 24, 64], "f32"), (16384, 8192, 64, [64, 9], "bf16"),
+], ids=str)
+@pytest.mark.parametrize("weight", ["nf4_dq", "nf4_f32"])
+def test_decode_rows_of_whole_banks(lq, torch, case, weight):
+    test_decode_sizes(lq, torch, case, weight)
+
+
 @pytest.mark.parametrize("N", [48, 16400])
 def test_decode_every_token_its_own_large_adapter(lq, torch, N):
     """64 adapters of rank 128 in float32: the most steps that the adapters' part can have."""

@@ -345,6 +345,38 @@ def test_slopes_of_large_finite_values(lq, torch, kind):
     inside(dB, s * d.T @ t, (6 * M + K + 34) * U * s * d.abs().T @ (X.abs() @ A.abs().T) + 2.0 ** -130, "dB")
 
 
+DECODE_FORMS = [
+    # N, K, M, ranks: every form of the projection by row groups, token tiles and waves; N % 4, odd K / 64, rows of
+    # a multiple of 64 blocks, ranks % 8
+    (4112, 192, 1, [16, 40]),            # flat, one token tile
+    (4117, 320, 16, [16, 7, 40]),
+    (5000, 1024, 9, [3, 16]),
+    (4112, 256, 30, [7, 16]),            # flat, two
+    (8206, 64, 17, [24, 8, 128]),
+    (264, 192, 20, [8, 33]),             # two row groups, eight waves
+    (250, 128, 32, [16] * 20),
+    (16400, 128, 5, [16, 24]),           # four row groups, four waves
+    (16390, 4096, 3, [16, 7]),
+    (16400, 192, 30, [16, 24, 1]),
+    (16400, 4096, 20, [8, 33]),
+    (4168, 192, 64, [8, 16, 32]),        # ... of four token tiles
+    (4166, 4096, 40, [24, 5]),
+    (4168, 320, 50, [64, 9, 64]),        # ... eight waves, where t leaves no room for two workgroups
+    (4168, 4096, 64, [64, 40] * 8),
+]
+
+
+@pytest.mark.parametrize("case", DECODE_FORMS, ids=str)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("weight", ["nf4_dq", "nf4_f32"])
+def test_decode_forms(lq, torch, case, out, weight):
+    L = Layer(lq, torch, *case, weight=weight, act=("silu", "gelu", "gelu_tanh")[case[2] % 3], seed=8)
+    H, saved = check_forward(lq, torch, L, out)
+    again = lq.gated_forward(L.pair, L.X, L.ids, out_dtype=H.dtype)
+    assert torch.equal(H, again[0]) and all(torch.equal(a, b) for a, b in zip(saved, again[1]))
+    assert torch.equal(H, lq.gated_forward(L.pair, L.X, L.ids, out_dtype=H.dtype, save=False)[0])
+
+
 def test_partial_outputs(lq, torch):
     L = Layer(lq, torch, 136, 192, 150, [16, 8], p=0.1)
     kept = lq.GatedSaved(L.g, L.u)
