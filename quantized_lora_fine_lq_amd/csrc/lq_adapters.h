@@ -48,7 +48,7 @@ struct DownJob {
   const float* given;      // Q null: t [M, r_max]
   uint16_t* terms;
   float* save;             // t [M, r_max] or null (zero past r_a and for tokens without an adapter)
-  float* part;             // adapter_down_ws_floats(M, C, rs)
+  float* part;             // adapter_down_ws_floats(M, C, rs, drops)
   DropView drop;           // element m C + c of Q
   float post;              // 1 for a given t
   AdapterView v;           // sets of one n
@@ -58,7 +58,7 @@ constexpr int kDownJobs = 4;
 struct DownJobs {
   DownJob j[kDownJobs];
 };
-size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs);
+size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs, bool drops);   // drops: of a call with dropout
 hipError_t launch_adapter_down(const DownJob* jobs, int njobs, int64_t M, const Route& rt, const uint16_t* zeros,
                                hipStream_t s);
 // The last part alone: `shares` partial sums of each job (or a given t) to terms.

@@ -647,13 +647,17 @@ bool down_tiled(int64_t M, int32_t rs) { return M * rs >= 65536; }
 
 // DROP: shares of each job's columns, of about `len` steps each, len chosen for the
 // shortest queue where three workgroups run on a CU, a share costing about three
-// steps more.
-constexpr int kDropShares = 16;
+// steps more. At most 16, and 4096 tiles of sums in all, 1 MB per rank (65536 tokens:
+// four shares instead of sixteen, 134 MB of rank 128 instead of 537), past which shares
+// only even out the last of many rounds.
+int64_t drop_shares_most(int64_t M) {
+  return std::max<int64_t>(1, std::min<int64_t>(16, 4096 / ((M + DT_M - 1) / DT_M)));
+}
 void drop_shares(int64_t M, const int64_t* steps, int n, int* shares) {
-  const int64_t tiles = (M + DT_M - 1) / DT_M;
+  const int64_t tiles = (M + DT_M - 1) / DT_M, limit = drop_shares_most(M);
   int64_t most = 1, best = INT64_MAX;
   for (int i = 0; i < n; ++i) most = std::max(most, steps[i]);
-  for (int64_t len = (most + kDropShares - 1) / kDropShares; len <= most; ++len) {
+  for (int64_t len = (most + limit - 1) / limit; len <= most; ++len) {
     int64_t all = 0;
     for (int i = 0; i < n; ++i) all += (steps[i] + len - 1) / len;
     const int64_t cost = (tiles * all + 767) / 768 * (len + 3);
@@ -949,9 +953,10 @@ hipError_t launch_adapter_prep(const int32_t* ids, int64_t M, const Prep* a, int
   return hipGetLastError();
 }
 
-size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs) {
-  const int64_t steps = (C + DT_K - 1) / DT_K;   // (with dropout up to kDropShares)
-  return down_tiled(M, rs) ? (size_t)std::max<int64_t>(down_shares(M, C), std::min<int64_t>(kDropShares, steps)) * M * rs : 0;
+size_t adapter_down_ws_floats(int64_t M, int64_t C, int32_t rs, bool drops) {
+  if (!down_tiled(M, rs)) return 0;
+  const int64_t steps = (C + DT_K - 1) / DT_K, most = drops ? std::min(drop_shares_most(M), steps) : 1;
+  return (size_t)std::max<int64_t>(down_shares(M, C), most) * M * rs;
 }
 
 hipError_t launch_adapter_join(const DownJob* jobs, int njobs, int64_t M, const Route& rt, hipStream_t s) {

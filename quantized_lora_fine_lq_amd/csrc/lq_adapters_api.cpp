@@ -39,20 +39,20 @@ using namespace lq;
 size_t forward_ws(const QWeight& q, int64_t M, const AdapterView& v, const lq_adapter_set* set, bool drops) {
   if (!drops && adapter_decode_supported(q, M)) return align_up(adapter_decode_ws_bytes(q, M, v));
   return align_up(route_bytes(M, v.n)) + bytes16(terms_elems(M, v)) + bytes16((size_t)q.N * q.K) + bytes16(8) +
-         align_up(adapter_down_ws_floats(M, q.K, v.rs) * sizeof(float)) +
+         align_up(adapter_down_ws_floats(M, q.K, v.rs, drops) * sizeof(float)) +
          (any_odd_rank(set) ? bytes16((size_t)sum_r8(set) * q.N) : 0);
 }
 
 // route, terms of u and t, A^T and B^T of the adapters, W'^T (and W' of a
 // codebook weight, which is transposed from it), partial sums of dA and dB, zeros
-size_t backward_ws(const QWeight& q, int64_t M, const AdapterView& v, int64_t r8) {
+size_t backward_ws(const QWeight& q, int64_t M, const AdapterView& v, int64_t r8, bool drops) {
   return align_up(route_bytes(M, v.n)) + 2 * bytes16(terms_elems(M, v)) + bytes16((size_t)r8 * q.K) +
          bytes16((size_t)r8 * q.N) + (q.format == LQ_FMT_NF4 ? 0 : bytes16((size_t)q.N * q.K)) +
          bytes16((size_t)q.K * ldb_of(q.N)) +
          align_up(adapter_col_ws_floats(M, q.K, v.rs) * sizeof(float)) +
          align_up(adapter_col_ws_floats(M, q.N, v.rs) * sizeof(float)) + bytes16(8) +
-         align_up(adapter_down_ws_floats(M, q.K, v.rs) * sizeof(float)) +
-         align_up(adapter_down_ws_floats(M, q.N, v.rs) * sizeof(float));
+         align_up(adapter_down_ws_floats(M, q.K, v.rs, drops) * sizeof(float)) +
+         align_up(adapter_down_ws_floats(M, q.N, v.rs, drops) * sizeof(float));
 }
 
 // The forward; d null: without dropout. Decode sizes with dropout run as larger ones.
@@ -83,7 +83,7 @@ int run_forward(const lq_qweight* w, const uint16_t* X, int64_t M, const lq_adap
   uint16_t* terms = cv.take<uint16_t>(terms_elems(M, v));
   uint16_t* wd = cv.take<uint16_t>((size_t)q.N * q.K);
   uint16_t* zeros = cv.take<uint16_t>(8);
-  float* part = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs));
+  float* part = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs, d != nullptr));
   uint16_t* bp = any_odd_rank(set) ? cv.take<uint16_t>((size_t)sum_r8(set) * q.N) : nullptr;
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
 
@@ -116,7 +116,7 @@ int run_backward(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int6
     return LQ_ERR_ARG;
   if (!valid_M(M) || q.N % 8 != 0 || (d && !drop_fits(M, q.K))) return LQ_ERR_SHAPE;
   const int64_t r8 = sum_r8(set);
-  if (!workspace || ws_bytes < backward_ws(q, M, v, r8)) return LQ_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < backward_ws(q, M, v, r8, d != nullptr)) return LQ_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   if ((st = debug_check_weight(q, s)) != LQ_OK) return st;
   Carver cv(workspace, ws_bytes);
@@ -131,8 +131,8 @@ int run_backward(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int6
   float* part_a = cv.take<float>(adapter_col_ws_floats(M, q.K, v.rs));
   float* part_b = cv.take<float>(adapter_col_ws_floats(M, q.N, v.rs));
   uint16_t* zeros = cv.take<uint16_t>(8);
-  float* down_t = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs));
-  float* down_u = cv.take<float>(adapter_down_ws_floats(M, q.N, v.rs));
+  float* down_t = cv.take<float>(adapter_down_ws_floats(M, q.K, v.rs, d != nullptr));
+  float* down_u = cv.take<float>(adapter_down_ws_floats(M, q.N, v.rs, d != nullptr));
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
   if (!grad_X && !dA && !dB) return LQ_OK;
 
@@ -202,7 +202,7 @@ size_t lq_adapters_backward_workspace(const lq_qweight* w, int64_t M, const lq_a
   QWeight q;
   AdapterView v;
   if (check_qweight(w, &q) != LQ_OK || !valid_M(M) || check_set(set, q.N, q.K, &v) != LQ_OK || q.N % 8 != 0) return 0;
-  return backward_ws(q, M, v, sum_r8(set));
+  return backward_ws(q, M, v, sum_r8(set), false);
 }
 
 int lq_adapters_backward(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int64_t M,
@@ -242,8 +242,11 @@ int lq_adapters_forward_dropout(const lq_qweight* w, const uint16_t* X, int64_t 
 
 size_t lq_adapters_backward_dropout_workspace(const lq_qweight* w, int64_t M, const lq_adapter_set* set) {
   QWeight q;
-  if (check_qweight(w, &q) != LQ_OK || !valid_M(M) || !drop_fits(M, q.K)) return 0;
-  return lq_adapters_backward_workspace(w, M, set);
+  AdapterView v;
+  if (check_qweight(w, &q) != LQ_OK || !valid_M(M) || check_set(set, q.N, q.K, &v) != LQ_OK || q.N % 8 != 0 ||
+      !drop_fits(M, q.K))
+    return 0;
+  return backward_ws(q, M, v, sum_r8(set), true);
 }
 
 int lq_adapters_backward_dropout(const lq_qweight* w, const uint16_t* X, const uint16_t* G, int64_t M,

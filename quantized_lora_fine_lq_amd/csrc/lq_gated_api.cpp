@@ -53,12 +53,12 @@ struct Forward {
   int32_t* route;
   uint16_t *terms[2], *wd[2], *bp[2], *zeros;
   float* part[2];
-  explicit Forward(Carver& cv, const Pair& p, int64_t M) {
+  explicit Forward(Carver& cv, const Pair& p, int64_t M, bool drops) {
     route = cv.take<int32_t>(route_words(M, p.v[0].n));
     for (int i = 0; i < 2; ++i) {
       terms[i] = cv.take<uint16_t>(terms_elems(M, p.v[i]));
       wd[i] = cv.take<uint16_t>((size_t)p.N * p.K);
-      part[i] = cv.take<float>(p.sets ? adapter_down_ws_floats(M, p.K, p.v[i].rs) : 0);
+      part[i] = cv.take<float>(p.sets ? adapter_down_ws_floats(M, p.K, p.v[i].rs, drops) : 0);
       bp[i] = p.sets && any_odd_rank(p.set[i]) ? cv.take<uint16_t>((size_t)sum_r8(p.set[i]) * p.N) : nullptr;
     }
     zeros = cv.take<uint16_t>(8);
@@ -69,7 +69,7 @@ struct Backward {
   int32_t* route;
   uint16_t *u[2], *t[2], *at[2], *bt[2], *wd[2], *wt, *D, *zeros;
   float *down_t[2], *down_u[2], *part_a[2], *part_b[2];
-  explicit Backward(Carver& cv, const Pair& p, int64_t M) {
+  explicit Backward(Carver& cv, const Pair& p, int64_t M, bool drops) {
     route = cv.take<int32_t>(route_words(M, p.v[0].n));
     for (int i = 0; i < 2; ++i) {
       const AdapterView& v = p.v[i];
@@ -79,7 +79,7 @@ struct Backward {
       at[i] = cv.take<uint16_t>(r8 * p.K);
       bt[i] = cv.take<uint16_t>(r8 * p.N);
       wd[i] = p.q[i].format == LQ_FMT_NF4 ? nullptr : cv.take<uint16_t>((size_t)p.N * p.K);
-      down_t[i] = cv.take<float>(p.sets ? adapter_down_ws_floats(M, p.K, v.rs) : 0);
+      down_t[i] = cv.take<float>(p.sets ? adapter_down_ws_floats(M, p.K, v.rs, drops) : 0);
       down_u[i] = cv.take<float>(gated_down_ws_floats(M, p.N, v));
       part_a[i] = cv.take<float>(adapter_col_ws_floats(M, p.K, v.rs));
       part_b[i] = cv.take<float>(adapter_col_ws_floats(M, p.N, v.rs));
@@ -94,15 +94,15 @@ struct Backward {
 bool decodes(const Pair& p, int64_t M, bool drops) { return !drops && gated_decode_supported(p.q, M, p.v); }
 
 template <class W>
-size_t ws_bytes_of(const Pair& p, int64_t M) {
+size_t ws_bytes_of(const Pair& p, int64_t M, bool drops) {
   Carver cv(nullptr, 0);
-  W w(cv, p, M);
+  W w(cv, p, M, drops);
   (void)w;
   return cv.used;
 }
 
 size_t forward_ws(const Pair& p, int64_t M, bool drops) {
-  return decodes(p, M, drops) ? align_up(gated_decode_ws_bytes(p.q[0], M, p.v)) : ws_bytes_of<Forward>(p, M);
+  return decodes(p, M, drops) ? align_up(gated_decode_ws_bytes(p.q[0], M, p.v)) : ws_bytes_of<Forward>(p, M, drops);
 }
 
 }  // namespace
@@ -143,7 +143,7 @@ int lq_gated_forward(const lq_gated* p, const uint16_t* X, int64_t M, const int3
   if (decodes(o, M, drops))
     return launch_status(launch_gated_decode(o.q, X, M, ids, o.v, workspace, o.act, t_gate, t_up, g, u, H, h_dtype == LQ_F32, s));
   Carver cv(workspace, ws_bytes);
-  const Forward w(cv, o, M);
+  const Forward w(cv, o, M, drops);
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
 
   Prep prep[2];
@@ -181,7 +181,7 @@ int lq_gated_forward(const lq_gated* p, const uint16_t* X, int64_t M, const int3
 size_t lq_gated_backward_workspace(const lq_gated* p, int64_t M) {
   Pair o;
   if (check_pair(p, &o) != LQ_OK || !valid_M(M) || o.N % 8 != 0) return 0;
-  return ws_bytes_of<Backward>(o, M);
+  return ws_bytes_of<Backward>(o, M, true);   // one size, with dropout or without
 }
 
 int lq_gated_backward(const lq_gated* p, const uint16_t* X, const uint16_t* G, int64_t M, const int32_t* ids,
@@ -205,12 +205,12 @@ int lq_gated_backward(const lq_gated* p, const uint16_t* X, const uint16_t* G, i
     return LQ_ERR_ARG;
   if (!valid_M(M) || o.N % 8 != 0) return LQ_ERR_SHAPE;
   if ((st = check_drops(o, M, drop_gate, drop_up, drop, factor)) != LQ_OK) return st;
-  if (!workspace || ws_bytes < ws_bytes_of<Backward>(o, M)) return LQ_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < ws_bytes_of<Backward>(o, M, true)) return LQ_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   for (int i = 0; i < 2; ++i)
     if ((st = debug_check_weight(o.q[i], s)) != LQ_OK) return st;
   Carver cv(workspace, ws_bytes);
-  const Backward w(cv, o, M);
+  const Backward w(cv, o, M, true);
   if (!cv.ok()) return LQ_ERR_WORKSPACE;
   if (!grad_X && !any_dA && !any_dB) return LQ_OK;
 

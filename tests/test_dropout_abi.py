@@ -112,3 +112,21 @@ def test_adapter_refusals(lq, ad, dr):
     assert fwd(w=wide, M=1 << 29) == lq.LQ_ERR_SHAPE and bwd(w=wide, M=1 << 29) == lq.LQ_ERR_SHAPE
     assert L.lq_adapters_forward_dropout_workspace(wide, 1 << 29, S) == 0
     assert L.lq_adapters_backward_dropout_workspace(wide, 1 << 29, S) == 0
+
+
+@pytest.mark.parametrize("M,rank,shares", [(1024, 64, 8), (4096, 64, 8), (16384, 64, 2), (65536, 128, 1)])
+def test_partial_sums_of_t_take_what_their_call_can_use(lq, ad, M, rank, shares):
+    """Workspaces of large calls: route, three terms, the weight, and as many partial sums of t as the tokens' 64-row
+    tiles leave CUs for; dropout may split the columns further, up to 4096 tiles of sums in all."""
+    N = K = 4096
+    w, s = ctypes.byref(nf4(lq, N, K)), ctypes.byref(make_set(ad, [rank] * 4))
+    plain, drops = lq.lib.lq_adapters_forward_workspace(w, M, s), lq.lib.lq_adapters_forward_dropout_workspace(w, M, s)
+    sums = 4 * M * rank
+    known = lq.lib.lq_adapter_route_bytes(M, 4) + 2 * 3 * M * rank + 2 * N * K
+    pieces = 8 * 256      # each begins at a multiple of 256 bytes
+    assert known + sums <= plain <= known + shares * sums + pieces
+    assert plain <= drops <= known + max(shares, min(16, 4096 * 64 // M)) * sums + pieces
+    known += 2 * (3 * M * rank) + 2 * 4 * rank * (N + K) + 2 * (2 * -(-M // 256) * rank * K * 4)
+    plain, drops = lq.lib.lq_adapters_backward_workspace(w, M, s), lq.lib.lq_adapters_backward_dropout_workspace(w, M, s)
+    assert known + 2 * sums <= plain <= known + 2 * shares * sums + 2 * pieces
+    assert plain <= drops <= known + 2 * max(shares, min(16, 4096 * 64 // M)) * sums + 2 * pieces

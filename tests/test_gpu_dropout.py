@@ -201,6 +201,12 @@ def test_large(lq, torch, case):
     check(lq, torch, Layer(lq, torch, N, K, M, ranks, ids, weight), 0.1, saved=False)
 
 
+@pytest.mark.parametrize("case", [(64, 1024, 20480, [16, 40], "runs", "nf4_dq"), (64, 192, 70000, [7], "mixed", "nf4_dq")], ids=str)
+def test_more_tokens_than_a_share_each(lq, torch, case):
+    """t in tiles of so many tokens that the columns' shares are fewer than they could be."""
+    test_large(lq, torch, case)
+
+
 def test_no_token_has_an_adapter(lq, torch):
     for N, K, M in ((128, 128, 70), (64, 4096, 2048), (64, 8192, 4096)):
         check(lq, torch, Layer(lq, torch, N, K, M, [16, 8], ids=np.full(M, -1)), 0.5)
