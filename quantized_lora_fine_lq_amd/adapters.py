@@ -170,7 +170,8 @@ def adapter_route(ids, n: int):
     M = ids.shape[0]
     size = lib.lq_adapter_route_bytes(M, n)
     route = torch.empty(max(size // 4, 1), dtype=torch.int32, device=ids.device)
-    _check(lib.lq_adapter_route(_ptr(ids), M, n, _ptr(route), size, _stream(ids.device)), "lq_adapter_route")
+    with on_device(torch, ids.device):
+        _check(lib.lq_adapter_route(_ptr(ids), M, n, _ptr(route), size, _stream(ids.device)), "lq_adapter_route")
     route.lq_route_of = (M, n)
     return route
 
@@ -209,9 +210,10 @@ def adapters_forward(qw: QWeight, X, adapters: AdapterSet, ids, out_dtype=None, 
         return H, t
     ws_bytes = lib.lq_adapters_forward_workspace(w, M, s)
     ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
-    _check(lib.lq_adapters_forward(w, X.data_ptr(), M, s, ids.data_ptr(), None if route is None else route.data_ptr(),
-                                   H.data_ptr(), LQ_F32 if f32 else LQ_BF16, t.data_ptr() if save_t else None,
-                                   ws.data_ptr(), ws_bytes, _stream(dev)), "lq_adapters_forward")
+    with on_device(torch, dev):
+        _check(lib.lq_adapters_forward(w, X.data_ptr(), M, s, ids.data_ptr(), None if route is None else route.data_ptr(),
+                                       H.data_ptr(), LQ_F32 if f32 else LQ_BF16, t.data_ptr() if save_t else None,
+                                       ws.data_ptr(), ws_bytes, _stream(dev)), "lq_adapters_forward")
     return H, t
 
 
@@ -248,8 +250,9 @@ def adapters_backward(qw: QWeight, X, G, adapters: AdapterSet, ids, t=None, need
         return gx, dA, dB
     ws_bytes = lib.lq_adapters_backward_workspace(w, M, s)
     ws = empty((max(ws_bytes, 1),), (1,), dtype=torch.uint8, device=dev)
-    _check(lib.lq_adapters_backward(w, _at(X), G.data_ptr(), M, s, ids.data_ptr(), _at(route), _at(t), _at(gx), _at(dA),
-                                    _at(dB), ws.data_ptr(), ws_bytes, _stream(dev)), "lq_adapters_backward")
+    with on_device(torch, dev):
+        _check(lib.lq_adapters_backward(w, _at(X), G.data_ptr(), M, s, ids.data_ptr(), _at(route), _at(t), _at(gx), _at(dA),
+                                        _at(dB), ws.data_ptr(), ws_bytes, _stream(dev)), "lq_adapters_backward")
     return gx, dA, dB
 
 
@@ -307,8 +310,9 @@ class GradList:
 def grad_norm(grads: GradList):
     """The L2 norm of each group's gradients (f32 [n_groups])."""
     norms, ws = grads._buffers()
-    _check(lib.lq_grad_norm(grads.ref(), norms.data_ptr(), ws.data_ptr(), grads._ws_bytes, _stream(grads.device)),
-           "lq_grad_norm")
+    with on_device(_torch(), grads.device):
+        _check(lib.lq_grad_norm(grads.ref(), norms.data_ptr(), ws.data_ptr(), grads._ws_bytes, _stream(grads.device)),
+               "lq_grad_norm")
     return norms
 
 
@@ -322,6 +326,7 @@ def clip_grad_norm(grads: GradList, max_norm: float, out: Optional[GradList] = N
     elif out.device != grads.device:
         raise ValueError("the lists are on different devices")
     norms, ws = grads._buffers()
-    _check(lib.lq_clip_grad_norm(grads.ref(), out.ref(), float(max_norm), float(eps), norms.data_ptr(), ws.data_ptr(),
-                                 grads._ws_bytes, _stream(grads.device)), "lq_clip_grad_norm")
+    with on_device(_torch(), grads.device):
+        _check(lib.lq_clip_grad_norm(grads.ref(), out.ref(), float(max_norm), float(eps), norms.data_ptr(), ws.data_ptr(),
+                                     grads._ws_bytes, _stream(grads.device)), "lq_clip_grad_norm")
     return norms
