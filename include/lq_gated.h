@@ -42,9 +42,13 @@ typedef struct lq_gated {
 int lq_check_gated(const lq_gated* p);
 
 /* Workspace bytes of lq_gated_forward (0 for an invalid argument); drops: 1 if
- * a dropout is given. Up to 64 tokens of NF4 weights with K <= 49152 without
- * dropout about the size of X and t, otherwise above all both weights in
- * bfloat16, 4 N K bytes. */
+ * a dropout is given. Up to 64 tokens of two NF4 weights with constants of one
+ * kind (both double-quantized or neither), K <= 49152, without dropout, about
+ * the size of X and t, as far as both sides' t and a workgroup's constants fit
+ * the chip's shared memory: where 2 K + 6 T (r + r') <= 130560, with T the
+ * tokens rounded up to 16, 32 or 64 and r, r' the sets' r_max rounded up to
+ * multiples of 8 (64 tokens: any ranks up to K = 16128). Otherwise above all both
+ * weights in bfloat16, 4 N K bytes. */
 size_t lq_gated_forward_workspace(const lq_gated* p, int64_t M, int32_t drops);
 
 /*

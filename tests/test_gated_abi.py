@@ -141,3 +141,24 @@ def test_backward_refusals(lq, ad, ga):
     assert bwd(p=ctypes.byref(odd)) == lq.LQ_ERR_SHAPE and bwd(M=0) == lq.LQ_ERR_SHAPE
     assert bwd(size=size - 1) == lq.LQ_ERR_WORKSPACE and bwd(ws=None) == lq.LQ_ERR_WORKSPACE
     assert bwd(gx=None, X=None, **none) == lq.LQ_OK      # nothing wanted: nothing launched
+
+
+def test_where_a_forward_keeps_the_packed_weights(lq, ad, ga):
+    """The sizes that the header promises a small workspace for, and those just past them."""
+    size = lambda M, drops=0, **kw: lq.lib.lq_gated_forward_workspace(ctypes.byref(pair(lq, ad, ga, **kw)), M, drops)
+    N = 4096
+
+    def both(K, r, **kw):
+        return dict(gate=nf4(lq, N, K), up=nf4(lq, N, K, **kw), ranks=([r, 3], [8, r]))
+    for T, M in ((16, 16), (32, 17), (64, 33), (64, 64)):
+        for r in (8, 33, 64, 128):
+            r8 = (r + 7) // 8 * 8
+            last = min((130560 - 6 * T * 2 * r8) // 2 // 64 * 64, 49152)
+            small = 2 * (8 * M * 2 * r8 * 4) + 2 * T * (last + 64) + (1 << 17)      # up to eight parts of t, X, the steps' list
+            assert size(M, **both(last, r)) <= small < 4 * N * last
+            past = min(last + 1024, 49152 + 64)      # (what fits is a little more than what is promised)
+            assert size(M, **both(past, r)) >= 4 * N * past
+        assert size(M, sets=False, **both(49152, 8)) < 4 * N * 49152 / 64
+        dq = dict(absmax=None, absmax_q=A, dq_scale=A, dq_mean=A)
+        assert size(M, **both(256, 16, **dq)) >= 4 * N * 256 and size(M, drops=1, **both(256, 16)) >= 4 * N * 256
+    assert size(65, **both(256, 16)) >= 4 * N * 256
