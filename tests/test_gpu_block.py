@@ -214,3 +214,43 @@ def test_gradients_against_differences(lq, torch, example):
 def test_example_runs(torch, example):
     losses, out = example.run(steps=5)
     assert len(losses) == 5 and all(np.isfinite(losses)) and bool(torch.isfinite(out.float()).all())
+
+
+def test_an_example_step_applies_each_gradient_to_its_matrix(lq, torch, example, monkeypatch):
+    """The clipped gradients of gate, up and down, adapter by adapter, reach their own matrices with the step's sign and
+    size, in float32 and then in the copies that the kernels read; the key counts the steps."""
+    keys, lists, steps = [], [], []
+    key, clip, backward = lq.dropout_key, lq.clip_grad_norm, example.Block.backward
+    monkeypatch.setattr(example.lq, "dropout_key", lambda *a: keys.append(key(*a)) or keys[-1])
+    monkeypatch.setattr(example.lq, "clip_grad_norm", lambda grads, *a: lists.append(grads) or clip(grads, *a))
+
+    def recorded(block, *a):
+        before = [t.clone() for s in (block.pair.gate_adapters, block.pair.up_adapters, block.down_set)
+                  for A, B, _ in s.adapters for t in (A, B)]
+        out = backward(block, *a)
+        steps.append((block, before, out[1]))
+        return out
+    monkeypatch.setattr(example.Block, "backward", recorded)
+    lr = 0.01
+    example.run(steps=1, lr=lr)
+    (block, before, flat), (grads,) = steps[0], lists
+    sets = (block.pair.gate_adapters, block.pair.up_adapters, block.down_set)
+    n = block.pair.n
+    own = [g for s, (dA, dB) in zip(sets, flat) for ab in s.split(dA, dB) for g in ab]
+    assert [g.data_ptr() for g in grads.tensors] == [g.data_ptr() for g in own]
+    assert grads.n_groups == n
+    after = [t for s in sets for A, B, _ in s.adapters for t in (A, B)]
+    for i, (old, new, g) in enumerate(zip(before, after, own)):      # (the clip worked in place)
+        g = g.double()
+        if i % 2:      # B began at zero
+            assert not old.any() and torch.equal(new, torch.zeros_like(g, dtype=torch.float32).sub_(g.float(), alpha=lr * 10).to(
+                torch.bfloat16))
+        else:          # A: the float32 value is within half a step of its first copy, and the new copy of the new value
+            assert ((new.double() - (old.double() - lr * 10 * g)).abs() <=
+                    2.0 ** -8 * (old.double().abs() * 1.01 + new.double().abs()) + 2.0 ** -22 * g.abs()).all()
+    assert any(g.any() for g in own[1::2])
+    # each adapter's gradients were clipped to norm 1 together
+    norms = [sum(float(own[2 * (k * n + a) + j].double().square().sum()) for k in range(3) for j in range(2)) ** 0.5 for a in range(n)]
+    assert all(x <= 1 + 1e-5 for x in norms)
+    example.run(steps=3)
+    assert keys[0].tolist() == [0, 1] and keys[1].tolist() == [0, 3]
