@@ -841,13 +841,33 @@ hipError_t launch_gated_decode(const QWeight (&w)[2], const uint16_t* X, int64_t
   const DecodeParams<true> p{xp, records, (int)M, parts, ids, H, {{w[0], v[0], t0, t_gate}, {w[1], v[1], t1, t_up}},
                              tables().lv, act, g, u};
   const int rg = decode_rg(w[0].N, w[0].K, tt, v[0].rs + v[1].rs, terms, true);
-  // Up to 32 tokens and between one and four times as many groups of 16 outputs
-  // as CUs: workgroups of four waves over one group, three on a CU and all of
-  // them at once, beat two rounds of larger ones (N = 11008, K = 4096: one token
-  // 22 us for 28, 16 tokens 27 for 36, 32 tokens 29 for 36; N = 4096: 17 for 16;
-  // N = 28672, K = 8192: 91 for 88).
+  // More groups of 16 outputs than CUs, up to 32 tokens: workgroups of four waves over
+  // one group, up to three on a CU, against those of rg. Where the latter hold four
+  // groups of outputs on a CU (rg = 4), the smaller ones win as a single round, and up
+  // to 16 tokens also in two rounds of either while the larger ones' second is mostly
+  // empty; where rg = 2 (long rows, large ranks), if they take no more rounds. K = 4096,
+  // 1 / 16 / 32 tokens, rank 16, smaller against larger, us: N = 5120 17.6 / 20.7 / 23.7
+  // against 20.8 / 23.4 / 25.3; 12288 23.1 / 25.5 / 30.1 against 27.5 / 30.0 / 32.0; 14336
+  // (two rounds against one) 29.6 / 33.8 / 39.2 against 27.6 / 30.1 / 32.7; 20480 (two
+  // each) 34.2 / 38.9 / 44.8 against 41.3 / 44.4 / 48.4; 28672 (three against two) 45.6 /
+  // 59.4 / 69.2 against 47.4 / 53.9 / 60.2; 4096 (no more groups than CUs) 15.6 / 18.3 /
+  // 20.3 against 14.2 / 16.5 / 19.0. K = 8192: 20480 64.0 / 71.6 / 85.8 against 69.1 / 74.8 /
+  // 81.0; 24576 77.9 / 81.8 / 101 against 74.3 / 77.2 / 85.5. Two of either on a CU: K =
+  // 16384, N = 28672 159 / 166 / 203 against 171 / 181 / 206; K = 4096, rank 128, N =
+  // 8192 21.0 / 37.9 / 46.6 against 24.4 / 39.4 / 53.4, N = 14336, 32 tokens 87 against 103.
   const int64_t groups = (w[0].N + 15) / 16;
-  const bool flat = tt <= 2 && groups > kCus && groups <= 4 * kCus;
+  const int nb = (int)(w[0].K / 64), rs = v[0].rs + v[1].rs;
+  auto rounds = [&](size_t lds, int64_t most) {   // of workgroups of one group
+    const int64_t slots = kCus * std::min<int64_t>(most, (int64_t)(kLdsBytes / lds));
+    return (groups + slots - 1) / slots;
+  };
+  bool flat = false;
+  if (tt <= 2 && groups > kCus) {
+    const size_t lds = dc_lds_bytes(2, tt, 4, nb, rs, terms);
+    const int64_t mine = rounds(lds, 3);
+    if (rg == 4) flat = mine == 1 || (tt == 1 && mine == 2 && groups > 4 * kCus && groups <= 5 * kCus);
+    else flat = mine <= rounds(dc_lds_bytes(2, tt, 8, nb, rs, terms), 2);
+  }
   if (flat && tt == 1) return launch_rg<2, 1, 4, true>(p, f32, s);
   if (flat) return launch_rg<2, 2, 4, true>(p, f32, s);
 #define LQ_RG(TT)                                          \

@@ -355,8 +355,10 @@ DECODE_FORMS = [
     (8206, 64, 17, [24, 8, 128]),
     (264, 192, 20, [8, 33]),             # two row groups, eight waves
     (250, 128, 32, [16] * 20),
-    (16400, 128, 5, [16, 24]),           # four row groups, four waves
+    (16400, 128, 5, [16, 24]),           # flat in two rounds
     (16390, 4096, 3, [16, 7]),
+    (12310, 128, 5, [16, 24]),           # four row groups, four waves
+    (14336, 4096, 3, [16, 7]),
     (16400, 192, 30, [16, 24, 1]),
     (16400, 4096, 20, [8, 33]),
     (4168, 192, 64, [8, 16, 32]),        # ... of four token tiles
