@@ -888,14 +888,18 @@ hipError_t launch_adapter_gemm(const AdapterGemm& g, hipStream_t s) {
   // Rounds of a chip full of tiles times a tile's time per step, in us as
   // measured over K = 4096: 1.7 (256 x 256), 1.05 (256 x 128) and for 64 x 64,
   // two workgroups per CU, 0.3 where the tiles number more than the CUs. (Fewer
-  // of them always win: 0.2.)
+  // of them always win: 0.2.) Of a pair these are slower: 0.45 where g and u are formed,
+  // whose tile has half the outputs (4096 -> 11008, calls of 64 x 64 / 256 x 128 / 256 x
+  // 256: 200 tokens 146 / 123 / 152 us, 400 193 / 183 / 157, 700 277 / 238 / 245; 1024 ->
+  // 2048, 1000 tokens 43 / 46 / 58, 1500 52 / 45 / 56), 0.7 in grad_X, whose contraction is long
+  // (512 tokens 321 / 389 / 526, 1000 529 / 423 / 550).
   auto tiles = [&](int64_t m, int64_t n) {
     const int64_t cols = tile_cols(g, n);
     return ((g.M + m - 1) / m) * ((g.Ncols + cols - 1) / cols);
   };
   auto cost = [&](int64_t count, int64_t slots, double us) { return (double)((count + slots - 1) / slots) * us; };
   const int64_t small = tiles(SM, SN);
-  const double c256 = cost(tiles(256, 256), 256, 1.7), c128 = cost(tiles(256, 128), 256, 1.05), c64 = cost(small, 512, 0.3);
+  const double c256 = cost(tiles(256, 256), 256, 1.7), c128 = cost(tiles(256, 128), 256, 1.05), c64 = cost(small, 512, g.mode == GEMM_GATED ? 0.45 : g.mode == GEMM_TWO ? 0.7 : 0.3);
   if (small <= 256) return launch_small<2>(g, small, s);
   if (c64 < c128 && c64 < c256) return launch_small<1>(g, small, s);
   return c256 <= c128 ? launch_tile<256>(g, s) : launch_tile<128>(g, s);

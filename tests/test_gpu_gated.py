@@ -249,6 +249,15 @@ def test_large(lq, torch, case):
         check_backward(lq, torch, L, saved_t=False)
 
 
+@pytest.mark.parametrize("case", [
+    # grad_X in 64 x 64 tiles above the CUs' count; the forward in 256 x 64 outputs
+    (200, 1088, 1500, [3, 64] * 20, "mixed", "nf4_dq", "silu", 0.0),
+    (1608, 1088, 1500, [16, 64], "runs", "codebook", "gelu", 0.2),
+], ids=str)
+def test_more_small_tiles_than_compute_units(lq, torch, case):
+    test_large(lq, torch, case)
+
+
 @pytest.mark.parametrize("M", [3, 64, 70, 300, 2048])
 def test_no_token_has_an_adapter(lq, torch, M):
     """Every id outside the set: the result without sets, zero t, zero gradients."""
