@@ -11,12 +11,11 @@
 #include "lq_act.h"
 #include "lq_adapters.h"
 #include "lq_device.h"
+#include "lq_route.h"
 
 namespace lq {
 namespace {
 
-__device__ __forceinline__ u32x4_t ld16(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 // set bits of m below the lane
 __device__ __forceinline__ int bits_below(uint64_t m) {
   return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));

@@ -9,20 +9,12 @@
 #include "lq_act.h"
 #include "lq_adapters.h"
 #include "lq_device.h"
+#include "lq_route.h"
 
 namespace lq {
 namespace {
 
-__device__ __forceinline__ u32x4_t ld16(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 constexpr int GM = 256, GK = 64, G_THREADS = 512;
-
-// Memory to LDS, 16 bytes a lane: lane i's 16 bytes land at dst + 16 i.
-__device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-}
 
 // Wait until at most `n` of the wave's memory operations are outstanding.
 template <int n>

@@ -526,11 +526,6 @@ __global__ __launch_bounds__(64 * W) void k_adapter_down(DownJobs jobs, int64_t 
 // ===========================================================================
 constexpr int DT_M = 64, DT_K = 64, DT_RING = 4;
 
-__device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-}
-
 template <int BN, bool DROP>
 __global__ __launch_bounds__(256) void k_adapter_down_tiles(DownJobs jobs, int64_t M, Route rt, const uint16_t* zeros) {
   constexpr int CT = BN / 16, QW = BN >= 32 ? BN / 32 : 1, RING = DROP ? 3 : DT_RING;

@@ -7,13 +7,12 @@
 // 4.9 TB/s, where a copy of 1 GiB reaches 5.05. Small ones are bound by the launch:
 // 300 x 1021 float16, 3 us.
 #include "lq_dropout.h"
+#include "lq_route.h"
 
 namespace lq {
 namespace {
 
 constexpr int DROP_THREADS = 256, DROP_U = 2;
-
-__device__ __forceinline__ u32x4_t ld16(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
 
 template <int DT>
 struct Elem;

@@ -1,4 +1,4 @@
-// Device helpers of the kernels that work on routed tokens: the runs of one
+// Device helpers of the kernels that work on routed tokens: loads, the runs of one
 // adapter's tokens, fragments read transposed from LDS, a barrier.
 #pragma once
 
@@ -8,6 +8,11 @@ namespace lq {
 
 __device__ __forceinline__ u32x4_t ld16(const void* p) { return *reinterpret_cast<const u32x4_t*>(p); }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+// Memory to LDS, 16 bytes a lane: lane i's 16 bytes land at dst + 16 i.
+__device__ __forceinline__ void load_lds16(const uint16_t* src, uint16_t* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
 
 // Item b of the segments [off[a], off[a + 1]), a < nseg, cut into pieces of
 // `rows` sorted positions: its segment, first position and row count. With
