@@ -87,8 +87,8 @@ constexpr int DC_RECORDS = 64 * 12 + DC_PAD;      // of a side
 // adds them. The workgroups past the adapters' lay X out for the projection's
 // fragments (xp, see XPack): a load of 16 rows is then 1 KB in one piece, where
 // the rows themselves are 64 pieces of 16 bytes in 32 cache lines. Bound by
-// latency: one token 4.4 us, 16 tokens of 16 adapters 5.6 (K = 4096), 64 tokens
-// of 32 adapters, K = 8192, 13.
+// latency: one token 4.3 us, 16 tokens of 16 adapters 5.1 (K = 4096), 64 tokens
+// of 32 adapters, K = 8192, 10.6.
 //
 // PAIR: the adapters of two sets, side 1's workgroups after side 0's, and its
 // steps after side 0's. A pair may have no sets (n = 0): the steps past the last
@@ -281,11 +281,11 @@ __global__ __launch_bounds__(64 * W) void k_decode_down(DecodeDown<PAIR> p) {
 //
 // Four row groups run in workgroups of four waves, two of them per CU, fewer in
 // workgroups of eight. Measured, 64 tokens, N = 28672, K = 8192, 32 adapters of
-// rank 8 to 32: 71 us, that is 1.7 TB/s of codes, the launch before it 13. A
+// rank 8 to 32: 71 us, that is 1.7 TB/s of codes, the launch before it 10.6. A
 // workgroup's 60 us are 9 of start, 10 of the adapters' part (B is read from
 // memory, 34 MB in all) and 38 of the stages, whose lookups and products wait
 // for one another at two waves a SIMD: 64 tokens' sums and X take 128 registers.
-// 16 tokens, N = K = 4096: 7.9 us after 5.6; one token: 7.5 after 4.4 (forming
+// 16 tokens, N = K = 4096: 7.8 us after 5.1; one token: 7.0 after 4.3 (forming
 // t in the projection instead took 14.0 in all).
 //
 // GATED: the first half of the row groups are the gate's, the second half the

@@ -177,7 +177,9 @@ __device__ __forceinline__ void with_act(int act, const F& f) {
 // belong to several adapters, their steps at its end.
 //
 // DROP (grad_X behind dropout): the adapters' part is always formed apart, after
-// the main loop, and added where the generator keeps the output.
+// the main loop, and added where the generator keeps the output. The masks spill 12
+// registers of the 256 x 256 tiles, a pair's 24, around the loop that adds; nothing else
+// here spills.
 //
 // GATED: a wave's 64 weight rows are 32 of the gate (part 0) and the same 32 of
 // up (part 1), so that a lane ends with g and u of the same outputs, whose
@@ -187,7 +189,7 @@ __device__ __forceinline__ void with_act(int act, const F& f) {
 // written once. In both, a tile whose tokens share one adapter runs on over its
 // steps of side 0, then of side 1 (a gated step multiplies its own side's rows
 // alone). Measured, both weights 4096 -> 11008: 4096 tokens of four adapters of
-// rank 64, g and u kept, 706 to 782 us (0.94 to 1.04 PFLOP/s), without adapters and
+// rank 64, g and u kept, 693 to 782 us (0.94 to 1.07 PFLOP/s), without adapters and
 // kept outputs 560; 1999 tokens of eight 331 to 368; grad_X 550 to 595. One library
 // product of both weights' rows takes 626 at 4096 tokens, 407 at 1999.
 template <int BN, bool OUT_F32, bool BWD, bool DROP, int MODE>

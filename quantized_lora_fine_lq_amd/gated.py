@@ -167,7 +167,8 @@ def gated_backward(pair: GatedPair, X, G, ids, saved: GatedSaved, need_grad_x: b
     """Gradients for G = dL/dH (bf16 [M, N]; N % 8 == 0) as GatedGrads, each None
     if not needed (without adapters: grad_X alone). saved: the forward's; its t
     may be None, to be formed again from X. dropout: the forward's, on the key as
-    it stood there."""
+    it stood there. dg and du are float32 in the adapters' gradients and bfloat16 in
+    grad_X's product with the weights."""
     torch = _torch()
     dev = pair.device
     N, K = pair.N, pair.K
