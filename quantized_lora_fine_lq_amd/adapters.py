@@ -10,6 +10,7 @@ memory and the current stream, the library's HIP kernels do the arithmetic.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple
 
 from . import (LQ_BF16, LQ_F32, QWeight, _check, _contig_cuda, _dtype_code, _ptr, _torch, c_f32, c_i32, c_i64,
@@ -133,9 +134,17 @@ class _Here:
 _HERE = _Here()
 
 
+@functools.lru_cache(maxsize=None)
+def _several_devices():
+    import torch
+    return torch.cuda.device_count() > 1
+
+
 def on_device(torch, dev):
     """A launch goes to the current device: makes dev that, where it is not."""
-    return _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
+    if not _several_devices() or torch._C._cuda_getDevice() == dev.index:
+        return _HERE
+    return torch.cuda.device(dev)
 
 
 def _tokens(torch, x, name, cols, device):
